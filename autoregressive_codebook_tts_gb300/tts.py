@@ -23,9 +23,10 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-TTS_F32, TTS_BF16, TTS_Q8_0 = 0, 1, 2
+TTS_F32, TTS_BF16, TTS_Q8_0, TTS_I8, TTS_E4M3 = 0, 1, 2, 3, 4
 Q8_0_BLOCK, Q8_0_BYTES = 32, 34  # entries and bytes of a Q8_0 block
 TTS_MAX_TABLES = 16
+TTS_MAX_TREE_NODES = 64
 TTS_KV_PREFETCH_BEFORE_WAIT = 1
 
 EFLAG_ID_RANGE = 1
@@ -49,6 +50,13 @@ EXPORTED = [
     "tts_decode_layer_scratch_size",
     "tts_decode_layer_launch_count",
     "tts_decode_layer",
+    "tts_rope_table_scaled",
+    "tts_rope_rows",
+    "tts_kv_write_rows",
+    "tts_kv_read_rows",
+    "tts_tree_attn_workspace_size",
+    "tts_tree_attn",
+    "tts_tree_commit",
 ]
 
 
@@ -72,6 +80,17 @@ class TtsLayerWeights(ctypes.Structure):
                 ("w_down", ctypes.c_void_p), ("gamma_attn", ctypes.c_void_p),
                 ("gamma_mlp", ctypes.c_void_p), ("gamma_q", ctypes.c_void_p),
                 ("gamma_k", ctypes.c_void_p), ("hidden", ctypes.c_int32), ("inter", ctypes.c_int32)]
+
+
+class TtsRopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("original_max_pos", ctypes.c_int32),
+                ("factor", ctypes.c_double), ("low_rotations", ctypes.c_double),
+                ("high_rotations", ctypes.c_double), ("attn_scale", ctypes.c_double)]
+
+
+class TtsKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 _P, _I32, _I64, _F, _D, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
@@ -109,6 +128,18 @@ _sigs = {
                           ctypes.POINTER(TtsKvDesc), _P, _F, _P, _SZ, _I32, _P, _P], _I32),
     "tts_prefill_step": ([_P, _P, _P, _I64, _P, _P, _F, _P, _I32, _P, _P,
                           ctypes.POINTER(TtsKvDesc), _P, _I32, _F, _P, _P, _SZ, _I32, _P, _P], _I32),
+    "tts_rope_table_scaled": ([_P, _I32, _I32, _D, ctypes.POINTER(TtsRopeScaling), _P], _I32),
+    "tts_rope_rows": ([_P, _I64, _P, _I64, _I32, _P, _I64, _P, _I64, _I32, _P, _P, _F, _P, _I32,
+                       _I32, _I32, _I32, _I32, _I32, _P, _I32, _P, _P], _I32),
+    "tts_kv_write_rows": ([_P, _P, _I32, _I64, ctypes.POINTER(TtsKvCache),
+                           ctypes.POINTER(TtsKvDesc), _P, _P, _I32, _P, _P], _I32),
+    "tts_kv_read_rows": ([ctypes.POINTER(TtsKvCache), ctypes.POINTER(TtsKvDesc), _P, _P, _I32, _P,
+                          _P, _I32, _I64, _P, _P], _I32),
+    "tts_tree_attn_workspace_size": ([ctypes.POINTER(TtsKvDesc), _I32, _I32], _SZ),
+    "tts_tree_attn": ([_P, _I32, _I64, ctypes.POINTER(TtsKvCache), ctypes.POINTER(TtsKvDesc), _P,
+                       _P, _P, _I32, _F, _P, _P, _SZ, _P, _P], _I32),
+    "tts_tree_commit": ([ctypes.POINTER(TtsKvCache), ctypes.POINTER(TtsKvDesc), _P, _P, _I64, _P,
+                         _I32, _P, _P], _I32),
 }
 for _name, (_args, _ret) in _sigs.items():
     _fn = getattr(_lib, _name)
@@ -162,12 +193,15 @@ def status_str(status: int) -> str:
 # ---------------------------------------------------------------------------
 # Descriptors
 # ---------------------------------------------------------------------------
+_KV_CODES = {"f32": TTS_F32, "bf16": TTS_BF16, "i8": TTS_I8, "e4m3": TTS_E4M3}
+
+
 def kv_desc(B, n_q_heads, n_kv_heads, head_dim, capacity, kv_dtype="f32", window_quantum=256,
             paged=False, page_size=16, n_pages=0, block_table=None, flags=0) -> TtsKvDesc:
     d = TtsKvDesc()
     d.B, d.n_q_heads, d.n_kv_heads, d.head_dim, d.capacity = B, n_q_heads, n_kv_heads, head_dim, capacity
     d.window_quantum = window_quantum
-    d.kv_dtype = TTS_F32 if kv_dtype == "f32" else TTS_BF16
+    d.kv_dtype = _KV_CODES.get(kv_dtype, TTS_BF16)
     d.paged = 1 if paged else 0
     d.page_size = page_size if paged else 0
     d.n_pages = n_pages if paged else 0
@@ -387,6 +421,211 @@ def tts_decode_layer(h, weights: TtsLayerWeights, eps, cs, max_pos, k_cache, v_c
                                  _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc), _ptr(cur_len),
                                  float(scale), _ptr(scratch), scratch.numel() * scratch.element_size(),
                                  n_splits, _ptr(err_flag), _stream(stream)), "tts_decode_layer")
+
+
+# ---------------------------------------------------------------------------
+# Drafted decoding over a quantised cache
+# ---------------------------------------------------------------------------
+_ROW_CODES = {torch.float32: TTS_F32, torch.bfloat16: TTS_BF16}
+_KV_TORCH = {TTS_F32: torch.float32, TTS_BF16: torch.bfloat16, TTS_I8: torch.int8,
+             TTS_E4M3: torch.float8_e4m3fn}
+_ROPE_KINDS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+
+def _rows(t, what, width=None):
+    """Checks a [rows, width] view whose rows are contiguous; returns (dtype code, stride)."""
+    code = _ROW_CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} must be float32 or bfloat16")
+    if t.dim() != 2 or t.stride(1) != 1 or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{what} must be a 2-d view of contiguous rows"
+                         + ("" if width is None else f" of {width} entries"))
+    # one row has no stride of its own
+    return code, t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _ints(t, what, n, dtype=torch.int32):
+    if t is None:
+        return
+    if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} entries")
+
+
+def _one_device(first, *others):
+    """Every tensor on first's device, and that device the current one (launches go there)."""
+    d = first.device
+    for t in others:
+        if t is not None and t.device != d:
+            raise ValueError(f"tensors on {d} and {t.device}: all arguments must be on one device")
+    if d.type != "cuda" or d.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {d}, which is not the current CUDA device")
+
+
+def kv_cache(k, v, k_scale=None, v_scale=None) -> TtsKvCache:
+    """A layer's cache: K and V tensors (float32, bfloat16, or 8-bit codes as int8 or
+    float8_e4m3fn), and for 8-bit codes the float32 scales of their rows (the shape of K
+    without its last dimension).  The caller keeps them alive."""
+    scaled = k.dtype in (torch.int8, torch.float8_e4m3fn)
+    if k.dtype not in _KV_TORCH.values() or v.dtype != k.dtype or v.shape != k.shape or \
+            not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError("K and V must be contiguous tensors of one cache dtype and shape")
+    for s in (k_scale, v_scale):
+        if scaled != (s is not None):
+            raise ValueError("8-bit caches, and only they, take k_scale and v_scale")
+        if scaled and (s.dtype != torch.float32 or s.shape != k.shape[:-1] or not s.is_contiguous()):
+            raise ValueError("scales must be contiguous float32, one per cache row")
+    for t in (v, k_scale, v_scale):
+        if t is not None and t.device != k.device:
+            raise ValueError("K, V and their scales must be on one device")
+    c = TtsKvCache(k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+                   None if v_scale is None else v_scale.data_ptr())
+    c.dtype, c.shape, c.device = k.dtype, tuple(k.shape), k.device
+    return c
+
+
+def _cache_fits(cache: TtsKvCache, desc: TtsKvDesc):
+    """The tensors behind `cache` are what `desc` says (the library only sees pointers)."""
+    rows = ((desc.n_pages, desc.n_kv_heads, desc.page_size, desc.head_dim) if desc.paged
+            else (desc.B, desc.n_kv_heads, desc.capacity, desc.head_dim))
+    if cache.dtype != _KV_TORCH.get(desc.kv_dtype) or cache.shape != rows:
+        raise ValueError(f"the descriptor's cache is {_KV_TORCH.get(desc.kv_dtype)} {rows}, "
+                         f"the tensors are {cache.dtype} {cache.shape}")
+
+
+def tts_rope_table_scaled(cs, max_pos, rot_dim, base, kind="none", factor=1.0, original_max_pos=1,
+                          low_rotations=1.0, high_rotations=32.0, attn_scale=1.0, stream=None):
+    """A (cos, sin) table cs [max_pos, rot_dim / 2, 2] for a longer window: kind "none",
+    "linear", "base" or "parts" (include/tts_decode.h states the formulas)."""
+    if kind not in _ROPE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(_ROPE_KINDS)}")
+    if cs.dtype != torch.float32 or not cs.is_contiguous() or cs.numel() < max_pos * rot_dim:
+        raise ValueError("cs must be contiguous float32 of max_pos * rot_dim entries")
+    _one_device(cs)
+    s = TtsRopeScaling(_ROPE_KINDS[kind], original_max_pos, float(factor), float(low_rotations),
+                       float(high_rotations), float(attn_scale))
+    _check(_lib.tts_rope_table_scaled(_ptr(cs), max_pos, rot_dim, float(base), ctypes.byref(s),
+                                      _stream(stream)), "tts_rope_table_scaled")
+
+
+def tts_rope_rows(q, k, q_out, k_out, pos, n_q_heads, n_kv_heads, head_dim, cs, gamma_q=None,
+                  gamma_k=None, eps=1e-6, interleaved=False, err_flag=None, stream=None):
+    """q [rows, n_q_heads * head_dim] and k (or None) rotated into q_out and k_out at pos
+    [rows]; cs [max_pos, rot_dim / 2, 2] sets how much of each head turns.  Rows may be
+    strided views; float32 or bfloat16 in and out; q_out and k_out may be q and k."""
+    if k is None:
+        n_kv_heads, k_out = 0, None
+    qd, kd = n_q_heads * head_dim, n_kv_heads * head_dim
+    dt, qs = _rows(q, "q", qd)
+    odt, qos = _rows(q_out, "q_out", qd)
+    ks = kos = 0
+    n = q.shape[0]
+    if k is not None:
+        kdt, ks = _rows(k, "k", kd)
+        kodt, kos = _rows(k_out, "k_out", kd)
+        if kdt != dt or kodt != odt or k.shape[0] != n or k_out.shape[0] != n:
+            raise ValueError("q and k must be of one dtype and row count, and so their outputs")
+    if q_out.shape[0] != n:
+        raise ValueError("q_out must have q's rows")
+    _ints(pos, "pos", n)
+    for gm in (gamma_q, gamma_k):
+        if gm is not None:
+            _ints(gm, "gamma", head_dim, torch.float32)
+    if cs.dim() != 3 or cs.dtype != torch.float32 or not cs.is_contiguous() or cs.shape[2] != 2:
+        raise ValueError("cs must be a contiguous float32 [max_pos, rot_dim / 2, 2] table")
+    _one_device(q, k, q_out, k_out, pos, cs, gamma_q, gamma_k, err_flag)
+    _check(_lib.tts_rope_rows(_ptr(q), qs, _ptr(k), ks, dt, _ptr(q_out), qos, _ptr(k_out), kos, odt,
+                              _ptr(gamma_q), _ptr(gamma_k), float(eps), _ptr(pos), n, n_q_heads,
+                              n_kv_heads, head_dim, 2 * cs.shape[1], int(bool(interleaved)), _ptr(cs),
+                              cs.shape[0], _ptr(err_flag), _stream(stream)), "tts_rope_rows")
+
+
+def tts_kv_write_rows(k, v, cache: TtsKvCache, desc: TtsKvDesc, start_pos, T, n_rows=None,
+                      err_flag=None, stream=None):
+    """k, v [B * T, n_kv_heads * head_dim] (row b * T + t) into the cache at start_pos[b] + t,
+    quantised to its dtype; n_rows [B]: only the first n_rows[b] of stream b."""
+    kd = desc.n_kv_heads * desc.head_dim
+    dt, ks = _rows(k, "k", kd)
+    vdt, vs = _rows(v, "v", kd)
+    if vdt != dt or vs != ks or k.shape[0] != desc.B * T or v.shape[0] != desc.B * T:
+        raise ValueError("k and v must share dtype and stride and hold B * T rows")
+    _cache_fits(cache, desc)
+    _ints(start_pos, "start_pos", desc.B)
+    _ints(n_rows, "n_rows", desc.B)
+    _one_device(k, v, cache, start_pos, n_rows, err_flag)
+    _check(_lib.tts_kv_write_rows(_ptr(k), _ptr(v), dt, ks, ctypes.byref(cache), ctypes.byref(desc),
+                                  _ptr(start_pos), _ptr(n_rows), T, _ptr(err_flag), _stream(stream)),
+           "tts_kv_write_rows")
+
+
+def tts_kv_read_rows(cache: TtsKvCache, desc: TtsKvDesc, start_pos, T, k_out, v_out, n_rows=None,
+                     err_flag=None, stream=None):
+    """Cache rows start_pos[b] + t, t < min(T, n_rows[b]), as values into rows b * T + t of
+    k_out and v_out [B * T, n_kv_heads * head_dim]; other rows are left as they were."""
+    kd = desc.n_kv_heads * desc.head_dim
+    dt, ks = _rows(k_out, "k_out", kd)
+    vdt, vs = _rows(v_out, "v_out", kd)
+    if vdt != dt or vs != ks or k_out.shape[0] != desc.B * T or v_out.shape[0] != desc.B * T:
+        raise ValueError("k_out and v_out must share dtype and stride and hold B * T rows")
+    _cache_fits(cache, desc)
+    _ints(start_pos, "start_pos", desc.B)
+    _ints(n_rows, "n_rows", desc.B)
+    _one_device(k_out, v_out, cache, start_pos, n_rows, err_flag)
+    _check(_lib.tts_kv_read_rows(ctypes.byref(cache), ctypes.byref(desc), _ptr(start_pos), _ptr(n_rows),
+                                 T, _ptr(k_out), _ptr(v_out), dt, ks, _ptr(err_flag), _stream(stream)),
+           "tts_kv_read_rows")
+
+
+def _row_code(q_dtype):
+    code = {"f32": TTS_F32, "bf16": TTS_BF16}.get(q_dtype, _ROW_CODES.get(q_dtype))
+    if code is None:
+        raise ValueError("q_dtype must be \"f32\", \"bf16\" or the torch dtype")
+    return code
+
+
+def tts_tree_attn_workspace_size(desc: TtsKvDesc, T: int, q_dtype="f32") -> int:
+    return int(_lib.tts_tree_attn_workspace_size(ctypes.byref(desc), T, _row_code(q_dtype)))
+
+
+def tree_workspace(desc: TtsKvDesc, T: int, q_dtype="f32", device="cuda"):
+    """Allocate (through torch) a workspace for trees of up to T nodes."""
+    n = max(tts_tree_attn_workspace_size(desc, t, q_dtype) for t in range(1, T + 1))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def tts_tree_attn(q, cache: TtsKvCache, desc: TtsKvDesc, n_past, T, scale, out, ws, n_nodes=None,
+                  tree_mask=None, err_flag=None, stream=None):
+    """Attention of T drafted nodes a stream: q [B * T, n_q_heads * head_dim] (float32 or
+    bfloat16), out dense of q's dtype, tree_mask int64 [B, T] (bit u: node t sees node u; None:
+    the chain), n_nodes [B] (None: T each).  T = 1 without a mask decodes one token."""
+    dt, qs = _rows(q, "q", desc.n_q_heads * desc.head_dim)
+    if q.shape[0] != desc.B * T:
+        raise ValueError("q must hold B * T rows")
+    if out.dtype != q.dtype or out.numel() != q.shape[0] * q.shape[1] or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's dtype and size")
+    _cache_fits(cache, desc)
+    _ints(n_past, "n_past", desc.B)
+    _ints(n_nodes, "n_nodes", desc.B)
+    _ints(tree_mask, "tree_mask", desc.B * T, torch.int64)
+    _one_device(q, cache, n_past, n_nodes, tree_mask, out, ws, err_flag)
+    _check(_lib.tts_tree_attn(_ptr(q), dt, qs, ctypes.byref(cache), ctypes.byref(desc), _ptr(n_past),
+                              _ptr(n_nodes), _ptr(tree_mask), T, float(scale), _ptr(out), _ptr(ws),
+                              0 if ws is None else ws.numel() * ws.element_size(), _ptr(err_flag),
+                              _stream(stream)), "tts_tree_attn")
+
+
+def tts_tree_commit(cache: TtsKvCache, desc: TtsKvDesc, n_past, path, n_accept, T, err_flag=None,
+                    stream=None):
+    """The accepted path's rows to the front of the tree's: path [B, T] int32 (rows may be
+    strided), its first n_accept[b] entries strictly ascending node indices."""
+    if path.dtype != torch.int32 or path.dim() != 2 or path.shape != (desc.B, T) or path.stride(1) != 1:
+        raise ValueError("path must be an int32 [B, T] view of contiguous rows")
+    _cache_fits(cache, desc)
+    _ints(n_past, "n_past", desc.B)
+    _ints(n_accept, "n_accept", desc.B)
+    _one_device(path, cache, n_past, n_accept, err_flag)
+    _check(_lib.tts_tree_commit(ctypes.byref(cache), ctypes.byref(desc), _ptr(n_past), _ptr(path),
+                                path.stride(0) if desc.B > 1 else T, _ptr(n_accept), T, _ptr(err_flag),
+                                _stream(stream)), "tts_tree_commit")
 
 
 def default_scale(head_dim: int) -> float:

@@ -66,8 +66,9 @@ extern "C" {
  * tts_abi_min_version() <= V <= tts_abi_version(); tts_abi_check(V) makes that test
  * inside the library and returns TTS_OK, or TTS_ERR_ABI for a V below the minimum or
  * above the current version.  (ABI 2 added tts_tables.dtype; ABI 3 added the `draw`
- * argument of tts_sample, tts_abi_check and Q8_0 codebook tables.) */
-#define TTS_ABI_VERSION 3
+ * argument of tts_sample, tts_abi_check and Q8_0 codebook tables; ABI 4 added the calls
+ * from tts_rope_table_scaled on, and changed no earlier one.) */
+#define TTS_ABI_VERSION 4
 #define TTS_ABI_MIN_VERSION 3
 int32_t tts_abi_version(void);
 int32_t tts_abi_min_version(void);
@@ -99,8 +100,10 @@ tts_status tts_abi_check(int32_t caller_version);
 #define TTS_EFLAG_TIMEOUT 16    /* a bounded in-kernel wait ran out; output invalid;
                                    re-zero the call's workspace before its next use */
 
-/* Element types.  KV caches: f32 or bf16.  Codebook tables: f32, bf16 or Q8_0. */
-typedef enum { TTS_F32 = 0, TTS_BF16 = 1, TTS_Q8_0 = 2 } tts_dtype;
+/* Element types.  KV caches: f32 or bf16; the calls that take a tts_kv_cache also I8 (signed
+ * 8-bit) and E4M3 (8-bit floating point: 4 exponent and 3 mantissa bits, largest value 448).
+ * Codebook tables: f32, bf16 or Q8_0. */
+typedef enum { TTS_F32 = 0, TTS_BF16 = 1, TTS_Q8_0 = 2, TTS_I8 = 3, TTS_E4M3 = 4 } tts_dtype;
 
 #define TTS_MAX_TABLES 16
 
@@ -444,6 +447,145 @@ tts_status tts_decode_layer(float* h, const tts_layer_weights* weights, float ep
                             void* v_cache, const tts_kv_desc* desc, const int32_t* cur_len,
                             float scale, void* scratch, size_t scratch_bytes, int32_t n_splits,
                             int32_t* err_flag, void* stream);
+
+/* ===========================================================================
+ * Drafted decoding over a quantised cache.  The paper has no counterpart: these calls
+ * extend the path above to steps that check several drafted tokens a stream at once (a
+ * tree of them), to 8-bit caches, and to other rotary layouts and longer windows.  They
+ * share its conventions (device pointers, stream order, status, err_flag, alignment).
+ * =========================================================================== */
+
+/* Rotary tables for long contexts.  With L = original_max_pos, f_i = base^(-2i/rot_dim),
+ * i < rot_dim/2:
+ *   TTS_ROPE_NONE    f_i
+ *   TTS_ROPE_LINEAR  f_i / factor                      (positions compressed)
+ *   TTS_ROPE_BASE    (base factor^(rot_dim/(rot_dim-2)))^(-2i/rot_dim)  (the base raised so
+ *                    that the slowest frequency is divided by factor, the fastest kept)
+ *   TTS_ROPE_PARTS   f_i (w_i + (1 - w_i) / factor), w_i = (r_i - low) / (high - low) clamped
+ *                    to [0, 1], r_i = L f_i / 2 pi the turns frequency i makes in the original
+ *                    window: frequencies of `high_rotations` turns or more are kept, those of
+ *                    `low_rotations` or fewer divided by factor
+ * and cs[p][i] = attn_scale * (cos, sin)(p f_i), angles in double, rounded to f32 once. */
+typedef enum { TTS_ROPE_NONE = 0, TTS_ROPE_LINEAR = 1, TTS_ROPE_BASE = 2, TTS_ROPE_PARTS = 3 } tts_rope_kind;
+typedef struct {
+  int32_t kind;             /* tts_rope_kind */
+  int32_t original_max_pos; /* PARTS: L, >= 1 */
+  double factor;            /* LINEAR, BASE, PARTS: >= 1 */
+  double low_rotations;     /* PARTS: >= 0, */
+  double high_rotations;    /*        above low_rotations */
+  double attn_scale;        /* every kind: finite, above 0 (1 = none) */
+} tts_rope_scaling;
+
+/* cs: device f32 [max_pos][rot_dim/2][2]; rot_dim even, 2..128 (BASE: at least 4). */
+tts_status tts_rope_table_scaled(float* cs, int32_t max_pos, int32_t rot_dim, double base,
+                                 const tts_rope_scaling* scaling, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions of q and k rows, with or without the per-head RMSNorm, out of place or
+ * in place.  Row r holds n_q_heads (n_kv_heads) heads of head_dim; for each head row x:
+ *   t = gamma ? x * (mean(x^2) + eps)^(-1/2) * gamma : x
+ *   (t_a, t_b) -> (t_a c - t_b s, t_a s + t_b c), (c, s) = rope_cs[pos[r]][i], i < rot_dim/2,
+ *   a = i, b = i + rot_dim/2 (half layout), or a = 2i, b = 2i + 1 (interleaved);
+ * entries from rot_dim on pass through (normed).  All arithmetic in f32, rounded to out_dtype
+ * once (bf16: to nearest even).
+ *   q, k: device rows of `dtype` (f32 or bf16), row r at q + r*q_stride elements; k may be NULL
+ *        with n_kv_heads 0.  Each stride keeps rows 16-byte aligned (a multiple of 4 f32 or 8
+ *        bf16 elements).
+ *   q_out, k_out: rows of out_dtype; may be q and k themselves (same dtype and stride), else
+ *        they must not overlap them.
+ *   gamma_q, gamma_k: device f32 [head_dim]; both NULL: no norm.
+ *   pos: device int32 [rows]; one outside [0, rope_max_pos) is clamped and sets
+ *        TTS_EFLAG_POS_RANGE.  rope_cs: a table of the same rot_dim (tts_rope_table with
+ *        head_dim = rot_dim, or tts_rope_table_scaled).
+ * ------------------------------------------------------------------------- */
+tts_status tts_rope_rows(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int32_t dtype,
+                         void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                         int32_t out_dtype, const float* gamma_q, const float* gamma_k, float eps,
+                         const int32_t* pos, int32_t rows, int32_t n_q_heads, int32_t n_kv_heads,
+                         int32_t head_dim, int32_t rot_dim, int32_t interleaved, const float* rope_cs,
+                         int32_t rope_max_pos, int32_t* err_flag, void* stream);
+
+/* A layer's K/V cache with its scales.  k and v as for tts_kv_desc, of its kv_dtype: f32,
+ * bf16, or 8-bit codes (I8, E4M3) with one f32 scale per cache row (position and kv head), at
+ * the same row index: contiguous k_scale[b][g][j], paged k_scale[page][g][slot].  A cache entry
+ * stands for code * scale.  k_scale and v_scale are NULL for f32 and bf16 caches. */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+} tts_kv_cache;
+
+/* ---------------------------------------------------------------------------
+ * Cache rows quantised as they are written.  Row r = b*T + t of k and v (n_kv_heads heads of
+ * head_dim, contiguous; `dtype` f32 or bf16; k + r*row_stride elements) goes to position
+ * start_pos[b] + t of stream b, for t < n_rows[b] (n_rows NULL: T rows of every stream):
+ *   8-bit, per head row x: s = f32(max|x| / Q), Q = 127 (I8) or 448 (E4M3); code = the code
+ *   nearest to the exact quotient x / s, ties to even, at most Q in magnitude; s = 0 (a row of
+ *   zeros, or below 2^-149 Q): codes 0; a row with a NaN or an infinity: scale NaN, codes 0
+ *   (so it reads back as NaN);
+ *   f32, bf16 caches: the entry itself, rounded to nearest even where bits are dropped.
+ * A position outside [0, capacity) or a page id outside [0, n_pages) skips that row and sets
+ * TTS_EFLAG_POS_RANGE / TTS_EFLAG_PAGE; n_rows[b] outside [0, T] is clamped and sets
+ * TTS_EFLAG_NVALID.  Nothing else in the cache is touched.  B*T must not exceed 2^24.
+ * Two streams whose block tables name one page must not write the same slot.
+ * ------------------------------------------------------------------------- */
+tts_status tts_kv_write_rows(const void* k, const void* v, int32_t dtype, int64_t row_stride,
+                             const tts_kv_cache* cache, const tts_kv_desc* desc, const int32_t* start_pos,
+                             const int32_t* n_rows, int32_t T, int32_t* err_flag, void* stream);
+
+/* The reverse: positions start_pos[b] + t, t < min(T, n_rows[b]), into rows r = b*T + t of k_out
+ * and v_out (n_kv_heads heads of head_dim; out_dtype f32 or bf16; row_stride elements), each
+ * entry the f32 product code * scale, for bf16 rounded to nearest even.  Rows t >= n_rows[b], and those whose position or page is
+ * out of range (flagged as above), are left as they were. */
+tts_status tts_kv_read_rows(const tts_kv_cache* cache, const tts_kv_desc* desc, const int32_t* start_pos,
+                            const int32_t* n_rows, int32_t T, void* k_out, void* v_out, int32_t out_dtype,
+                            int64_t row_stride, int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of a tree of drafted tokens over a cache.  Stream b holds n_past[b] committed rows
+ * and then the rows of its n = n_nodes[b] nodes at positions n_past[b] + u (written before, e.g.
+ * by tts_kv_write_rows; NULL n_nodes: T nodes in every stream).  Node t < n sees position j iff
+ *   j < n_past[b], or j = n_past[b] + u with u < n and bit u of tree_mask[b*T + t] set
+ * (a node sees its own row only through its own bit; tree_mask NULL: the chain, u <= t).
+ *   out[b][t][h] = sum_j softmax_j(scale * q[b][t][h] . K[b][g][j]) V[b][g][j],  g = h / (Hq/Hkv)
+ * over the positions it sees; a node that sees none gives 0.  Rows outside what a node sees,
+ * whatever they hold, do not affect it; a visible NaN or infinity gives NaN or infinity as the
+ * formula does.  T = 1 with a NULL mask is the single-token form: the window [0, n_past + 1).
+ *   q: device rows r = b*T + t of q_dtype (f32 or bf16), q + r*q_stride elements, heads
+ *        contiguous, rows 16-byte aligned.  out: q_dtype, dense [B][T][Hq][D]; rows t >= n are
+ *        left as they were.
+ *   n_past, n_nodes: device int32 [B].  n_nodes outside [0, T], n_past below 0, or more than
+ *        `capacity` rows in all are clamped (the nodes first) and set TTS_EFLAG_NVALID; a page id
+ *        outside [0, n_pages) inside the window reads page 0 and sets TTS_EFLAG_PAGE.
+ *   tree_mask: device uint64 [B][T], T <= TTS_MAX_TREE_NODES.
+ *   workspace: at least tts_tree_attn_workspace_size() bytes (computed for the device that runs
+ *        the call), 256-byte aligned; needs no clearing, and holds nothing between calls.  Calls
+ *        that overlap in time on the GPU must not share one.
+ * Statistics and sums in f32; with f32 q every product too.  With bf16 q over a bf16 or 8-bit
+ * cache the products run on the tensor cores, exact in q and K, with the softmax weights rounded
+ * to bf16 (nearest even) where they meet V.  Results do not depend on timing.
+ * ------------------------------------------------------------------------- */
+#define TTS_MAX_TREE_NODES 64
+size_t tts_tree_attn_workspace_size(const tts_kv_desc* desc, int32_t T, int32_t q_dtype);
+
+tts_status tts_tree_attn(const void* q, int32_t q_dtype, int64_t q_stride, const tts_kv_cache* cache,
+                         const tts_kv_desc* desc, const int32_t* n_past, const int32_t* n_nodes,
+                         const uint64_t* tree_mask, int32_t T, float scale, void* out, void* workspace,
+                         size_t ws_bytes, int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The accepted path of a tree moves to the front of the tree's rows: for i < n_accept[b], the
+ * cache row (K, V and scales) at n_past[b] + path[b*path_stride + i] goes to n_past[b] + i.  The
+ * path lists node indices below T, strictly ascending (parents come before children).  A
+ * stream whose path breaks that, or whose n_accept is outside [0, T], is left as it was and
+ * sets TTS_EFLAG_ID_RANGE; one whose rows would leave [0, capacity) likewise with
+ * TTS_EFLAG_POS_RANGE, one with a page id outside [0, n_pages) among those rows with
+ * TTS_EFLAG_PAGE.  n_past is only read: add n_accept to it afterwards (once for all layers).
+ * ------------------------------------------------------------------------- */
+tts_status tts_tree_commit(const tts_kv_cache* cache, const tts_kv_desc* desc, const int32_t* n_past,
+                           const int32_t* path, int64_t path_stride, const int32_t* n_accept, int32_t T,
+                           int32_t* err_flag, void* stream);
 
 #ifdef __cplusplus
 }
