@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libttsdecode.so")
 SOURCES = ["attn.cu", "small_kernels.cu", "api.cu", "noalloc.cu", "sample.cu", "layer.cu", "gemv_mma.cu", "prefill_attn.cu", "prefill_attn_tc.cu",
-           "draft_api.cu", "kv_rows.cu", "rope.cu", "tree_attn.cu"]
+           "draft_api.cu", "kv_rows.cu", "rope.cu", "tree_attn.cu", "tree_attn_tc.cu"]
 HEADERS = ["common.cuh", "kernels.h", "table_rows.cuh", "checks.h", "draft_kernels.h", "cache_view.cuh", "tree_plan.cuh"]
 ROOT = os.path.dirname(HERE)
 PUBLIC_HEADER = os.path.join(ROOT, "include", "tts_decode.h")

@@ -49,19 +49,21 @@ tts_status check_rows(const tts_kv_desc* d, int32_t dtype, int64_t stride, int32
 
 // The launch of a tree attention: row blocks, tiles and CTAs from shapes alone.
 struct TreePlan {
+  bool tc;              // tensor cores
   int rows, n_rb, tile, n_cta, whole;
   size_t part, total;   // bytes of the partial rows, and of the whole workspace
 };
 TreePlan tree_plan(const tts_kv_desc* d, int T, int q_dtype) {
-  (void)q_dtype;
   TreePlan t = {};
   const int rows = T * (d->n_q_heads / d->n_kv_heads);
-  t.rows = rows <= 8 ? 8 : 32;
+  // f32 operands would lose bits on the tensor cores
+  t.tc = q_dtype == TTS_BF16 && d->kv_dtype != TTS_F32;
+  t.rows = t.tc ? (rows <= 32 ? 32 : rows <= 64 ? 64 : 128) : (rows <= 8 ? 8 : 32);
   t.n_rb = (rows + t.rows - 1) / t.rows;
-  t.tile = 64;
+  t.tile = t.tc ? 128 : 64;
   const int64_t items = static_cast<int64_t>(d->B) * d->n_kv_heads * t.n_rb;
   t.whole = d->capacity <= 4 * t.tile;
-  t.n_cta = t.whole ? static_cast<int>(items) : 2 * sm_count();
+  t.n_cta = t.whole ? static_cast<int>(items) : (t.tc ? 1 : 2) * sm_count();
   if (!t.whole) {
     const size_t slots = static_cast<size_t>(t.n_cta) * 2 * t.rows;
     t.part = round256(slots * d->head_dim * sizeof(float));
@@ -240,7 +242,8 @@ tts_status tts_tree_attn(const void* q, int32_t q_dtype, int64_t q_stride, const
   p.n_cta = t.n_cta;
   p.whole = t.whole;
   p.err = err_flag;
-  const cudaError_t e = launch_tree_attn(p, d->kv_dtype, d->head_dim, as_stream(stream));
+  const cudaError_t e = t.tc ? launch_tree_attn_tc(p, d->kv_dtype, d->head_dim, as_stream(stream))
+                             : launch_tree_attn(p, d->kv_dtype, d->head_dim, as_stream(stream));
   if (e != cudaSuccess || p.whole) return from_cuda(e);
   return from_cuda(launch_tree_combine(p, d->head_dim, as_stream(stream)));
 }

@@ -83,7 +83,7 @@ __device__ __forceinline__ void write_head_row(void* cache, float* scale, int64_
     if (!live) return;
     using Code = typename CodeOf<KvT>::type;
     const bool bad = top >= 0x7f800000u;
-    const float s = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) / Code::kTop;
+    const float s = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) * (1.0f / Code::kTop);
     store_codes<Code>(static_cast<uint8_t*>(cache), at, x, s, bad || s == 0.f);
     if (lr == 0) scale[row] = s;
   } else {

@@ -1,0 +1,878 @@
+// Attention of a tree of drafted tokens over a bf16 or 8-bit cache, on the 5th-generation
+// tensor cores (bf16 queries).
+//
+// An item's query rows (nodes times the q heads of the kv head) are the MMA's M = 128, the
+// 128 cache rows of a tile its N.  With 32 or 64 rows to fill, the rows are there F = 4 or 2
+// times over: replica f of a row owns columns [f 128 / F, (f + 1) 128 / F) of every tile and
+// keeps its own softmax statistics and output row, so a thread has 128 / F scores a tile and
+// no two threads ever exchange anything inside the loop.  Two softmax warpgroups take even
+// and odd tiles, each with its own scores, statistics and output in tensor memory; so a row
+// ends as 2 F partial rows, which meet once per item in shared memory.
+//
+//   S = Q K^T          Q and K exact in bf16 (8-bit codes are; their scale multiplies S)
+//   P = 2^(S c - m)    f32, rounded to bf16 times V's row scale, and written over S in tensor
+//                      memory as the A operand of the second product
+//   O += P V           V as the MN-major operand.  The maximum in use moves only when a row's
+//                      grows by more than 2^8; then O is rescaled in tensor memory.
+//
+// Cache rows come by 16-byte asynchronous copies of four producer warps, which take any page
+// size and fill rows past the window with zeros.  bf16 rows land in the 128-byte swizzled
+// layout of the MMA directly.  8-bit rows land in a staging slot of the thread that copies
+// them; the same thread widens them to bf16 (integer and bf16 arithmetic, exact) into the
+// operand tile, and refills the slot at once, so two tiles stay in flight.
+//
+// Bound: HBM (a bf16 tile of 64 KB takes an SM 1.5 us of its share, its products 0.54 us on the
+// tensor cores); over 8-bit caches the widening, 4 (int8) to 5 (e4m3) operations a pair of
+// entries, is of the order of the tile's 0.75 us.
+//
+// The window is cut over one CTA per SM by cost (tree_plan.cuh).  Non-finite V entries of node
+// rows are handled as in tree_attn.cu.  Every wait is bounded; on expiry TTS_EFLAG_TIMEOUT is
+// set and the CTA winds down.
+#include <mutex>
+#include <type_traits>
+
+#include "tree_plan.cuh"
+
+namespace tts {
+namespace {
+
+constexpr int kM = 128, kN = 128;
+constexpr int kSmxThreads = 256, kProdThreads = 128;
+constexpr int kProducerWarp = 8, kMmaWarp = 12;
+constexpr int kThreads = 416;
+constexpr int kTmemCols = 512;            // S (P over it) 2 x 128, O 2 x 128
+constexpr int kBadSlots = 8;              // pieces the producers may be ahead of an epilogue, and more
+
+template <int D, typename KvT>
+struct TcCfg {
+  static constexpr bool k8 = CacheElem<KvT>::kScaled;
+  static constexpr int kTileBytes = kN * D * 2;                 // an operand tile
+  static constexpr int kStages = k8 ? 2 : (D == 128 ? 3 : 5);   // operand tiles of K, and of V
+  static constexpr int kStageBytes = k8 ? kN * D : 0;           // staged 8-bit tile (K or V)
+  static constexpr int kStaged = 2;                             // staged tiles
+  static constexpr int kQBytes = 32768;                         // Q, and the epilogue's 256 x 32 f32
+  static constexpr int kOffK = kQBytes, kOffV = kOffK + kStages * kTileBytes;
+  static constexpr int kOffStage = kOffV + kStages * kTileBytes;
+  static constexpr int kOffScale = kOffStage + kStaged * 2 * kStageBytes;   // [2][K, V][128] f32
+  static constexpr int kOffBar = kOffScale + (k8 ? 2048 : 0);
+  static constexpr size_t kSmem = kOffBar + 320;
+};
+
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);   // 128-byte swizzle
+}
+
+// Byte offset of 16-byte unit u of row r of a 128-row operand tile: chunks of 64 columns, 128
+// bytes a row, unit u of a chunk's row at u ^ r % 8.
+__device__ __forceinline__ uint32_t unit_off(int r, int u) {
+  return static_cast<uint32_t>((u >> 3) * (kN * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+               ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr) : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(taddr), "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+        "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+        "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+        "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+        "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+        "r"(__float_as_uint(v[15])), "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])),
+        "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])), "r"(__float_as_uint(v[20])),
+        "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
+        "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])),
+        "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])),
+        "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 bytes global -> shared; zeros when fill is false (the source is then not read).
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(copy ? 16 : 0) : "memory");
+}
+// Arrives on bar once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds128a(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// Named barrier over the softmax threads, and the same with the AND of every thread's v.
+__device__ __forceinline__ void smx_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool smx_sync_and(bool v) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\t"
+      "bar.red.and.pred po, 1, 256, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(out) : "r"(static_cast<uint32_t>(v)) : "memory");
+  return out != 0;
+}
+
+// Two 8-bit codes as packed bf16 values; x holds them in its two 16-bit halves.
+//   int8 (low bytes, 0 above): with the sign bit s and the low 7 bits m, 0x4300 | m is 128 + m
+//   and 0x4300 | s << 7 is 128 or 256: their difference is the code, exactly.
+//   e4m3 (high bytes): the exponent and mantissa bits shifted to bf16's places stand for the
+//   value times 2^-120 (subnormals too); the product with 2^120 is exact.
+__device__ __forceinline__ uint32_t widen_i8(uint32_t x) {
+  const uint32_t a = (x & 0x007f007fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t widen_e4m3(uint32_t x) {
+  const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+  const uint32_t k = 0x7b807b80u;   // 2^120
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Whether a word of four e4m3 codes holds a NaN (all seven low bits set).
+__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// 16 codes as 16 bf16 values (two 16-byte units).
+template <typename KvT>
+__device__ __forceinline__ void widen16(const uint4 v, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same<KvT, CodeI8>::value) {
+      o[2 * i] = widen_i8(__byte_perm(w[i], 0, 0x4140));
+      o[2 * i + 1] = widen_i8(__byte_perm(w[i], 0, 0x4342));
+    } else {
+      o[2 * i] = widen_e4m3(__byte_perm(w[i], 0, 0x1404));
+      o[2 * i + 1] = widen_e4m3(__byte_perm(w[i], 0, 0x3424));
+    }
+  }
+  if constexpr (std::is_same<KvT, CodeE4m3>::value) {
+    if ((e4m3_nan(w[0]) | e4m3_nan(w[1]) | e4m3_nan(w[2]) | e4m3_nan(w[3])) != 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t n = e4m3_nan(w[i]);
+        if (n & 0x00000080u) o[2 * i] = (o[2 * i] & 0xffff0000u) | 0x7fc0u;
+        if (n & 0x00008000u) o[2 * i] = (o[2 * i] & 0x0000ffffu) | 0x7fc00000u;
+        if (n & 0x00800000u) o[2 * i + 1] = (o[2 * i + 1] & 0xffff0000u) | 0x7fc0u;
+        if (n & 0x80000000u) o[2 * i + 1] = (o[2 * i + 1] & 0x0000ffffu) | 0x7fc00000u;
+      }
+    }
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// Replaces the non-finite ones of eight bf16 values by 0; whether there were any.
+__device__ __forceinline__ bool clear_nonfinite(uint4& v) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7f80u) == 0x7f80u) {
+      any = true;
+      w[i] &= 0xffff0000u;
+    }
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) {
+      any = true;
+      w[i] &= 0x0000ffffu;
+    }
+  }
+  v = make_uint4(w[0], w[1], w[2], w[3]);
+  return any;
+}
+
+// Every tile of a CTA's pieces, in order.
+struct TileWalk {
+  PieceWalk walk;
+  Piece it;
+  int tile, piece;
+  bool have;
+  __device__ __forceinline__ void init(const TreeParams& p, int cta) {
+    walk.init(p, cta);
+    piece = 0;
+    have = walk.get(p, it);
+    tile = it.t0;
+  }
+  __device__ __forceinline__ void next(const TreeParams& p) {
+    if (++tile >= it.t1) {
+      have = walk.get(p, it);
+      tile = it.t0;
+      ++piece;
+    }
+  }
+};
+
+// Addresses of the NR cache rows (row0 + i * step of a tile) that a producer thread copies.
+template <int NR>
+__device__ __forceinline__ void tile_rows(const TreeParams& p, const Piece& it, int tile, int row0, int step,
+                                          int64_t (&row)[NR], bool (&live)[NR]) {
+  const CacheView& c = p.cache;
+  const int r0 = tile * kN + row0, n_total = it.w.past + it.w.nodes;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int pos = r0 + i * step;
+    live[i] = pos < n_total;
+    row[i] = 0;
+    if (live[i]) {
+      int page = 0;
+      if (c.paged) {
+        page = cache_page(c, it.b, pos);
+        if (page < 0) {
+          bad = true;
+          page = 0;
+        }
+      }
+      row[i] = cache_row(c, it.b, it.g, pos, page);
+    }
+  }
+  if (bad) set_err(p.err, TTS_EFLAG_PAGE);
+}
+
+// Which of 32 columns a row sees, the first at node offset off (below 0: committed rows).
+__device__ __forceinline__ uint32_t visible32(int off, uint64_t see) {
+  if (off >= 64) return 0u;
+  if (off >= 0) return static_cast<uint32_t>(see >> off);
+  if (off > -32) return static_cast<uint32_t>(see << -off) | ((1u << -off) - 1u);
+  return ~0u;
+}
+
+// The largest of a row's 32 scores (8-bit caches: times the columns' scales).
+template <bool k8>
+__device__ __forceinline__ float max_scores(const float (&s)[32], const float* ksc, bool masked, uint32_t vis) {
+  float z[32];
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    float4 k = make_float4(1.f, 1.f, 1.f, 1.f);
+    if constexpr (k8) k = *reinterpret_cast<const float4*>(ksc + e);
+    z[e] = k8 ? s[e] * k.x : s[e];
+    z[e + 1] = k8 ? s[e + 1] * k.y : s[e + 1];
+    z[e + 2] = k8 ? s[e + 2] * k.z : s[e + 2];
+    z[e + 3] = k8 ? s[e + 3] * k.w : s[e + 3];
+  }
+  if (masked) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) z[e] = (vis >> e) & 1u ? z[e] : -INFINITY;
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+    for (int e = 0; e < o; ++e) z[e] = fmaxf(z[e], z[e + o]);
+  return z[0];
+}
+
+// The weights 2^(score - ms) of 32 columns, rounded to bf16 times the columns' V scales, and
+// their unrounded sum (without the scales).
+template <bool k8>
+__device__ __forceinline__ float weights(const float (&s)[32], const float* ksc, const float* vsc, float c, float ms,
+                                         bool masked, uint32_t vis, uint32_t (&pk)[16]) {
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  const float2 neg = make_float2(-ms, -ms);
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    float4 k = make_float4(c, c, c, c), v;
+    if constexpr (k8) {
+      k = *reinterpret_cast<const float4*>(ksc + e);
+      v = *reinterpret_cast<const float4*>(vsc + e);
+    }
+    float2 a = __ffma2_rn(make_float2(s[e], s[e + 1]), make_float2(k.x, k.y), neg);
+    float2 b = __ffma2_rn(make_float2(s[e + 2], s[e + 3]), make_float2(k.z, k.w), neg);
+    if (masked) {
+      a.x = (vis >> e) & 1u ? a.x : -INFINITY;
+      a.y = (vis >> (e + 1)) & 1u ? a.y : -INFINITY;
+      b.x = (vis >> (e + 2)) & 1u ? b.x : -INFINITY;
+      b.y = (vis >> (e + 3)) & 1u ? b.y : -INFINITY;
+    }
+    a.x = ex2(a.x); a.y = ex2(a.y); b.x = ex2(b.x); b.y = ex2(b.y);
+    sum[0] = __fadd2_rn(sum[0], a);
+    sum[1] = __fadd2_rn(sum[1], b);
+    if constexpr (k8) {
+      a = __fmul2_rn(a, make_float2(v.x, v.y));
+      b = __fmul2_rn(b, make_float2(v.z, v.w));
+      if (masked) {   // a row that is not seen has weight 0 whatever its scale
+        a.x = (vis >> e) & 1u ? a.x : 0.f;
+        a.y = (vis >> (e + 1)) & 1u ? a.y : 0.f;
+        b.x = (vis >> (e + 2)) & 1u ? b.x : 0.f;
+        b.y = (vis >> (e + 3)) & 1u ? b.y : 0.f;
+      }
+    }
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(b.x, b.y);
+    pk[e / 2] = *reinterpret_cast<const uint32_t*>(&x);
+    pk[e / 2 + 1] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  const float2 t = __fadd2_rn(sum[0], sum[1]);
+  return t.x + t.y;
+}
+
+// 2^(m - M) of a partial row; one that saw nothing has weight 0, one that only saw NaN scores
+// (which no maximum holds) passes its NaN on.
+__device__ __forceinline__ float partial_weight(float m, float l, float M) {
+  return m == -INFINITY ? (l != l ? 1.f : 0.f) : ex2(m - M);
+}
+
+// Adds the non-finite V entries of the node rows in `bits`, columns [col, col + 4).
+template <typename KvT, int D>
+__device__ __noinline__ void add_bad_v(const TreeParams& p, const Piece& it, unsigned long long bits, int col, float4& a) {
+  const CacheView& c = p.cache;
+  while (bits != 0) {
+    const int u = __ffsll(static_cast<long long>(bits)) - 1;
+    bits &= bits - 1;
+    const int pos = it.w.past + u, page = c.paged ? max(cache_page(c, it.b, pos), 0) : 0;
+    const int64_t row = cache_row(c, it.b, it.g, pos, page);
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (CacheElem<KvT>::kScaled)
+        x[e] = E4m3Code::value(static_cast<const uint8_t*>(c.v)[row * D + col + e]);   // int8 codes are finite
+      else
+        x[e] = static_cast<float>(static_cast<const __nv_bfloat16*>(c.v)[row * D + col + e]);
+      if ((__float_as_uint(x[e]) & 0x7f800000u) != 0x7f800000u) x[e] = 0.f;
+    }
+    a.x += x[0]; a.y += x[1]; a.z += x[2]; a.w += x[3];
+  }
+}
+
+template <int D, typename KvT, int F>
+__global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(const TreeParams p) {
+  using C = TcCfg<D, KvT>;
+  constexpr bool k8 = C::k8;
+  constexpr int NS = C::kStages;
+  constexpr int RP = kM / F;        // query rows of an item (padded)
+  constexpr int W = kN / F;         // columns a replica owns
+  extern __shared__ __align__(1024) unsigned char smem[];
+  float* stage = reinterpret_cast<float*>(smem);                          // epilogue: [256][32]
+  float* s_scale = reinterpret_cast<float*>(smem + C::kOffScale);         // [2][2][128]
+  uint64_t* fullK = reinterpret_cast<uint64_t*>(smem + C::kOffBar);       // [NS] K tile written
+  uint64_t* emptyK = fullK + NS;                                          // [NS] its product done
+  uint64_t* fullV = emptyK + NS;
+  uint64_t* emptyV = fullV + NS;
+  uint64_t* qready = emptyV + NS;                                         // the piece's query rows written, O free
+  uint64_t* sready = qready + 1;                                          // [2] S of the group's tile (and its scales)
+  uint64_t* pready = sready + 2;                                          // [2] P written, O rescaled
+  uint64_t* odone = pready + 2;                                           // [2] the group's last product of a piece
+  uint64_t* drained = odone + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
+  unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(drained + 2);   // [kBadSlots]
+  static_assert((4 * NS + 1 + 6 + 2 + kBadSlots) * 8 <= 320, "barrier area");
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&fullK[s], kProdThreads);
+      mbar_init(&emptyK[s], 1);
+      mbar_init(&fullV[s], kProdThreads);
+      mbar_init(&emptyV[s], 1);
+    }
+    mbar_init(qready, kSmxThreads);
+    for (int i = 0; i < 2; ++i) {
+      // the products' commit, and the issuer's own arrival, which passes on what it has seen
+      // of the producers' plain stores (scales, noted rows)
+      mbar_init(&sready[i], 2);
+      mbar_init(&pready[i], 128);
+      mbar_init(&odone[i], 2);
+    }
+    mbar_init(drained, 1);
+    for (int i = 0; i < kBadSlots; ++i) s_bad[i] = 0;
+    mbar_init_fence();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_u32(s_tmem)), "n"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const uint32_t tO = tmem + 2 * kN;
+  grid_wait();
+  grid_launch_dependents();
+
+  if (warp >= kProducerWarp && warp < kMmaWarp) {
+    // ---------------------------------------------------------------- producers
+    const int pt = tid - kProducerWarp * 32;
+    const CacheView& c = p.cache;
+    const unsigned char* gk = static_cast<const unsigned char*>(c.k);
+    const unsigned char* gv = static_cast<const unsigned char*>(c.v);
+    bool ok = true;
+    if constexpr (!k8) {
+      constexpr int UR = D / 8;                 // 16-byte units of a row
+      constexpr int STEP = kProdThreads / UR;   // rows the threads cover at once
+      constexpr int NR = kN / STEP;
+      const int u = pt % UR, row0 = pt / UR;
+      TileWalk w;
+      w.init(p, blockIdx.x);
+      for (int t = 0; w.have; ++t, w.next(p)) {
+        const int s = t % NS;
+        const uint32_t ph = static_cast<uint32_t>(t / NS - 1) & 1u;
+        int64_t row[NR];
+        bool live[NR];
+        tile_rows(p, w.it, w.tile, row0, STEP, row, live);
+        const uint32_t kd = smem_u32(smem + C::kOffK + s * C::kTileBytes), vd = smem_u32(smem + C::kOffV + s * C::kTileBytes);
+        if (t >= NS && !mbar_wait(&emptyK[s], ph)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) cp16(kd + unit_off(row0 + i * STEP, u), gk + row[i] * (D * 2) + u * 16, live[i]);
+        cp_arrive(&fullK[s]);
+        if (t >= NS && !mbar_wait(&emptyV[s], ph)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) cp16(vd + unit_off(row0 + i * STEP, u), gv + row[i] * (D * 2) + u * 16, live[i]);
+        if (w.tile * kN + kN > w.it.w.past) {
+          // node rows: non-finite entries are noted and cleared before the product
+          cp_commit();
+          cp_wait<0>();
+#pragma unroll 1
+          for (int i = 0; i < NR; ++i) {
+            const int pos = w.tile * kN + row0 + i * STEP;
+            if (pos < w.it.w.past || pos >= w.it.w.past + w.it.w.nodes) continue;
+            const uint32_t at = vd + unit_off(row0 + i * STEP, u);
+            uint4 x = lds128a(at);
+            if (clear_nonfinite(x)) {
+              sts128(at, x);
+              atomicOr(&s_bad[w.piece % kBadSlots], 1ull << (pos - w.it.w.past));
+            }
+          }
+          mbar_arrive(&fullV[s]);
+        } else {
+          cp_arrive(&fullV[s]);
+        }
+      }
+    } else {
+      constexpr int UR = D / 16;                // 16-byte units (16 codes) of a row
+      constexpr int STEP = kProdThreads / UR;
+      constexpr int NR = kN / STEP;
+      const int u = pt % UR, row0 = pt / UR;
+      const float sl = fabsf(p.scale_log2);
+      // this thread's slot i of staged tile s: at stage0 + s * 2 tiles + i * 2048 (K), + a tile (V)
+      const uint32_t stage0 = smem_u32(smem + C::kOffStage) + pt * 16;
+      TileWalk wi, w;   // tiles being copied, and being widened
+      wi.init(p, blockIdx.x);
+      w = wi;
+      float ks[2] = {0.f, 0.f}, vs[2] = {0.f, 0.f};   // scales of row pt of the staged tiles
+      auto scales = [&](float& k, float& v) {
+        int64_t r[1];
+        bool l[1];
+        tile_rows(p, wi.it, wi.tile, pt, 0, r, l);
+        k = l[0] ? __ldcg(c.k_scale + r[0]) * sl : 0.f;
+        v = l[0] ? __ldcg(c.v_scale + r[0]) : 0.f;
+      };
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (wi.have) {
+          int64_t row[NR];
+          bool live[NR];
+          tile_rows(p, wi.it, wi.tile, row0, STEP, row, live);
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            cp16(stage0 + s * 2 * C::kStageBytes + i * (kProdThreads * 16), gk + row[i] * D + u * 16, live[i]);
+            cp16(stage0 + (s * 2 + 1) * C::kStageBytes + i * (kProdThreads * 16), gv + row[i] * D + u * 16, live[i]);
+          }
+          scales(ks[s], vs[s]);
+          wi.next(p);
+        }
+        cp_commit();
+      }
+      // one tile: widen it from its slots, copying the tile two ahead into each as it empties
+      auto step = [&](int t, int s, float& ksr, float& vsr) {
+        const uint32_t ph = static_cast<uint32_t>(t / 2 - 1) & 1u;
+        int64_t row[NR];
+        bool live[NR];
+        const bool more = wi.have;
+        if (more) tile_rows(p, wi.it, wi.tile, row0, STEP, row, live);
+        cp_wait<1>();
+        const uint32_t kd = smem_u32(smem + C::kOffK + s * C::kTileBytes), vd = smem_u32(smem + C::kOffV + s * C::kTileBytes);
+        // the scales' slot is free once the product that used V(t - 2) is done
+        if (t >= 2 && (!mbar_wait(&emptyK[s], ph) || !mbar_wait(&emptyV[s], ph))) return false;
+        s_scale[s * 256 + pt] = ksr;
+        s_scale[s * 256 + 128 + pt] = vsr;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const uint32_t at = stage0 + s * 2 * C::kStageBytes + i * (kProdThreads * 16);
+          uint4 lo, hi;
+          widen16<KvT>(lds128a(at), lo, hi);
+          sts128(kd + unit_off(row0 + i * STEP, 2 * u), lo);
+          sts128(kd + unit_off(row0 + i * STEP, 2 * u + 1), hi);
+          if (more) cp16(at, gk + row[i] * D + u * 16, live[i]);
+        }
+        fence_async_smem();
+        mbar_arrive(&fullK[s]);
+        const bool nodes = std::is_same<KvT, CodeE4m3>::value && w.tile * kN + kN > w.it.w.past;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const uint32_t at = stage0 + (s * 2 + 1) * C::kStageBytes + i * (kProdThreads * 16);
+          uint4 lo, hi;
+          widen16<KvT>(lds128a(at), lo, hi);
+          if (nodes) {
+            const int pos = w.tile * kN + row0 + i * STEP;
+            const bool a = clear_nonfinite(lo), b = clear_nonfinite(hi);
+            if ((a || b) && pos >= w.it.w.past && pos < w.it.w.past + w.it.w.nodes)
+              atomicOr(&s_bad[w.piece % kBadSlots], 1ull << (pos - w.it.w.past));
+          }
+          sts128(vd + unit_off(row0 + i * STEP, 2 * u), lo);
+          sts128(vd + unit_off(row0 + i * STEP, 2 * u + 1), hi);
+          if (more) cp16(at, gv + row[i] * D + u * 16, live[i]);
+        }
+        fence_async_smem();
+        mbar_arrive(&fullV[s]);
+        if (more) {
+          scales(ksr, vsr);
+          wi.next(p);
+        }
+        cp_commit();
+        w.next(p);
+        return true;
+      };
+      for (int t = 0; w.have && ok; t += 2) {
+        ok = step(t, 0, ks[0], vs[0]);
+        if (ok && w.have) ok = step(t + 1, 1, ks[1], vs[1]);
+      }
+    }
+    if (!ok) set_err(p.err, TTS_EFLAG_TIMEOUT);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == kMmaWarp) {
+    // -------------------------------------------------------------- MMA issuer
+    PieceWalk walk;
+    walk.init(p, blockIdx.x);
+    if (lane == 0) {
+      // kind::f16, f32 accumulator, bf16 A and B, M = 128; S: N = 128, B (K) K-major; O: N = D,
+      // B (V) MN-major (bit 16)
+      constexpr uint32_t base = (1u << 4) | (1u << 7) | (1u << 10) | ((kM >> 4) << 24);
+      constexpr uint32_t idS = base | ((kN >> 3) << 17), idO = base | (1u << 16) | ((D >> 3) << 17);
+      const uint32_t qa = smem_u32(smem);
+      int gk = 0, gv = 0;                 // K and V tiles taken so far
+      uint32_t pph[2] = {0, 0};           // phases of pready
+      bool ok = true;
+      auto issue_s = [&](int wg) {
+        const int s = gk % NS;
+        if (!mbar_wait(&fullK[s], static_cast<uint32_t>(gk / NS) & 1u)) return false;
+        if (!k8) fence_async_smem();      // the copies' writes, before the products read them
+        tc_fence_after();
+        const uint32_t kb = smem_u32(smem + C::kOffK + s * C::kTileBytes), d = tmem + wg * kN;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          const uint32_t o = (j >> 2) * (kN * 128) + (j & 3) * 32;
+          mma_ss(d, smem_desc(qa + o, 16, 1024), smem_desc(kb + o, 16, 1024), idS, j > 0 ? 1u : 0u);
+        }
+        mma_commit(&sready[wg]);
+        mma_commit(&emptyK[s]);
+        mbar_arrive(&sready[wg]);
+        ++gk;
+        return true;
+      };
+      Piece it;
+      for (uint32_t piece = 0; ok && walk.get(p, it); ++piece) {
+        const int n = it.t1 - it.t0;
+        ok = mbar_wait(qready, piece & 1u) && issue_s(0) && (n < 2 || issue_s(1));
+        for (int i = 0; ok && i < n; ++i) {
+          const int wg = i & 1, s = gv % NS;
+          if (!mbar_wait(&pready[wg], pph[wg]) || !mbar_wait(&fullV[s], static_cast<uint32_t>(gv / NS) & 1u)) {
+            ok = false;
+            break;
+          }
+          pph[wg] ^= 1u;
+          if (!k8) fence_async_smem();
+          tc_fence_after();
+          const uint32_t vb = smem_u32(smem + C::kOffV + s * C::kTileBytes), a = tmem + wg * kN, d = tO + wg * D;
+#pragma unroll
+          for (int j = 0; j < kN / 16; ++j)
+            mma_ts(d, a + j * 8, smem_desc(vb + j * 2048, kN * 128, 1024), idO, (i > 1 || j > 0) ? 1u : 0u);
+          mma_commit(&emptyV[s]);
+          ++gv;
+          if (i + 2 < n) {
+            ok = issue_s(wg);
+          } else {
+            mma_commit(&odone[wg]);
+            mbar_arrive(&odone[wg]);
+          }
+        }
+      }
+      // no product is in flight when the CTA gives its tensor memory back
+      mma_commit(drained);
+      if (!mbar_wait(drained, 0)) ok = false;
+      if (!ok) set_err(p.err, TTS_EFLAG_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- softmax warps
+    const int wg = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;        // row of the MMA = TMEM lane
+    const int f = r / RP, rr = r % RP;           // replica (uniform in a warp), query row
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + wg * kN + lane_base, tOw = tO + wg * D + lane_base;
+    const float c = fabsf(p.scale_log2);
+    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;   // a negative scale turns q round
+    PieceWalk walk;
+    walk.init(p, blockIdx.x);
+    if (blockIdx.x == 0 && p.err != nullptr) {
+      bool any = false;
+      for (int b = tid; b < p.cache.B; b += kSmxThreads) {
+        bool bad;
+        tree_window(p, b, &bad);
+        any = any || bad;
+      }
+      if (any) set_err(p.err, TTS_EFLAG_NVALID);
+    }
+    uint32_t sph = 0, oph = 0;
+    int taken = 0;   // tiles of the pieces before
+    bool ok = true;
+    Piece it;
+    for (uint32_t piece = 0; walk.get(p, it); ++piece) {
+      const int first = it.rb * RP;   // of the stream and kv head's query rows
+      // the query rows, each written F times; rows without a node are 0
+      {
+        constexpr int UR = D / 8;
+        for (int i = tid; i < RP * UR; i += kSmxThreads) {
+          const int row = i / UR, u = i % UR, t = (first + row) / p.group, h = first + row - t * p.group;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (t < it.w.nodes) {
+            v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                      (static_cast<int64_t>(it.b) * p.T + t) * p.q_stride +
+                                                      (it.g * p.group + h) * D) + u);
+            v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+          }
+#pragma unroll
+          for (int k = 0; k < F; ++k) *reinterpret_cast<uint4*>(smem + unit_off(k * RP + row, u)) = v;
+        }
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(qready);
+      }
+      const int node = (first + rr) / p.group;
+      const uint64_t see = node < it.w.nodes ? seen_nodes(p, it.b, node, it.w.nodes) : 0ull;
+      const int n = it.t1 - it.t0;
+      float m = -INFINITY, l = 0.f;
+      for (int i = wg; ok && i < n; i += 2) {
+        const int base = (it.t0 + i) * kN + f * W;   // position of this thread's first column
+        const bool masked = (it.t0 + i) * kN + kN > it.w.past;
+        if (!__all_sync(kFull, mbar_wait(&sready[wg], sph))) {
+          ok = false;
+          break;
+        }
+        sph ^= 1u;
+        tc_fence_after();
+        // the scales of this thread's columns (8-bit; K's times |scale| log2 e): the slot is
+        // the operand stage of the tile
+        const float* ksc = s_scale + (((taken + i) & 1) * 256 + f * W);
+        const float* vsc = ksc + 128;
+        const int off = base - it.w.past;
+        float sv[32];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int cc = 0; cc < W / 32; ++cc) {
+          tmem_ld32(tS + f * W + 32 * cc, sv);
+          const uint32_t vis = masked ? visible32(off + 32 * cc, see) : ~0u;
+          mx = fmaxf(mx, max_scores<k8>(sv, ksc + 32 * cc, masked, vis));
+        }
+        if (!k8 && mx > -INFINITY) mx *= c;
+        const bool move = mx > m + 8.0f;
+        const bool rescale = move && m > -INFINITY;
+        const float alpha = rescale ? ex2(m - mx) : 1.0f;
+        if (__any_sync(kFull, rescale)) {
+          // O is complete up to the group's tile before: its product was issued before S
+#pragma unroll
+          for (int cc = 0; cc < D / 32; ++cc) {
+            float o[32];
+            tmem_ld32(tOw + 32 * cc, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tmem_st32(tOw + 32 * cc, o);
+          }
+        }
+        if (move) {
+          l *= alpha;
+          m = mx;
+        }
+        const float ms = m == -INFINITY ? 0.f : m;
+        // P over S: chunk cc's 16 packed columns lie below every S column still to be read
+#pragma unroll
+        for (int cc = 0; cc < W / 32; ++cc) {
+          if (W > 32) tmem_ld32(tS + f * W + 32 * cc, sv);
+          const uint32_t vis = masked ? visible32(off + 32 * cc, see) : ~0u;
+          uint32_t pk[16];
+          l += weights<k8>(sv, ksc + 32 * cc, vsc + 32 * cc, c, ms, masked, vis, pk);
+          tmem_st16(tS + (f * W + 32 * cc) / 2, pk);
+        }
+        if (F > 1) {
+          // the columns of the other replicas
+          const uint32_t zero[16] = {};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k / (4 / F) != f) tmem_st16(tS + 16 * k, zero);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&pready[wg]);
+      }
+      taken += n;
+      // ------------------------------------------------------------- epilogue
+      const bool had = wg < n;
+      if (ok && had) {
+        ok = __all_sync(kFull, mbar_wait(&odone[wg], oph));
+        oph ^= 1u;
+      }
+      ok = smx_sync_and(ok);   // every product of the piece is done: the query rows are free
+      if (!ok) break;
+      tc_fence_after();
+      float2* s_ml = reinterpret_cast<float2*>(stage);
+      s_ml[wg * kM + r] = had ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+      smx_sync();
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int x = 0; x < 2 * F; ++x) M = fmaxf(M, s_ml[(x & 1) * kM + (x >> 1) * RP + rr].x);
+#pragma unroll
+      for (int x = 0; x < 2 * F; ++x) {
+        const float2 ml = s_ml[(x & 1) * kM + (x >> 1) * RP + rr];
+        L = fmaf(ml.y, partial_weight(ml.x, ml.y, M), L);
+      }
+      const bool complete = it.complete();
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + it.slot();
+      float wt = had ? partial_weight(m, l, M) : 0.f;
+      if (complete) {
+        // nothing seen: 0; only scores of -inf: NaN, as the formula's 0 / 0
+        wt *= L == 0.f ? (it.w.past > 0 || see != 0 ? __uint_as_float(0x7fc00000u) : 0.f) : 1.f / L;
+      } else if (tid < RP) {
+        p.ml[slot * RP + rr] = make_float2(M, L);
+      }
+      const unsigned long long bad_v = s_bad[piece % kBadSlots];
+      smx_sync();   // the statistics are read; everyone has the noted rows
+      if (tid == 0) s_bad[piece % kBadSlots] = 0;
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        float o[32];
+        if (had) {
+          tmem_ld32(tOw + 32 * cc, o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= wt;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+        float* mine = stage + (wg * kM + r) * 32;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          *reinterpret_cast<float4*>(mine + ((u ^ (r & 7)) << 2)) = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        smx_sync();
+        for (int i = tid; i < RP * 8; i += kSmxThreads) {
+          const int row = i >> 3, u = i & 7, t = (first + row) / p.group, h = first + row - t * p.group;
+          if (t >= it.w.nodes) continue;
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int x = 0; x < 2 * F; ++x) {
+            const float4 v = *reinterpret_cast<const float4*>(stage + ((x & 1) * kM + (x >> 1) * RP + row) * 32 + ((u ^ (row & 7)) << 2));
+            a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+          }
+          if (bad_v != 0) add_bad_v<KvT, D>(p, it, bad_v & seen_nodes(p, it.b, t, it.w.nodes), 32 * cc + 4 * u, a);
+          if (complete)
+            store_tree_row4(p, it.b, t, it.g * p.group + h, D, 32 * cc + 4 * u, a, 1.f);
+          else
+            *reinterpret_cast<float4*>(p.part + (slot * RP + row) * D + 32 * cc + 4 * u) = a;
+        }
+        smx_sync();
+      }
+    }
+    if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
+  }
+}
+
+template <int D, typename KvT, int F>
+cudaError_t launch_t(const TreeParams& p, cudaStream_t s) {
+  auto kern = tree_attn_tc_kernel<D, KvT, F>;
+  constexpr size_t smem = TcCfg<D, KvT>::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(p.n_cta), dim3(kThreads), smem, s, p);
+}
+template <int D, typename KvT>
+cudaError_t launch_f(const TreeParams& p, cudaStream_t s) {
+  switch (p.rows) {
+    case 32: return launch_t<D, KvT, 4>(p, s);
+    case 64: return launch_t<D, KvT, 2>(p, s);
+    case 128: return launch_t<D, KvT, 1>(p, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+template <int D>
+cudaError_t launch_kv(const TreeParams& p, int kv_dtype, cudaStream_t s) {
+  switch (kv_dtype) {
+    case TTS_BF16: return launch_f<D, __nv_bfloat16>(p, s);
+    case TTS_I8: return launch_f<D, CodeI8>(p, s);
+    case TTS_E4M3: return launch_f<D, CodeE4m3>(p, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_attn_tc(const TreeParams& p, int kv_dtype, int head_dim, cudaStream_t s) {
+  return head_dim == 64 ? launch_kv<64>(p, kv_dtype, s) : launch_kv<128>(p, kv_dtype, s);
+}
+
+}  // namespace tts

@@ -520,10 +520,11 @@ typedef struct {
  * Cache rows quantised as they are written.  Row r = b*T + t of k and v (n_kv_heads heads of
  * head_dim, contiguous; `dtype` f32 or bf16; k + r*row_stride elements) goes to position
  * start_pos[b] + t of stream b, for t < n_rows[b] (n_rows NULL: T rows of every stream):
- *   8-bit, per head row x: s = f32(max|x| / Q), Q = 127 (I8) or 448 (E4M3); code = the code
- *   nearest to the exact quotient x / s, ties to even, at most Q in magnitude; s = 0 (a row of
- *   zeros, or below 2^-149 Q): codes 0; a row with a NaN or an infinity: scale NaN, codes 0
- *   (so it reads back as NaN);
+ *   8-bit, per head row x: s = max|x| * (1 / Q) in f32 (the constant 1 / Q rounded once, the
+ *   product once), Q = 127 (I8) or 448 (E4M3); code = the code nearest to the exact quotient
+ *   x / s, ties to even, at most Q in magnitude; s = 0 (a row of zeros, or so small that the
+ *   product is 0): codes 0; a row with a NaN or an infinity: scale NaN, codes 0 (so it reads
+ *   back as NaN);
  *   f32, bf16 caches: the entry itself, rounded to nearest even where bits are dropped.
  * A position outside [0, capacity) or a page id outside [0, n_pages) skips that row and sets
  * TTS_EFLAG_POS_RANGE / TTS_EFLAG_PAGE; n_rows[b] outside [0, T] is clamped and sets

@@ -29,7 +29,7 @@ def quantise(x, kv):
     top = np.abs(x).max(-1)
     bad = ~np.isfinite(x).all(-1)
     with np.errstate(all="ignore"):
-        s = (top / np.float32(TOP[kv])).astype(np.float32)
+        s = top * (np.float32(1) / np.float32(TOP[kv]))
         s[bad] = np.nan
         zero = bad | (s == 0)
         q = x.astype(np.float64) / np.where(zero, 1.0, s.astype(np.float64))[..., None]
