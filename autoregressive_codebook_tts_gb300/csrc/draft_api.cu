@@ -57,7 +57,7 @@ TreePlan tree_plan(const tts_kv_desc* d, int T, int q_dtype) {
   TreePlan t = {};
   const int rows = T * (d->n_q_heads / d->n_kv_heads);
   // f32 operands would lose bits on the tensor cores
-  t.tc = q_dtype == TTS_BF16 && d->kv_dtype != TTS_F32;
+  t.tc = q_dtype == TTS_BF16 && tree_attn_tc_supported(d);
   t.rows = t.tc ? (rows <= 32 ? 32 : rows <= 64 ? 64 : 128) : (rows <= 8 ? 8 : 32);
   t.n_rb = (rows + t.rows - 1) / t.rows;
   t.tile = t.tc ? 128 : 64;

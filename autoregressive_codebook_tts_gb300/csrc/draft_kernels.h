@@ -91,6 +91,7 @@ cudaError_t launch_commit(const CommitParams& p, cudaStream_t s);
 cudaError_t launch_rope_rows(const RopeRowsParams& p, cudaStream_t s);
 cudaError_t launch_rope_table_scaled(const RopeTableParams& p, cudaStream_t s);
 cudaError_t launch_tree_attn(const TreeParams& p, int kv_dtype, int head_dim, cudaStream_t s);
+bool tree_attn_tc_supported(const tts_kv_desc* d);
 cudaError_t launch_tree_attn_tc(const TreeParams& p, int kv_dtype, int head_dim, cudaStream_t s);
 cudaError_t launch_tree_combine(const TreeParams& p, int head_dim, cudaStream_t s);
 

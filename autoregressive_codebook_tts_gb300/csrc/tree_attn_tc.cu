@@ -15,11 +15,11 @@
 //   O += P V           V as the MN-major operand.  The maximum in use moves only when a row's
 //                      grows by more than 2^8; then O is rescaled in tensor memory.
 //
-// Cache rows come by 16-byte asynchronous copies of four producer warps, which take any page
-// size and fill rows past the window with zeros.  bf16 rows land in the 128-byte swizzled
-// layout of the MMA directly.  8-bit rows land in a staging slot of the thread that copies
-// them; the same thread widens them to bf16 (integer and bf16 arithmetic, exact) into the
-// operand tile, and refills the slot at once, so two tiles stay in flight.
+// One loader warp streams the cache with the TMA engine: a bf16 tile as tensor-map boxes (the
+// whole tile, or one box per page and 64 columns) that land in the 128-byte swizzled layout of
+// the MMA; an 8-bit tile as plain bulk copies into a staging tile, which four warps widen to
+// bf16 (integer and bf16 arithmetic, exact) into the operand tile.  In tiles with node rows, V
+// rows past the window are zeroed before their product (whatever a page holds there).
 //
 // Bound: HBM (a bf16 tile of 64 KB takes an SM 1.5 us of its share, its products 0.54 us on the
 // tensor cores); over 8-bit caches the widening, 4 (int8) to 5 (e4m3) operations a pair of
@@ -31,29 +31,31 @@
 #include <mutex>
 #include <type_traits>
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "tree_plan.cuh"
 
 namespace tts {
 namespace {
 
 constexpr int kM = 128, kN = 128;
-constexpr int kSmxThreads = 256, kProdThreads = 128;
-constexpr int kProducerWarp = 8, kMmaWarp = 12;
-constexpr int kThreads = 416;
+constexpr int kSmxThreads = 256, kWidenThreads = 128;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kWidenWarp = 10;
 constexpr int kTmemCols = 512;            // S (P over it) 2 x 128, O 2 x 128
-constexpr int kBadSlots = 8;              // pieces the producers may be ahead of an epilogue, and more
 
 template <int D, typename KvT>
 struct TcCfg {
   static constexpr bool k8 = CacheElem<KvT>::kScaled;
+  static constexpr int kThreads = k8 ? 448 : 320;
   static constexpr int kTileBytes = kN * D * 2;                 // an operand tile
   static constexpr int kStages = k8 ? 2 : (D == 128 ? 3 : 5);   // operand tiles of K, and of V
-  static constexpr int kStageBytes = k8 ? kN * D : 0;           // staged 8-bit tile (K or V)
-  static constexpr int kStaged = 2;                             // staged tiles
+  static constexpr int kRawBytes = k8 ? kN * D : 0;             // a staged 8-bit tile (K or V)
+  static constexpr int kRaw = 2;                                // staged tiles of K, and of V
   static constexpr int kQBytes = 32768;                         // Q, and the epilogue's 256 x 32 f32
   static constexpr int kOffK = kQBytes, kOffV = kOffK + kStages * kTileBytes;
-  static constexpr int kOffStage = kOffV + kStages * kTileBytes;
-  static constexpr int kOffScale = kOffStage + kStaged * 2 * kStageBytes;   // [2][K, V][128] f32
+  static constexpr int kOffRawK = kOffV + kStages * kTileBytes, kOffRawV = kOffRawK + kRaw * kRawBytes;
+  static constexpr int kOffScale = kOffRawV + kRaw * kRawBytes; // [2][K, V][128] f32
   static constexpr int kOffBar = kOffScale + (k8 ? 2048 : 0);
   static constexpr size_t kSmem = kOffBar + 320;
 };
@@ -74,21 +76,34 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// The products and their commits are issued by one elected lane of a converged warp, so every
+// operand is warp-uniform (the instructions take uniform registers).
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
       ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
       ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               ::"r"(smem_u32(bar)) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar)) : "memory");
+}
+// One arrival for a warp, after what all its lanes did before.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// A bounded wait of a converged warp, its outcome common to the lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(kFull, mbar_wait(bar, parity));
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
@@ -137,17 +152,15 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 16 bytes global -> shared; zeros when fill is false (the source is then not read).
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool copy) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(copy ? 16 : 0) : "memory");
+// A box of a tensor map at (column 0, row, 64-column chunk) into shared memory.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int row, int chunk, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(smem_u32(bar)),
+        "l"(policy)
+      : "memory");
 }
-// Arrives on bar once this thread's copies so far have landed.
-__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -259,33 +272,6 @@ struct TileWalk {
   }
 };
 
-// Addresses of the NR cache rows (row0 + i * step of a tile) that a producer thread copies.
-template <int NR>
-__device__ __forceinline__ void tile_rows(const TreeParams& p, const Piece& it, int tile, int row0, int step,
-                                          int64_t (&row)[NR], bool (&live)[NR]) {
-  const CacheView& c = p.cache;
-  const int r0 = tile * kN + row0, n_total = it.w.past + it.w.nodes;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int pos = r0 + i * step;
-    live[i] = pos < n_total;
-    row[i] = 0;
-    if (live[i]) {
-      int page = 0;
-      if (c.paged) {
-        page = cache_page(c, it.b, pos);
-        if (page < 0) {
-          bad = true;
-          page = 0;
-        }
-      }
-      row[i] = cache_row(c, it.b, it.g, pos, page);
-    }
-  }
-  if (bad) set_err(p.err, TTS_EFLAG_PAGE);
-}
-
 // Which of 32 columns a row sees, the first at node offset off (below 0: committed rows).
 __device__ __forceinline__ uint32_t visible32(int off, uint64_t see) {
   if (off >= 64) return 0u;
@@ -389,47 +375,140 @@ __device__ __noinline__ void add_bad_v(const TreeParams& p, const Piece& it, uns
   }
 }
 
+// One tile of K or V into `dst`, by a whole warp: bf16 in the operand layout (boxes of the
+// tensor map), 8-bit as it lies (bulk copies).  Rows past the window are not asked for, but for
+// the rest of a box.  `page` is the lane's entry of the tile's pages (lane pages apart).
+template <int D, typename KvT>
+__device__ __forceinline__ void load_tile(const TreeParams& p, const CUtensorMap* map, const unsigned char* base,
+                                          const Piece& it, int r0, int lane, unsigned char* dst, uint64_t* bar,
+                                          uint64_t policy) {
+  constexpr bool k8 = CacheElem<KvT>::kScaled;
+  const CacheView& c = p.cache;
+  const int n = min(kN, it.w.past + it.w.nodes - r0);   // rows of the window in the tile
+  const int ps = 1 << c.page_shift;
+  if (!c.paged || ps >= kN) {
+    if (lane == 0) {
+      int page = 0;
+      if (c.paged) {
+        page = cache_page(c, it.b, r0);
+        if (page < 0) {
+          set_err(p.err, TTS_EFLAG_PAGE);
+          page = 0;
+        }
+      }
+      const int64_t row = cache_row(c, it.b, it.g, r0, page);
+      if constexpr (k8) {
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * D));
+        bulk_g2s(dst, base + row * D, static_cast<uint32_t>(n * D), bar, policy);
+      } else {
+        mbar_arrive_expect_tx(bar, kN * D * 2);
+        tma_box(dst, map, static_cast<int>(row), 0, bar, policy);
+      }
+    }
+    return;
+  }
+  const int pages = (n + ps - 1) >> c.page_shift;
+  if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>((k8 ? n : pages << c.page_shift) * D * (k8 ? 1 : 2)));
+  __syncwarp();
+  for (int i = lane; i < pages; i += 32) {
+    const int pos = r0 + (i << c.page_shift);
+    int page = cache_page(c, it.b, pos);
+    if (page < 0) {
+      set_err(p.err, TTS_EFLAG_PAGE);
+      page = 0;
+    }
+    const int64_t row = cache_row(c, it.b, it.g, pos, page);
+    if constexpr (k8) {
+      const int rows = min(ps, n - (i << c.page_shift));
+      bulk_g2s(dst + (i << c.page_shift) * D, base + row * D, static_cast<uint32_t>(rows * D), bar, policy);
+    } else {
+#pragma unroll
+      for (int ch = 0; ch < D / 64; ++ch)
+        tma_box(dst + ch * (kN * 128) + (i << c.page_shift) * 128, map, static_cast<int>(row), ch, bar, policy);
+    }
+  }
+}
+
+// 128 x D codes of a staged tile to bf16 in the operand layout, by the widening threads: four
+// 16-code vectors of a thread at a time.
+template <int D, typename KvT>
+__device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned char* dst, int wt) {
+  constexpr int UR = D / 16, STEP = kWidenThreads / UR, NR = kN / STEP, BATCH = NR < 4 ? NR : 4;
+  const int u = wt % UR, row0 = wt / UR;
+  // half of the lanes that write one row store their second unit first: a phase's eight
+  // 16-byte units then lie in eight different bank groups
+  const int first = u >= UR / 2 ? 1 : 0;
+  // (rolled: the roles' loops together have to stay in the instruction cache)
+#pragma unroll 1
+  for (int i0 = 0; i0 < NR; i0 += BATCH) {
+    uint4 x[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) x[i] = *reinterpret_cast<const uint4*>(raw + wt * 16 + (i0 + i) * (kWidenThreads * 16));
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      uint4 lo, hi;
+      widen16<KvT>(x[i], lo, hi);
+      const int r = row0 + (i0 + i) * STEP;
+      *reinterpret_cast<uint4*>(dst + unit_off(r, 2 * u + first)) = first ? hi : lo;
+      *reinterpret_cast<uint4*>(dst + unit_off(r, 2 * u + 1 - first)) = first ? lo : hi;
+    }
+  }
+}
+
 template <int D, typename KvT, int F>
-__global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
+    tree_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                        const TreeParams p) {
   using C = TcCfg<D, KvT>;
   constexpr bool k8 = C::k8;
   constexpr int NS = C::kStages;
   constexpr int RP = kM / F;        // query rows of an item (padded)
   constexpr int W = kN / F;         // columns a replica owns
+  constexpr int UR = D / 8;         // 16-byte units of a bf16 row
   extern __shared__ __align__(1024) unsigned char smem[];
   float* stage = reinterpret_cast<float*>(smem);                          // epilogue: [256][32]
   float* s_scale = reinterpret_cast<float*>(smem + C::kOffScale);         // [2][2][128]
-  uint64_t* fullK = reinterpret_cast<uint64_t*>(smem + C::kOffBar);       // [NS] K tile written
+  uint64_t* fullK = reinterpret_cast<uint64_t*>(smem + C::kOffBar);       // [NS] operand tile written
   uint64_t* emptyK = fullK + NS;                                          // [NS] its product done
   uint64_t* fullV = emptyK + NS;
   uint64_t* emptyV = fullV + NS;
-  uint64_t* qready = emptyV + NS;                                         // the piece's query rows written, O free
+  uint64_t* rawK = emptyV + NS;                                           // [2] staged 8-bit tile landed
+  uint64_t* rawKe = rawK + 2;                                             // [2] and widened
+  uint64_t* rawV = rawKe + 2;
+  uint64_t* rawVe = rawV + 2;
+  uint64_t* qready = rawVe + 2;                                           // the piece's query rows written, O free
   uint64_t* sready = qready + 1;                                          // [2] S of the group's tile (and its scales)
   uint64_t* pready = sready + 2;                                          // [2] P written, O rescaled
   uint64_t* odone = pready + 2;                                           // [2] the group's last product of a piece
   uint64_t* drained = odone + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
-  unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(drained + 2);   // [kBadSlots]
-  static_assert((4 * NS + 1 + 6 + 2 + kBadSlots) * 8 <= 320, "barrier area");
+  unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(drained + 2);   // node rows with non-finite V
+  static_assert((4 * NS + 8 + 1 + 6 + 2 + 1) * 8 <= 320, "barrier area");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&fullK[s], kProdThreads);
+      mbar_init(&fullK[s], k8 ? kWidenThreads / 32 : 1);   // (arrivals are one a warp)
       mbar_init(&emptyK[s], 1);
-      mbar_init(&fullV[s], kProdThreads);
+      mbar_init(&fullV[s], k8 ? kWidenThreads / 32 : 1);
       mbar_init(&emptyV[s], 1);
     }
-    mbar_init(qready, kSmxThreads);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&rawK[i], 1);
+      mbar_init(&rawKe[i], kWidenThreads / 32);
+      mbar_init(&rawV[i], 1);
+      mbar_init(&rawVe[i], kWidenThreads / 32);
+    }
+    mbar_init(qready, kSmxThreads / 32);
     for (int i = 0; i < 2; ++i) {
       // the products' commit, and the issuer's own arrival, which passes on what it has seen
-      // of the producers' plain stores (scales, noted rows)
+      // of the widening threads' plain stores (the scales)
       mbar_init(&sready[i], 2);
-      mbar_init(&pready[i], 128);
-      mbar_init(&odone[i], 2);
+      mbar_init(&pready[i], 4);
+      mbar_init(&odone[i], 1);
     }
     mbar_init(drained, 1);
-    for (int i = 0; i < kBadSlots; ++i) s_bad[i] = 0;
+    *s_bad = 0;
     mbar_init_fence();
   }
   if (warp == kMmaWarp) {
@@ -445,215 +524,157 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(const TreePar
   grid_wait();
   grid_launch_dependents();
 
-  if (warp >= kProducerWarp && warp < kMmaWarp) {
-    // ---------------------------------------------------------------- producers
-    const int pt = tid - kProducerWarp * 32;
-    const CacheView& c = p.cache;
-    const unsigned char* gk = static_cast<const unsigned char*>(c.k);
-    const unsigned char* gv = static_cast<const unsigned char*>(c.v);
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------------ loader
+    constexpr int NL = k8 ? C::kRaw : NS;   // tiles of the ring that it fills
+    unsigned char* dk = smem + (k8 ? C::kOffRawK : C::kOffK);
+    unsigned char* dv = smem + (k8 ? C::kOffRawV : C::kOffV);
+    constexpr int bytes = k8 ? C::kRawBytes : C::kTileBytes;
+    uint64_t *fk = k8 ? rawK : fullK, *ek = k8 ? rawKe : emptyK, *fv = k8 ? rawV : fullV, *ev = k8 ? rawVe : emptyV;
+    const unsigned char* gk = static_cast<const unsigned char*>(p.cache.k);
+    const unsigned char* gv = static_cast<const unsigned char*>(p.cache.v);
+    const uint64_t policy = l2_evict_first_policy();
+    TileWalk w;
+    w.init(p, blockIdx.x);
     bool ok = true;
-    if constexpr (!k8) {
-      constexpr int UR = D / 8;                 // 16-byte units of a row
-      constexpr int STEP = kProdThreads / UR;   // rows the threads cover at once
-      constexpr int NR = kN / STEP;
-      const int u = pt % UR, row0 = pt / UR;
+    int nk = 0, nv = 0;
+    for (; w.have; w.next(p)) {
+      const int s = nk % NL, r0 = w.tile * kN;
+      const uint32_t ph = static_cast<uint32_t>(nk / NL - 1) & 1u;
+      if (nk >= NL && !warp_wait(&ek[s], ph)) {
+        ok = false;
+        break;
+      }
+      load_tile<D, KvT>(p, &kmap, gk, w.it, r0, lane, dk + s * bytes, &fk[s], policy);
+      ++nk;
+      if (nv >= NL && !warp_wait(&ev[s], ph)) {
+        ok = false;
+        break;
+      }
+      load_tile<D, KvT>(p, &vmap, gv, w.it, r0, lane, dv + s * bytes, &fv[s], policy);
+      ++nv;
+    }
+    if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
+    // every copy still in flight lands before the CTA ends (earlier ones were consumed)
+    for (int t = max(0, nk - NL); t < nk; ++t) mbar_wait(&fk[t % NL], static_cast<uint32_t>(t / NL) & 1u);
+    for (int t = max(0, nv - NL); t < nv; ++t) mbar_wait(&fv[t % NL], static_cast<uint32_t>(t / NL) & 1u);
+  } else if (k8 && warp >= kWidenWarp) {
+    // ----------------------------------------------------------------- widening
+    if constexpr (k8) {
+      const int wt = tid - kWidenWarp * 32;
+      const CacheView& c = p.cache;
+      const float sl = fabsf(p.scale_log2);
       TileWalk w;
       w.init(p, blockIdx.x);
-      for (int t = 0; w.have; ++t, w.next(p)) {
-        const int s = t % NS;
-        const uint32_t ph = static_cast<uint32_t>(t / NS - 1) & 1u;
-        int64_t row[NR];
-        bool live[NR];
-        tile_rows(p, w.it, w.tile, row0, STEP, row, live);
-        const uint32_t kd = smem_u32(smem + C::kOffK + s * C::kTileBytes), vd = smem_u32(smem + C::kOffV + s * C::kTileBytes);
-        if (t >= NS && !mbar_wait(&emptyK[s], ph)) {
-          ok = false;
-          break;
+      // the scales of row wt of the next tile (K's times |scale| log2 e), 0 past the window
+      float ks = 0.f, vs = 0.f;
+      auto scales = [&]() {
+        const int pos = w.tile * kN + wt;
+        ks = vs = 0.f;
+        if (w.have && pos < w.it.w.past + w.it.w.nodes) {
+          const int page = c.paged ? max(cache_page(c, w.it.b, pos), 0) : 0;
+          const int64_t row = cache_row(c, w.it.b, w.it.g, pos, page);
+          ks = __ldcg(c.k_scale + row);
+          vs = __ldcg(c.v_scale + row);
         }
-#pragma unroll
-        for (int i = 0; i < NR; ++i) cp16(kd + unit_off(row0 + i * STEP, u), gk + row[i] * (D * 2) + u * 16, live[i]);
-        cp_arrive(&fullK[s]);
-        if (t >= NS && !mbar_wait(&emptyV[s], ph)) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int i = 0; i < NR; ++i) cp16(vd + unit_off(row0 + i * STEP, u), gv + row[i] * (D * 2) + u * 16, live[i]);
-        if (w.tile * kN + kN > w.it.w.past) {
-          // node rows: non-finite entries are noted and cleared before the product
-          cp_commit();
-          cp_wait<0>();
-#pragma unroll 1
-          for (int i = 0; i < NR; ++i) {
-            const int pos = w.tile * kN + row0 + i * STEP;
-            if (pos < w.it.w.past || pos >= w.it.w.past + w.it.w.nodes) continue;
-            const uint32_t at = vd + unit_off(row0 + i * STEP, u);
-            uint4 x = lds128a(at);
-            if (clear_nonfinite(x)) {
-              sts128(at, x);
-              atomicOr(&s_bad[w.piece % kBadSlots], 1ull << (pos - w.it.w.past));
-            }
-          }
-          mbar_arrive(&fullV[s]);
-        } else {
-          cp_arrive(&fullV[s]);
-        }
-      }
-    } else {
-      constexpr int UR = D / 16;                // 16-byte units (16 codes) of a row
-      constexpr int STEP = kProdThreads / UR;
-      constexpr int NR = kN / STEP;
-      const int u = pt % UR, row0 = pt / UR;
-      const float sl = fabsf(p.scale_log2);
-      // this thread's slot i of staged tile s: at stage0 + s * 2 tiles + i * 2048 (K), + a tile (V)
-      const uint32_t stage0 = smem_u32(smem + C::kOffStage) + pt * 16;
-      TileWalk wi, w;   // tiles being copied, and being widened
-      wi.init(p, blockIdx.x);
-      w = wi;
-      float ks[2] = {0.f, 0.f}, vs[2] = {0.f, 0.f};   // scales of row pt of the staged tiles
-      auto scales = [&](float& k, float& v) {
-        int64_t r[1];
-        bool l[1];
-        tile_rows(p, wi.it, wi.tile, pt, 0, r, l);
-        k = l[0] ? __ldcg(c.k_scale + r[0]) * sl : 0.f;
-        v = l[0] ? __ldcg(c.v_scale + r[0]) : 0.f;
       };
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (wi.have) {
-          int64_t row[NR];
-          bool live[NR];
-          tile_rows(p, wi.it, wi.tile, row0, STEP, row, live);
-#pragma unroll
-          for (int i = 0; i < NR; ++i) {
-            cp16(stage0 + s * 2 * C::kStageBytes + i * (kProdThreads * 16), gk + row[i] * D + u * 16, live[i]);
-            cp16(stage0 + (s * 2 + 1) * C::kStageBytes + i * (kProdThreads * 16), gv + row[i] * D + u * 16, live[i]);
-          }
-          scales(ks[s], vs[s]);
-          wi.next(p);
-        }
-        cp_commit();
-      }
-      // one tile: widen it from its slots, copying the tile two ahead into each as it empties
-      auto step = [&](int t, int s, float& ksr, float& vsr) {
-        const uint32_t ph = static_cast<uint32_t>(t / 2 - 1) & 1u;
-        int64_t row[NR];
-        bool live[NR];
-        const bool more = wi.have;
-        if (more) tile_rows(p, wi.it, wi.tile, row0, STEP, row, live);
-        cp_wait<1>();
-        const uint32_t kd = smem_u32(smem + C::kOffK + s * C::kTileBytes), vd = smem_u32(smem + C::kOffV + s * C::kTileBytes);
-        // the scales' slot is free once the product that used V(t - 2) is done
-        if (t >= 2 && (!mbar_wait(&emptyK[s], ph) || !mbar_wait(&emptyV[s], ph))) return false;
-        s_scale[s * 256 + pt] = ksr;
-        s_scale[s * 256 + 128 + pt] = vsr;
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const uint32_t at = stage0 + s * 2 * C::kStageBytes + i * (kProdThreads * 16);
-          uint4 lo, hi;
-          widen16<KvT>(lds128a(at), lo, hi);
-          sts128(kd + unit_off(row0 + i * STEP, 2 * u), lo);
-          sts128(kd + unit_off(row0 + i * STEP, 2 * u + 1), hi);
-          if (more) cp16(at, gk + row[i] * D + u * 16, live[i]);
-        }
-        fence_async_smem();
-        mbar_arrive(&fullK[s]);
-        const bool nodes = std::is_same<KvT, CodeE4m3>::value && w.tile * kN + kN > w.it.w.past;
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const uint32_t at = stage0 + (s * 2 + 1) * C::kStageBytes + i * (kProdThreads * 16);
-          uint4 lo, hi;
-          widen16<KvT>(lds128a(at), lo, hi);
-          if (nodes) {
-            const int pos = w.tile * kN + row0 + i * STEP;
-            const bool a = clear_nonfinite(lo), b = clear_nonfinite(hi);
-            if ((a || b) && pos >= w.it.w.past && pos < w.it.w.past + w.it.w.nodes)
-              atomicOr(&s_bad[w.piece % kBadSlots], 1ull << (pos - w.it.w.past));
-          }
-          sts128(vd + unit_off(row0 + i * STEP, 2 * u), lo);
-          sts128(vd + unit_off(row0 + i * STEP, 2 * u + 1), hi);
-          if (more) cp16(at, gv + row[i] * D + u * 16, live[i]);
-        }
-        fence_async_smem();
-        mbar_arrive(&fullV[s]);
-        if (more) {
-          scales(ksr, vsr);
-          wi.next(p);
-        }
-        cp_commit();
+      scales();
+      bool ok = true;
+      for (int t = 0; w.have; ++t) {
+        const int s = t & 1;
+        const uint32_t ph = static_cast<uint32_t>(t >> 1) & 1u;
+        const float k = ks * sl, v = vs;
         w.next(p);
-        return true;
-      };
-      for (int t = 0; w.have && ok; t += 2) {
-        ok = step(t, 0, ks[0], vs[0]);
-        if (ok && w.have) ok = step(t + 1, 1, ks[1], vs[1]);
+        scales();   // in flight while this tile is widened
+        // the operand tile and the scales' slot are free once tile t - 2 is through
+        if ((t >= 2 && (!warp_wait(&emptyK[s], ph ^ 1u) || !warp_wait(&emptyV[s], ph ^ 1u))) || !warp_wait(&rawK[s], ph)) {
+          ok = false;
+          break;
+        }
+        s_scale[s * 256 + wt] = k;
+        s_scale[s * 256 + 128 + wt] = v;
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {   // K, then V
+          if (x == 1 && !warp_wait(&rawV[s], ph)) {
+            ok = false;
+            break;
+          }
+          widen_tile<D, KvT>(smem + (x ? C::kOffRawV : C::kOffRawK) + s * C::kRawBytes,
+                             smem + (x ? C::kOffV : C::kOffK) + s * C::kTileBytes, wt);
+          fence_async_smem();
+          warp_arrive(x ? &fullV[s] : &fullK[s]);
+          warp_arrive(x ? &rawVe[s] : &rawKe[s]);
+        }
+        if (!ok) break;
       }
+      if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
     }
-    if (!ok) set_err(p.err, TTS_EFLAG_TIMEOUT);
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------- MMA issuer
     PieceWalk walk;
     walk.init(p, blockIdx.x);
-    if (lane == 0) {
+    {
       // kind::f16, f32 accumulator, bf16 A and B, M = 128; S: N = 128, B (K) K-major; O: N = D,
       // B (V) MN-major (bit 16)
       constexpr uint32_t base = (1u << 4) | (1u << 7) | (1u << 10) | ((kM >> 4) << 24);
       constexpr uint32_t idS = base | ((kN >> 3) << 17), idO = base | (1u << 16) | ((D >> 3) << 17);
-      const uint32_t qa = smem_u32(smem);
-      int gk = 0, gv = 0;                 // K and V tiles taken so far
-      uint32_t pph[2] = {0, 0};           // phases of pready
+      const uint64_t qd = smem_desc(smem_u32(smem), 16, 1024);
+      const uint64_t kd0 = smem_desc(smem_u32(smem + C::kOffK), 16, 1024);
+      const uint64_t vd0 = smem_desc(smem_u32(smem + C::kOffV), kN * 128, 1024);
+      int ks = 0, vs = 0;                 // next K and V operand tiles
+      uint32_t kph = 0, vph = 0, pph[2] = {0, 0};
       bool ok = true;
       auto issue_s = [&](int wg) {
-        const int s = gk % NS;
-        if (!mbar_wait(&fullK[s], static_cast<uint32_t>(gk / NS) & 1u)) return false;
-        if (!k8) fence_async_smem();      // the copies' writes, before the products read them
+        if (!warp_wait(&fullK[ks], kph)) return false;
         tc_fence_after();
-        const uint32_t kb = smem_u32(smem + C::kOffK + s * C::kTileBytes), d = tmem + wg * kN;
+        const uint64_t kd = kd0 + static_cast<uint64_t>(ks * (C::kTileBytes >> 4));
+        const uint32_t d = tmem + wg * kN;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-          const uint32_t o = (j >> 2) * (kN * 128) + (j & 3) * 32;
-          mma_ss(d, smem_desc(qa + o, 16, 1024), smem_desc(kb + o, 16, 1024), idS, j > 0 ? 1u : 0u);
+          constexpr uint64_t chunk = kN * 128 >> 4;
+          mma_ss(d, qd + (j >> 2) * chunk + (j & 3) * 2, kd + (j >> 2) * chunk + (j & 3) * 2, idS, j > 0 ? 1u : 0u);
         }
         mma_commit(&sready[wg]);
-        mma_commit(&emptyK[s]);
-        mbar_arrive(&sready[wg]);
-        ++gk;
+        mma_commit(&emptyK[ks]);
+        warp_arrive(&sready[wg]);
+        if (++ks == NS) {
+          ks = 0;
+          kph ^= 1u;
+        }
         return true;
       };
       Piece it;
       for (uint32_t piece = 0; ok && walk.get(p, it); ++piece) {
         const int n = it.t1 - it.t0;
-        ok = mbar_wait(qready, piece & 1u) && issue_s(0) && (n < 2 || issue_s(1));
+        ok = warp_wait(qready, piece & 1u) && issue_s(0) && (n < 2 || issue_s(1));
         for (int i = 0; ok && i < n; ++i) {
-          const int wg = i & 1, s = gv % NS;
-          if (!mbar_wait(&pready[wg], pph[wg]) || !mbar_wait(&fullV[s], static_cast<uint32_t>(gv / NS) & 1u)) {
+          const int wg = i & 1;
+          if (!warp_wait(&fullV[vs], vph) || !warp_wait(&pready[wg], pph[wg])) {
             ok = false;
             break;
           }
           pph[wg] ^= 1u;
-          if (!k8) fence_async_smem();
           tc_fence_after();
-          const uint32_t vb = smem_u32(smem + C::kOffV + s * C::kTileBytes), a = tmem + wg * kN, d = tO + wg * D;
+          const uint64_t vd = vd0 + static_cast<uint64_t>(vs * (C::kTileBytes >> 4));
+          const uint32_t a = tmem + wg * kN, d = tO + wg * D;
 #pragma unroll
-          for (int j = 0; j < kN / 16; ++j)
-            mma_ts(d, a + j * 8, smem_desc(vb + j * 2048, kN * 128, 1024), idO, (i > 1 || j > 0) ? 1u : 0u);
-          mma_commit(&emptyV[s]);
-          ++gv;
-          if (i + 2 < n) {
-            ok = issue_s(wg);
-          } else {
-            mma_commit(&odone[wg]);
-            mbar_arrive(&odone[wg]);
+          for (int j = 0; j < kN / 16; ++j) mma_ts(d, a + j * 8, vd + j * (2048 >> 4), idO, (i > 1 || j > 0) ? 1u : 0u);
+          mma_commit(&emptyV[vs]);
+          if (++vs == NS) {
+            vs = 0;
+            vph ^= 1u;
           }
+          if (i + 2 < n)
+            ok = issue_s(wg);
+          else
+            mma_commit(&odone[wg]);
         }
       }
       // no product is in flight when the CTA gives its tensor memory back
       mma_commit(drained);
-      if (!mbar_wait(drained, 0)) ok = false;
-      if (!ok) set_err(p.err, TTS_EFLAG_TIMEOUT);
+      if (!warp_wait(drained, 0)) ok = false;
+      if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
     }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------- softmax warps
     const int wg = warp >> 2;
@@ -677,28 +698,39 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(const TreePar
     uint32_t sph = 0, oph = 0;
     int taken = 0;   // tiles of the pieces before
     bool ok = true;
-    Piece it;
-    for (uint32_t piece = 0; walk.get(p, it); ++piece) {
-      const int first = it.rb * RP;   // of the stream and kv head's query rows
-      // the query rows, each written F times; rows without a node are 0
-      {
-        constexpr int UR = D / 8;
-        for (int i = tid; i < RP * UR; i += kSmxThreads) {
-          const int row = i / UR, u = i % UR, t = (first + row) / p.group, h = first + row - t * p.group;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (t < it.w.nodes) {
-            v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                      (static_cast<int64_t>(it.b) * p.T + t) * p.q_stride +
-                                                      (it.g * p.group + h) * D) + u);
-            v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
-          }
+    // a piece's query rows, loaded while the piece before is finished: 16-byte units
+    // tid, tid + 256, ... of its RP rows; rows without a node are 0
+    constexpr int QU = RP * UR / kSmxThreads;
+    uint4 qv[QU];
+    auto load_q = [&](const Piece& x) {
 #pragma unroll
-          for (int k = 0; k < F; ++k) *reinterpret_cast<uint4*>(smem + unit_off(k * RP + row, u)) = v;
-        }
-        fence_async_smem();
-        tc_fence_before();
-        mbar_arrive(qready);
+      for (int k = 0; k < QU; ++k) {
+        const int i = tid + k * kSmxThreads, row = i / UR, u = i % UR, t = (x.rb * RP + row) / p.group,
+                  h = x.rb * RP + row - t * p.group;
+        qv[k] = make_uint4(0, 0, 0, 0);
+        if (t < x.w.nodes)
+          qv[k] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                        (static_cast<int64_t>(x.b) * p.T + t) * p.q_stride +
+                                                        (x.g * p.group + h) * D) + u);
       }
+    };
+    Piece it, next;
+    bool have = walk.get(p, next);
+    if (have) load_q(next);
+    while (have) {
+      it = next;
+      const int first = it.rb * RP;   // of the stream and kv head's query rows
+      // each query row F times
+#pragma unroll
+      for (int k = 0; k < QU; ++k) {
+        const int i = tid + k * kSmxThreads, row = i / UR, u = i % UR;
+        const uint4 v = make_uint4(qv[k].x ^ flip, qv[k].y ^ flip, qv[k].z ^ flip, qv[k].w ^ flip);
+#pragma unroll
+        for (int x = 0; x < F; ++x) *reinterpret_cast<uint4*>(smem + unit_off(x * RP + row, u)) = v;
+      }
+      fence_async_smem();
+      tc_fence_before();
+      warp_arrive(qready);
       const int node = (first + rr) / p.group;
       const uint64_t see = node < it.w.nodes ? seen_nodes(p, it.b, node, it.w.nodes) : 0ull;
       const int n = it.t1 - it.t0;
@@ -706,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(const TreePar
       for (int i = wg; ok && i < n; i += 2) {
         const int base = (it.t0 + i) * kN + f * W;   // position of this thread's first column
         const bool masked = (it.t0 + i) * kN + kN > it.w.past;
-        if (!__all_sync(kFull, mbar_wait(&sready[wg], sph))) {
+        if (!warp_wait(&sready[wg], sph)) {
           ok = false;
           break;
         }
@@ -719,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(const TreePar
         const int off = base - it.w.past;
         float sv[32];
         float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < W / 32; ++cc) {
           tmem_ld32(tS + f * W + 32 * cc, sv);
           const uint32_t vis = masked ? visible32(off + 32 * cc, see) : ~0u;
@@ -731,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(const TreePar
         const float alpha = rescale ? ex2(m - mx) : 1.0f;
         if (__any_sync(kFull, rescale)) {
           // O is complete up to the group's tile before: its product was issued before S
-#pragma unroll
+#pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             float o[32];
             tmem_ld32(tOw + 32 * cc, o);
@@ -746,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(const TreePar
         }
         const float ms = m == -INFINITY ? 0.f : m;
         // P over S: chunk cc's 16 packed columns lie below every S column still to be read
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < W / 32; ++cc) {
           if (W > 32) tmem_ld32(tS + f * W + 32 * cc, sv);
           const uint32_t vis = masked ? visible32(off + 32 * cc, see) : ~0u;
@@ -762,14 +794,46 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(const TreePar
             if (k / (4 / F) != f) tmem_st16(tS + 16 * k, zero);
         }
         tmem_wait_st();
+        if constexpr (!std::is_same<KvT, CodeI8>::value) {
+          // V's node rows: non-finite entries are noted and cleared, rows past the window (which
+          // the copies left as they were, or filled from the page) zeroed.  Widened int8 is
+          // finite whatever the staging tile held.
+          if (masked) {
+            const int s = (taken + i) % NS;
+            if (!warp_wait(&fullV[s], static_cast<uint32_t>((taken + i) / NS) & 1u)) {
+              ok = false;
+              break;
+            }
+            const int node_row = (it.t0 + i) * kN + r - it.w.past;
+            if (node_row >= 0) {
+              unsigned char* vt = smem + C::kOffV + s * C::kTileBytes;
+              bool any = false;
+#pragma unroll 1
+              for (int u = 0; u < UR; ++u) {
+                uint4* at = reinterpret_cast<uint4*>(vt + unit_off(r, u));
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (node_row < it.w.nodes) {
+                  x = *at;
+                  if (!clear_nonfinite(x)) continue;
+                  any = true;
+                }
+                *at = x;
+              }
+              if (any) atomicOr(s_bad, 1ull << node_row);
+            }
+            fence_async_smem();
+          }
+        }
         tc_fence_before();
-        mbar_arrive(&pready[wg]);
+        warp_arrive(&pready[wg]);
       }
       taken += n;
+      have = walk.get(p, next);
+      if (have) load_q(next);
       // ------------------------------------------------------------- epilogue
       const bool had = wg < n;
       if (ok && had) {
-        ok = __all_sync(kFull, mbar_wait(&odone[wg], oph));
+        ok = warp_wait(&odone[wg], oph);
         oph ^= 1u;
       }
       ok = smx_sync_and(ok);   // every product of the piece is done: the query rows are free
@@ -795,9 +859,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(const TreePar
       } else if (tid < RP) {
         p.ml[slot * RP + rr] = make_float2(M, L);
       }
-      const unsigned long long bad_v = s_bad[piece % kBadSlots];
+      const unsigned long long bad_v = *s_bad;
       smx_sync();   // the statistics are read; everyone has the noted rows
-      if (tid == 0) s_bad[piece % kBadSlots] = 0;
+      if (tid == 0) *s_bad = 0;
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
         float o[32];
@@ -842,13 +906,49 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(const TreePar
   }
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static std::mutex mtx;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::lock_guard<std::mutex> lock(mtx);
+  if (fn == nullptr) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    else
+      cudaGetLastError();
+  }
+  return fn;
+}
+
 template <int D, typename KvT, int F>
 cudaError_t launch_t(const TreeParams& p, cudaStream_t s) {
   auto kern = tree_attn_tc_kernel<D, KvT, F>;
   constexpr size_t smem = TcCfg<D, KvT>::kSmem;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(p.n_cta), dim3(kThreads), smem, s, p);
+  CUtensorMap maps[2] = {};
+  if (!TcCfg<D, KvT>::k8) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    if (enc == nullptr) return cudaErrorNotSupported;
+    // the cache as [chunks of 64 columns][rows][64]; a box is a tile, or a page's 64 columns
+    const CacheView& c = p.cache;
+    const int ps = 1 << c.page_shift;
+    const bool whole = !c.paged || ps >= kN;
+    const uint64_t rows = c.paged ? static_cast<uint64_t>(c.n_pages) * c.n_kv_heads * ps
+                                  : static_cast<uint64_t>(c.B) * c.n_kv_heads * c.capacity;
+    cuuint64_t dims[3] = {64, rows, D / 64};
+    cuuint64_t strides[2] = {D * 2, 128};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(whole ? kN : ps), static_cast<cuuint32_t>(whole ? D / 64 : 1)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    for (int i = 0; i < 2; ++i)
+      if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, i == 0 ? c.k : c.v, dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+  }
+  return launch_pdl(kern, dim3(p.n_cta), dim3(TcCfg<D, KvT>::kThreads), smem, s, maps[0], maps[1], p);
 }
 template <int D, typename KvT>
 cudaError_t launch_f(const TreeParams& p, cudaStream_t s) {
@@ -870,6 +970,14 @@ cudaError_t launch_kv(const TreeParams& p, int kv_dtype, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool tree_attn_tc_supported(const tts_kv_desc* d) {
+  if (d->kv_dtype == TTS_I8 || d->kv_dtype == TTS_E4M3) return true;
+  // tensor-map boxes: whole swizzle groups of eight rows, 32-bit row coordinates
+  const int64_t rows = d->paged ? static_cast<int64_t>(d->n_pages) * d->n_kv_heads * d->page_size
+                                : static_cast<int64_t>(d->B) * d->n_kv_heads * d->capacity;
+  return d->kv_dtype == TTS_BF16 && (!d->paged || d->page_size >= 8) && rows < (int64_t{1} << 31) - kN;
+}
 
 cudaError_t launch_tree_attn_tc(const TreeParams& p, int kv_dtype, int head_dim, cudaStream_t s) {
   return head_dim == 64 ? launch_kv<64>(p, kv_dtype, s) : launch_kv<128>(p, kv_dtype, s);
