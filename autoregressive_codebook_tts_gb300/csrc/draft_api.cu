@@ -42,6 +42,7 @@ tts_status check_cache(const tts_kv_cache* c, const tts_kv_desc* d, CacheView& v
 tts_status check_rows(const tts_kv_desc* d, int32_t dtype, int64_t stride, int32_t T) {
   if (!row_dtype_ok(dtype)) return TTS_ERR_DTYPE;
   if (T < 1 || static_cast<int64_t>(d->B) * T > (int64_t{1} << 24) ||
+      static_cast<int64_t>(T) * d->n_kv_heads >= (int64_t{1} << 31) - (1 << 16) ||
       stride < static_cast<int64_t>(d->n_kv_heads) * d->head_dim)
     return TTS_ERR_SHAPE;
   return stride % row_quantum(dtype) == 0 ? TTS_OK : TTS_ERR_ALIGN;

@@ -2,10 +2,10 @@
 // dtypes), read back from it, and moved inside it when a tree's path is accepted.
 //
 // All three only move bytes, so they are bound by HBM on long inputs and by launch latency
-// on one decode step.  A row of head_dim entries is held by the lanes of one quarter to one
-// whole warp, VE entries a lane, so a row's largest magnitude is a few shuffles and nothing
-// goes through shared memory; each lane takes U rows at once (all loads issued first) when
-// there are rows enough to fill the GPU, else one.
+// on one decode step.  A row of head_dim entries is held by the lanes of an eighth to half a
+// warp, so a row's largest magnitude is a few shuffles and nothing goes through shared memory.
+// K and V of a row go through the same lane (two loads in flight at least); many rows to read
+// are read two a lane.
 #include "cache_view.cuh"
 #include "draft_kernels.h"
 
@@ -16,16 +16,26 @@ constexpr int kWarps = 8;
 
 template <typename SrcT> struct Src;
 template <> struct Src<float> {
-  static constexpr int kVec = 4;  // entries of a lane: 16 bytes
-  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[4]) {
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+  static constexpr int kVec = 8;   // entries of a lane: 32 bytes
+  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[8]) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 v = __ldcs(q), w = __ldcs(q + 1);
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; f[4] = w.x; f[5] = w.y; f[6] = w.z; f[7] = w.w;
   }
 };
 template <> struct Src<__nv_bfloat16> {
-  static constexpr int kVec = 8;
-  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[8]) {
-    unpack_bf16x8(__ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i)), f);
+  static constexpr int kVec = 16;
+  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[16]) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+    const uint4 v = __ldcs(q), w = __ldcs(q + 1);
+    float a[8], b[8];
+    unpack_bf16x8(v, a);
+    unpack_bf16x8(w, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f[e] = a[e];
+      f[8 + e] = b[e];
+    }
   }
 };
 
@@ -43,24 +53,18 @@ __device__ __forceinline__ void store_row(float* p, int64_t i, const float (&x)[
 template <int N>
 __device__ __forceinline__ void store_row(__nv_bfloat16* p, int64_t i, const float (&x)[N]) {
 #pragma unroll
-  for (int e = 0; e < N; e += 4)
-    *reinterpret_cast<uint2*>(p + i + e) = make_uint2(bf16_pair(x[e], x[e + 1]), bf16_pair(x[e + 2], x[e + 3]));
+  for (int e = 0; e < N; e += 8)
+    *reinterpret_cast<uint4*>(p + i + e) = make_uint4(bf16_pair(x[e], x[e + 1]), bf16_pair(x[e + 2], x[e + 3]),
+                                                      bf16_pair(x[e + 4], x[e + 5]), bf16_pair(x[e + 6], x[e + 7]));
 }
 template <typename Code, int N>
 __device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, const float (&x)[N], float s, bool zero) {
-  const float inv = zero ? 0.f : 1.0f / s;
-  uint32_t w[N / 4];
-#pragma unroll
-  for (int e = 0; e < N / 4; ++e) {
-    w[e] = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (!zero) w[e] |= Code::code(x[4 * e + k], s, inv) << (8 * k);
-  }
-  if constexpr (N == 4) {
-    *reinterpret_cast<uint32_t*>(p + i) = w[0];
-  } else {
+  uint32_t w[N / 4] = {};
+  if (!zero) codes<Code>(x, s, w);
+  if constexpr (N == 8) {
     *reinterpret_cast<uint2*>(p + i) = make_uint2(w[0], w[1]);
+  } else {
+    *reinterpret_cast<uint4*>(p + i) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -91,62 +95,51 @@ __device__ __forceinline__ void write_head_row(void* cache, float* scale, int64_
   }
 }
 
-// Head row i of the call: (b, t, g) with g fastest, K and V together.
-template <typename SrcT, typename KvT, int D, int U>
+// Head row i of stream b: (t, g) with g fastest, K and V together.
+template <typename SrcT, typename KvT, int D>
 __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const KvRowsParams p) {
   constexpr int VE = Src<SrcT>::kVec, LPR = D / VE, RPW = 32 / LPR;
   grid_wait();
   grid_launch_dependents();
   const CacheView& c = p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lr = lane % LPR;
-  const int64_t n = static_cast<int64_t>(c.B) * p.T * c.n_kv_heads;
-  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * (RPW * U) + lane / LPR;
-  int64_t row[U];
-  float xk[U][VE], xv[U][VE];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t i = i0 + u * RPW;
-    row[u] = -1;
-#pragma unroll
-    for (int e = 0; e < VE; ++e) xk[u][e] = xv[u][e] = 0.f;
-    if (i >= n) continue;
-    const int64_t r = i / c.n_kv_heads;
-    const int g = static_cast<int>(i - r * c.n_kv_heads);
-    const int b = static_cast<int>(r / p.T), t = static_cast<int>(r - static_cast<int64_t>(b) * p.T);
-    const bool first = g == 0 && lr == 0;   // the thread that reports for (b, t)
-    if (p.n_rows != nullptr) {
-      const int nr = __ldcg(p.n_rows + b);
-      if (first && t == 0 && (nr < 0 || nr > p.T)) set_err(p.err, TTS_EFLAG_NVALID);
-      if (t >= nr) continue;
-    }
-    const int64_t pos = static_cast<int64_t>(__ldcg(p.start + b)) + t;
-    if (pos < 0 || pos >= c.capacity) {
-      if (first) set_err(p.err, TTS_EFLAG_POS_RANGE);
-      continue;
-    }
-    int page = 0;
-    if (c.paged) {
-      page = cache_page(c, b, static_cast<int>(pos));
-      if (page < 0) {
-        if (first) set_err(p.err, TTS_EFLAG_PAGE);
-        continue;
-      }
-    }
-    row[u] = cache_row(c, b, g, static_cast<int>(pos), page);
-    const int64_t src = r * p.row_stride + static_cast<int64_t>(g) * D + lr * VE;
-    Src<SrcT>::load(p.k, src, xk[u]);
-    Src<SrcT>::load(p.v, src, xv[u]);
+  const int b = blockIdx.y;
+  const uint32_t i = (blockIdx.x * kWarps + warp) * RPW + lane / LPR;
+  // (once a warp: every block of a stream asks the same two words of L2)
+  const int64_t start = __ldcg(p.start + b);
+  const int nr = p.n_rows == nullptr ? p.T : __ldcg(p.n_rows + b);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (nr < 0 || nr > p.T)) set_err(p.err, TTS_EFLAG_NVALID);
+  const int t = static_cast<int>(i / c.n_kv_heads), g = static_cast<int>(i) - t * c.n_kv_heads;
+  const int64_t pos = start + t;
+  const bool first = g == 0 && lr == 0;   // the thread that reports for (b, t)
+  bool live = t < min(nr, p.T);
+  float xk[VE] = {}, xv[VE] = {};
+  if (live) {
+    const int64_t src = (static_cast<int64_t>(b) * p.T + t) * p.row_stride + static_cast<int64_t>(g) * D + lr * VE;
+    Src<SrcT>::load(p.k, src, xk);
+    Src<SrcT>::load(p.v, src, xv);
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    write_head_row<KvT, VE, LPR>(c.k, c.k_scale, row[u], D, lr, row[u] >= 0, xk[u]);
-    write_head_row<KvT, VE, LPR>(c.v, c.v_scale, row[u], D, lr, row[u] >= 0, xv[u]);
+  if (live && (pos < 0 || pos >= c.capacity)) {
+    if (first) set_err(p.err, TTS_EFLAG_POS_RANGE);
+    live = false;
   }
+  int page = 0;
+  if (live && c.paged) {
+    page = cache_page(c, b, static_cast<int>(pos));
+    if (page < 0) {
+      if (first) set_err(p.err, TTS_EFLAG_PAGE);
+      live = false;
+    }
+  }
+  const int64_t row = cache_row(c, b, g, live ? static_cast<int>(pos) : 0, live ? page : 0);
+  write_head_row<KvT, VE, LPR>(c.k, c.k_scale, row, D, lr, live, xk);
+  write_head_row<KvT, VE, LPR>(c.v, c.v_scale, row, D, lr, live, xv);
 }
 
-// Eight entries of a lane as read from the cache.
-template <typename KvT> struct Load8;
-template <> struct Load8<float> {
+// The entries of a lane as read from the cache: 16 bytes (f32: 32).
+template <typename KvT> struct LaneRow;
+template <> struct LaneRow<float> {
+  static constexpr int kVec = 8;
   float4 a, b;
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
@@ -157,63 +150,67 @@ template <> struct Load8<float> {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
 };
-template <> struct Load8<__nv_bfloat16> {
+template <> struct LaneRow<__nv_bfloat16> {
+  static constexpr int kVec = 8;
   uint4 a;
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i));
   }
   __device__ __forceinline__ void values(float (&f)[8]) const { unpack_bf16x8(a, f); }
 };
-template <typename Code> struct Load8Codes {
-  uint2 a;
+template <typename KvT> struct LaneCodes {
+  static constexpr int kVec = 16;
+  uint4 a;
   __device__ __forceinline__ void load(const void* p, int64_t i) {
-    a = __ldcg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + i));
+    a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i));
   }
-  __device__ __forceinline__ void values(float (&f)[8]) const {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = Code::value((e < 4 ? a.x : a.y) >> (8 * (e & 3)));
-  }
+  __device__ __forceinline__ void values(float (&f)[16]) const { CacheElem<KvT>::values(a, f); }
 };
-template <> struct Load8<CodeI8> : Load8Codes<I8Code> {};
-template <> struct Load8<CodeE4m3> : Load8Codes<E4m3Code> {};
+template <> struct LaneRow<CodeI8> : LaneCodes<CodeI8> {};
+template <> struct LaneRow<CodeE4m3> : LaneCodes<CodeE4m3> {};
 
-__device__ __forceinline__ void stream_out(float* p, int64_t i, const float (&f)[8]) {
-  __stcs(reinterpret_cast<float4*>(p + i), make_float4(f[0], f[1], f[2], f[3]));
-  __stcs(reinterpret_cast<float4*>(p + i) + 1, make_float4(f[4], f[5], f[6], f[7]));
+template <int N>
+__device__ __forceinline__ void stream_out(float* p, int64_t i, const float (&f)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 4)
+    __stcs(reinterpret_cast<float4*>(p + i + e), make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]));
 }
-__device__ __forceinline__ void stream_out(__nv_bfloat16* p, int64_t i, const float (&f)[8]) {
-  __stcs(reinterpret_cast<uint4*>(p + i), make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]),
-                                                     bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])));
+template <int N>
+__device__ __forceinline__ void stream_out(__nv_bfloat16* p, int64_t i, const float (&f)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 8)
+    __stcs(reinterpret_cast<uint4*>(p + i + e), make_uint4(bf16_pair(f[e], f[e + 1]), bf16_pair(f[e + 2], f[e + 3]),
+                                                           bf16_pair(f[e + 4], f[e + 5]), bf16_pair(f[e + 6], f[e + 7])));
 }
 
 template <typename KvT, typename OutT, int D, int U>
 __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const KvRowsParams p) {
-  constexpr int VE = 8, LPR = D / VE, RPW = 32 / LPR;
+  constexpr int VE = LaneRow<KvT>::kVec, LPR = D / VE, RPW = 32 / LPR;
   grid_wait();
   grid_launch_dependents();
   const CacheView& c = p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lr = lane % LPR;
-  const int64_t n = static_cast<int64_t>(c.B) * p.T * c.n_kv_heads;
-  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * (RPW * U) + lane / LPR;
+  const int b = blockIdx.y;
+  const uint32_t n = static_cast<uint32_t>(p.T) * c.n_kv_heads;   // head rows of a stream (below 2^31)
+  const uint32_t i0 = (blockIdx.x * kWarps + warp) * (RPW * U) + lane / LPR;
+  // (once a warp: every block of a stream asks the same two words of L2)
+  const int64_t start = __ldcg(p.start + b);
+  const int nr = p.n_rows == nullptr ? p.T : __ldcg(p.n_rows + b);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (nr < 0 || nr > p.T)) set_err(p.err, TTS_EFLAG_NVALID);
   int64_t dst[U];
-  Load8<KvT> k[U], v[U];
+  LaneRow<KvT> k[U], v[U];
   float sk[U], sv[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t i = i0 + u * RPW;
+    const uint32_t i = i0 + u * RPW;
     dst[u] = -1;
     sk[u] = sv[u] = 1.f;
     if (i >= n) continue;
-    const int64_t r = i / c.n_kv_heads;
-    const int g = static_cast<int>(i - r * c.n_kv_heads);
-    const int b = static_cast<int>(r / p.T), t = static_cast<int>(r - static_cast<int64_t>(b) * p.T);
+    const int t = static_cast<int>(i / c.n_kv_heads), g = static_cast<int>(i) - t * c.n_kv_heads;
+    const int64_t r = static_cast<int64_t>(b) * p.T + t;
+    if (t >= nr) continue;
     const bool first = g == 0 && lr == 0;
-    if (p.n_rows != nullptr) {
-      const int nr = __ldcg(p.n_rows + b);
-      if (first && t == 0 && (nr < 0 || nr > p.T)) set_err(p.err, TTS_EFLAG_NVALID);
-      if (t >= nr) continue;
-    }
-    const int64_t pos = static_cast<int64_t>(__ldcg(p.start + b)) + t;
+    const int64_t pos = start + t;
     if (pos < 0 || pos >= c.capacity) {
       if (first) set_err(p.err, TTS_EFLAG_POS_RANGE);
       continue;
@@ -238,34 +235,33 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const KvRowsParams
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (dst[u] < 0) continue;
-    float f[8];
+    float f[VE];
     k[u].values(f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = CacheElem<KvT>::kScaled ? f[e] * sk[u] : f[e];
+    for (int e = 0; e < VE; ++e) f[e] = CacheElem<KvT>::kScaled ? f[e] * sk[u] : f[e];
     stream_out(static_cast<OutT*>(p.k_out), dst[u], f);
     v[u].values(f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = CacheElem<KvT>::kScaled ? f[e] * sv[u] : f[e];
+    for (int e = 0; e < VE; ++e) f[e] = CacheElem<KvT>::kScaled ? f[e] * sv[u] : f[e];
     stream_out(static_cast<OutT*>(p.v_out), dst[u], f);
   }
 }
 
-// Rows a lane takes at once: four when one each would already be over four blocks an SM.
-template <int RPW>
-int64_t row_blocks(const KvRowsParams& p, bool& four) {
-  const int64_t n = static_cast<int64_t>(p.cache.B) * p.T * p.cache.n_kv_heads;
-  four = n > static_cast<int64_t>(p.n_sm) * 4 * kWarps * RPW;
-  const int64_t per = static_cast<int64_t>(kWarps) * RPW * (four ? 4 : 1);
-  return (n + per - 1) / per;
+// Rows a lane takes at once: U when one each would already be over four blocks an SM.
+template <int RPW, int U>
+dim3 row_grid(const KvRowsParams& p, bool& many) {
+  const int64_t n = static_cast<int64_t>(p.T) * p.cache.n_kv_heads;
+  many = n * p.cache.B > static_cast<int64_t>(p.n_sm) * 4 * kWarps * RPW;
+  const int64_t per = static_cast<int64_t>(kWarps) * RPW * (many ? U : 1);
+  return dim3(static_cast<unsigned>((n + per - 1) / per), p.cache.B);
 }
 
 template <typename SrcT, typename KvT, int D>
 cudaError_t launch_write(const KvRowsParams& p, cudaStream_t s) {
-  constexpr int RPW = 32 / (D / Src<SrcT>::kVec);
-  bool four;
-  const dim3 grid(static_cast<unsigned>(row_blocks<RPW>(p, four)));
-  return four ? launch_pdl(kv_write_kernel<SrcT, KvT, D, 4>, grid, dim3(kWarps * 32), 0, s, p)
-              : launch_pdl(kv_write_kernel<SrcT, KvT, D, 1>, grid, dim3(kWarps * 32), 0, s, p);
+  constexpr int per = kWarps * (32 / (D / Src<SrcT>::kVec));
+  const int64_t n = static_cast<int64_t>(p.T) * p.cache.n_kv_heads;
+  const dim3 grid(static_cast<unsigned>((n + per - 1) / per), p.cache.B);
+  return launch_pdl(kv_write_kernel<SrcT, KvT, D>, grid, dim3(kWarps * 32), 0, s, p);
 }
 template <typename SrcT, typename KvT>
 cudaError_t launch_write_d(const KvRowsParams& p, cudaStream_t s) {
@@ -283,10 +279,10 @@ cudaError_t launch_write_kv(const KvRowsParams& p, cudaStream_t s) {
 
 template <typename KvT, typename OutT, int D>
 cudaError_t launch_read(const KvRowsParams& p, cudaStream_t s) {
-  constexpr int RPW = 32 / (D / 8);
-  bool four;
-  const dim3 grid(static_cast<unsigned>(row_blocks<RPW>(p, four)));
-  return four ? launch_pdl(kv_read_kernel<KvT, OutT, D, 4>, grid, dim3(kWarps * 32), 0, s, p)
+  constexpr int RPW = 32 / (D / LaneRow<KvT>::kVec);
+  bool many;
+  const dim3 grid = row_grid<RPW, 2>(p, many);
+  return many ? launch_pdl(kv_read_kernel<KvT, OutT, D, 2>, grid, dim3(kWarps * 32), 0, s, p)
               : launch_pdl(kv_read_kernel<KvT, OutT, D, 1>, grid, dim3(kWarps * 32), 0, s, p);
 }
 template <typename KvT, typename OutT>

@@ -353,26 +353,27 @@ __device__ __forceinline__ float partial_weight(float m, float l, float M) {
   return m == -INFINITY ? (l != l ? 1.f : 0.f) : ex2(m - M);
 }
 
-// Adds the non-finite V entries of the node rows in `bits`, columns [col, col + 4).
+// The non-finite ones among entries [col, col + 4) of the V rows of the nodes in `bits`, added up.
 template <typename KvT, int D>
-__device__ __noinline__ void add_bad_v(const TreeParams& p, const Piece& it, unsigned long long bits, int col, float4& a) {
-  const CacheView& c = p.cache;
+__device__ __forceinline__ float4 bad_v_sum(const CacheView& c, int b, int g, int past, unsigned long long bits, int col) {
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
   while (bits != 0) {
     const int u = __ffsll(static_cast<long long>(bits)) - 1;
     bits &= bits - 1;
-    const int pos = it.w.past + u, page = c.paged ? max(cache_page(c, it.b, pos), 0) : 0;
-    const int64_t row = cache_row(c, it.b, it.g, pos, page);
-    float x[4];
+    const int pos = past + u, page = c.paged ? max(cache_page(c, b, pos), 0) : 0;
+    const int64_t row = cache_row(c, b, g, pos, page);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+      float x;
       if constexpr (CacheElem<KvT>::kScaled)
-        x[e] = E4m3Code::value(static_cast<const uint8_t*>(c.v)[row * D + col + e]);   // int8 codes are finite
+        x = E4m3Code::value(static_cast<const uint8_t*>(c.v)[row * D + col + e]);   // int8 codes are finite
       else
-        x[e] = static_cast<float>(static_cast<const __nv_bfloat16*>(c.v)[row * D + col + e]);
-      if ((__float_as_uint(x[e]) & 0x7f800000u) != 0x7f800000u) x[e] = 0.f;
+        x = static_cast<float>(static_cast<const __nv_bfloat16*>(c.v)[row * D + col + e]);
+      if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) a[e] += x;
     }
-    a.x += x[0]; a.y += x[1]; a.z += x[2]; a.w += x[3];
   }
+  return make_float4(a[0], a[1], a[2], a[3]);
 }
 
 // One tile of K or V into `dst`, by a whole warp: bf16 in the operand layout (boxes of the
@@ -430,27 +431,31 @@ __device__ __forceinline__ void load_tile(const TreeParams& p, const CUtensorMap
 }
 
 // 128 x D codes of a staged tile to bf16 in the operand layout, by the widening threads: four
-// 16-code vectors of a thread at a time.
+// 16-code vectors of a thread at a time.  Which thread takes which vector: a phase's eight lanes
+// read from every bank once, and what they write lies in eight different bank groups (the even
+// units of an even row and the odd places they take in an odd one).
 template <int D, typename KvT>
 __device__ __forceinline__ void widen_tile(const unsigned char* raw, unsigned char* dst, int wt) {
-  constexpr int UR = D / 16, STEP = kWidenThreads / UR, NR = kN / STEP, BATCH = NR < 4 ? NR : 4;
-  const int u = wt % UR, row0 = wt / UR;
-  // half of the lanes that write one row store their second unit first: a phase's eight
-  // 16-byte units then lie in eight different bank groups
-  const int first = u >= UR / 2 ? 1 : 0;
+  constexpr int UR = D / 16, STEP = kWidenThreads / UR, NR = kN / STEP, BATCH = 4;
+  const int half = (wt >> 2) & 1;
+  const int u = D == 128 ? half * 4 + (wt & 3) : wt & 3;
+  const int row0 = D == 128 ? (wt >> 4) * 2 + (half ^ ((wt >> 3) & 1)) : wt >> 2;
+  const unsigned char* src = raw + row0 * D + u * 16;
+  // (rows are STEP, a multiple of eight, apart: the swizzle is the same for all of them)
+  unsigned char* lo_at = dst + unit_off(row0, 2 * u);
+  unsigned char* hi_at = dst + unit_off(row0, 2 * u + 1);
   // (rolled: the roles' loops together have to stay in the instruction cache)
 #pragma unroll 1
   for (int i0 = 0; i0 < NR; i0 += BATCH) {
     uint4 x[BATCH];
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) x[i] = *reinterpret_cast<const uint4*>(raw + wt * 16 + (i0 + i) * (kWidenThreads * 16));
+    for (int i = 0; i < BATCH; ++i) x[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * (STEP * D));
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       uint4 lo, hi;
       widen16<KvT>(x[i], lo, hi);
-      const int r = row0 + (i0 + i) * STEP;
-      *reinterpret_cast<uint4*>(dst + unit_off(r, 2 * u + first)) = first ? hi : lo;
-      *reinterpret_cast<uint4*>(dst + unit_off(r, 2 * u + 1 - first)) = first ? lo : hi;
+      *reinterpret_cast<uint4*>(lo_at + (i0 + i) * (STEP * 128)) = lo;
+      *reinterpret_cast<uint4*>(hi_at + (i0 + i) * (STEP * 128)) = hi;
     }
   }
 }
@@ -887,7 +892,11 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
             const float4 v = *reinterpret_cast<const float4*>(stage + ((x & 1) * kM + (x >> 1) * RP + row) * 32 + ((u ^ (row & 7)) << 2));
             a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
           }
-          if (bad_v != 0) add_bad_v<KvT, D>(p, it, bad_v & seen_nodes(p, it.b, t, it.w.nodes), 32 * cc + 4 * u, a);
+          if (bad_v != 0) {
+            const float4 x = bad_v_sum<KvT, D>(p.cache, it.b, it.g, it.w.past, bad_v & seen_nodes(p, it.b, t, it.w.nodes),
+                                               32 * cc + 4 * u);
+            a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+          }
           if (complete)
             store_tree_row4(p, it.b, t, it.g * p.group + h, D, 32 * cc + 4 * u, a, 1.f);
           else
