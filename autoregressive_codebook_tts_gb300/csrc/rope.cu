@@ -7,161 +7,198 @@ namespace tts {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Rows.  A head row is held by D/4 lanes, four entries each (one 16-byte load of f32, 8 bytes
-// of bf16).  A pair's two entries sit in different lanes, at a distance that is any number up
-// to D/2, so the normed row goes through a warp-private patch of shared memory and each lane
-// reads its partners back from there (four neighbours of a vector's entries are a vector too
-// unless rot_dim / 2 is not a multiple of four).  A warp takes U (one or six) heads of one row, all loads
-// issued first; the row's (cos, sin) are loaded once and serve them all.  Bound by HBM on a
-// prompt's rows, by launch latency on one decode step.
+// Rows.  A head row is held by D/8 lanes, eight entries each.  In the half layout a pair's two
+// entries sit in different lanes, at a distance that is any number up to D/2, so the normed row
+// goes through a warp-private patch of shared memory and each lane reads its partners back from
+// there (as vectors unless rot_dim / 2 is not a multiple of four).  A lane takes U (one or three)
+// heads of one row, all loads issued first; the row's (cos, sin) are loaded once and serve them
+// all.  Bound by HBM on a prompt's rows, by launch latency on one decode step.
 // ---------------------------------------------------------------------------
 constexpr int kRopeWarps = 4;
 
+// Eight entries of a lane.
 template <typename T> struct Io;
 template <> struct Io<float> {
-  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&x)[4]) {
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&x)[8]) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 v = __ldcg(q), w = __ldcg(q + 1);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w; x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
   }
-  static __device__ __forceinline__ void store(void* p, int64_t i, const float (&x)[4]) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
+  static __device__ __forceinline__ void store(void* p, int64_t i, const float (&x)[8]) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    q[0] = make_float4(x[0], x[1], x[2], x[3]);
+    q[1] = make_float4(x[4], x[5], x[6], x[7]);
   }
 };
 template <> struct Io<__nv_bfloat16> {
-  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&x)[4]) {
-    const uint2 v = __ldcg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i));
-    x[0] = __uint_as_float(v.x << 16);
-    x[1] = __uint_as_float(v.x & 0xffff0000u);
-    x[2] = __uint_as_float(v.y << 16);
-    x[3] = __uint_as_float(v.y & 0xffff0000u);
+  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&x)[8]) {
+    unpack_bf16x8(__ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i)), x);
   }
-  static __device__ __forceinline__ void store(void* p, int64_t i, const float (&x)[4]) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  static __device__ __forceinline__ void store(void* p, int64_t i, const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+      w[e] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 
+// a^(-1/2): the fast instruction and one Newton step (about one unit in the last place; 0 and
+// infinity as they are).
+__device__ __forceinline__ float inv_sqrt(float a) {
+  const float r = rsqrtf(a);
+  return a > 0.f && a < 3e38f ? r * fmaf(-0.5f * a * r, r, 1.5f) : r;
+}
+
+// Blocks of a many-row grid walk the rows, kRowBlocks a multiprocessor.  (The norm's weights are
+// read once a block: read once a row, or once a warp, they are a few lines of L2 that the whole
+// GPU asks for at once, and cost more than the rows.)
+constexpr int kRowBlocks = 7;
+
 template <typename InT, typename OutT, int D, int U>
-__global__ void __launch_bounds__(kRopeWarps * 32) rope_rows_kernel(const RopeRowsParams p) {
-  constexpr int LPR = D / 4, HPW = 32 / LPR;   // lanes of a head, heads of a warp at once
-  __shared__ float patch[kRopeWarps][32 * 4];
+__global__ void __launch_bounds__(kRopeWarps * 32, kRowBlocks) rope_rows_kernel(const RopeRowsParams p) {
+  constexpr int LPR = D / 8, HPW = 32 / LPR;   // lanes of a head, heads of a warp at once
+  __shared__ float patch[kRopeWarps][32 * 8];
+  __shared__ float s_gamma[2][D];
   grid_wait();
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lr = lane % LPR;
   const int n_heads = p.n_q_heads + p.n_kv_heads;
-  const int64_t r = blockIdx.x;
   const int h0 = (blockIdx.y * kRopeWarps + warp) * (HPW * U) + lane / LPR;
+  int64_t r = blockIdx.x;
   int pos = __ldcg(p.pos + r);
-  float x[U][4];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * HPW;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[u][e] = 0.f;
-    if (h < p.n_q_heads)
-      Io<InT>::load(p.q, r * p.q_stride + static_cast<int64_t>(h) * D + lr * 4, x[u]);
-    else if (h < n_heads)
-      Io<InT>::load(p.k, r * p.k_stride + static_cast<int64_t>(h - p.n_q_heads) * D + lr * 4, x[u]);
-  }
-  // the norm's weights, of the kinds of head that the warp has (every warp of the grid reads the
-  // same few lines)
-  float4 gq = make_float4(1.f, 1.f, 1.f, 1.f), gk = gq;
   if (p.gamma_q != nullptr) {
-    if (h0 < p.n_q_heads) gq = __ldcg(reinterpret_cast<const float4*>(p.gamma_q) + lr);
-    if (h0 + (U - 1) * HPW >= p.n_q_heads && p.n_kv_heads > 0)
-      gk = __ldcg(reinterpret_cast<const float4*>(p.gamma_k) + lr);
+    if (threadIdx.x < D) {
+      s_gamma[0][threadIdx.x] = __ldcg(p.gamma_q + threadIdx.x);
+      if (p.n_kv_heads > 0) s_gamma[1][threadIdx.x] = __ldcg(p.gamma_k + threadIdx.x);
+    }
+    __syncthreads();
   }
-  if (pos < 0 || pos >= p.max_pos) {
-    if (h0 == 0 && lr == 0) set_err(p.err, TTS_EFLAG_POS_RANGE);
-    pos = min(max(pos, 0), p.max_pos - 1);
-  }
-  // entry e: its partner's index, and its own and its partner's factors (1, 0 past rot_dim)
   const int half = p.rot_dim / 2;
   const bool by_vector = !p.interleaved && (half & 3) == 0;
-  const float2* cs = p.cs + static_cast<int64_t>(pos) * half;
-  int partner[4];
-  float fc[4] = {1.f, 1.f, 1.f, 1.f}, fs[4] = {0.f, 0.f, 0.f, 0.f};
-  if (by_vector) {
-    const bool first = lr * 4 < half;
-    partner[0] = lr * 4 < p.rot_dim ? (first ? lr * 4 + half : lr * 4 - half) : lr * 4;
-    if (lr * 4 < p.rot_dim) {
-      const float4* c4 = reinterpret_cast<const float4*>(cs + (first ? lr * 4 : lr * 4 - half));
-      const float4 a = __ldcg(c4), b = __ldcg(c4 + 1);
-      fc[0] = a.x; fc[1] = a.z; fc[2] = b.x; fc[3] = b.z;
-      fs[0] = a.y; fs[1] = a.w; fs[2] = b.y; fs[3] = b.w;
-      if (first) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) fs[e] = -fs[e];   // t_a c - t_b s, t_b c + t_a s
-      }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = lr * 4 + e;
-      partner[e] = i;
-      if (i < p.rot_dim) {
-        const bool first = p.interleaved ? (i & 1) == 0 : i < half;
-        partner[e] = p.interleaved ? i ^ 1 : (first ? i + half : i - half);
-        const float2 v = __ldcg(cs + (p.interleaved ? i >> 1 : (first ? i : i - half)));
-        fc[e] = v.x;
-        fs[e] = first ? -v.y : v.y;
-      }
-    }
-  }
   float* mine = patch[warp] + (lane / LPR) * D;
+#pragma unroll 1
+  for (; r < p.rows; r += gridDim.x) {
+    float x[U][8];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * HPW;
-    float t[4] = {x[u][0], x[u][1], x[u][2], x[u][3]};
-    if (p.gamma_q != nullptr) {
-      float ss = fmaf(t[0], t[0], fmaf(t[1], t[1], fmaf(t[2], t[2], t[3] * t[3])));
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * HPW;
 #pragma unroll
-      for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-      const float rn = 1.0f / sqrtf(ss / static_cast<float>(D) + p.eps);
-      const float4 gm = h < p.n_q_heads ? gq : gk;
-      t[0] = t[0] * rn * gm.x;
-      t[1] = t[1] * rn * gm.y;
-      t[2] = t[2] * rn * gm.z;
-      t[3] = t[3] * rn * gm.w;
+      for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
+      if (h < p.n_q_heads)
+        Io<InT>::load(p.q, r * p.q_stride + static_cast<int64_t>(h) * D + lr * 8, x[u]);
+      else if (h < n_heads)
+        Io<InT>::load(p.k, r * p.k_stride + static_cast<int64_t>(h - p.n_q_heads) * D + lr * 8, x[u]);
     }
-    // pairs of neighbours are a lane's own; others come from the patch
-    float pt[4] = {t[1], t[0], t[3], t[2]};
-    if (!p.interleaved) {
-      __syncwarp();
-      *reinterpret_cast<float4*>(mine + lr * 4) = make_float4(t[0], t[1], t[2], t[3]);
-      __syncwarp();
+    if (pos < 0 || pos >= p.max_pos) {
+      if (h0 == 0 && lr == 0) set_err(p.err, TTS_EFLAG_POS_RANGE);
+      pos = min(max(pos, 0), p.max_pos - 1);
+    }
+    // entry e: its partner's index, and its own and its partner's factors (1, 0 past rot_dim)
+    const float2* cs = p.cs + static_cast<int64_t>(pos) * half;
+    if (r + gridDim.x < p.rows) pos = __ldcg(p.pos + r + gridDim.x);   // the next row's
+    int partner[8];
+    float fc[8], fs[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      const int i0 = lr * 8 + j;
       if (by_vector) {
-        const float4 v = *reinterpret_cast<const float4*>(mine + partner[0]);
-        pt[0] = v.x; pt[1] = v.y; pt[2] = v.z; pt[3] = v.w;
+        // four neighbours turn alike: their partners and factors are vectors too
+        const bool first = i0 < half, turns = i0 < p.rot_dim;
+        partner[j] = !turns ? i0 : first ? i0 + half : i0 - half;
+        float4 a = make_float4(1.f, 0.f, 1.f, 0.f), b = a;
+        if (turns) {
+          const float4* c4 = reinterpret_cast<const float4*>(cs + (first ? i0 : i0 - half));
+          a = __ldcg(c4);
+          b = __ldcg(c4 + 1);
+        }
+        const float sign = first ? -1.f : 1.f;   // t_a c - t_b s, t_b c + t_a s
+        fc[j] = a.x; fc[j + 1] = a.z; fc[j + 2] = b.x; fc[j + 3] = b.z;
+        fs[j] = a.y * sign; fs[j + 1] = a.w * sign; fs[j + 2] = b.y * sign; fs[j + 3] = b.w * sign;
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pt[e] = mine[partner[e]];
+        for (int e = j; e < j + 4; ++e) {
+          const int i = lr * 8 + e;
+          const bool first = p.interleaved ? (i & 1) == 0 : i < half;
+          partner[e] = i;
+          fc[e] = 1.f;
+          fs[e] = 0.f;
+          if (i < p.rot_dim) {
+            partner[e] = p.interleaved ? i ^ 1 : (first ? i + half : i - half);
+            const float2 v = __ldcg(cs + (p.interleaved ? i >> 1 : (first ? i : i - half)));
+            fc[e] = v.x;
+            fs[e] = first ? -v.y : v.y;
+          }
+        }
       }
     }
-    float y[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = lr * 4 + e < p.rot_dim ? fmaf(t[e], fc[e], pt[e] * fs[e]) : t[e];
-    if (h < p.n_q_heads)
-      Io<OutT>::store(p.q_out, r * p.q_out_stride + static_cast<int64_t>(h) * D + lr * 4, y);
-    else if (h < n_heads)
-      Io<OutT>::store(p.k_out, r * p.k_out_stride + static_cast<int64_t>(h - p.n_q_heads) * D + lr * 4, y);
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * HPW;
+      float t[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = x[u][e];
+      if (p.gamma_q != nullptr) {
+        const float* gamma = s_gamma[h < p.n_q_heads ? 0 : 1];
+        const float4 ga = *reinterpret_cast<const float4*>(gamma + 8 * lr), gb = *reinterpret_cast<const float4*>(gamma + 8 * lr + 4);
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(t[e], t[e], ss);
+#pragma unroll
+        for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+        const float rn = inv_sqrt(ss * (1.0f / D) + p.eps);
+        const float gm[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] *= rn * gm[e];
+      }
+      // pairs of neighbours are a lane's own; others come from the patch
+      float pt[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) pt[e] = t[e ^ 1];
+      if (!p.interleaved) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; j += 4)
+          *reinterpret_cast<float4*>(mine + lr * 8 + j) = make_float4(t[j], t[j + 1], t[j + 2], t[j + 3]);
+        __syncwarp();
+        if (by_vector) {
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(mine + partner[j]);
+            pt[j] = v.x; pt[j + 1] = v.y; pt[j + 2] = v.z; pt[j + 3] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) pt[e] = mine[partner[e]];
+        }
+      }
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = lr * 8 + e < p.rot_dim ? fmaf(t[e], fc[e], pt[e] * fs[e]) : t[e];
+      if (h < p.n_q_heads)
+        Io<OutT>::store(p.q_out, r * p.q_out_stride + static_cast<int64_t>(h) * D + lr * 8, y);
+      else if (h < n_heads)
+        Io<OutT>::store(p.k_out, r * p.k_out_stride + static_cast<int64_t>(h - p.n_q_heads) * D + lr * 8, y);
+    }
   }
 }
 
 template <typename InT, typename OutT, int D, int U>
 cudaError_t launch_rows(const RopeRowsParams& p, cudaStream_t s) {
-  constexpr int per = 32 / (D / 4) * U * kRopeWarps;   // heads of a block
+  constexpr int per = 32 / (D / 8) * U * kRopeWarps;   // heads of a block
   const int gy = (p.n_q_heads + p.n_kv_heads + per - 1) / per;
-  const dim3 grid(static_cast<unsigned>(p.rows), gy);
+  const int64_t most = gy > kRowBlocks * p.n_sm ? 1 : kRowBlocks * p.n_sm / gy;
+  const dim3 grid(static_cast<unsigned>(p.rows < most ? p.rows : most), gy);
   return launch_pdl(rope_rows_kernel<InT, OutT, D, U>, grid, dim3(kRopeWarps * 32), 0, s, p);
 }
 template <typename InT, typename OutT, int D>
 cudaError_t launch_rows_u(const RopeRowsParams& p, cudaStream_t s) {
-  // six heads a warp (a row of 24 heads is then one block) once one each would give every SM
-  // over 32 warps
-  const int64_t warps = static_cast<int64_t>(p.rows) * (p.n_q_heads + p.n_kv_heads) / (32 / (D / 4));
-  return warps > static_cast<int64_t>(p.n_sm) * 32 ? launch_rows<InT, OutT, D, 6>(p, s)
+  // three heads a lane (at head_dim 128 a row of 24 heads is then one block) once one each would
+  // give every SM over 16 warps
+  const int64_t warps = static_cast<int64_t>(p.rows) * (p.n_q_heads + p.n_kv_heads) / (32 / (D / 8));
+  return warps > static_cast<int64_t>(p.n_sm) * 16 ? launch_rows<InT, OutT, D, 3>(p, s)
                                                    : launch_rows<InT, OutT, D, 1>(p, s);
 }
 template <typename InT, typename OutT>
