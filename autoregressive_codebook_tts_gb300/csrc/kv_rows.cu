@@ -105,10 +105,16 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const KvRowsParam
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lr = lane % LPR;
   const int b = blockIdx.y;
   const uint32_t i = (blockIdx.x * kWarps + warp) * RPW + lane / LPR;
-  // (once a warp: every block of a stream asks the same two words of L2)
-  const int64_t start = __ldcg(p.start + b);
-  const int nr = p.n_rows == nullptr ? p.T : __ldcg(p.n_rows + b);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && (nr < 0 || nr > p.T)) set_err(p.err, TTS_EFLAG_NVALID);
+  __shared__ int s_start, s_rows;
+  if (threadIdx.x == 0) {
+    // (once a block: every block of a stream asks the same two words of L2)
+    s_start = __ldcg(p.start + b);
+    s_rows = p.n_rows == nullptr ? p.T : __ldcg(p.n_rows + b);
+    if (blockIdx.x == 0 && (s_rows < 0 || s_rows > p.T)) set_err(p.err, TTS_EFLAG_NVALID);
+  }
+  __syncthreads();
+  const int64_t start = s_start;
+  const int nr = s_rows;
   const int t = static_cast<int>(i / c.n_kv_heads), g = static_cast<int>(i) - t * c.n_kv_heads;
   const int64_t pos = start + t;
   const bool first = g == 0 && lr == 0;   // the thread that reports for (b, t)
@@ -193,10 +199,16 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const KvRowsParams
   const int b = blockIdx.y;
   const uint32_t n = static_cast<uint32_t>(p.T) * c.n_kv_heads;   // head rows of a stream (below 2^31)
   const uint32_t i0 = (blockIdx.x * kWarps + warp) * (RPW * U) + lane / LPR;
-  // (once a warp: every block of a stream asks the same two words of L2)
-  const int64_t start = __ldcg(p.start + b);
-  const int nr = p.n_rows == nullptr ? p.T : __ldcg(p.n_rows + b);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && (nr < 0 || nr > p.T)) set_err(p.err, TTS_EFLAG_NVALID);
+  __shared__ int s_start, s_rows;
+  if (threadIdx.x == 0) {
+    // (once a block: every block of a stream asks the same two words of L2)
+    s_start = __ldcg(p.start + b);
+    s_rows = p.n_rows == nullptr ? p.T : __ldcg(p.n_rows + b);
+    if (blockIdx.x == 0 && (s_rows < 0 || s_rows > p.T)) set_err(p.err, TTS_EFLAG_NVALID);
+  }
+  __syncthreads();
+  const int64_t start = s_start;
+  const int nr = s_rows;
   int64_t dst[U];
   LaneRow<KvT> k[U], v[U];
   float sk[U], sv[U];
