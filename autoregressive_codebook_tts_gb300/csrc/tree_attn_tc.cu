@@ -15,7 +15,7 @@
 //   O += P V           V as the MN-major operand.  The maximum in use moves only when a row's
 //                      grows by more than 2^8; then O is rescaled in tensor memory.
 //
-// One loader warp streams the cache with the TMA engine: a bf16 tile as tensor-map boxes (the
+// Two loader warps (K, V) stream the cache with the TMA engine: a bf16 tile as tensor-map boxes (the
 // whole tile, or one box per page and 64 columns) that land in the 128-byte swizzled layout of
 // the MMA; an 8-bit tile as plain bulk copies into a staging tile, which four warps widen to
 // bf16 (integer and bf16 arithmetic, exact) into the operand tile.  In tiles with node rows, V
@@ -41,13 +41,13 @@ namespace {
 
 constexpr int kM = 128, kN = 128;
 constexpr int kSmxThreads = 256, kWidenThreads = 128;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kWidenWarp = 10;
+constexpr int kLoadWarp = 8, kMmaWarp = 10, kWidenWarp = 11;   // (a loader for K, one for V)
 constexpr int kTmemCols = 512;            // S (P over it) 2 x 128, O 2 x 128
 
 template <int D, typename KvT>
 struct TcCfg {
   static constexpr bool k8 = CacheElem<KvT>::kScaled;
-  static constexpr int kThreads = k8 ? 448 : 320;
+  static constexpr int kThreads = k8 ? 480 : 352;
   static constexpr int kTileBytes = kN * D * 2;                 // an operand tile
   static constexpr int kStages = k8 ? 2 : (D == 128 ? 3 : 5);   // operand tiles of K, and of V
   static constexpr int kRawBytes = k8 ? kN * D : 0;             // a staged 8-bit tile (K or V)
@@ -529,40 +529,35 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
   grid_wait();
   grid_launch_dependents();
 
-  if (warp == kLoadWarp) {
-    // ------------------------------------------------------------------ loader
-    constexpr int NL = k8 ? C::kRaw : NS;   // tiles of the ring that it fills
-    unsigned char* dk = smem + (k8 ? C::kOffRawK : C::kOffK);
-    unsigned char* dv = smem + (k8 ? C::kOffRawV : C::kOffV);
+  if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+    // ----------------------------------------------------------------- loaders
+    // K and V stream side by side: a K tile is free once its scores are done, a V tile one
+    // softmax later
+    const bool is_v = warp != kLoadWarp;
+    constexpr int NL = k8 ? C::kRaw : NS;   // tiles of the ring that they fill
     constexpr int bytes = k8 ? C::kRawBytes : C::kTileBytes;
-    uint64_t *fk = k8 ? rawK : fullK, *ek = k8 ? rawKe : emptyK, *fv = k8 ? rawV : fullV, *ev = k8 ? rawVe : emptyV;
-    const unsigned char* gk = static_cast<const unsigned char*>(p.cache.k);
-    const unsigned char* gv = static_cast<const unsigned char*>(p.cache.v);
+    unsigned char* ring = smem + (k8 ? (is_v ? C::kOffRawV : C::kOffRawK) : (is_v ? C::kOffV : C::kOffK));
+    uint64_t* full = k8 ? (is_v ? rawV : rawK) : (is_v ? fullV : fullK);
+    uint64_t* empty = k8 ? (is_v ? rawVe : rawKe) : (is_v ? emptyV : emptyK);
+    const unsigned char* cache = static_cast<const unsigned char*>(is_v ? p.cache.v : p.cache.k);
+    const CUtensorMap* map = is_v ? &vmap : &kmap;
     const uint64_t policy = l2_evict_first_policy();
     TileWalk w;
     w.init(p, blockIdx.x);
     bool ok = true;
-    int nk = 0, nv = 0;
+    int n = 0;
     for (; w.have; w.next(p)) {
-      const int s = nk % NL, r0 = w.tile * kN;
-      const uint32_t ph = static_cast<uint32_t>(nk / NL - 1) & 1u;
-      if (nk >= NL && !warp_wait(&ek[s], ph)) {
+      const int s = n % NL;
+      if (n >= NL && !warp_wait(&empty[s], static_cast<uint32_t>(n / NL - 1) & 1u)) {
         ok = false;
         break;
       }
-      load_tile<D, KvT>(p, &kmap, gk, w.it, r0, lane, dk + s * bytes, &fk[s], policy);
-      ++nk;
-      if (nv >= NL && !warp_wait(&ev[s], ph)) {
-        ok = false;
-        break;
-      }
-      load_tile<D, KvT>(p, &vmap, gv, w.it, r0, lane, dv + s * bytes, &fv[s], policy);
-      ++nv;
+      load_tile<D, KvT>(p, map, cache, w.it, w.tile * kN, lane, ring + s * bytes, &full[s], policy);
+      ++n;
     }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
     // every copy still in flight lands before the CTA ends (earlier ones were consumed)
-    for (int t = max(0, nk - NL); t < nk; ++t) mbar_wait(&fk[t % NL], static_cast<uint32_t>(t / NL) & 1u);
-    for (int t = max(0, nv - NL); t < nv; ++t) mbar_wait(&fv[t % NL], static_cast<uint32_t>(t / NL) & 1u);
+    for (int t = max(0, n - NL); t < n; ++t) mbar_wait(&full[t % NL], static_cast<uint32_t>(t / NL) & 1u);
   } else if (k8 && warp >= kWidenWarp) {
     // ----------------------------------------------------------------- widening
     if constexpr (k8) {
