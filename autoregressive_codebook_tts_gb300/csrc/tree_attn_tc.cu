@@ -55,8 +55,10 @@ struct TcCfg {
   static constexpr int kQBytes = 32768;                         // Q, and the epilogue's 256 x 32 f32
   static constexpr int kOffK = kQBytes, kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffRawK = kOffV + kStages * kTileBytes, kOffRawV = kOffRawK + kRaw * kRawBytes;
-  static constexpr int kOffScale = kOffRawV + kRaw * kRawBytes; // [2][K, V][128] f32
-  static constexpr int kOffBar = kOffScale + (k8 ? 2048 : 0);
+  static constexpr int kOffScale = kOffRawV + kRaw * kRawBytes; // [2][K, V][128] f32: scales of a tile's rows
+  static constexpr int kOffVmax = kOffScale + (k8 ? 2048 : 0);  // [2][4] f32: the largest V scale, by warp
+  static constexpr int kOffQs = kOffVmax + (k8 ? 32 : 0);       // [128] f32: the power of two q was divided by
+  static constexpr int kOffBar = kOffQs + (k8 ? 512 : 0);
   static constexpr size_t kSmem = kOffBar + 320;
 };
 
@@ -182,26 +184,8 @@ __device__ __forceinline__ bool smx_sync_and(bool v) {
   return out != 0;
 }
 
-// Two 8-bit codes as packed bf16 values; x holds them in its two 16-bit halves.
-//   int8 (low bytes, 0 above): with the sign bit s and the low 7 bits m, 0x4300 | m is 128 + m
-//   and 0x4300 | s << 7 is 128 or 256: their difference is the code, exactly.
-//   e4m3 (high bytes): the exponent and mantissa bits shifted to bf16's places stand for the
-//   value times 2^-120 (subnormals too); the product with 2^120 is exact.
-__device__ __forceinline__ uint32_t widen_i8(uint32_t x) {
-  const uint32_t a = (x & 0x007f007fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t widen_e4m3(uint32_t x) {
-  const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
-  const uint32_t k = 0x7b807b80u;   // 2^120
-  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&k));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-// Whether a word of four e4m3 codes holds a NaN (all seven low bits set).
-__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-
-// 16 codes as 16 bf16 values (two 16-byte units).
+// 16 codes as 16 f16 values (two 16-byte units), exactly.  int8: with 128 added, a code is the low
+// byte of the f16 number 1024 + code + 128.
 template <typename KvT>
 __device__ __forceinline__ void widen16(const uint4 v, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -209,22 +193,18 @@ __device__ __forceinline__ void widen16(const uint4 v, uint4& lo, uint4& hi) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (std::is_same<KvT, CodeI8>::value) {
-      o[2 * i] = widen_i8(__byte_perm(w[i], 0, 0x4140));
-      o[2 * i + 1] = widen_i8(__byte_perm(w[i], 0, 0x4342));
-    } else {
-      o[2 * i] = widen_e4m3(__byte_perm(w[i], 0, 0x1404));
-      o[2 * i + 1] = widen_e4m3(__byte_perm(w[i], 0, 0x3424));
-    }
-  }
-  if constexpr (std::is_same<KvT, CodeE4m3>::value) {
-    if ((e4m3_nan(w[0]) | e4m3_nan(w[1]) | e4m3_nan(w[2]) | e4m3_nan(w[3])) != 0) {
+      const uint32_t u = w[i] ^ 0x80808080u, off = 0x64806480u;   // 1152
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t n = e4m3_nan(w[i]);
-        if (n & 0x00000080u) o[2 * i] = (o[2 * i] & 0xffff0000u) | 0x7fc0u;
-        if (n & 0x00008000u) o[2 * i] = (o[2 * i] & 0x0000ffffu) | 0x7fc00000u;
-        if (n & 0x00800000u) o[2 * i + 1] = (o[2 * i + 1] & 0xffff0000u) | 0x7fc0u;
-        if (n & 0x80000000u) o[2 * i + 1] = (o[2 * i + 1] & 0x0000ffffu) | 0x7fc00000u;
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t x = __byte_perm(u, 0x64646464u, k == 0 ? 0x4140 : 0x4342);
+        const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&off));
+        o[2 * i + k] = *reinterpret_cast<const uint32_t*>(&r);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i] >> (16 * k)), __NV_E4M3);
+        o[2 * i + k] = static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
       }
     }
   }
@@ -232,17 +212,19 @@ __device__ __forceinline__ void widen16(const uint4 v, uint4& lo, uint4& hi) {
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// Replaces the non-finite ones of eight bf16 values by 0; whether there were any.
+// Replaces the non-finite ones of eight 16-bit values by 0 (kExp: the exponent bits of their
+// type); whether there were any.
+template <uint32_t kExp>
 __device__ __forceinline__ bool clear_nonfinite(uint4& v) {
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
   bool any = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if ((w[i] & 0x7f80u) == 0x7f80u) {
+    if ((w[i] & kExp) == kExp) {
       any = true;
       w[i] &= 0xffff0000u;
     }
-    if ((w[i] & 0x7f800000u) == 0x7f800000u) {
+    if ((w[i] & (kExp << 16)) == (kExp << 16)) {
       any = true;
       w[i] &= 0x0000ffffu;
     }
@@ -280,68 +262,63 @@ __device__ __forceinline__ uint32_t visible32(int off, uint64_t see) {
   return ~0u;
 }
 
-// The largest of a row's 32 scores (8-bit caches: times the columns' scales).
+// 32 scores of a row from tensor memory: times the columns' K scales (8-bit), -inf where the row
+// does not see the column.
 template <bool k8>
-__device__ __forceinline__ float max_scores(const float (&s)[32], const float* ksc, bool masked, uint32_t vis) {
-  float z[32];
+__device__ __forceinline__ void load_scores(uint32_t taddr, const float* ksc, bool masked, uint32_t vis, float (&s)[32]) {
+  tmem_ld32(taddr, s);
+  if constexpr (k8) {
 #pragma unroll
-  for (int e = 0; e < 32; e += 4) {
-    float4 k = make_float4(1.f, 1.f, 1.f, 1.f);
-    if constexpr (k8) k = *reinterpret_cast<const float4*>(ksc + e);
-    z[e] = k8 ? s[e] * k.x : s[e];
-    z[e + 1] = k8 ? s[e + 1] * k.y : s[e + 1];
-    z[e + 2] = k8 ? s[e + 2] * k.z : s[e + 2];
-    z[e + 3] = k8 ? s[e + 3] * k.w : s[e + 3];
+    for (int e = 0; e < 32; e += 4) {
+      const float4 k = *reinterpret_cast<const float4*>(ksc + e);
+      const float2 a = __fmul2_rn(make_float2(s[e], s[e + 1]), make_float2(k.x, k.y));
+      const float2 b = __fmul2_rn(make_float2(s[e + 2], s[e + 3]), make_float2(k.z, k.w));
+      s[e] = a.x; s[e + 1] = a.y; s[e + 2] = b.x; s[e + 3] = b.y;
+    }
   }
   if (masked) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) z[e] = (vis >> e) & 1u ? z[e] : -INFINITY;
+    for (int e = 0; e < 32; ++e) s[e] = (vis >> e) & 1u ? s[e] : -INFINITY;
   }
+}
+
+__device__ __forceinline__ float max32(const float (&s)[32]) {
+  float z[16];
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1)
+  for (int e = 0; e < 16; ++e) z[e] = fmaxf(s[e], s[e + 16]);
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1)
 #pragma unroll
     for (int e = 0; e < o; ++e) z[e] = fmaxf(z[e], z[e + o]);
   return z[0];
 }
 
-// The weights 2^(score - ms) of 32 columns, rounded to bf16 times the columns' V scales, and
-// their unrounded sum (without the scales).
+// The weights 2^(s c - ms) of 32 columns, packed to 16 bits (8-bit caches: f16, times the
+// columns' V scales and g; else bf16), and their unrounded sum (without the scales).
 template <bool k8>
-__device__ __forceinline__ float weights(const float (&s)[32], const float* ksc, const float* vsc, float c, float ms,
-                                         bool masked, uint32_t vis, uint32_t (&pk)[16]) {
+__device__ __forceinline__ float weights(const float (&s)[32], const float* vsc, float g, float c, float ms,
+                                         uint32_t (&pk)[16]) {
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  const float2 neg = make_float2(-ms, -ms);
+  const float2 neg = make_float2(-ms, -ms), c2 = make_float2(c, c), g2 = make_float2(g, g);
 #pragma unroll
   for (int e = 0; e < 32; e += 4) {
-    float4 k = make_float4(c, c, c, c), v;
-    if constexpr (k8) {
-      k = *reinterpret_cast<const float4*>(ksc + e);
-      v = *reinterpret_cast<const float4*>(vsc + e);
-    }
-    float2 a = __ffma2_rn(make_float2(s[e], s[e + 1]), make_float2(k.x, k.y), neg);
-    float2 b = __ffma2_rn(make_float2(s[e + 2], s[e + 3]), make_float2(k.z, k.w), neg);
-    if (masked) {
-      a.x = (vis >> e) & 1u ? a.x : -INFINITY;
-      a.y = (vis >> (e + 1)) & 1u ? a.y : -INFINITY;
-      b.x = (vis >> (e + 2)) & 1u ? b.x : -INFINITY;
-      b.y = (vis >> (e + 3)) & 1u ? b.y : -INFINITY;
-    }
+    float2 a = __ffma2_rn(make_float2(s[e], s[e + 1]), c2, neg);
+    float2 b = __ffma2_rn(make_float2(s[e + 2], s[e + 3]), c2, neg);
     a.x = ex2(a.x); a.y = ex2(a.y); b.x = ex2(b.x); b.y = ex2(b.y);
     sum[0] = __fadd2_rn(sum[0], a);
     sum[1] = __fadd2_rn(sum[1], b);
     if constexpr (k8) {
-      a = __fmul2_rn(a, make_float2(v.x, v.y));
-      b = __fmul2_rn(b, make_float2(v.z, v.w));
-      if (masked) {   // a row that is not seen has weight 0 whatever its scale
-        a.x = (vis >> e) & 1u ? a.x : 0.f;
-        a.y = (vis >> (e + 1)) & 1u ? a.y : 0.f;
-        b.x = (vis >> (e + 2)) & 1u ? b.x : 0.f;
-        b.y = (vis >> (e + 3)) & 1u ? b.y : 0.f;
-      }
+      const float4 v = *reinterpret_cast<const float4*>(vsc + e);
+      a = __fmul2_rn(a, __fmul2_rn(make_float2(v.x, v.y), g2));
+      b = __fmul2_rn(b, __fmul2_rn(make_float2(v.z, v.w), g2));
+      const __half2 x = __floats2half2_rn(a.x, a.y), y = __floats2half2_rn(b.x, b.y);
+      pk[e / 2] = *reinterpret_cast<const uint32_t*>(&x);
+      pk[e / 2 + 1] = *reinterpret_cast<const uint32_t*>(&y);
+    } else {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(b.x, b.y);
+      pk[e / 2] = *reinterpret_cast<const uint32_t*>(&x);
+      pk[e / 2 + 1] = *reinterpret_cast<const uint32_t*>(&y);
     }
-    const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(b.x, b.y);
-    pk[e / 2] = *reinterpret_cast<const uint32_t*>(&x);
-    pk[e / 2 + 1] = *reinterpret_cast<const uint32_t*>(&y);
   }
   const float2 t = __fadd2_rn(sum[0], sum[1]);
   return t.x + t.y;
@@ -366,9 +343,10 @@ __device__ __forceinline__ float4 bad_v_sum(const CacheView& c, int b, int g, in
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float x;
-      if constexpr (CacheElem<KvT>::kScaled)
-        x = E4m3Code::value(static_cast<const uint8_t*>(c.v)[row * D + col + e]);   // int8 codes are finite
-      else
+      if constexpr (CacheElem<KvT>::kScaled) {
+        const uint32_t code = static_cast<const uint8_t*>(c.v)[row * D + col + e];
+        x = (std::is_same<KvT, CodeI8>::value ? I8Code::value(code) : E4m3Code::value(code)) * c.v_scale[row];
+      } else
         x = static_cast<float>(static_cast<const __nv_bfloat16*>(c.v)[row * D + col + e]);
       if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) a[e] += x;
     }
@@ -473,6 +451,8 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   float* stage = reinterpret_cast<float*>(smem);                          // epilogue: [256][32]
   float* s_scale = reinterpret_cast<float*>(smem + C::kOffScale);         // [2][2][128]
+  float* s_vmax = reinterpret_cast<float*>(smem + C::kOffVmax);           // [2][4]
+  float* s_qs = reinterpret_cast<float*>(smem + C::kOffQs);               // [128]
   uint64_t* fullK = reinterpret_cast<uint64_t*>(smem + C::kOffBar);       // [NS] operand tile written
   uint64_t* emptyK = fullK + NS;                                          // [NS] its product done
   uint64_t* fullV = emptyK + NS;
@@ -563,10 +543,9 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
     if constexpr (k8) {
       const int wt = tid - kWidenWarp * 32;
       const CacheView& c = p.cache;
-      const float sl = fabsf(p.scale_log2);
       TileWalk w;
       w.init(p, blockIdx.x);
-      // the scales of row wt of the next tile (K's times |scale| log2 e), 0 past the window
+      // the scales of row wt of the next tile, 0 past the window
       float ks = 0.f, vs = 0.f;
       auto scales = [&]() {
         const int pos = w.tile * kN + wt;
@@ -576,6 +555,9 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
           const int64_t row = cache_row(c, w.it.b, w.it.g, pos, page);
           ks = __ldcg(c.k_scale + row);
           vs = __ldcg(c.v_scale + row);
+          // a node row's non-finite V scale may not meet the weight 0 of the rows that do not see
+          // it (the epilogue adds it to those that do)
+          if (pos >= w.it.w.past && (__float_as_uint(vs) & 0x7f800000u) == 0x7f800000u) vs = 0.f;
         }
       };
       scales();
@@ -583,7 +565,7 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
       for (int t = 0; w.have; ++t) {
         const int s = t & 1;
         const uint32_t ph = static_cast<uint32_t>(t >> 1) & 1u;
-        const float k = ks * sl, v = vs;
+        const float k = ks, v = vs;
         w.next(p);
         scales();   // in flight while this tile is widened
         // the operand tile and the scales' slot are free once tile t - 2 is through
@@ -593,6 +575,10 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
         }
         s_scale[s * 256 + wt] = k;
         s_scale[s * 256 + 128 + wt] = v;
+        // (magnitudes order as their bits do; what is not finite does not count)
+        const uint32_t vb = __float_as_uint(v) & 0x7fffffffu;
+        const uint32_t top = __reduce_max_sync(kFull, vb < 0x7f800000u ? vb : 0u);
+        if (lane == 0) s_vmax[s * 4 + (wt >> 5)] = __uint_as_float(top);
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {   // K, then V
           if (x == 1 && !warp_wait(&rawV[s], ph)) {
@@ -614,9 +600,10 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
     PieceWalk walk;
     walk.init(p, blockIdx.x);
     {
-      // kind::f16, f32 accumulator, bf16 A and B, M = 128; S: N = 128, B (K) K-major; O: N = D,
-      // B (V) MN-major (bit 16)
-      constexpr uint32_t base = (1u << 4) | (1u << 7) | (1u << 10) | ((kM >> 4) << 24);
+      // kind::f16, f32 accumulator, A and B bf16 (over 8-bit caches f16), M = 128; S: N = 128, B (K)
+      // K-major; O: N = D, B (V) MN-major (bit 16)
+      constexpr uint32_t type = k8 ? 0u : 1u;
+      constexpr uint32_t base = (1u << 4) | (type << 7) | (type << 10) | ((kM >> 4) << 24);
       constexpr uint32_t idS = base | ((kN >> 3) << 17), idO = base | (1u << 16) | ((D >> 3) << 17);
       const uint64_t qd = smem_desc(smem_u32(smem), 16, 1024);
       const uint64_t kd0 = smem_desc(smem_u32(smem + C::kOffK), 16, 1024);
@@ -629,10 +616,11 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
         tc_fence_after();
         const uint64_t kd = kd0 + static_cast<uint64_t>(ks * (C::kTileBytes >> 4));
         const uint32_t d = tmem + wg * kN;
-#pragma unroll
+        // (rolled, as all loops here: see widen_tile)
+#pragma unroll 1
         for (int j = 0; j < D / 16; ++j) {
-          constexpr uint64_t chunk = kN * 128 >> 4;
-          mma_ss(d, qd + (j >> 2) * chunk + (j & 3) * 2, kd + (j >> 2) * chunk + (j & 3) * 2, idS, j > 0 ? 1u : 0u);
+          const uint32_t o = (j >> 2) * (kN * 128 >> 4) + (j & 3) * 2;
+          mma_ss(d, qd + o, kd + o, idS, j);
         }
         mma_commit(&sready[wg]);
         mma_commit(&emptyK[ks]);
@@ -657,8 +645,8 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
           tc_fence_after();
           const uint64_t vd = vd0 + static_cast<uint64_t>(vs * (C::kTileBytes >> 4));
           const uint32_t a = tmem + wg * kN, d = tO + wg * D;
-#pragma unroll
-          for (int j = 0; j < kN / 16; ++j) mma_ts(d, a + j * 8, vd + j * (2048 >> 4), idO, (i > 1 || j > 0) ? 1u : 0u);
+#pragma unroll 1
+          for (int j = 0; j < kN / 16; ++j) mma_ts(d, a + j * 8, vd + j * (2048 >> 4), idO, i > 1 ? 1 : j);
           mma_commit(&emptyV[vs]);
           if (++vs == NS) {
             vs = 0;
@@ -682,8 +670,9 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
     const int f = r / RP, rr = r % RP;           // replica (uniform in a warp), query row
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + wg * kN + lane_base, tOw = tO + wg * D + lane_base;
-    const float c = fabsf(p.scale_log2);
-    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;   // a negative scale turns q round
+    // a negative scale turns q round; a scale of 0 (equal weights) may not meet -inf scores
+    const float c = fmaxf(fabsf(p.scale_log2), 1e-30f);
+    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     PieceWalk walk;
     walk.init(p, blockIdx.x);
     if (blockIdx.x == 0 && p.err != nullptr) {
@@ -720,11 +709,28 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
     while (have) {
       it = next;
       const int first = it.rb * RP;   // of the stream and kv head's query rows
-      // each query row F times
+      // each query row F times; over 8-bit caches as f16, times the power of two that takes its
+      // largest entry to [2^14, 2^15) (bf16's eight bits are exact there down to 2^-28 of that)
 #pragma unroll
       for (int k = 0; k < QU; ++k) {
         const int i = tid + k * kSmxThreads, row = i / UR, u = i % UR;
-        const uint4 v = make_uint4(qv[k].x ^ flip, qv[k].y ^ flip, qv[k].z ^ flip, qv[k].w ^ flip);
+        uint4 v = make_uint4(qv[k].x ^ flip, qv[k].y ^ flip, qv[k].z ^ flip, qv[k].w ^ flip);
+        if constexpr (k8) {
+          uint32_t w[4] = {v.x, v.y, v.z, v.w}, top = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+#pragma unroll
+          for (int o = UR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+          const int up = min(141 - static_cast<int>(top >> 7), 126);   // (at least -114)
+          const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 h = __floats2half2_rn(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          v = make_uint4(w[0], w[1], w[2], w[3]);
+          if (u == 0) s_qs[row] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        }
 #pragma unroll
         for (int x = 0; x < F; ++x) *reinterpret_cast<uint4*>(smem + unit_off(x * RP + row, u)) = v;
       }
@@ -734,7 +740,15 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
       const int node = (first + rr) / p.group;
       const uint64_t see = node < it.w.nodes ? seen_nodes(p, it.b, node, it.w.nodes) : 0ull;
       const int n = it.t1 - it.t0;
+      // the V scale of node tid, where the piece holds its row
+      float node_scale = 0.f;
+      if (k8 && tid < it.w.nodes && it.w.past + tid >= it.t0 * kN && it.w.past + tid < it.t1 * kN) {
+        const CacheView& cv = p.cache;
+        const int pos = it.w.past + tid, page = cv.paged ? max(cache_page(cv, it.b, pos), 0) : 0;
+        node_scale = __ldcg(cv.v_scale + cache_row(cv, it.b, it.g, pos, page));
+      }
       float m = -INFINITY, l = 0.f;
+      int ve = 127, ve_top = 0;   // exponent of 1 / g, and of the largest V scale so far
       for (int i = wg; ok && i < n; i += 2) {
         const int base = (it.t0 + i) * kN + f * W;   // position of this thread's first column
         const bool masked = (it.t0 + i) * kN + kN > it.w.past;
@@ -744,24 +758,40 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
         }
         sph ^= 1u;
         tc_fence_after();
-        // the scales of this thread's columns (8-bit; K's times |scale| log2 e): the slot is
-        // the operand stage of the tile
-        const float* ksc = s_scale + (((taken + i) & 1) * 256 + f * W);
+        // the scales of this thread's columns (8-bit): the slot is the operand stage of the tile
+        const int slot = (taken + i) & 1;
+        const float* ksc = s_scale + (slot * 256 + f * W);
         const float* vsc = ksc + 128;
-        const int off = base - it.w.past;
+        const int off = base - it.w.past, node_row = off - f * W + r;   // (of row r of the tile)
+        const float cr = k8 ? c * s_qs[rr] : c;
         float sv[32];
         float mx = -INFINITY;
 #pragma unroll 1
         for (int cc = 0; cc < W / 32; ++cc) {
-          tmem_ld32(tS + f * W + 32 * cc, sv);
-          const uint32_t vis = masked ? visible32(off + 32 * cc, see) : ~0u;
-          mx = fmaxf(mx, max_scores<k8>(sv, ksc + 32 * cc, masked, vis));
+          load_scores<k8>(tS + f * W + 32 * cc, ksc + 32 * cc, masked, masked ? visible32(off + 32 * cc, see) : ~0u, sv);
+          mx = fmaxf(mx, max32(sv));
         }
-        if (!k8 && mx > -INFINITY) mx *= c;
+        if (mx > -INFINITY) mx *= cr;
         const bool move = mx > m + 8.0f;
-        const bool rescale = move && m > -INFINITY;
-        const float alpha = rescale ? ex2(m - mx) : 1.0f;
-        if (__any_sync(kFull, rescale)) {
+        float alpha = move && m > -INFINITY ? ex2(m - mx) : 1.0f;
+        if (move) {
+          l *= alpha;
+          m = mx;
+        }
+        if constexpr (k8) {
+          // V's scales times g = 2^(127 - ve): a tile's largest stays between 2^-8 and 2^6, so that
+          // the weights (up to 2^8 of it) lie well in f16's range; O is in units of 1 / g.  (ve never falls
+          // below the largest so far less 60: O stays finite.)
+          const float4 v4 = *reinterpret_cast<const float4*>(s_vmax + slot * 4);
+          const int e = static_cast<int>(__float_as_uint(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w))) >> 23);
+          if (e > 0 && (e > ve + 5 || e < ve - 8)) {
+            ve_top = max(ve_top, e);
+            const int to = min(max(e, ve_top - 60), 253);
+            if (i > 1) alpha *= exp2f(static_cast<float>(ve - to));
+            ve = to;
+          }
+        }
+        if (i > 1 && __any_sync(kFull, alpha != 1.0f)) {
           // O is complete up to the group's tile before: its product was issued before S
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
@@ -772,18 +802,15 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
             tmem_st32(tOw + 32 * cc, o);
           }
         }
-        if (move) {
-          l *= alpha;
-          m = mx;
-        }
         const float ms = m == -INFINITY ? 0.f : m;
+        const float g = __uint_as_float(static_cast<uint32_t>(254 - ve) << 23);
         // P over S: chunk cc's 16 packed columns lie below every S column still to be read
 #pragma unroll 1
         for (int cc = 0; cc < W / 32; ++cc) {
-          if (W > 32) tmem_ld32(tS + f * W + 32 * cc, sv);
-          const uint32_t vis = masked ? visible32(off + 32 * cc, see) : ~0u;
+          if (W > 32)
+            load_scores<k8>(tS + f * W + 32 * cc, ksc + 32 * cc, masked, masked ? visible32(off + 32 * cc, see) : ~0u, sv);
           uint32_t pk[16];
-          l += weights<k8>(sv, ksc + 32 * cc, vsc + 32 * cc, c, ms, masked, vis, pk);
+          l += weights<k8>(sv, vsc + 32 * cc, g, cr, ms, pk);
           tmem_st16(tS + (f * W + 32 * cc) / 2, pk);
         }
         if (F > 1) {
@@ -804,7 +831,6 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
               ok = false;
               break;
             }
-            const int node_row = (it.t0 + i) * kN + r - it.w.past;
             if (node_row >= 0) {
               unsigned char* vt = smem + C::kOffV + s * C::kTileBytes;
               bool any = false;
@@ -814,7 +840,7 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
                 uint4 x = make_uint4(0, 0, 0, 0);
                 if (node_row < it.w.nodes) {
                   x = *at;
-                  if (!clear_nonfinite(x)) continue;
+                  if (!clear_nonfinite<k8 ? 0x7c00u : 0x7f80u>(x)) continue;
                   any = true;
                 }
                 *at = x;
@@ -836,6 +862,7 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
         ok = warp_wait(&odone[wg], oph);
         oph ^= 1u;
       }
+      if (k8 && (__float_as_uint(node_scale) & 0x7f800000u) == 0x7f800000u) atomicOr(s_bad, 1ull << tid);
       ok = smx_sync_and(ok);   // every product of the piece is done: the query rows are free
       if (!ok) break;
       tc_fence_after();
@@ -853,6 +880,7 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
       const bool complete = it.complete();
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + it.slot();
       float wt = had ? partial_weight(m, l, M) : 0.f;
+      if (k8) wt *= __uint_as_float(static_cast<uint32_t>(ve) << 23);   // O's unit
       if (complete) {
         // nothing seen: 0; only scores of -inf: NaN, as the formula's 0 / 0
         wt *= L == 0.f ? (it.w.past > 0 || see != 0 ? __uint_as_float(0x7fc00000u) : 0.f) : 1.f / L;
