@@ -465,10 +465,11 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
   uint64_t* sready = qready + 1;                                          // [2] S of the group's tile (and its scales)
   uint64_t* pready = sready + 2;                                          // [2] P written, O rescaled
   uint64_t* odone = pready + 2;                                           // [2] the group's last product of a piece
-  uint64_t* drained = odone + 2;
+  uint64_t* scfree = odone + 2;                                           // [2] scales of the slot's tile used
+  uint64_t* drained = scfree + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
   unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(drained + 2);   // node rows with non-finite V
-  static_assert((4 * NS + 8 + 1 + 6 + 2 + 1) * 8 <= 320, "barrier area");
+  static_assert((4 * NS + 8 + 1 + 6 + 2 + 2 + 1) * 8 <= 320, "barrier area");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -491,6 +492,7 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
       mbar_init(&sready[i], 2);
       mbar_init(&pready[i], 4);
       mbar_init(&odone[i], 1);
+      mbar_init(&scfree[i], 4);
     }
     mbar_init(drained, 1);
     *s_bad = 0;
@@ -547,17 +549,17 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
       w.init(p, blockIdx.x);
       // the scales of row wt of the next tile, 0 past the window
       float ks = 0.f, vs = 0.f;
+      bool node = false;
       auto scales = [&]() {
         const int pos = w.tile * kN + wt;
         ks = vs = 0.f;
+        node = false;
         if (w.have && pos < w.it.w.past + w.it.w.nodes) {
           const int page = c.paged ? max(cache_page(c, w.it.b, pos), 0) : 0;
           const int64_t row = cache_row(c, w.it.b, w.it.g, pos, page);
           ks = __ldcg(c.k_scale + row);
           vs = __ldcg(c.v_scale + row);
-          // a node row's non-finite V scale may not meet the weight 0 of the rows that do not see
-          // it (the epilogue adds it to those that do)
-          if (pos >= w.it.w.past && (__float_as_uint(vs) & 0x7f800000u) == 0x7f800000u) vs = 0.f;
+          node = pos >= w.it.w.past;
         }
       };
       scales();
@@ -565,23 +567,26 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
       for (int t = 0; w.have; ++t) {
         const int s = t & 1;
         const uint32_t ph = static_cast<uint32_t>(t >> 1) & 1u;
-        const float k = ks, v = vs;
+        // a node row's non-finite V scale may not meet the weight 0 of the rows that do not see it
+        // (the epilogue adds it to those that do)
+        const uint32_t vb = __float_as_uint(vs) & 0x7fffffffu;
+        const float k = ks, v = node && vb >= 0x7f800000u ? 0.f : vs;
         w.next(p);
         scales();   // in flight while this tile is widened
-        // the operand tile and the scales' slot are free once tile t - 2 is through
-        if ((t >= 2 && (!warp_wait(&emptyK[s], ph ^ 1u) || !warp_wait(&emptyV[s], ph ^ 1u))) || !warp_wait(&rawK[s], ph)) {
+        // K's operand tile is free once the scores of tile t - 2 are done, the scales' slot once its
+        // weights are, V's operand tile once its product is
+        if ((t >= 2 && (!warp_wait(&emptyK[s], ph ^ 1u) || !warp_wait(&scfree[s], ph ^ 1u))) || !warp_wait(&rawK[s], ph)) {
           ok = false;
           break;
         }
         s_scale[s * 256 + wt] = k;
         s_scale[s * 256 + 128 + wt] = v;
         // (magnitudes order as their bits do; what is not finite does not count)
-        const uint32_t vb = __float_as_uint(v) & 0x7fffffffu;
         const uint32_t top = __reduce_max_sync(kFull, vb < 0x7f800000u ? vb : 0u);
         if (lane == 0) s_vmax[s * 4 + (wt >> 5)] = __uint_as_float(top);
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {   // K, then V
-          if (x == 1 && !warp_wait(&rawV[s], ph)) {
+          if (x == 1 && (!warp_wait(&rawV[s], ph) || (t >= 2 && !warp_wait(&emptyV[s], ph ^ 1u)))) {
             ok = false;
             break;
           }
@@ -612,7 +617,6 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
       uint32_t kph = 0, vph = 0, pph[2] = {0, 0};
       bool ok = true;
       auto issue_s = [&](int wg) {
-        if (!warp_wait(&fullK[ks], kph)) return false;
         tc_fence_after();
         const uint64_t kd = kd0 + static_cast<uint64_t>(ks * (C::kTileBytes >> 4));
         const uint32_t d = tmem + wg * kN;
@@ -629,33 +633,43 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
           ks = 0;
           kph ^= 1u;
         }
-        return true;
       };
+      auto issue_pv = [&](int i, bool last) {
+        const int wg = i & 1;
+        pph[wg] ^= 1u;
+        tc_fence_after();
+        const uint64_t vd = vd0 + static_cast<uint64_t>(vs * (C::kTileBytes >> 4));
+        const uint32_t a = tmem + wg * kN, d = tO + wg * D;
+#pragma unroll 1
+        for (int j = 0; j < kN / 16; ++j) mma_ts(d, a + j * 8, vd + j * (2048 >> 4), idO, i > 1 ? 1 : j);
+        mma_commit(&emptyV[vs]);
+        if (last) mma_commit(&odone[wg]);
+        if (++vs == NS) {
+          vs = 0;
+          vph ^= 1u;
+        }
+      };
+      auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_try_wait(bar, parity)); };
       Piece it;
       for (uint32_t piece = 0; ok && walk.get(p, it); ++piece) {
         const int n = it.t1 - it.t0;
-        ok = warp_wait(qready, piece & 1u) && issue_s(0) && (n < 2 || issue_s(1));
-        for (int i = 0; ok && i < n; ++i) {
-          const int wg = i & 1;
-          if (!warp_wait(&fullV[vs], vph) || !warp_wait(&pready[wg], pph[wg])) {
-            ok = false;
-            break;
+        ok = warp_wait(qready, piece & 1u);
+        // tile ns's scores go out once K is there and the product that read its tensor memory has
+        // been issued, tile np's product once P and V are: whichever is ready first
+        int ns = 0, np = 0;
+        long long start = clock64();
+        while (ok && np < n) {
+          if (ns < n && ns < np + 2 && ready(&fullK[ks], kph)) {
+            issue_s(ns & 1);
+            ++ns;
+            start = clock64();
+          } else if (np < ns && ready(&pready[np & 1], pph[np & 1]) && ready(&fullV[vs], vph)) {
+            issue_pv(np, np + 2 >= n);
+            ++np;
+            start = clock64();
+          } else {
+            ok = __all_sync(kFull, clock64() - start <= kWaitLimitCycles);
           }
-          pph[wg] ^= 1u;
-          tc_fence_after();
-          const uint64_t vd = vd0 + static_cast<uint64_t>(vs * (C::kTileBytes >> 4));
-          const uint32_t a = tmem + wg * kN, d = tO + wg * D;
-#pragma unroll 1
-          for (int j = 0; j < kN / 16; ++j) mma_ts(d, a + j * 8, vd + j * (2048 >> 4), idO, i > 1 ? 1 : j);
-          mma_commit(&emptyV[vs]);
-          if (++vs == NS) {
-            vs = 0;
-            vph ^= 1u;
-          }
-          if (i + 2 < n)
-            ok = issue_s(wg);
-          else
-            mma_commit(&odone[wg]);
         }
       }
       // no product is in flight when the CTA gives its tensor memory back
@@ -813,6 +827,7 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
           l += weights<k8>(sv, vsc + 32 * cc, g, cr, ms, pk);
           tmem_st16(tS + (f * W + 32 * cc) / 2, pk);
         }
+        if constexpr (k8) warp_arrive(&scfree[slot]);
         if (F > 1) {
           // the columns of the other replicas
           const uint32_t zero[16] = {};
