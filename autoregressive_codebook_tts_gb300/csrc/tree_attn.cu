@@ -285,12 +285,14 @@ __global__ void __launch_bounds__(kThreads) tree_combine_kernel(const TreeParams
   const int per_stream = c.n_kv_heads * p.n_rb;
   const int b = blockIdx.x / per_stream, k = blockIdx.x - b * per_stream;
   const int g = k / p.n_rb, rb = k - g * p.n_rb;
-  const TreeWindow w = tree_window(p, b, nullptr);
+  Axis axis;
+  int64_t before;
+  int at_b = b;
+  axis.find(p, 0, at_b, before);
+  const TreeWindow w = axis.window(p, b);
   const int tiles = tree_tiles(p, w);
   if (tiles == 0) return;
-  const int64_t before = cost_of(p, 0, b);
-  const int64_t total = before + cost_of(p, b, c.B);
-  const int64_t per = cost_per_cta(total, p.n_cta), cost = item_cost(tiles);
+  const int64_t per = cost_per_cta(axis.total, p.n_cta), cost = item_cost(tiles);
   const int64_t start = before + cost * k;
   const int c0 = static_cast<int>(start / per), c1 = static_cast<int>((start + cost - 1) / per);
   // the CTAs whose pieces hold tiles are consecutive: the first whose range ends past tile 0

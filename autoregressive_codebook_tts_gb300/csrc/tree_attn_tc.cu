@@ -146,6 +146,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr) : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -216,7 +224,12 @@ __device__ __forceinline__ void widen16(const uint4 v, uint4& lo, uint4& hi) {
 // type); whether there were any.
 template <uint32_t kExp>
 __device__ __forceinline__ bool clear_nonfinite(uint4& v) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t w[4] = {v.x, v.y, v.z, v.w}, hit = 0;
+  // (all exponent bits set: one more at their lowest place carries into the sign's)
+  constexpr uint32_t both = kExp | (kExp << 16), one = both & ~(both << 1);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) hit |= (w[i] & both) + one;
+  if ((hit & 0x80008000u) == 0) return false;
   bool any = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -322,6 +335,20 @@ __device__ __forceinline__ float weights(const float (&s)[32], const float* vsc,
   }
   const float2 t = __fadd2_rn(sum[0], sum[1]);
   return t.x + t.y;
+}
+
+// A packed pair of weights times a (rounded once more: only weights of a tile whose maximum moved
+// after they were written).
+template <bool k8>
+__device__ __forceinline__ uint32_t scale_pair(uint32_t w, float a) {
+  if constexpr (k8) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    const __half2 y = __floats2half2_rn(x.x * a, x.y * a);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(w << 16) * a, __uint_as_float(w & 0xffff0000u) * a);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
 }
 
 // 2^(m - M) of a partial row; one that saw nothing has weight 0, one that only saw NaN scores
@@ -778,20 +805,7 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
         const float* vsc = ksc + 128;
         const int off = base - it.w.past, node_row = off - f * W + r;   // (of row r of the tile)
         const float cr = k8 ? c * s_qs[rr] : c;
-        float sv[32];
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int cc = 0; cc < W / 32; ++cc) {
-          load_scores<k8>(tS + f * W + 32 * cc, ksc + 32 * cc, masked, masked ? visible32(off + 32 * cc, see) : ~0u, sv);
-          mx = fmaxf(mx, max32(sv));
-        }
-        if (mx > -INFINITY) mx *= cr;
-        const bool move = mx > m + 8.0f;
-        float alpha = move && m > -INFINITY ? ex2(m - mx) : 1.0f;
-        if (move) {
-          l *= alpha;
-          m = mx;
-        }
+        float unit = 1.0f;   // what O's unit changes by
         if constexpr (k8) {
           // V's scales times g = 2^(127 - ve): a tile's largest stays between 2^-8 and 2^6, so that
           // the weights (up to 2^8 of it) lie well in f16's range; O is in units of 1 / g.  (ve never falls
@@ -801,31 +815,53 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
           if (e > 0 && (e > ve + 5 || e < ve - 8)) {
             ve_top = max(ve_top, e);
             const int to = min(max(e, ve_top - 60), 253);
-            if (i > 1) alpha *= exp2f(static_cast<float>(ve - to));
+            unit = exp2f(static_cast<float>(ve - to));
             ve = to;
           }
         }
-        if (i > 1 && __any_sync(kFull, alpha != 1.0f)) {
-          // O is complete up to the group's tile before: its product was issued before S
-#pragma unroll 1
-          for (int cc = 0; cc < D / 32; ++cc) {
-            float o[32];
-            tmem_ld32(tOw + 32 * cc, o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-            tmem_st32(tOw + 32 * cc, o);
-          }
-        }
-        const float ms = m == -INFINITY ? 0.f : m;
         const float g = __uint_as_float(static_cast<uint32_t>(254 - ve) << 23);
-        // P over S: chunk cc's 16 packed columns lie below every S column still to be read
+        // chunks of 32 columns, P over S (a chunk's 16 packed columns lie below every S column
+        // still to be read).  A chunk that moves the maximum rescales O and the chunks before it.
 #pragma unroll 1
         for (int cc = 0; cc < W / 32; ++cc) {
-          if (W > 32)
-            load_scores<k8>(tS + f * W + 32 * cc, ksc + 32 * cc, masked, masked ? visible32(off + 32 * cc, see) : ~0u, sv);
+          float sv[32];
+          load_scores<k8>(tS + f * W + 32 * cc, ksc + 32 * cc, masked, masked ? visible32(off + 32 * cc, see) : ~0u, sv);
+          float mx = max32(sv);
+          if (mx > -INFINITY) mx *= cr;
+          const bool move = mx > m + 8.0f;
+          const float alpha = move && m > -INFINITY ? ex2(m - mx) : 1.0f;
+          if (move) {
+            l *= alpha;
+            m = mx;
+          }
+          if (__any_sync(kFull, alpha != 1.0f || (cc == 0 && unit != 1.0f))) {
+            if (i > 1) {
+              // O is complete up to the group's tile before: its product was issued before S
+              const float by = cc == 0 ? alpha * unit : alpha;
+#pragma unroll 1
+              for (int k = 0; k < D / 32; ++k) {
+                float o[32];
+                tmem_ld32(tOw + 32 * k, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= by;
+                tmem_st32(tOw + 32 * k, o);
+              }
+            }
+            if (cc > 0) {
+              tmem_wait_st();
+#pragma unroll 1
+              for (int k = 0; k < cc; ++k) {
+                uint32_t pk[16];
+                tmem_ld16(tS + f * (W / 2) + 16 * k, pk);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[e] = scale_pair<k8>(pk[e], alpha);
+                tmem_st16(tS + f * (W / 2) + 16 * k, pk);
+              }
+            }
+          }
           uint32_t pk[16];
-          l += weights<k8>(sv, vsc + 32 * cc, g, cr, ms, pk);
-          tmem_st16(tS + (f * W + 32 * cc) / 2, pk);
+          l += weights<k8>(sv, vsc + 32 * cc, g, cr, m == -INFINITY ? 0.f : m, pk);
+          tmem_st16(tS + f * (W / 2) + 16 * cc, pk);
         }
         if constexpr (k8) warp_arrive(&scfree[slot]);
         if (F > 1) {
@@ -849,16 +885,22 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
             if (node_row >= 0) {
               unsigned char* vt = smem + C::kOffV + s * C::kTileBytes;
               bool any = false;
+              if (node_row >= it.w.nodes) {
+#pragma unroll 4
+                for (int u = 0; u < UR; ++u) *reinterpret_cast<uint4*>(vt + unit_off(r, u)) = make_uint4(0, 0, 0, 0);
+              } else {
 #pragma unroll 1
-              for (int u = 0; u < UR; ++u) {
-                uint4* at = reinterpret_cast<uint4*>(vt + unit_off(r, u));
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (node_row < it.w.nodes) {
-                  x = *at;
-                  if (!clear_nonfinite<k8 ? 0x7c00u : 0x7f80u>(x)) continue;
-                  any = true;
+                for (int u0 = 0; u0 < UR; u0 += 4) {
+                  uint4 x[4];
+#pragma unroll
+                  for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const uint4*>(vt + unit_off(r, u0 + u));
+#pragma unroll
+                  for (int u = 0; u < 4; ++u)
+                    if (clear_nonfinite<k8 ? 0x7c00u : 0x7f80u>(x[u])) {
+                      any = true;
+                      *reinterpret_cast<uint4*>(vt + unit_off(r, u0 + u)) = x[u];
+                    }
                 }
-                *at = x;
               }
               if (any) atomicOr(s_bad, 1ull << node_row);
             }
@@ -905,40 +947,46 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
       const unsigned long long bad_v = *s_bad;
       smx_sync();   // the statistics are read; everyone has the noted rows
       if (tid == 0) *s_bad = 0;
+      // the item's rows, in passes of 32 columns, or of 64 or 128 where few enough rows leave the
+      // room: partial row x of row rr at slot x * (RP >> wide) + rr, its 16-byte units turned by rr
+      const int rows = min(RP, it.w.nodes * p.group - first);
+      const int wide = rows * 4 <= RP && D == 128 ? 2 : rows * 2 <= RP ? 1 : 0;
+      const int per = RP >> wide, units = 8 << wide;
 #pragma unroll 1
-      for (int cc = 0; cc < D / 32; ++cc) {
-        float o[32];
-        if (had) {
-          tmem_ld32(tOw + 32 * cc, o);
+      for (int c0 = 0; c0 < D; c0 += 32 << wide) {
+        float* mine = stage + ((wg * F + f) * per + rr) * (32 << wide);
+#pragma unroll 1
+        for (int k = 0; k < 1 << wide; ++k) {
+          float o[32];
+          if (had) tmem_ld32(tOw + c0 + 32 * k, o);
+          if (rr < rows) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= wt;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            for (int u = 0; u < 8; ++u)
+              *reinterpret_cast<float4*>(mine + ((8 * k + (u ^ (rr & 7))) << 2)) =
+                  had ? make_float4(o[4 * u] * wt, o[4 * u + 1] * wt, o[4 * u + 2] * wt, o[4 * u + 3] * wt)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
         }
-        float* mine = stage + (wg * kM + r) * 32;
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          *reinterpret_cast<float4*>(mine + ((u ^ (r & 7)) << 2)) = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
         smx_sync();
-        for (int i = tid; i < RP * 8; i += kSmxThreads) {
-          const int row = i >> 3, u = i & 7, t = (first + row) / p.group, h = first + row - t * p.group;
-          if (t >= it.w.nodes) continue;
+#pragma unroll 1
+        for (int i = tid; i < rows * units; i += kSmxThreads) {
+          const int row = i / units, u = i - row * units, t = (first + row) / p.group, h = first + row - t * p.group;
+          const float* src = stage + row * (32 << wide) + ((u ^ (row & 7)) << 2);
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int x = 0; x < 2 * F; ++x) {
-            const float4 v = *reinterpret_cast<const float4*>(stage + ((x & 1) * kM + (x >> 1) * RP + row) * 32 + ((u ^ (row & 7)) << 2));
+            const float4 v = *reinterpret_cast<const float4*>(src + x * per * (32 << wide));
             a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
           }
+          const int col = c0 + 4 * u;
           if (bad_v != 0) {
-            const float4 x = bad_v_sum<KvT, D>(p.cache, it.b, it.g, it.w.past, bad_v & seen_nodes(p, it.b, t, it.w.nodes),
-                                               32 * cc + 4 * u);
+            const float4 x = bad_v_sum<KvT, D>(p.cache, it.b, it.g, it.w.past, bad_v & seen_nodes(p, it.b, t, it.w.nodes), col);
             a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
           }
           if (complete)
-            store_tree_row4(p, it.b, t, it.g * p.group + h, D, 32 * cc + 4 * u, a, 1.f);
+            store_tree_row4(p, it.b, t, it.g * p.group + h, D, col, a, 1.f);
           else
-            *reinterpret_cast<float4*>(p.part + (slot * RP + row) * D + 32 * cc + 4 * u) = a;
+            *reinterpret_cast<float4*>(p.part + (slot * RP + row) * D + col) = a;
         }
         smx_sync();
       }

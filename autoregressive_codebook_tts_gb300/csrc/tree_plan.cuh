@@ -68,8 +68,74 @@ struct Piece {
   __device__ __forceinline__ int slot() const { return t0 > 0 ? 0 : 1; }
 };
 
+// Where on the cost axis a stream lies, and how long the axis is.  By a whole warp; up to 32
+// streams take one round trip to memory (this stands before everything else a launch does).
+struct Axis {
+  int lane_past, lane_nodes;   // up to 32 streams: lane b's window
+  int64_t total;
+
+  __device__ __forceinline__ TreeWindow window(const TreeParams& p, int b) const {
+    if (p.cache.B > 32) return tree_window(p, b, nullptr);
+    return {__shfl_sync(kFull, lane_past, b), __shfl_sync(kFull, lane_nodes, b)};
+  }
+  // Sums the axis; `start`: of stream b (b >= 0), or with b < 0 b becomes the stream that holds
+  // unit lo(per_cta) * cta (B when none does).
+  __device__ void find(const TreeParams& p, int cta, int& b, int64_t& start) {
+    const int lane = threadIdx.x & 31, B = p.cache.B;
+    lane_past = lane_nodes = 0;
+    if (B <= 32) {
+      int64_t own = 0;
+      if (lane < B) {
+        const TreeWindow w = tree_window(p, lane, nullptr);
+        lane_past = w.past;
+        lane_nodes = w.nodes;
+        own = item_cost(tree_tiles(p, w)) * (p.cache.n_kv_heads * p.n_rb);
+      }
+      int64_t end = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(kFull, end, o);
+        if (lane >= o) end += x;
+      }
+      total = __shfl_sync(kFull, end, 31);
+      if (b < 0) {
+        const unsigned over = __ballot_sync(kFull, end > cost_per_cta(total, p.n_cta) * cta);
+        b = over == 0 ? B : __ffs(static_cast<int>(over)) - 1;
+      }
+      start = b < B ? __shfl_sync(kFull, end - own, b) : total;
+      return;
+    }
+    total = cost_of(p, 0, B);
+    if (b >= 0) {
+      start = cost_of(p, 0, b);
+      return;
+    }
+    const int64_t lo = cost_per_cta(total, p.n_cta) * cta;
+    start = 0;
+    b = B;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      const int64_t own = b0 + lane < B ? stream_cost(p, b0 + lane) : 0;
+      int64_t end = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(kFull, end, o);
+        if (lane >= o) end += x;
+      }
+      const unsigned over = __ballot_sync(kFull, start + end > lo);
+      if (over != 0) {
+        const int at = __ffs(static_cast<int>(over)) - 1;
+        b = b0 + at;
+        start += __shfl_sync(kFull, end - own, at);
+        break;
+      }
+      start += __shfl_sync(kFull, end, 31);
+    }
+  }
+};
+
 // The pieces of one CTA, in order.  Every call is by a whole warp.
 struct PieceWalk {
+  Axis axis;
   int64_t lo, hi;    // the CTA's units
   int64_t start;     // where item `next` starts
   int b, next;       // stream, and item of the stream (g * n_rb + rb), of the next item
@@ -78,13 +144,12 @@ struct PieceWalk {
 
   __device__ __forceinline__ void set_stream(const TreeParams& p) {
     if (b < p.cache.B) {
-      w = tree_window(p, b, nullptr);
+      w = p.whole ? tree_window(p, b, nullptr) : axis.window(p, b);
       tiles = tree_tiles(p, w);
     }
   }
 
   __device__ void init(const TreeParams& p, int cta) {
-    const int lane = threadIdx.x & 31;
     if (p.whole) {
       // items dealt out one by one
       b = cta / (p.cache.n_kv_heads * p.n_rb);
@@ -94,31 +159,12 @@ struct PieceWalk {
       set_stream(p);
       return;
     }
-    const int64_t per = cost_per_cta(cost_of(p, 0, p.cache.B), p.n_cta);
+    b = -1;
+    axis.find(p, cta, b, start);
+    const int64_t per = cost_per_cta(axis.total, p.n_cta);
     lo = per * cta;
     hi = lo + per;
-    // the stream whose units hold lo: 32 streams a step, their ends by a warp scan
-    int64_t before = 0;
-    b = p.cache.B;
-    for (int b0 = 0; b0 < p.cache.B; b0 += 32) {
-      const int64_t own = b0 + lane < p.cache.B ? stream_cost(p, b0 + lane) : 0;
-      int64_t end = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(kFull, end, o);
-        if (lane >= o) end += x;
-      }
-      const unsigned over = __ballot_sync(kFull, before + end > lo);
-      if (over != 0) {
-        const int at = __ffs(static_cast<int>(over)) - 1;
-        b = b0 + at;
-        before += __shfl_sync(kFull, end - own, at);
-        break;
-      }
-      before += __shfl_sync(kFull, end, 31);
-    }
     next = 0;
-    start = before;
     set_stream(p);
     if (b < p.cache.B) {
       const int64_t c = item_cost(tiles);
