@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
     }
     if (any) set_err(p.err, TTS_EFLAG_NVALID);
   }
+  const int gs = p.group >> 1;   // log2 of the group (1, 2 or 4)
   PieceWalk walk;
   Piece it;
   walk.init(p, blockIdx.x);
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
     const int r_first = it.rb * RB;
     // query rows, zero past the nodes
     for (int i = tid; i < RB * C4; i += kThreads) {
-      const int r = i / C4, d4 = i - r * C4, t = (r_first + r) / p.group, h = (r_first + r) - t * p.group;
+      const int r = i / C4, d4 = i - r * C4, t = (r_first + r) >> gs, h = (r_first + r) & (p.group - 1);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (t < it.w.nodes) {
         const int64_t at = (static_cast<int64_t>(it.b) * p.T + t) * p.q_stride + (it.g * p.group + h) * D + d4 * 4;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
       *reinterpret_cast<float4*>(&s.q[r][d4 * 4]) = x;
     }
     if (tid < RB) {
-      const int t = (r_first + tid) / p.group;
+      const int t = (r_first + tid) >> gs;
       s.m[tid] = -INFINITY;
       s.l[tid] = 0.f;
       s.see[tid] = t < it.w.nodes ? seen_nodes(p, it.b, t, it.w.nodes) : 0ull;
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
     if (og < RB) {
 #pragma unroll
       for (int i = 0; i < RV; ++i) {
-        const int r = og * RV + i, t = (r_first + r) / p.group, h = (r_first + r) - t * p.group;
+        const int r = og * RV + i, t = (r_first + r) >> gs, h = (r_first + r) & (p.group - 1);
         if (t >= it.w.nodes) continue;
         if (it.complete()) {
           const float l = s.l[r];
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) tree_combine_kernel(const TreeParams
   while (first < c1 && tile_at(per * (first + 1) - start, tiles) == 0) ++first;
   if (tile_at(per * (first + 1) - start, tiles) >= tiles) return;   // finished by one CTA
   for (int r = blockIdx.y * kWarps + warp; r < p.rows; r += gridDim.y * kWarps) {
-    const int t = (rb * p.rows + r) / p.group, h = rb * p.rows + r - t * p.group;
+    const int t = (rb * p.rows + r) >> (p.group >> 1), h = (rb * p.rows + r) & (p.group - 1);
     if (t >= w.nodes) break;
     float M = -INFINITY;
     for (int x = first + lane; x <= c1; x += 32) {

@@ -714,6 +714,7 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
     // a negative scale turns q round; a scale of 0 (equal weights) may not meet -inf scores
     const float c = fmaxf(fabsf(p.scale_log2), 1e-30f);
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const int gs = p.group >> 1;   // log2 of the group (1, 2 or 4)
     PieceWalk walk;
     walk.init(p, blockIdx.x);
     if (blockIdx.x == 0 && p.err != nullptr) {
@@ -735,8 +736,8 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
     auto load_q = [&](const Piece& x) {
 #pragma unroll
       for (int k = 0; k < QU; ++k) {
-        const int i = tid + k * kSmxThreads, row = i / UR, u = i % UR, t = (x.rb * RP + row) / p.group,
-                  h = x.rb * RP + row - t * p.group;
+        const int i = tid + k * kSmxThreads, row = i / UR, u = i % UR, q = x.rb * RP + row, t = q >> gs,
+                  h = q & (p.group - 1);
         qv[k] = make_uint4(0, 0, 0, 0);
         if (t < x.w.nodes)
           qv[k] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
       fence_async_smem();
       tc_fence_before();
       warp_arrive(qready);
-      const int node = (first + rr) / p.group;
+      const int node = (first + rr) >> gs;
       const uint64_t see = node < it.w.nodes ? seen_nodes(p, it.b, node, it.w.nodes) : 0ull;
       const int n = it.t1 - it.t0;
       // the V scale of node tid, where the piece holds its row
@@ -970,7 +971,7 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
         smx_sync();
 #pragma unroll 1
         for (int i = tid; i < rows * units; i += kSmxThreads) {
-          const int row = i / units, u = i - row * units, t = (first + row) / p.group, h = first + row - t * p.group;
+          const int row = i >> (3 + wide), u = i & (units - 1), t = (first + row) >> gs, h = (first + row) & (p.group - 1);
           const float* src = stage + row * (32 << wide) + ((u ^ (row & 7)) << 2);
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
