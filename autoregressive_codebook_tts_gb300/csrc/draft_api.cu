@@ -59,7 +59,7 @@ TreePlan tree_plan(const tts_kv_desc* d, int T, int q_dtype) {
   const int rows = T * (d->n_q_heads / d->n_kv_heads);
   // f32 operands would lose bits on the tensor cores
   t.tc = q_dtype == TTS_BF16 && tree_attn_tc_supported(d);
-  t.rows = t.tc ? (rows <= 32 ? 32 : rows <= 64 ? 64 : 128) : (rows <= 8 ? 8 : 32);
+  t.rows = t.tc ? (rows <= 32 ? 32 : rows <= 64 ? 64 : 128) : (rows <= 8 ? 8 : rows <= 16 ? 16 : 32);
   t.n_rb = (rows + t.rows - 1) / t.rows;
   t.tile = t.tc ? 128 : 64;
   const int64_t items = static_cast<int64_t>(d->B) * d->n_kv_heads * t.n_rb;
@@ -74,7 +74,9 @@ TreePlan tree_plan(const tts_kv_desc* d, int T, int q_dtype) {
 }
 
 bool tree_shape_ok(const tts_kv_desc* d, int32_t T) {
-  return T >= 1 && T <= TTS_MAX_TREE_NODES && static_cast<int64_t>(d->B) * d->n_kv_heads * T < (int64_t{1} << 30);
+  // (the work's units, at most 8 (12 + capacity / 16) a stream and kv head, are counted in 32 bits)
+  return T >= 1 && T <= TTS_MAX_TREE_NODES && d->B <= 65535 && d->n_kv_heads <= 65535 &&
+         static_cast<int64_t>(d->B) * d->n_kv_heads * (static_cast<int64_t>(d->capacity) + 192) < (int64_t{1} << 32);
 }
 
 }  // namespace

@@ -49,11 +49,10 @@ struct TreeSmem {
   float m[RB], l[RB], alpha[RB];
   unsigned long long see[RB];
   unsigned long long bad_v;  // node rows with non-finite V entries (in this piece)
-  int64_t row[kTile];
 };
 
 template <int D, typename KvT, int RB>
-__global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const TreeParams p) {
   using E = CacheElem<KvT>;
   constexpr int RW = RB / kWarps;              // query rows of a warp
   constexpr int C4 = D / 4;                    // 4-column groups of a row
@@ -79,7 +78,40 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
   Piece it;
   walk.init(p, blockIdx.x);
   while (walk.get(p, it)) {
-    const int r_first = it.rb * RB;
+    const int r_first = it.rb * RB, n_total = it.w.past + it.w.nodes;
+    // A tile's vectors of K and V: loaded to registers (the first before anything else waits, the
+    // next while a tile is worked on), then widened into shared memory.
+    constexpr int CV = D / E::kVec;   // 16-byte vectors of a cache row
+    constexpr int N = kTile * CV, NV = N / kThreads;
+    static_assert(N % kThreads == 0, "whole vectors a thread");
+    uint4 kr[NV], vr[NV];
+    float sk[NV], sv[NV];
+    auto fetch = [&](int tile) {
+      const int r0 = tile * kTile, nrow = min(kTile, n_total - r0);
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        const int i = n * kThreads + tid, r = i / CV, u = i - r * CV;
+        kr[n] = vr[n] = make_uint4(0, 0, 0, 0);
+        sk[n] = sv[n] = 0.f;
+        if (r >= nrow) continue;
+        int page = 0;
+        if (c.paged) {
+          page = cache_page(c, it.b, r0 + r);
+          if (page < 0) {
+            set_err(p.err, TTS_EFLAG_PAGE);
+            page = 0;
+          }
+        }
+        const int64_t row = cache_row(c, it.b, it.g, r0 + r, page);
+        kr[n] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(c.k) + row * (D * E::kBytes)) + u);
+        vr[n] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(c.v) + row * (D * E::kBytes)) + u);
+        if constexpr (E::kScaled) {
+          sk[n] = __ldcg(c.k_scale + row);
+          sv[n] = __ldcg(c.v_scale + row);
+        }
+      }
+    };
+    fetch(it.t0);
     // query rows, zero past the nodes
     for (int i = tid; i < RB * C4; i += kThreads) {
       const int r = i / C4, d4 = i - r * C4, t = (r_first + r) >> gs, h = (r_first + r) & (p.group - 1);
@@ -107,54 +139,31 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
 #pragma unroll
     for (int i = 0; i < RV; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     const int oc = tid % C4, og = tid / C4;
-    const int n_total = it.w.past + it.w.nodes;
     for (int tile = it.t0; tile < it.t1; ++tile) {
-      const int r0 = tile * kTile, nrow = min(kTile, n_total - r0);
+      const int r0 = tile * kTile;
       __syncthreads();   // the tile before is consumed
-      if (tid < nrow) {
-        int page = 0;
-        if (c.paged) {
-          page = cache_page(c, it.b, r0 + tid);
-          if (page < 0) {
-            set_err(p.err, TTS_EFLAG_PAGE);
-            page = 0;
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        const int i = n * kThreads + tid, r = i / CV, u = i - r * CV;
+        float kf[E::kVec], vf[E::kVec];
+        E::values(kr[n], kf);
+        E::values(vr[n], vf);
+        if constexpr (E::kScaled) {
+#pragma unroll
+          for (int e = 0; e < E::kVec; ++e) {
+            kf[e] *= sk[n];
+            vf[e] *= sv[n];
           }
         }
-        s.row[tid] = cache_row(c, it.b, it.g, r0 + tid, page);
-      }
-      __syncthreads();
-      constexpr int CV = D / E::kVec;   // 16-byte vectors of a cache row
-      constexpr int N = kTile * CV;
-      static_assert(N % kThreads == 0, "whole vectors a thread");
+        if (r0 + r >= it.w.past && r0 + r < n_total) {
+          bool any = false;
 #pragma unroll
-      for (int i0 = 0; i0 < N; i0 += kThreads) {
-        const int i = i0 + tid, r = i / CV, u = i - r * CV;
-        float kf[E::kVec], vf[E::kVec];
-        if (r < nrow) {
-          const int64_t row = s.row[r];
-          E::values(__ldcg(reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(c.k) + row * (D * E::kBytes)) + u), kf);
-          E::values(__ldcg(reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(c.v) + row * (D * E::kBytes)) + u), vf);
-          if constexpr (E::kScaled) {
-            const float sk = __ldcg(c.k_scale + row), sv = __ldcg(c.v_scale + row);
-#pragma unroll
-            for (int e = 0; e < E::kVec; ++e) {
-              kf[e] *= sk;
-              vf[e] *= sv;
+          for (int e = 0; e < E::kVec; ++e)
+            if (!finite_f32(vf[e])) {
+              any = true;
+              vf[e] = 0.f;
             }
-          }
-          if (r0 + r >= it.w.past) {
-            bool any = false;
-#pragma unroll
-            for (int e = 0; e < E::kVec; ++e)
-              if (!finite_f32(vf[e])) {
-                any = true;
-                vf[e] = 0.f;
-              }
-            if (any) atomicOr(&s.bad_v, 1ull << (r0 + r - it.w.past));
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < E::kVec; ++e) kf[e] = vf[e] = 0.f;
+          if (any) atomicOr(&s.bad_v, 1ull << (r0 + r - it.w.past));
         }
 #pragma unroll
         for (int e = 0; e < E::kVec; e += 4) {
@@ -163,6 +172,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
         }
       }
       __syncthreads();
+      if (tile + 1 < it.t1) fetch(tile + 1);
       // scores of cache rows lane and lane + 32 for the warp's query rows
       float a[RW][2];
 #pragma unroll
@@ -275,10 +285,12 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
 }
 
 // Merges the pieces of an item's row in CTA order: M = max m, L = sum l 2^(m - M),
-// out = sum O 2^(m - M) / L.  One warp a row, the row's columns in its lanes.
+// out = sum O 2^(m - M) / L.  One warp a row, the row's columns in its lanes; 32 pieces at a
+// time, a lane each for their statistics, their rows eight loads in flight.
 template <int D>
 __global__ void __launch_bounds__(kThreads) tree_combine_kernel(const TreeParams p) {
   constexpr int PL = D / 32;   // columns a lane
+  using Vec = typename std::conditional<PL == 4, float4, float2>::type;
   grid_wait();
   grid_launch_dependents();
   const CacheView& c = p.cache;
@@ -287,54 +299,79 @@ __global__ void __launch_bounds__(kThreads) tree_combine_kernel(const TreeParams
   const int b = blockIdx.x / per_stream, k = blockIdx.x - b * per_stream;
   const int g = k / p.n_rb, rb = k - g * p.n_rb;
   Axis axis;
-  int64_t before;
-  int at_b = b;
+  int at_b = b, before;
   axis.find(p, 0, at_b, before);
   const TreeWindow w = axis.window(p, b);
   const int tiles = tree_tiles(p, w);
   if (tiles == 0) return;
-  const int64_t per = cost_per_cta(axis.total, p.n_cta), cost = item_cost(tiles);
-  const int64_t start = before + cost * k;
-  const int c0 = static_cast<int>(start / per), c1 = static_cast<int>((start + cost - 1) / per);
-  // the CTAs whose pieces hold tiles are consecutive: the first whose range ends past tile 0
+  const int per = cost_per_cta(axis.total, p.n_cta), cost = item_cost(tiles);
+  const int start = before + cost * k;
+  const int c0 = start / per, c1 = (start + cost - 1) / per;
+  // the CTAs whose pieces hold tiles are consecutive, first .. c1; the first whose range ends past
+  // tile 0.  (A range that starts in the item's fixed units has no tiles of its own before it.)
   int first = c0;
   while (first < c1 && tile_at(per * (first + 1) - start, tiles) == 0) ++first;
   if (tile_at(per * (first + 1) - start, tiles) >= tiles) return;   // finished by one CTA
   for (int r = blockIdx.y * kWarps + warp; r < p.rows; r += gridDim.y * kWarps) {
     const int t = (rb * p.rows + r) >> (p.group >> 1), h = (rb * p.rows + r) & (p.group - 1);
     if (t >= w.nodes) break;
-    float M = -INFINITY;
-    for (int x = first + lane; x <= c1; x += 32) {
-      const int t0 = tile_at(per * x - start, tiles), t1 = tile_at(per * (x + 1) - start, tiles);
-      if (t0 < t1) M = fmaxf(M, __ldcg(p.ml + (static_cast<int64_t>(x) * 2 + (t0 > 0 ? 0 : 1)) * p.rows + r).x);
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    const float m_use = M == -INFINITY ? 0.f : M;
-    float L = 0.f, acc[PL];
+    float M = -INFINITY, L = 0.f, acc[PL];
 #pragma unroll
     for (int e = 0; e < PL; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int x = first; x <= c1; ++x) {
+    for (int x0 = first; x0 <= c1; x0 += 32) {
+      const int x = x0 + lane;
       const int t0 = tile_at(per * x - start, tiles), t1 = tile_at(per * (x + 1) - start, tiles);
-      if (t0 >= t1) continue;
-      const int64_t at = (static_cast<int64_t>(x) * 2 + (t0 > 0 ? 0 : 1)) * p.rows + r;
-      const float2 ml = __ldcg(p.ml + at);
-      const float* src = p.part + at * D + lane * PL;
-      float f[PL];
-      if constexpr (PL == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-        f[0] = v.x; f[1] = v.y;
-      }
-      // a piece that saw nothing (all masked) has maximum -inf and weight 0; a NaN maximum
-      // cannot be (fmaxf drops NaN), NaN sums and rows pass through
-      const float e = ml.x == -INFINITY ? (ml.y != ml.y ? 1.f : 0.f) : ex2(ml.x - m_use);
-      L = fmaf(ml.y, e, L);
+      // row of the lane's piece in the partials (any row, and no weight, where it has no tiles)
+      const bool has = x <= c1 && t0 < t1;
+      const int at = ((has ? x : first) * 2 + (has && t0 > 0 ? 0 : 1)) * p.rows + r;
+      const float2 ml = has ? __ldcg(p.ml + at) : make_float2(-INFINITY, 0.f);
+      const int n = min(32, c1 + 1 - x0);
+      // the first rows travel with the statistics
+      constexpr int BATCH = 8;
+      Vec v[BATCH];
+      auto fetch = [&](int j0) {
 #pragma unroll
-      for (int i = 0; i < PL; ++i) acc[i] = fmaf(f[i], e, acc[i]);
+        for (int j = 0; j < BATCH; ++j) {
+          const int src = __shfl_sync(kFull, at, (j0 + j) & 31);
+          const bool live = __shfl_sync(kFull, static_cast<int>(has), (j0 + j) & 31) != 0 && j0 + j < n;
+          v[j] = Vec{};
+          if (live) v[j] = __ldcg(reinterpret_cast<const Vec*>(p.part + static_cast<int64_t>(src) * D) + lane);
+        }
+      };
+      fetch(0);
+      float top = ml.x;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      const float M1 = fmaxf(M, top), use = M1 == -INFINITY ? 0.f : M1;
+      if (M1 > M && M > -INFINITY) {
+        const float a = ex2(M - M1);
+        L *= a;
+#pragma unroll
+        for (int e = 0; e < PL; ++e) acc[e] *= a;
+      }
+      M = M1;
+      // a piece that saw nothing (all masked) has maximum -inf and weight 0; one that only saw NaN
+      // scores (which no maximum holds) passes its NaN on
+      const float wt = ml.x == -INFINITY ? (ml.y != ml.y ? 1.f : 0.f) : ex2(ml.x - use);
+      float sum = ml.y * wt;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      L += sum;
+      for (int j0 = 0; j0 < n; j0 += BATCH) {
+        if (j0 > 0) fetch(j0);
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+          const float e = __shfl_sync(kFull, wt, (j0 + j) & 31);
+          if (j0 + j < n) {
+            acc[0] = fmaf(v[j].x, e, acc[0]);
+            acc[1] = fmaf(v[j].y, e, acc[1]);
+            if constexpr (PL == 4) {
+              acc[2] = fmaf(v[j].z, e, acc[2]);
+              acc[3] = fmaf(v[j].w, e, acc[3]);
+            }
+          }
+        }
+      }
     }
     const bool sees = w.past > 0 || seen_nodes(p, b, t, w.nodes) != 0;
     const float inv = L == 0.f ? (sees ? __uint_as_float(0x7fc00000u) : 0.f) : 1.f / L;
@@ -365,6 +402,7 @@ cudaError_t launch_t(const TreeParams& p, cudaStream_t s) {
 template <int D, typename KvT>
 cudaError_t launch_r(const TreeParams& p, cudaStream_t s) {
   if (p.rows == 8) return launch_t<D, KvT, 8>(p, s);
+  if (p.rows == 16) return launch_t<D, KvT, 16>(p, s);
   if (p.rows == 32) return launch_t<D, KvT, 32>(p, s);
   return cudaErrorInvalidValue;
 }

@@ -35,29 +35,29 @@ __device__ __forceinline__ TreeWindow tree_window(const TreeParams& p, int b, bo
 __device__ __forceinline__ int tree_tiles(const TreeParams& p, TreeWindow w) {
   return w.nodes == 0 ? 0 : (w.past + w.nodes + p.tile - 1) / p.tile;
 }
-__device__ __forceinline__ int64_t item_cost(int tiles) { return kFixedCost + static_cast<int64_t>(tiles) * kTileCost; }
-__device__ __forceinline__ int64_t stream_cost(const TreeParams& p, int b) {
+// (units fit 32 bits: the entry point refuses more)
+__device__ __forceinline__ int item_cost(int tiles) { return kFixedCost + tiles * kTileCost; }
+__device__ __forceinline__ int stream_cost(const TreeParams& p, int b) {
   return item_cost(tree_tiles(p, tree_window(p, b, nullptr))) * (p.cache.n_kv_heads * p.n_rb);
 }
 
 // First tile at or after unit x of an item.
-__device__ __forceinline__ int tile_at(int64_t x, int tiles) {
-  if (x <= kFixedCost) return 0;
-  const int64_t t = (x - kFixedCost + kTileCost - 1) / kTileCost;
-  return t < tiles ? static_cast<int>(t) : tiles;
+__device__ __forceinline__ int tile_at(int x, int tiles) {
+  return min(max(x - kFixedCost + kTileCost - 1, 0) / kTileCost, tiles);
 }
 
 // Sum of the costs of streams [b0, b1), by a whole warp.
-__device__ __forceinline__ int64_t cost_of(const TreeParams& p, int b0, int b1) {
+__device__ __forceinline__ int cost_of(const TreeParams& p, int b0, int b1) {
   const int lane = threadIdx.x & 31;
-  int64_t sum = 0;
+  int sum = 0;
   for (int b = b0 + lane; b < b1; b += 32) sum += stream_cost(p, b);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
   return sum;
 }
 
-__device__ __forceinline__ int64_t cost_per_cta(int64_t total, int n_cta) { return (total + n_cta - 1) / n_cta; }
+// (a CTA's range may end past the axis: the ranges' ends stay below 2^32)
+__device__ __forceinline__ int cost_per_cta(int total, int n_cta) { return (total + n_cta - 1) / n_cta; }
 
 struct Piece {
   int b, g, rb;      // the item
@@ -72,7 +72,7 @@ struct Piece {
 // streams take one round trip to memory (this stands before everything else a launch does).
 struct Axis {
   int lane_past, lane_nodes;   // up to 32 streams: lane b's window
-  int64_t total;
+  int total;
 
   __device__ __forceinline__ TreeWindow window(const TreeParams& p, int b) const {
     if (p.cache.B > 32) return tree_window(p, b, nullptr);
@@ -80,21 +80,21 @@ struct Axis {
   }
   // Sums the axis; `start`: of stream b (b >= 0), or with b < 0 b becomes the stream that holds
   // unit lo(per_cta) * cta (B when none does).
-  __device__ void find(const TreeParams& p, int cta, int& b, int64_t& start) {
+  __device__ void find(const TreeParams& p, int cta, int& b, int& start) {
     const int lane = threadIdx.x & 31, B = p.cache.B;
     lane_past = lane_nodes = 0;
     if (B <= 32) {
-      int64_t own = 0;
+      int own = 0;
       if (lane < B) {
         const TreeWindow w = tree_window(p, lane, nullptr);
         lane_past = w.past;
         lane_nodes = w.nodes;
         own = item_cost(tree_tiles(p, w)) * (p.cache.n_kv_heads * p.n_rb);
       }
-      int64_t end = own;
+      int end = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(kFull, end, o);
+        const int x = __shfl_up_sync(kFull, end, o);
         if (lane >= o) end += x;
       }
       total = __shfl_sync(kFull, end, 31);
@@ -110,15 +110,15 @@ struct Axis {
       start = cost_of(p, 0, b);
       return;
     }
-    const int64_t lo = cost_per_cta(total, p.n_cta) * cta;
+    const int lo = cost_per_cta(total, p.n_cta) * cta;
     start = 0;
     b = B;
     for (int b0 = 0; b0 < B; b0 += 32) {
-      const int64_t own = b0 + lane < B ? stream_cost(p, b0 + lane) : 0;
-      int64_t end = own;
+      const int own = b0 + lane < B ? stream_cost(p, b0 + lane) : 0;
+      int end = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(kFull, end, o);
+        const int x = __shfl_up_sync(kFull, end, o);
         if (lane >= o) end += x;
       }
       const unsigned over = __ballot_sync(kFull, start + end > lo);
@@ -136,8 +136,8 @@ struct Axis {
 // The pieces of one CTA, in order.  Every call is by a whole warp.
 struct PieceWalk {
   Axis axis;
-  int64_t lo, hi;    // the CTA's units
-  int64_t start;     // where item `next` starts
+  int lo, hi;        // the CTA's units
+  int start;         // where item `next` starts
   int b, next;       // stream, and item of the stream (g * n_rb + rb), of the next item
   TreeWindow w;
   int tiles;
@@ -161,14 +161,14 @@ struct PieceWalk {
     }
     b = -1;
     axis.find(p, cta, b, start);
-    const int64_t per = cost_per_cta(axis.total, p.n_cta);
+    const int per = cost_per_cta(axis.total, p.n_cta);
     lo = per * cta;
     hi = lo + per;
     next = 0;
     set_stream(p);
     if (b < p.cache.B) {
-      const int64_t c = item_cost(tiles);
-      next = static_cast<int>((lo - start) / c);
+      const int c = item_cost(tiles);
+      next = (lo - start) / c;
       start += c * next;
     }
   }

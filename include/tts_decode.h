@@ -559,7 +559,8 @@ tts_status tts_kv_read_rows(const tts_kv_cache* cache, const tts_kv_desc* desc, 
  *   n_past, n_nodes: device int32 [B].  n_nodes outside [0, T], n_past below 0, or more than
  *        `capacity` rows in all are clamped (the nodes first) and set TTS_EFLAG_NVALID; a page id
  *        outside [0, n_pages) inside the window reads page 0 and sets TTS_EFLAG_PAGE.
- *   tree_mask: device uint64 [B][T], T <= TTS_MAX_TREE_NODES.
+ *   tree_mask: device uint64 [B][T], T <= TTS_MAX_TREE_NODES.  B * n_kv_heads * (capacity + 192)
+ *        must be below 2^32.
  *   workspace: at least tts_tree_attn_workspace_size() bytes (computed for the device that runs
  *        the call), 256-byte aligned; needs no clearing, and holds nothing between calls.  Calls
  *        that overlap in time on the GPU must not share one.
