@@ -89,8 +89,12 @@ class TtsRopeScaling(ctypes.Structure):
 
 
 class TtsKvCache(ctypes.Structure):
+    """Built by kv_cache, which also notes what the tensors behind it are."""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+    def get_device(self):
+        return self.device_index
 
 
 _P, _I32, _I64, _F, _D, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
@@ -446,19 +450,26 @@ def _rows(t, what, width=None):
 
 def _ints(t, what, n, dtype=torch.int32):
     if t is None:
-        return
+        return   # optional arguments only; the library refuses a missing required one
     if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} entries")
 
 
-def _one_device(first, *others):
-    """Every tensor on first's device, and that device the current one (launches go there)."""
-    d = first.device
+def _p(t):
+    """A tensor's address as a plain int (ctypes converts it), None for None."""
+    return None if t is None else t.data_ptr()
+
+
+def _on_device(stream, first, *others):
+    """Every tensor on first's device, and that device the current one (launches go there);
+    returns the stream's handle (default: the current one)."""
+    d = first.get_device()
     for t in others:
-        if t is not None and t.device != d:
-            raise ValueError(f"tensors on {d} and {t.device}: all arguments must be on one device")
-    if d.type != "cuda" or d.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {d}, which is not the current CUDA device")
+        if t is not None and t.get_device() != d:
+            raise ValueError("all tensors must be on one device")
+    if d < 0 or d != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {first.device}, which is not the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
 
 
 def kv_cache(k, v, k_scale=None, v_scale=None) -> TtsKvCache:
@@ -479,7 +490,7 @@ def kv_cache(k, v, k_scale=None, v_scale=None) -> TtsKvCache:
             raise ValueError("K, V and their scales must be on one device")
     c = TtsKvCache(k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
                    None if v_scale is None else v_scale.data_ptr())
-    c.dtype, c.shape, c.device = k.dtype, tuple(k.shape), k.device
+    c.dtype, c.shape, c.device_index = k.dtype, tuple(k.shape), k.get_device()
     return c
 
 
@@ -500,11 +511,11 @@ def tts_rope_table_scaled(cs, max_pos, rot_dim, base, kind="none", factor=1.0, o
         raise ValueError(f"kind must be one of {sorted(_ROPE_KINDS)}")
     if cs.dtype != torch.float32 or not cs.is_contiguous() or cs.numel() < max_pos * rot_dim:
         raise ValueError("cs must be contiguous float32 of max_pos * rot_dim entries")
-    _one_device(cs)
+    st = _on_device(stream, cs)
     s = TtsRopeScaling(_ROPE_KINDS[kind], original_max_pos, float(factor), float(low_rotations),
                        float(high_rotations), float(attn_scale))
-    _check(_lib.tts_rope_table_scaled(_ptr(cs), max_pos, rot_dim, float(base), ctypes.byref(s),
-                                      _stream(stream)), "tts_rope_table_scaled")
+    _check(_lib.tts_rope_table_scaled(_p(cs), max_pos, rot_dim, float(base), ctypes.byref(s), st),
+           "tts_rope_table_scaled")
 
 
 def tts_rope_rows(q, k, q_out, k_out, pos, n_q_heads, n_kv_heads, head_dim, cs, gamma_q=None,
@@ -532,11 +543,11 @@ def tts_rope_rows(q, k, q_out, k_out, pos, n_q_heads, n_kv_heads, head_dim, cs, 
             _ints(gm, "gamma", head_dim, torch.float32)
     if cs.dim() != 3 or cs.dtype != torch.float32 or not cs.is_contiguous() or cs.shape[2] != 2:
         raise ValueError("cs must be a contiguous float32 [max_pos, rot_dim / 2, 2] table")
-    _one_device(q, k, q_out, k_out, pos, cs, gamma_q, gamma_k, err_flag)
-    _check(_lib.tts_rope_rows(_ptr(q), qs, _ptr(k), ks, dt, _ptr(q_out), qos, _ptr(k_out), kos, odt,
-                              _ptr(gamma_q), _ptr(gamma_k), float(eps), _ptr(pos), n, n_q_heads,
-                              n_kv_heads, head_dim, 2 * cs.shape[1], int(bool(interleaved)), _ptr(cs),
-                              cs.shape[0], _ptr(err_flag), _stream(stream)), "tts_rope_rows")
+    st = _on_device(stream, q, k, q_out, k_out, pos, cs, gamma_q, gamma_k, err_flag)
+    _check(_lib.tts_rope_rows(_p(q), qs, _p(k), ks, dt, _p(q_out), qos, _p(k_out), kos, odt,
+                              _p(gamma_q), _p(gamma_k), float(eps), _p(pos), n, n_q_heads,
+                              n_kv_heads, head_dim, 2 * cs.shape[1], int(bool(interleaved)), _p(cs),
+                              cs.shape[0], _p(err_flag), st), "tts_rope_rows")
 
 
 def tts_kv_write_rows(k, v, cache: TtsKvCache, desc: TtsKvDesc, start_pos, T, n_rows=None,
@@ -551,10 +562,9 @@ def tts_kv_write_rows(k, v, cache: TtsKvCache, desc: TtsKvDesc, start_pos, T, n_
     _cache_fits(cache, desc)
     _ints(start_pos, "start_pos", desc.B)
     _ints(n_rows, "n_rows", desc.B)
-    _one_device(k, v, cache, start_pos, n_rows, err_flag)
-    _check(_lib.tts_kv_write_rows(_ptr(k), _ptr(v), dt, ks, ctypes.byref(cache), ctypes.byref(desc),
-                                  _ptr(start_pos), _ptr(n_rows), T, _ptr(err_flag), _stream(stream)),
-           "tts_kv_write_rows")
+    st = _on_device(stream, k, v, cache, start_pos, n_rows, err_flag)
+    _check(_lib.tts_kv_write_rows(_p(k), _p(v), dt, ks, ctypes.byref(cache), ctypes.byref(desc),
+                                  _p(start_pos), _p(n_rows), T, _p(err_flag), st), "tts_kv_write_rows")
 
 
 def tts_kv_read_rows(cache: TtsKvCache, desc: TtsKvDesc, start_pos, T, k_out, v_out, n_rows=None,
@@ -569,10 +579,9 @@ def tts_kv_read_rows(cache: TtsKvCache, desc: TtsKvDesc, start_pos, T, k_out, v_
     _cache_fits(cache, desc)
     _ints(start_pos, "start_pos", desc.B)
     _ints(n_rows, "n_rows", desc.B)
-    _one_device(k_out, v_out, cache, start_pos, n_rows, err_flag)
-    _check(_lib.tts_kv_read_rows(ctypes.byref(cache), ctypes.byref(desc), _ptr(start_pos), _ptr(n_rows),
-                                 T, _ptr(k_out), _ptr(v_out), dt, ks, _ptr(err_flag), _stream(stream)),
-           "tts_kv_read_rows")
+    st = _on_device(stream, k_out, v_out, cache, start_pos, n_rows, err_flag)
+    _check(_lib.tts_kv_read_rows(ctypes.byref(cache), ctypes.byref(desc), _p(start_pos), _p(n_rows), T,
+                                 _p(k_out), _p(v_out), dt, ks, _p(err_flag), st), "tts_kv_read_rows")
 
 
 def _row_code(q_dtype):
@@ -606,11 +615,11 @@ def tts_tree_attn(q, cache: TtsKvCache, desc: TtsKvDesc, n_past, T, scale, out, 
     _ints(n_past, "n_past", desc.B)
     _ints(n_nodes, "n_nodes", desc.B)
     _ints(tree_mask, "tree_mask", desc.B * T, torch.int64)
-    _one_device(q, cache, n_past, n_nodes, tree_mask, out, ws, err_flag)
-    _check(_lib.tts_tree_attn(_ptr(q), dt, qs, ctypes.byref(cache), ctypes.byref(desc), _ptr(n_past),
-                              _ptr(n_nodes), _ptr(tree_mask), T, float(scale), _ptr(out), _ptr(ws),
-                              0 if ws is None else ws.numel() * ws.element_size(), _ptr(err_flag),
-                              _stream(stream)), "tts_tree_attn")
+    st = _on_device(stream, q, cache, n_past, n_nodes, tree_mask, out, ws, err_flag)
+    _check(_lib.tts_tree_attn(_p(q), dt, qs, ctypes.byref(cache), ctypes.byref(desc), _p(n_past),
+                              _p(n_nodes), _p(tree_mask), T, float(scale), _p(out), _p(ws),
+                              0 if ws is None else ws.numel() * ws.element_size(), _p(err_flag), st),
+           "tts_tree_attn")
 
 
 def tts_tree_commit(cache: TtsKvCache, desc: TtsKvDesc, n_past, path, n_accept, T, err_flag=None,
@@ -622,10 +631,10 @@ def tts_tree_commit(cache: TtsKvCache, desc: TtsKvDesc, n_past, path, n_accept, 
     _cache_fits(cache, desc)
     _ints(n_past, "n_past", desc.B)
     _ints(n_accept, "n_accept", desc.B)
-    _one_device(path, cache, n_past, n_accept, err_flag)
-    _check(_lib.tts_tree_commit(ctypes.byref(cache), ctypes.byref(desc), _ptr(n_past), _ptr(path),
-                                path.stride(0) if desc.B > 1 else T, _ptr(n_accept), T, _ptr(err_flag),
-                                _stream(stream)), "tts_tree_commit")
+    st = _on_device(stream, path, cache, n_past, n_accept, err_flag)
+    _check(_lib.tts_tree_commit(ctypes.byref(cache), ctypes.byref(desc), _p(n_past), _p(path),
+                                path.stride(0) if desc.B > 1 else T, _p(n_accept), T, _p(err_flag), st),
+           "tts_tree_commit")
 
 
 def default_scale(head_dim: int) -> float:
