@@ -76,7 +76,7 @@ TreePlan tree_plan(const tts_kv_desc* d, int T, int q_dtype) {
 bool tree_shape_ok(const tts_kv_desc* d, int32_t T) {
   // (the work's units, at most 8 (12 + capacity / 16) a stream and kv head, are counted in 32 bits)
   return T >= 1 && T <= TTS_MAX_TREE_NODES && d->B <= 65535 && d->n_kv_heads <= 65535 &&
-         static_cast<int64_t>(d->B) * d->n_kv_heads * (static_cast<int64_t>(d->capacity) + 192) < (int64_t{1} << 32);
+         static_cast<int64_t>(d->B) * d->n_kv_heads * (static_cast<int64_t>(d->capacity) + 192) < (int64_t{1} << 31);
 }
 
 }  // namespace

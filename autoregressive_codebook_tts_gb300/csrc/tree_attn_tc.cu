@@ -9,21 +9,29 @@
 // and odd tiles, each with its own scores, statistics and output in tensor memory; so a row
 // ends as 2 F partial rows, which meet once per item in shared memory.
 //
-//   S = Q K^T          Q and K exact in bf16 (8-bit codes are; their scale multiplies S)
-//   P = 2^(S c - m)    f32, rounded to bf16 times V's row scale, and written over S in tensor
-//                      memory as the A operand of the second product
+//   S = Q K^T          exact products, f32 sums.  bf16 caches: bf16 operands.  8-bit caches: f16,
+//                      which holds every code, and a bf16 row of q once it is scaled by a power
+//                      of two; the K row's scale multiplies S.
+//   P = 2^(S c - m)    f32, rounded to bf16 (8-bit caches: times V's row scale, to f16) and
+//                      written over S in tensor memory as the A operand of the second product
 //   O += P V           V as the MN-major operand.  The maximum in use moves only when a row's
 //                      grows by more than 2^8; then O is rescaled in tensor memory.
 //
-// Two loader warps (K, V) stream the cache with the TMA engine: a bf16 tile as tensor-map boxes (the
-// whole tile, or one box per page and 64 columns) that land in the 128-byte swizzled layout of
-// the MMA; an 8-bit tile as plain bulk copies into a staging tile, which four warps widen to
-// bf16 (integer and bf16 arithmetic, exact) into the operand tile.  In tiles with node rows, V
-// rows past the window are zeroed before their product (whatever a page holds there).
+// Two loader warps (K, V) stream the cache with the TMA engine: a bf16 tile as tensor-map boxes
+// (the whole tile, or one box per page and 64 columns) that land in the 128-byte swizzled layout
+// of the MMA; an 8-bit tile as plain bulk copies into a staging tile, which four warps widen to
+// f16 in the operand layout (f16 and not bf16: 1.4 against 2.5 operations an entry).  In tiles
+// with node rows, V rows past the window are zeroed before their product (whatever a page holds
+// there).  One warp issues both products of either group, whichever has its operands first.
 //
-// Bound: HBM (a bf16 tile of 64 KB takes an SM 1.5 us of its share, its products 0.54 us on the
-// tensor cores); over 8-bit caches the widening, 4 (int8) to 5 (e4m3) operations a pair of
-// entries, is of the order of the tile's 0.75 us.
+// Measured (cycles of one CTA's steady state, 128-row tiles, head_dim 128): a bf16 tile every 2120
+// (64 KB: 58 GB/s an SM, the HBM's share being 44) with few query rows; an int8 tile every 2650,
+// set by the chain widening (650) - scores (650) - weights (1000) - output (600) of each group;
+// with 128 rows the weights of a tile (4450: 128 a thread) set 3650.  An item's end costs 3000 to
+// 12000 more (query rows, partial rows, their merge), which the cut counts as two tiles.  All
+// roles' loops share the instruction cache: rolled, they are 2 to 4 times faster than unrolled.
+// 32 streams of 1500..4000 rows, one node: bf16 66 us (5.4 TB/s, 0.80 of the measured copy rate),
+// int8 70 us, e4m3 78 us; 63 nodes: bf16 99 us, int8 140 us, e4m3 144 us.
 //
 // The window is cut over one CTA per SM by cost (tree_plan.cuh).  Non-finite V entries of node
 // rows are handled as in tree_attn.cu.  Every wait is bounded; on expiry TTS_EFLAG_TIMEOUT is
@@ -805,7 +813,8 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
         const float* ksc = s_scale + (slot * 256 + f * W);
         const float* vsc = ksc + 128;
         const int off = base - it.w.past, node_row = off - f * W + r;   // (of row r of the tile)
-        const float cr = k8 ? c * s_qs[rr] : c;
+        // (kept off 0: scores of -inf times it)
+        const float cr = k8 ? fmaxf(c * s_qs[rr], 1e-37f) : c;
         float unit = 1.0f;   // what O's unit changes by
         if constexpr (k8) {
           // V's scales times g = 2^(127 - ve): a tile's largest stays between 2^-8 and 2^6, so that

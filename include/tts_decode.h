@@ -560,13 +560,14 @@ tts_status tts_kv_read_rows(const tts_kv_cache* cache, const tts_kv_desc* desc, 
  *        `capacity` rows in all are clamped (the nodes first) and set TTS_EFLAG_NVALID; a page id
  *        outside [0, n_pages) inside the window reads page 0 and sets TTS_EFLAG_PAGE.
  *   tree_mask: device uint64 [B][T], T <= TTS_MAX_TREE_NODES.  B * n_kv_heads * (capacity + 192)
- *        must be below 2^32.
+ *        must be below 2^31.
  *   workspace: at least tts_tree_attn_workspace_size() bytes (computed for the device that runs
  *        the call), 256-byte aligned; needs no clearing, and holds nothing between calls.  Calls
  *        that overlap in time on the GPU must not share one.
- * Statistics and sums in f32; with f32 q every product too.  With bf16 q over a bf16 or 8-bit
- * cache the products run on the tensor cores, exact in q and K, with the softmax weights rounded
- * to bf16 (nearest even) where they meet V.  Results do not depend on timing.
+ * Statistics and sums in f32; with f32 q or an f32 cache every product too.  With bf16 q over a
+ * bf16 or 8-bit cache (bf16 pages of fewer than 8 rows excepted) the products run on the tensor
+ * cores, exact in q and K, with the softmax weights rounded where they meet V: to bf16 over a
+ * bf16 cache, to f16 times the row's scale over an 8-bit one.  Results do not depend on timing.
  * ------------------------------------------------------------------------- */
 #define TTS_MAX_TREE_NODES 64
 size_t tts_tree_attn_workspace_size(const tts_kv_desc* desc, int32_t T, int32_t q_dtype);

@@ -521,6 +521,133 @@ def test_many_streams(tts, q_dt):
         assert (out[b, nodes[b]:] == 9).all()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "i8", "e4m3", "f32"])
+@pytest.mark.parametrize("q_dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [2, 20, 64])
+def test_maxima_that_keep_moving(tts, kv, q_dt, T):
+    """Scores that grow along the window, within tiles and across them: every rescaling path."""
+    hq, hkv, d, cap, past = 4, 2, 128, 900, 820
+    c = R.Cache(1, hkv, d, cap, kv, 0, seed=8)
+    ramp = torch.linspace(0.0, 6.0, cap)
+    rng = np.random.default_rng(2)
+    direction = torch.from_numpy(rng.standard_normal(d).astype(np.float32))
+    direction /= direction.norm()
+    rows = 0.2 * torch.from_numpy(rng.standard_normal((1, hkv, cap, d)).astype(np.float32)) + \
+        (ramp * 8)[None, None, :, None] * direction
+    c.k, c.ks = R.to_cache(rows.numpy(), kv)
+    c.to_device(tts, hq)
+    q = (direction + 0.05 * torch.from_numpy(rng.standard_normal((1, T, hq, d)).astype(np.float32))).to(R.TORCH[q_dt])
+    m = masks(1, T, 3)
+    out, _ = run_tree(tts, c, q.cuda(), [past], [T], m, T, 1.0)
+    ref, mag = R.tree_attn(c, q.double(), [past], [T], m, 1.0)
+    # scores of up to 50: their f32 sums (2^-24 of a sum of magnitudes of about 60, a few
+    # roundings) move a weight by up to 2e-5 of itself; a weight whose tile's maximum moved after
+    # it was written is rounded a second time
+    bound = 4e-5 * mag + 1e-5 * ref.abs().amax(-1, keepdim=True)
+    if q_dt == "bf16":
+        bound = bound + 2.0 ** -8 * ref.abs() + 2.0 ** -7 * mag
+    assert ((out.cpu().double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("kv", ["i8", "e4m3"])
+@pytest.mark.parametrize("q_dt", ["bf16", "f32"])
+def test_scales_and_queries_of_all_sizes(tts, kv, q_dt):
+    """Row scales from 2^-60 to 2^60 (also negative ones and zero rows), query rows from 2^-90 to
+    2^30 and of zeros: what the f16 operands' powers of two have to follow."""
+    T, hq, hkv, d, cap, past = 8, 4, 2, 128, 1200, 1100
+    rng = np.random.default_rng(4)
+    for case in range(4):
+        c = R.Cache(1, hkv, d, cap, kv, 0, seed=9 + case)
+        if case == 0:      # V scales that grow, fall and jump from tile to tile
+            e = np.repeat(rng.integers(-60, 60, (cap + 99) // 100), 100)[:cap]
+        elif case == 1:    # and from row to row
+            e = rng.integers(-20, 20, cap)
+        else:
+            e = np.full(cap, -100 if case == 2 else 100)
+        c.vs *= torch.from_numpy(np.exp2(e).astype(np.float32))
+        c.vs[:, :, ::7] *= -1
+        c.ks[:, :, ::5] *= -1
+        c.vs[:, :, 3::11] = 0
+        c.ks[:, :, 4::13] = 0
+        c.to_device(tts, hq)
+        q = torch.from_numpy(rng.standard_normal((1, T, hq, d)).astype(np.float32))
+        q *= torch.from_numpy(np.exp2(np.array([0, -90, 0, -3, 2, 0, -20, 1])).astype(np.float32))[None, :, None, None]
+        q[0, 2] = 0
+        q = q.to(R.TORCH[q_dt])
+        for scale in (0.09, 0.0):
+            out, _ = run_tree(tts, c, q.cuda(), [past], [T], None, T, scale)
+            check_tree(out, *R.tree_attn(c, q.double(), [past], [T], None, scale), [T])
+    # one row of q so large that the scores need its power of two: all weight on the best row
+    q = torch.from_numpy(rng.standard_normal((1, T, hq, d)).astype(np.float32) * 2.0 ** 30).to(R.TORCH[q_dt])
+    out, _ = run_tree(tts, c, q.cuda(), [past], [T], None, T, 2.0 ** -30 * 0.09)
+    check_tree(out, *R.tree_attn(c, q.double(), [past], [T], None, 2.0 ** -30 * 0.09), [T])
+
+
+@pytest.mark.parametrize("q_dt", ["bf16", "f32"])
+def test_codes_that_are_not_numbers(tts, q_dt):
+    # e4m3 NaN codes (which writing never makes) in rows that only some nodes see
+    T, hq, hkv, d, cap, past = 6, 2, 1, 128, 400, 300
+    c = R.Cache(1, hkv, d, cap, "e4m3", 0, seed=3)
+    c.v.view(torch.uint8)[0, 0, past + 2, 9] = 0x7F
+    c.k.view(torch.uint8)[0, 0, past + 4, 0] = 0xFF
+    c.to_device(tts, hq)
+    m = np.array([[1, 3, 7, 1 | 8, 1 | 16, 1 | 32]], np.int64)
+    q = torch.randn(1, T, hq, d, generator=torch.Generator().manual_seed(1)).to(R.TORCH[q_dt])
+    out, _ = run_tree(tts, c, q.cuda(), [past], [T], m, T, 0.1)
+    ref, mag = R.tree_attn(c, q.double(), [past], [T], m, 0.1)
+    o = out.cpu()
+    assert o[0, 2, :, 9].isnan().all() and o[0, 4].isnan().all()
+    keep = [i for i in range(d) if i != 9]
+    check_tree(out[:, :4][..., keep], ref[:, :4][..., keep], mag[:, :4][..., keep], [4])
+    check_tree(out[:, [0, 1, 3, 5]], ref[:, [0, 1, 3, 5]], mag[:, [0, 1, 3, 5]], [4])
+
+
+@pytest.mark.parametrize("kv,q_dt", [("i8", "bf16"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_row_blocks_beyond_the_nodes(tts, kv, q_dt):
+    # 64 nodes of 4 q heads are several row blocks; a stream with few nodes leaves some empty
+    B, T, hq, hkv, d, cap = 3, 64, 4, 1, 64, 1500
+    past, nodes = [1300, 40, 700], [64, 5, 33]
+    c = R.Cache(B, hkv, d, cap, kv, 0, seed=2, fill=[p + n for p, n in zip(past, nodes)]).to_device(tts, hq)
+    q = torch.randn(B, T, hq, d, generator=torch.Generator().manual_seed(5)).to(R.TORCH[q_dt])
+    out, ef = run_tree(tts, c, q.cuda(), past, nodes, None, T, 0.125)
+    assert ef == 0
+    check_tree(out, *R.tree_attn(c, q.double(), past, nodes, None, 0.125), nodes)
+    for b in range(B):
+        assert (out[b, nodes[b]:] == 9).all()
+
+
+def test_two_graphs_that_share_a_workspace_take_turns(tts):
+    # each graph is captured over one workspace; replayed one after the other on one stream, each
+    # gives its own result
+    B, T, hq, hkv, d, cap = 2, 4, 4, 2, 128, 3000
+    g = torch.Generator().manual_seed(6)
+    caches = [R.Cache(B, hkv, d, cap, "i8", 0, seed=s, fill=[2500, 2900]).to_device(tts, hq) for s in (1, 2)]
+    qs = [torch.randn(B * T, hq * d, generator=g).bfloat16().cuda() for _ in range(2)]
+    past = ints([2496, 2896])
+    ws = tts.tree_workspace(caches[0].desc, T, torch.bfloat16)
+    outs = [torch.empty(B, T, hq, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    eager = []
+    for c, q, o in zip(caches, qs, outs):
+        tts.tts_tree_attn(q, c.cache, c.desc, past, T, 0.1, o, ws)
+        eager.append(o.clone())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(s):
+        for c, q, o in zip(caches, qs, outs):
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr, stream=s):
+                tts.tts_tree_attn(q, c.cache, c.desc, past, T, 0.1, o, ws)
+            graphs.append(gr)
+        for o in outs:
+            o.zero_()
+        for _ in range(20):
+            graphs[0].replay()
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], eager[0]) and torch.equal(outs[1], eager[1])
+
+
 # ---------------------------------------------------------------------------
 # Commit
 # ---------------------------------------------------------------------------
