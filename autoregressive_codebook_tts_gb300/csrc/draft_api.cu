@@ -51,7 +51,7 @@ tts_status check_rows(const tts_kv_desc* d, int32_t dtype, int64_t stride, int32
 // The launch of a tree attention: row blocks, tiles and CTAs from shapes alone.
 struct TreePlan {
   bool tc;              // tensor cores
-  int rows, n_rb, tile, n_cta, whole;
+  int rows, n_rb, tile, n_cta, whole, fixed;
   size_t part, total;   // bytes of the partial rows, and of the whole workspace
 };
 TreePlan tree_plan(const tts_kv_desc* d, int T, int q_dtype) {
@@ -63,7 +63,13 @@ TreePlan tree_plan(const tts_kv_desc* d, int T, int q_dtype) {
   t.n_rb = (rows + t.rows - 1) / t.rows;
   t.tile = t.tc ? 128 : 64;
   const int64_t items = static_cast<int64_t>(d->B) * d->n_kv_heads * t.n_rb;
+  // Up to four tiles an item: cutting it further saves less than the combine launch costs (a
+  // window of 260 rows whole, in 64-row tiles: 27 us; cut: 14.5; of 256 or less either way the same).
   t.whole = d->capacity <= 4 * t.tile;
+  // An item's query rows, epilogue and partials in units of a quarter tile: two tiles' time, four
+  // with 128 query rows on the tensor cores.  (32 streams, 63 nodes, e4m3: 8 144 us, 20 136 us;
+  // one node, int8: 8 39.3 us, 14 40.2 us, 20 41.5 us; f32, 16 nodes: 8 126 us, 14 136 us.)
+  t.fixed = t.tc && t.rows == 128 ? 18 : 8;
   t.n_cta = t.whole ? static_cast<int>(items) : (t.tc ? 1 : 2) * sm_count();
   if (!t.whole) {
     const size_t slots = static_cast<size_t>(t.n_cta) * 2 * t.rows;
@@ -74,7 +80,8 @@ TreePlan tree_plan(const tts_kv_desc* d, int T, int q_dtype) {
 }
 
 bool tree_shape_ok(const tts_kv_desc* d, int32_t T) {
-  // (the work's units, at most 8 (12 + capacity / 16) a stream and kv head, are counted in 32 bits)
+  // (the work's units, at most 8 (12 + capacity / 16) or 2 (22 + capacity / 32) a stream and kv
+  // head, are counted in 32 bits)
   return T >= 1 && T <= TTS_MAX_TREE_NODES && d->B <= 65535 && d->n_kv_heads <= 65535 &&
          static_cast<int64_t>(d->B) * d->n_kv_heads * (static_cast<int64_t>(d->capacity) + 192) < (int64_t{1} << 31);
 }
@@ -243,6 +250,7 @@ tts_status tts_tree_attn(const void* q, int32_t q_dtype, int64_t q_stride, const
   p.rows = t.rows;
   p.tile = t.tile;
   p.n_cta = t.n_cta;
+  p.fixed = t.fixed;
   p.whole = t.whole;
   p.err = err_flag;
   const cudaError_t e = t.tc ? launch_tree_attn_tc(p, d->kv_dtype, d->head_dim, as_stream(stream))

@@ -79,6 +79,7 @@ struct TreeParams {
   int n_rb, rows;              // row blocks of a (stream, kv head), rows of a block
   int tile;                    // cache rows of a tile
   int n_cta;                   // CTAs the work is cut over
+  int fixed;                   // an item's cost beside its tiles (a tile costs 4)
   int whole;                   // 1: one CTA takes whole items only (no partials)
   float* part;                 // partial rows [n_cta][2][rows][D]
   float2* ml;                  // their (maximum, sum) [n_cta][2][rows]

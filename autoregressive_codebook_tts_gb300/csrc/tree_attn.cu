@@ -304,14 +304,14 @@ __global__ void __launch_bounds__(kThreads) tree_combine_kernel(const TreeParams
   const TreeWindow w = axis.window(p, b);
   const int tiles = tree_tiles(p, w);
   if (tiles == 0) return;
-  const int per = cost_per_cta(axis.total, p.n_cta), cost = item_cost(tiles);
+  const int per = cost_per_cta(axis.total, p.n_cta), cost = item_cost(p, tiles);
   const int start = before + cost * k;
   const int c0 = start / per, c1 = (start + cost - 1) / per;
   // the CTAs whose pieces hold tiles are consecutive, first .. c1; the first whose range ends past
   // tile 0.  (A range that starts in the item's fixed units has no tiles of its own before it.)
   int first = c0;
-  while (first < c1 && tile_at(per * (first + 1) - start, tiles) == 0) ++first;
-  if (tile_at(per * (first + 1) - start, tiles) >= tiles) return;   // finished by one CTA
+  while (first < c1 && tile_at(p, per * (first + 1) - start, tiles) == 0) ++first;
+  if (tile_at(p, per * (first + 1) - start, tiles) >= tiles) return;   // finished by one CTA
   for (int r = blockIdx.y * kWarps + warp; r < p.rows; r += gridDim.y * kWarps) {
     const int t = (rb * p.rows + r) >> (p.group >> 1), h = (rb * p.rows + r) & (p.group - 1);
     if (t >= w.nodes) break;
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads) tree_combine_kernel(const TreeParams
     for (int e = 0; e < PL; ++e) acc[e] = 0.f;
     for (int x0 = first; x0 <= c1; x0 += 32) {
       const int x = x0 + lane;
-      const int t0 = tile_at(per * x - start, tiles), t1 = tile_at(per * (x + 1) - start, tiles);
+      const int t0 = tile_at(p, per * x - start, tiles), t1 = tile_at(p, per * (x + 1) - start, tiles);
       // row of the lane's piece in the partials (any row, and no weight, where it has no tiles)
       const bool has = x <= c1 && t0 < t1;
       const int at = ((has ? x : first) * 2 + (has && t0 > 0 ? 0 : 1)) * p.rows + r;

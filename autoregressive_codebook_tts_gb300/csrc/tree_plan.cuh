@@ -2,8 +2,8 @@
 // device data, so every warp that needs the cut derives it from them, the same way.
 //
 // Items (stream, kv head, row block), in this order, are laid end to end on a cost axis: an
-// item costs kFixedCost (its query rows, epilogue and partials) plus kTileCost per tile of
-// its window.  CTA r takes the units [r per, (r + 1) per); a piece of an item is the tiles
+// item costs p.fixed (its query rows, epilogue and partials) plus kTileCost per tile of its
+// window.  CTA r takes the units [r per, (r + 1) per); a piece of an item is the tiles
 // whose units fall into a CTA's range.  An item that one CTA takes whole is finished there;
 // the pieces of others leave partial rows, which the combine launch merges in CTA order.
 // A CTA has at most one piece that starts inside its item (its first: slot 0) and one that
@@ -16,7 +16,6 @@
 namespace tts {
 
 constexpr int kTileCost = 4;
-constexpr int kFixedCost = 8;   // about two tiles' time
 
 // A stream's committed rows and nodes, clamped into the cache; *bad when they had to be.
 struct TreeWindow {
@@ -36,14 +35,14 @@ __device__ __forceinline__ int tree_tiles(const TreeParams& p, TreeWindow w) {
   return w.nodes == 0 ? 0 : (w.past + w.nodes + p.tile - 1) / p.tile;
 }
 // (units fit 32 bits: the entry point refuses more)
-__device__ __forceinline__ int item_cost(int tiles) { return kFixedCost + tiles * kTileCost; }
+__device__ __forceinline__ int item_cost(const TreeParams& p, int tiles) { return p.fixed + tiles * kTileCost; }
 __device__ __forceinline__ int stream_cost(const TreeParams& p, int b) {
-  return item_cost(tree_tiles(p, tree_window(p, b, nullptr))) * (p.cache.n_kv_heads * p.n_rb);
+  return item_cost(p, tree_tiles(p, tree_window(p, b, nullptr))) * (p.cache.n_kv_heads * p.n_rb);
 }
 
 // First tile at or after unit x of an item.
-__device__ __forceinline__ int tile_at(int x, int tiles) {
-  return min(max(x - kFixedCost + kTileCost - 1, 0) / kTileCost, tiles);
+__device__ __forceinline__ int tile_at(const TreeParams& p, int x, int tiles) {
+  return min(max(x - p.fixed + kTileCost - 1, 0) / kTileCost, tiles);
 }
 
 // Sum of the costs of streams [b0, b1), by a whole warp.
@@ -89,7 +88,7 @@ struct Axis {
         const TreeWindow w = tree_window(p, lane, nullptr);
         lane_past = w.past;
         lane_nodes = w.nodes;
-        own = item_cost(tree_tiles(p, w)) * (p.cache.n_kv_heads * p.n_rb);
+        own = item_cost(p, tree_tiles(p, w)) * (p.cache.n_kv_heads * p.n_rb);
       }
       int end = own;
 #pragma unroll
@@ -167,7 +166,7 @@ struct PieceWalk {
     next = 0;
     set_stream(p);
     if (b < p.cache.B) {
-      const int c = item_cost(tiles);
+      const int c = item_cost(p, tiles);
       next = (lo - start) / c;
       start += c * next;
     }
@@ -186,9 +185,9 @@ struct PieceWalk {
         start = hi;
         return tiles > 0;
       }
-      out.t0 = tile_at(lo - start, tiles);
-      out.t1 = tile_at(hi - start, tiles);
-      start += item_cost(tiles);
+      out.t0 = tile_at(p, lo - start, tiles);
+      out.t1 = tile_at(p, hi - start, tiles);
+      start += item_cost(p, tiles);
       if (++next == p.cache.n_kv_heads * p.n_rb) {
         next = 0;
         ++b;
