@@ -63,9 +63,11 @@ TreePlan tree_plan(const tts_kv_desc* d, int T, int q_dtype) {
   t.n_rb = (rows + t.rows - 1) / t.rows;
   t.tile = t.tc ? 128 : 64;
   const int64_t items = static_cast<int64_t>(d->B) * d->n_kv_heads * t.n_rb;
-  // Up to four tiles an item: cutting it further saves less than the combine launch costs (a
-  // window of 260 rows whole, in 64-row tiles: 27 us; cut: 14.5; of 256 or less either way the same).
-  t.whole = d->capacity <= 4 * t.tile;
+  // Short windows are one CTA's each: the combine launch costs more than cutting them saves.  (Five
+  // nodes, one / eight streams, whole against cut.  Tensor cores, bf16: 250 rows 7.0 / 7.5 against
+  // 12.0 / 13.3 us, 500 rows 9.2 / 9.6 against 12.2 / 14.8, about 1.1 us a tile more.  CUDA cores,
+  // f32: 120 rows 12.9 / 13.0 against 12.4 / 15.6 us, 250 rows 22.8 / 23.0 against 14.5 / 23.3.)
+  t.whole = d->capacity <= (t.tc ? 6 : 2) * t.tile;
   // An item's query rows, epilogue and partials in units of a quarter tile: two tiles' time, four
   // with 128 query rows on the tensor cores.  (32 streams, 63 nodes, e4m3: 8 144 us, 20 136 us;
   // one node, int8: 8 39.3 us, 14 40.2 us, 20 41.5 us; f32, 16 nodes: 8 126 us, 14 136 us.)
