@@ -70,7 +70,8 @@ TreePlan tree_plan(const tts_kv_desc* d, int T, int q_dtype) {
   t.whole = d->capacity <= (t.tc ? 6 : 2) * t.tile;
   // An item's query rows, epilogue and partials in units of a quarter tile: two tiles' time, four
   // with 128 query rows on the tensor cores.  (32 streams, 63 nodes, e4m3: 8 144 us, 20 136 us;
-  // one node, int8: 8 39.3 us, 14 40.2 us, 20 41.5 us; f32, 16 nodes: 8 126 us, 14 136 us.)
+  // one node, int8: 8 39.3 us, 14 40.2 us, 20 41.5 us; f32, 16 nodes: 8 126 us, 14 136 us;
+  // int8, 16 nodes, is the exception: 8 80.9 us, 14 77.7 us.)
   t.fixed = t.tc && t.rows == 128 ? 18 : 8;
   t.n_cta = t.whole ? static_cast<int>(items) : (t.tc ? 1 : 2) * sm_count();
   if (!t.whole) {

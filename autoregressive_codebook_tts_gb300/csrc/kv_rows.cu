@@ -6,6 +6,11 @@
 // warp, so a row's largest magnitude is a few shuffles and nothing goes through shared memory.
 // K and V of a row go through the same lane (two loads in flight at least); many rows to read
 // are read two a lane.
+//
+// 16 x 1024 rows of 8 heads, bf16 into int8: 37 us (2.7 TB/s; 0.68 of the issue slots, the quantiser's);
+// 36.8 k rows back to bf16: 47 us (4.8 TB/s, 0.73 of the measured copy rate; waits on loads).  One row
+// of 32 streams: 2.4 and 1.8 us, a launch.  Both of the first took 208 us with
+// codes by double division and narrower lanes.
 #include "cache_view.cuh"
 #include "draft_kernels.h"
 

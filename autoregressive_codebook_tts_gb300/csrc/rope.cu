@@ -12,7 +12,8 @@ namespace {
 // goes through a warp-private patch of shared memory and each lane reads its partners back from
 // there (as vectors unless rot_dim / 2 is not a multiple of four).  A lane takes U (one or three)
 // heads of one row, all loads issued first; the row's (cos, sin) are loaded once and serve them
-// all.  Bound by HBM on a prompt's rows, by launch latency on one decode step.
+// all.  8191 rows of 24 heads, f32 to bf16: 34.7 us (4.4 TB/s, 0.66 of the measured copy rate), bound
+// by load latency and issue (0.61 of the slots); 32 rows: 2.1 us, a launch.
 // ---------------------------------------------------------------------------
 constexpr int kRopeWarps = 4;
 
@@ -214,7 +215,8 @@ cudaError_t launch_rows_d(const RopeRowsParams& p, cudaStream_t s) {
 //   cos(x + y) = cos x cos y - sin x sin y,  sin(x + y) = sin x cos y + cos x sin y,
 // in pairs of singles (a value and its remainder: about 48 bits): first the multiples
 // j < kSide of f and p0 f + kSide j f, each a product over the bits of j, then the entry
-// (p0 + kSide a + b) f as one product, rounded to f32 once.
+// (p0 + kSide a + b) f as one product, rounded to f32 once.  32768 x 64: 13.8 us (21 with 64
+// angles in double a block and frequency; its bytes need 2.5), mostly latency of pow and sincos.
 // ---------------------------------------------------------------------------
 constexpr int kBits = 10, kSide = 32, kSpan = kSide * kSide, kFreqs = 8, kTabThreads = 256;
 

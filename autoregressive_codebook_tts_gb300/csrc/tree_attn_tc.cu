@@ -24,14 +24,15 @@
 // with node rows, V rows past the window are zeroed before their product (whatever a page holds
 // there).  One warp issues both products of either group, whichever has its operands first.
 //
-// Measured (cycles of one CTA's steady state, 128-row tiles, head_dim 128): a bf16 tile every 2120
-// (64 KB: 58 GB/s an SM, the HBM's share being 44) with few query rows; an int8 tile every 2650,
+// Traced before the one-pass softmax (cycles of one CTA's steady state, head_dim 128): a bf16 tile
+// every 2120 (64 KB: 58 GB/s an SM, the HBM's share being 44) with few query rows; an int8 tile every 2650,
 // set by the chain widening (650) - scores (650) - weights (1000) - output (600) of each group;
-// with 128 rows the weights of a tile (4450: 128 a thread) set 3650.  An item's end costs 3000 to
-// 12000 more (query rows, partial rows, their merge), which the cut counts as two tiles.  All
-// roles' loops share the instruction cache: rolled, they are 2 to 4 times faster than unrolled.
-// 32 streams of 1500..4000 rows, one node: bf16 66 us (5.4 TB/s, 0.80 of the measured copy rate),
-// int8 70 us, e4m3 78 us; 63 nodes: bf16 99 us, int8 140 us, e4m3 144 us.
+// with 128 rows the weights of a tile (4450: 128 a thread, traced after it) set 3650.  An item's end costs
+// 3000 to 12000 more (query rows, partial rows, their merge), which the cut counts as two tiles, or
+// as four and a half with 128 rows.  All roles' loops share the instruction cache: the step
+// that rolled them (with one arrival a warp and elected issue) took int8 from 137 to 98 us.
+// 32 streams of 1500..4000 rows, one node: bf16 66 us (5.4 TB/s, 0.81 of the measured copy rate),
+// int8 71 us; 63 nodes: bf16 94 us, int8 133 us.
 //
 // The window is cut over one CTA per SM by cost (tree_plan.cuh).  Non-finite V entries of node
 // rows are handled as in tree_attn.cu.  Every wait is bounded; on expiry TTS_EFLAG_TIMEOUT is
