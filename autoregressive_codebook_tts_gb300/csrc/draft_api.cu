@@ -97,7 +97,8 @@ tts_status tts_rope_table_scaled(float* cs, int32_t max_pos, int32_t rot_dim, do
                                  void* stream) {
   if (cs == nullptr || s == nullptr) return TTS_ERR_NULL;
   if (s->kind < TTS_ROPE_NONE || s->kind > TTS_ROPE_PARTS) return TTS_ERR_DTYPE;
-  if (max_pos < 1 || max_pos > (1 << 26) || rot_dim < 2 || rot_dim > 128 || rot_dim % 2 != 0 || !(base > 1.0) ||
+  // (a grid holds 65535 blocks of 1024 positions)
+  if (max_pos < 1 || max_pos > 65535 * 1024 || rot_dim < 2 || rot_dim > 128 || rot_dim % 2 != 0 || !(base > 1.0) ||
       !std::isfinite(base) || !(s->attn_scale > 0.0) || !std::isfinite(s->attn_scale))
     return TTS_ERR_SHAPE;
   if (s->kind != TTS_ROPE_NONE && (!(s->factor >= 1.0) || !std::isfinite(s->factor))) return TTS_ERR_SHAPE;

@@ -476,7 +476,8 @@ typedef struct {
   double attn_scale;        /* every kind: finite, above 0 (1 = none) */
 } tts_rope_scaling;
 
-/* cs: device f32 [max_pos][rot_dim/2][2]; rot_dim even, 2..128 (BASE: at least 4). */
+/* cs: device f32 [max_pos][rot_dim/2][2]; max_pos 1..65535*1024; rot_dim even, 2..128 (BASE: at
+ * least 4). */
 tts_status tts_rope_table_scaled(float* cs, int32_t max_pos, int32_t rot_dim, double base,
                                  const tts_rope_scaling* scaling, void* stream);
 

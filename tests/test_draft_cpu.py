@@ -184,6 +184,14 @@ def test_binding_refuses_what_the_library_cannot_see(tts):
         tts.tts_rope_rows(rows, None, rows, None, torch.zeros(4, dtype=torch.int32), 8, 0, 128, torch.zeros(4, 64))
 
 
+@no_gpu
+def test_rope_table_scaled_refuses_more_rows_than_a_grid_holds(tts):
+    # blocks of 1024 positions, at most 65535 of them
+    sc = tts.TtsRopeScaling(0, 1, 1.0, 1.0, 32.0, 1.0)
+    for n in (65535 * 1024 + 1, 1 << 26):
+        assert tts._lib.tts_rope_table_scaled(P(16), n, 64, 1e6, ctypes.byref(sc), None) == 2, n
+
+
 # The reference's own quantiser against facts of the formats.
 def test_reference_codes():
     assert R.E4M3.size == 127 and R.E4M3[-1] == 448.0 and R.E4M3[1] == 2.0 ** -9
