@@ -228,7 +228,7 @@ tts_status tts_tree_attn(const void* q, int32_t q_dtype, int64_t q_stride, const
   if (st != TTS_OK) return st;
   if (q == nullptr || n_past == nullptr || out == nullptr) return TTS_ERR_NULL;
   if (!row_dtype_ok(q_dtype)) return TTS_ERR_DTYPE;
-  if (!tree_shape_ok(d, T) || q_stride < static_cast<int64_t>(d->n_q_heads) * d->head_dim || !std::isfinite(scale))
+  if (!tree_shape_ok(d, T) || q_stride < static_cast<int64_t>(d->n_q_heads) * d->head_dim || !std::isfinite(scale * 1.4426950408889634f))
     return TTS_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(out) || !aligned16(tree_mask) || q_stride % row_quantum(q_dtype) != 0)
     return TTS_ERR_ALIGN;

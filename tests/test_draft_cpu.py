@@ -192,6 +192,14 @@ def test_rope_table_scaled_refuses_more_rows_than_a_grid_holds(tts):
         assert tts._lib.tts_rope_table_scaled(P(16), n, 64, 1e6, ctypes.byref(sc), None) == 2, n
 
 
+@no_gpu
+def test_tree_attn_refuses_scales_that_overflow_in_base_2(tts):
+    d, c = tts.kv_desc(2, 16, 8, 128, 4096, "bf16"), cache_of(tts)
+    for scale in (3e38, -3e38):   # times log2(e): beyond the largest f32
+        assert tts._lib.tts_tree_attn(P(16), 0, 2048, ctypes.byref(c), ctypes.byref(d), P(16), None, None, 8, scale,
+                                      P(1 << 20), P(256), 1 << 30, None, None) == 2, scale
+
+
 # The reference's own quantiser against facts of the formats.
 def test_reference_codes():
     assert R.E4M3.size == 127 and R.E4M3[-1] == 448.0 and R.E4M3[1] == 2.0 ** -9
