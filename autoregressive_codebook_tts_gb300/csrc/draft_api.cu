@@ -239,6 +239,8 @@ tts_status tts_tree_attn(const void* q, int32_t q_dtype, int64_t q_stride, const
     p.part = static_cast<float*>(workspace);
     p.ml = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + t.part);
   }
+  // a row of q is read by every CTA of its item, some after another has written out
+  if (q == out) return TTS_ERR_LAYOUT;
   p.q = q;
   p.q_stride = q_stride;
   p.q_bf16 = q_dtype == TTS_BF16;

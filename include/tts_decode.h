@@ -556,7 +556,8 @@ tts_status tts_kv_read_rows(const tts_kv_cache* cache, const tts_kv_desc* desc, 
  * formula does.  T = 1 with a NULL mask is the single-token form: the window [0, n_past + 1).
  *   q: device rows r = b*T + t of q_dtype (f32 or bf16), q + r*q_stride elements, heads
  *        contiguous, rows 16-byte aligned.  out: q_dtype, dense [B][T][Hq][D]; rows t >= n are
- *        left as they were.
+ *        left as they were.  out must not overlap q (q == out is refused), the cache or the
+ *        workspace.
  *   scale: finite, also times log2(e) (the softmax is taken in base 2).
  *   n_past, n_nodes: device int32 [B].  n_nodes outside [0, T], n_past below 0, or more than
  *        `capacity` rows in all are clamped (the nodes first) and set TTS_EFLAG_NVALID; a page id

@@ -200,6 +200,14 @@ def test_tree_attn_refuses_scales_that_overflow_in_base_2(tts):
                                       P(1 << 20), P(256), 1 << 30, None, None) == 2, scale
 
 
+@no_gpu
+def test_tree_attn_refuses_out_over_q(tts):
+    d, c = tts.kv_desc(2, 16, 8, 128, 4096, "bf16"), cache_of(tts)
+    for q_dtype in (0, 1):
+        assert tts._lib.tts_tree_attn(P(1 << 20), q_dtype, 2048, ctypes.byref(c), ctypes.byref(d), P(16), None, None, 8,
+                                      0.1, P(1 << 20), P(256), 1 << 30, None, None) == 4
+
+
 # The reference's own quantiser against facts of the formats.
 def test_reference_codes():
     assert R.E4M3.size == 127 and R.E4M3[-1] == 448.0 and R.E4M3[1] == 2.0 ** -9
