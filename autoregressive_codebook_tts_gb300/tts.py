@@ -543,6 +543,7 @@ def tts_rope_rows(q, k, q_out, k_out, pos, n_q_heads, n_kv_heads, head_dim, cs, 
             _ints(gm, "gamma", head_dim, torch.float32)
     if cs.dim() != 3 or cs.dtype != torch.float32 or not cs.is_contiguous() or cs.shape[2] != 2:
         raise ValueError("cs must be a contiguous float32 [max_pos, rot_dim / 2, 2] table")
+    _ints(err_flag, "err_flag", 1)
     st = _on_device(stream, q, k, q_out, k_out, pos, cs, gamma_q, gamma_k, err_flag)
     _check(_lib.tts_rope_rows(_p(q), qs, _p(k), ks, dt, _p(q_out), qos, _p(k_out), kos, odt,
                               _p(gamma_q), _p(gamma_k), float(eps), _p(pos), n, n_q_heads,
@@ -562,6 +563,7 @@ def tts_kv_write_rows(k, v, cache: TtsKvCache, desc: TtsKvDesc, start_pos, T, n_
     _cache_fits(cache, desc)
     _ints(start_pos, "start_pos", desc.B)
     _ints(n_rows, "n_rows", desc.B)
+    _ints(err_flag, "err_flag", 1)
     st = _on_device(stream, k, v, cache, start_pos, n_rows, err_flag)
     _check(_lib.tts_kv_write_rows(_p(k), _p(v), dt, ks, ctypes.byref(cache), ctypes.byref(desc),
                                   _p(start_pos), _p(n_rows), T, _p(err_flag), st), "tts_kv_write_rows")
@@ -579,6 +581,7 @@ def tts_kv_read_rows(cache: TtsKvCache, desc: TtsKvDesc, start_pos, T, k_out, v_
     _cache_fits(cache, desc)
     _ints(start_pos, "start_pos", desc.B)
     _ints(n_rows, "n_rows", desc.B)
+    _ints(err_flag, "err_flag", 1)
     st = _on_device(stream, k_out, v_out, cache, start_pos, n_rows, err_flag)
     _check(_lib.tts_kv_read_rows(ctypes.byref(cache), ctypes.byref(desc), _p(start_pos), _p(n_rows), T,
                                  _p(k_out), _p(v_out), dt, ks, _p(err_flag), st), "tts_kv_read_rows")
@@ -615,6 +618,9 @@ def tts_tree_attn(q, cache: TtsKvCache, desc: TtsKvDesc, n_past, T, scale, out, 
     _ints(n_past, "n_past", desc.B)
     _ints(n_nodes, "n_nodes", desc.B)
     _ints(tree_mask, "tree_mask", desc.B * T, torch.int64)
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    _ints(err_flag, "err_flag", 1)
     st = _on_device(stream, q, cache, n_past, n_nodes, tree_mask, out, ws, err_flag)
     _check(_lib.tts_tree_attn(_p(q), dt, qs, ctypes.byref(cache), ctypes.byref(desc), _p(n_past),
                               _p(n_nodes), _p(tree_mask), T, float(scale), _p(out), _p(ws),
@@ -631,6 +637,7 @@ def tts_tree_commit(cache: TtsKvCache, desc: TtsKvDesc, n_past, path, n_accept, 
     _cache_fits(cache, desc)
     _ints(n_past, "n_past", desc.B)
     _ints(n_accept, "n_accept", desc.B)
+    _ints(err_flag, "err_flag", 1)
     st = _on_device(stream, path, cache, n_past, n_accept, err_flag)
     _check(_lib.tts_tree_commit(ctypes.byref(cache), ctypes.byref(desc), _p(n_past), _p(path),
                                 path.stride(0) if desc.B > 1 else T, _p(n_accept), T, _p(err_flag), st),

@@ -208,6 +208,25 @@ def test_tree_attn_refuses_out_over_q(tts):
                                       0.1, P(1 << 20), P(256), 1 << 30, None, None) == 4
 
 
+def test_binding_refuses_small_flags_and_expanded_workspaces(tts):
+    k, s = torch.zeros(2, 8, 256, 128, dtype=torch.int8), torch.zeros(2, 8, 256)
+    c, d = tts.kv_cache(k, k, s, s), tts.kv_desc(2, 16, 8, 128, 256, "i8")
+    rows, q, pos = torch.zeros(4, 1024), torch.zeros(4, 2048), torch.zeros(2, dtype=torch.int32)
+    path, byte = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.uint8)
+    ws = torch.zeros(1, dtype=torch.uint8).expand(1 << 20)
+    calls = (lambda **kw: tts.tts_kv_write_rows(rows, rows, c, d, pos, 2, **kw),
+             lambda **kw: tts.tts_kv_read_rows(c, d, pos, 2, rows, rows, **kw),
+             lambda **kw: tts.tts_tree_attn(q, c, d, pos, 2, 0.1, torch.empty_like(q), None, **kw),
+             lambda **kw: tts.tts_tree_commit(c, d, pos, path, pos, 2, **kw),
+             lambda **kw: tts.tts_rope_rows(rows, None, torch.empty_like(rows), None, torch.zeros(4, dtype=torch.int32),
+                                            8, 0, 128, torch.zeros(4, 64, 2), **kw))
+    for call in calls:
+        with pytest.raises(ValueError, match="err_flag"):
+            call(err_flag=byte)
+    with pytest.raises(ValueError, match="workspace"):
+        tts.tts_tree_attn(q, c, d, pos, 2, 0.1, torch.empty_like(q), ws)
+
+
 # The reference's own quantiser against facts of the formats.
 def test_reference_codes():
     assert R.E4M3.size == 127 and R.E4M3[-1] == 448.0 and R.E4M3[1] == 2.0 ** -9
