@@ -211,6 +211,45 @@ def test_rows_written_and_read_back(tts, kv, src, B, T, hkv, d, cap, page):
             assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(0), b.nan_to_num(0))
 
 
+# Every border of a format, both signs, in rows whose largest magnitude is Q 2^e: the scale is then
+# 2^e exactly (Q * f32(1 / Q) = 1 for both Q), the quotients are the borders exactly, and each has
+# two nearest codes, of which the even one is to be taken.  All entries fit in bf16.
+@pytest.mark.parametrize("kv", ["i8", "e4m3"])
+@pytest.mark.parametrize("src", ["f32", "bf16"])
+def test_ties_take_the_even_code(tts, kv, src):
+    if kv == "i8":
+        codes = np.arange(-127, 128)
+        borders = codes[:-1] + 0.5
+        want = np.where(codes[:-1] % 2 == 0, codes[:-1], codes[:-1] + 1) & 0xff
+    else:
+        value = lambda c: (c % 8) * 2.0 ** -9 if c < 8 else (8 + c % 8) * 2.0 ** (c // 8 - 10)  # noqa: E731
+        low = np.arange(126)
+        mid = np.array([(value(c) + value(c + 1)) / 2 for c in low])
+        even = np.where(low % 2 == 0, low, low + 1)
+        borders, want = np.concatenate([mid, -mid]), np.concatenate([even, even | 0x80])
+    top, n = (127.0 if kv == "i8" else 448.0), len(borders)
+    quot, code = np.zeros((2, 128)), np.zeros((2, 128), np.int64)
+    for i in range(2):
+        part = slice(i * (n // 2), (i + 1) * (n // 2))
+        quot[i, 0], code[i, 0] = top, 127 if kv == "i8" else 126
+        quot[i, 1:1 + n // 2], code[i, 1:1 + n // 2] = borders[part], want[part]
+    exps = list(range(-30, 31))
+    x64 = np.stack([quot * 2.0 ** e for e in exps])                     # [61][2][128]
+    x = torch.from_numpy(x64.astype(np.float32)).to(R.TORCH[src])
+    assert np.array_equal(x.double().numpy(), x64)
+    rows = x.reshape(len(exps), 256).cuda()                             # two kv heads a row
+    c = R.Cache(1, 2, 128, 64, kv, 0, seed=5).to_device(tts, 4)
+    tts.tts_kv_write_rows(rows, rows, c.cache, c.desc, ints([0]), len(exps))
+    for t, scale in ((c.dk, c.dks), (c.dv, c.dvs)):
+        got = t.view(torch.uint8)[0, :, :len(exps)].permute(1, 0, 2).cpu().numpy().astype(np.int64)
+        zero = (code & 0x7f) == 0 if kv == "e4m3" else np.zeros_like(code, bool)
+        got = np.where(zero[None] & (got == 0x80), 0, got)              # (a zero's sign)
+        ref = np.where(zero, 0, code)
+        assert np.array_equal(got, np.broadcast_to(ref, got.shape))
+        assert np.array_equal(scale[0, :, :len(exps)].cpu().double().numpy(),
+                              np.broadcast_to(2.0 ** np.array(exps), (2, len(exps))))
+
+
 def test_rows_out_of_range_are_skipped_and_flagged(tts):
     for page in (0, 16):
         c = R.Cache(4, 2, 64, 64, "i8", page, seed=5).to_device(tts, 4)
