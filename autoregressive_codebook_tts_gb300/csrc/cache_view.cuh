@@ -109,7 +109,8 @@ struct E4m3Code {
     float q = x * inv;
     q = fmaf(fmaf(-q, s, x), inv, q);
     const float left = fmaf(-q, s, x);
-    if (left != 0.f) {
+    // (a quotient that underflows is a zero of its sign already: no last place below it)
+    if (left != 0.f && q != 0.f) {
       uint32_t u = __float_as_uint(q);
       if ((left < 0.f) != (q < 0.f)) --u;   // |q| is above the quotient
       q = __uint_as_float(u | 1u);
