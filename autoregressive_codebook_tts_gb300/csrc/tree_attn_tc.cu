@@ -818,14 +818,15 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
         const float cr = k8 ? fmaxf(c * s_qs[rr], 1e-37f) : c;
         float unit = 1.0f;   // what O's unit changes by
         if constexpr (k8) {
-          // V's scales times g = 2^(127 - ve): a tile's largest stays between 2^-8 and 2^6, so that
-          // the weights (up to 2^8 of it) lie well in f16's range; O is in units of 1 / g.  (ve never falls
-          // below the largest so far less 60: O stays finite.)
+          // V's scales times g = 2^(127 - ve): a tile's largest stays between 2^2 and 2^7, near the top
+          // of what f16 holds of weights up to 2^8 of it, so that weights are lost (rounded to 0) only
+          // below 2^-27 of the largest: the many small ones beside a dominant row count.  O is in
+          // units of 1 / g.  (ve never falls below the largest so far less 64: O stays finite.)
           const float4 v4 = *reinterpret_cast<const float4*>(s_vmax + slot * 4);
           const int e = static_cast<int>(__float_as_uint(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w))) >> 23);
-          if (e > 0 && (e > ve + 5 || e < ve - 8)) {
+          if (e > 0 && (e > ve + 6 || e < ve + 2)) {
             ve_top = max(ve_top, e);
-            const int to = min(max(e, ve_top - 60), 253);
+            const int to = min(max(max(e, ve_top - 60) - 4, 1), 253);
             unit = exp2f(static_cast<float>(ve - to));
             ve = to;
           }
