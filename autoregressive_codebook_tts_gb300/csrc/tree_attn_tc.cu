@@ -12,8 +12,9 @@
 //   S = Q K^T          exact products, f32 sums.  bf16 caches: bf16 operands.  8-bit caches: f16,
 //                      which holds every code, and a bf16 row of q once it is scaled by a power
 //                      of two; the K row's scale multiplies S.
-//   P = 2^(S c - m)    f32, rounded to bf16 (8-bit caches: times V's row scale, to f16) and
-//                      written over S in tensor memory as the A operand of the second product
+//   P = 2^(S c - m)    f32, rounded to bf16 (8-bit caches: times V's row scale, to f16 in a unit
+//                      that follows the row's largest such product) and written over S in tensor
+//                      memory as the A operand of the second product
 //   O += P V           V as the MN-major operand.  The maximum in use moves only when a row's
 //                      grows by more than 2^8; then O is rescaled in tensor memory.
 //
@@ -65,8 +66,7 @@ struct TcCfg {
   static constexpr int kOffK = kQBytes, kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffRawK = kOffV + kStages * kTileBytes, kOffRawV = kOffRawK + kRaw * kRawBytes;
   static constexpr int kOffScale = kOffRawV + kRaw * kRawBytes; // [2][K, V][128] f32: scales of a tile's rows
-  static constexpr int kOffVmax = kOffScale + (k8 ? 2048 : 0);  // [2][4] f32: the largest V scale, by warp
-  static constexpr int kOffQs = kOffVmax + (k8 ? 32 : 0);       // [128] f32: the power of two q was divided by
+  static constexpr int kOffQs = kOffScale + (k8 ? 2048 : 0);    // [128] f32: the power of two q was divided by
   static constexpr int kOffBar = kOffQs + (k8 ? 512 : 0);
   static constexpr size_t kSmem = kOffBar + 320;
 };
@@ -316,12 +316,14 @@ __device__ __forceinline__ float max32(const float (&s)[32]) {
 }
 
 // The weights 2^(s c - ms) of 32 columns, packed to 16 bits (8-bit caches: f16, times the
-// columns' V scales and g; else bf16), and their unrounded sum (without the scales).
+// columns' V scales and g; else bf16), and their unrounded sum (without the scales).  `top`
+// (8-bit): the largest magnitude packed; infinity when one does not fit.
 template <bool k8>
 __device__ __forceinline__ float weights(const float (&s)[32], const float* vsc, float g, float c, float ms,
-                                         uint32_t (&pk)[16]) {
+                                         uint32_t (&pk)[16], float& top) {
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const float2 neg = make_float2(-ms, -ms), c2 = make_float2(c, c), g2 = make_float2(g, g);
+  __half2 t2[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
 #pragma unroll
   for (int e = 0; e < 32; e += 4) {
     float2 a = __ffma2_rn(make_float2(s[e], s[e + 1]), c2, neg);
@@ -330,10 +332,13 @@ __device__ __forceinline__ float weights(const float (&s)[32], const float* vsc,
     sum[0] = __fadd2_rn(sum[0], a);
     sum[1] = __fadd2_rn(sum[1], b);
     if constexpr (k8) {
+      // (weight times scale first: a weight of 0 stays 0 whatever finite scale it meets)
       const float4 v = *reinterpret_cast<const float4*>(vsc + e);
-      a = __fmul2_rn(a, __fmul2_rn(make_float2(v.x, v.y), g2));
-      b = __fmul2_rn(b, __fmul2_rn(make_float2(v.z, v.w), g2));
+      a = __fmul2_rn(__fmul2_rn(a, make_float2(v.x, v.y)), g2);
+      b = __fmul2_rn(__fmul2_rn(b, make_float2(v.z, v.w)), g2);
       const __half2 x = __floats2half2_rn(a.x, a.y), y = __floats2half2_rn(b.x, b.y);
+      t2[0] = __hmax2(t2[0], __habs2(x));
+      t2[1] = __hmax2(t2[1], __habs2(y));
       pk[e / 2] = *reinterpret_cast<const uint32_t*>(&x);
       pk[e / 2 + 1] = *reinterpret_cast<const uint32_t*>(&y);
     } else {
@@ -342,20 +347,59 @@ __device__ __forceinline__ float weights(const float (&s)[32], const float* vsc,
       pk[e / 2 + 1] = *reinterpret_cast<const uint32_t*>(&y);
     }
   }
+  if constexpr (k8) {
+    const float2 t = __half22float2(__hmax2(t2[0], t2[1]));
+    top = fmaxf(t.x, t.y);
+  }
   const float2 t = __fadd2_rn(sum[0], sum[1]);
   return t.x + t.y;
 }
 
-// A packed pair of weights times a (rounded once more: only weights of a tile whose maximum moved
-// after they were written).
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// The same weights times V scales once more, when the unit 2^(ve - 127) no longer suits them: the
+// largest product so far (`top` units, before these 32) or of these is to be 2^6 to 2^7 units.
+// Returns the power of two that what was summed in the old unit is to be multiplied by.
+__device__ __forceinline__ int weights_in_new_unit(const float (&s)[32], const float* vsc, float c, float ms, int& ve,
+                                                   float& top, uint32_t (&pk)[16]) {
+  // 2^9 down, so that no weight (up to 2^8) times a finite scale overflows; what is not finite does
+  // not choose the unit
+  float x[32], most = 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    x[e] = ex2(fmaf(s[e], c, -ms)) * pow2(-9) * vsc[e];
+    const float a = fabsf(x[e]);
+    most = fmaxf(most, a < INFINITY ? a : 0.f);
+  }
+  const auto exponent = [](float a) { return static_cast<int>(__float_as_uint(a) >> 23) - 127; };
+  const int old = ve;
+  int e = -1000;
+  if (top > 0.f) e = exponent(top) + ve - 127;
+  if (most > 0.f) e = max(e, exponent(most) + 9);
+  const int at = e + 127 - ve;   // the exponent of the largest in units
+  if (e > -1000 && (at < 0 || at > 14)) ve = min(max(e + 121, 10), 253);
+  const int up = old - ve;
+  const float g = pow2(136 - ve);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const __half2 h = __floats2half2_rn(x[2 * k] * g, x[2 * k + 1] * g);
+    pk[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  top = fmaxf(top * pow2(up / 2) * pow2(up - up / 2), most * g);
+  return up;
+}
+
+// A packed pair of weights times a and b (rounded once more: only weights of a tile whose maximum
+// or unit moved after they were written).
 template <bool k8>
-__device__ __forceinline__ uint32_t scale_pair(uint32_t w, float a) {
+__device__ __forceinline__ uint32_t scale_pair(uint32_t w, float a, float b) {
   if constexpr (k8) {
     const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    const __half2 y = __floats2half2_rn(x.x * a, x.y * a);
+    const __half2 y = __floats2half2_rn(x.x * a * b, x.y * a * b);
     return *reinterpret_cast<const uint32_t*>(&y);
   } else {
     const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(w << 16) * a, __uint_as_float(w & 0xffff0000u) * a);
+    (void)b;
     return *reinterpret_cast<const uint32_t*>(&y);
   }
 }
@@ -487,7 +531,6 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   float* stage = reinterpret_cast<float*>(smem);                          // epilogue: [256][32]
   float* s_scale = reinterpret_cast<float*>(smem + C::kOffScale);         // [2][2][128]
-  float* s_vmax = reinterpret_cast<float*>(smem + C::kOffVmax);           // [2][4]
   float* s_qs = reinterpret_cast<float*>(smem + C::kOffQs);               // [128]
   uint64_t* fullK = reinterpret_cast<uint64_t*>(smem + C::kOffBar);       // [NS] operand tile written
   uint64_t* emptyK = fullK + NS;                                          // [NS] its product done
@@ -605,8 +648,7 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
         const uint32_t ph = static_cast<uint32_t>(t >> 1) & 1u;
         // a node row's non-finite V scale may not meet the weight 0 of the rows that do not see it
         // (the epilogue adds it to those that do)
-        const uint32_t vb = __float_as_uint(vs) & 0x7fffffffu;
-        const float k = ks, v = node && vb >= 0x7f800000u ? 0.f : vs;
+        const float k = ks, v = node && (__float_as_uint(vs) & 0x7f800000u) == 0x7f800000u ? 0.f : vs;
         w.next(p);
         scales();   // in flight while this tile is widened
         // K's operand tile is free once the scores of tile t - 2 are done, the scales' slot once its
@@ -617,9 +659,6 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
         }
         s_scale[s * 256 + wt] = k;
         s_scale[s * 256 + 128 + wt] = v;
-        // (magnitudes order as their bits do; what is not finite does not count)
-        const uint32_t top = __reduce_max_sync(kFull, vb < 0x7f800000u ? vb : 0u);
-        if (lane == 0) s_vmax[s * 4 + (wt >> 5)] = __uint_as_float(top);
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {   // K, then V
           if (x == 1 && (!warp_wait(&rawV[s], ph) || (t >= 2 && !warp_wait(&emptyV[s], ph ^ 1u)))) {
@@ -799,7 +838,10 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
         node_scale = __ldcg(cv.v_scale + cache_row(cv, it.b, it.g, pos, page));
       }
       float m = -INFINITY, l = 0.f;
-      int ve = 127, ve_top = 0;   // exponent of 1 / g, and of the largest V scale so far
+      // (8-bit) P and O are in units of 2^(ve - 127), at first 2^-12: rows of deviation 1 have V scales
+      // of about 2^-5 (int8) and 2^-7 (e4m3); `top`: the largest product so far, in that unit
+      int ve = 115;
+      float top = 0.f;
       for (int i = wg; ok && i < n; i += 2) {
         const int base = (it.t0 + i) * kN + f * W;   // position of this thread's first column
         const bool masked = (it.t0 + i) * kN + kN > it.w.past;
@@ -816,28 +858,14 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
         const int off = base - it.w.past, node_row = off - f * W + r;   // (of row r of the tile)
         // (kept off 0: scores of -inf times it)
         const float cr = k8 ? fmaxf(c * s_qs[rr], 1e-37f) : c;
-        float unit = 1.0f;   // what O's unit changes by
-        if constexpr (k8) {
-          // V's scales times g = 2^(127 - ve): a tile's largest stays between 2^2 and 2^7, near the top
-          // of what f16 holds of weights up to 2^8 of it, so that weights are lost (rounded to 0) only
-          // below 2^-27 of the largest: the many small ones beside a dominant row count.  O is in
-          // units of 1 / g.  (ve never falls below the largest so far less 64: O stays finite.)
-          const float4 v4 = *reinterpret_cast<const float4*>(s_vmax + slot * 4);
-          const int e = static_cast<int>(__float_as_uint(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w))) >> 23);
-          if (e > 0 && (e > ve + 6 || e < ve + 2)) {
-            ve_top = max(ve_top, e);
-            const int to = min(max(max(e, ve_top - 60) - 4, 1), 253);
-            unit = exp2f(static_cast<float>(ve - to));
-            ve = to;
-          }
-        }
-        const float g = __uint_as_float(static_cast<uint32_t>(254 - ve) << 23);
         // chunks of 32 columns, P over S (a chunk's 16 packed columns lie below every S column
-        // still to be read).  A chunk that moves the maximum rescales O and the chunks before it.
+        // still to be read).  A chunk that moves the maximum or the unit rescales O and the chunks
+        // before it.
 #pragma unroll 1
         for (int cc = 0; cc < W / 32; ++cc) {
           float sv[32];
-          load_scores<k8>(tS + f * W + 32 * cc, ksc + 32 * cc, masked, masked ? visible32(off + 32 * cc, see) : ~0u, sv);
+          const uint32_t vis = masked ? visible32(off + 32 * cc, see) : ~0u;
+          load_scores<k8>(tS + f * W + 32 * cc, ksc + 32 * cc, masked, vis, sv);
           float mx = max32(sv);
           if (mx > -INFINITY) mx *= cr;
           const bool move = mx > m + 8.0f;
@@ -846,16 +874,34 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
             l *= alpha;
             m = mx;
           }
-          if (__any_sync(kFull, alpha != 1.0f || (cc == 0 && unit != 1.0f))) {
+          const float ms = m == -INFINITY ? 0.f : m;
+          uint32_t pk[16];
+          float now = 0.f;
+          l += weights<k8>(sv, vsc + 32 * cc, pow2(127 - ve), cr, ms, pk, now);
+          int up = 0;   // O's unit changes by 2^-up
+          if constexpr (k8) {
+            // The unit follows the largest product of weight and V scale of what this row sees: the
+            // largest so far stays between 1 and f16's 65504 of it, so that products are lost
+            // (rounded to 0) only below 2^-25 of that, and mostly below 2^-31.  Rows that are not
+            // seen, or of no weight, do not matter whatever their scale.
+            top *= alpha;
+            const bool off_unit = !(now < INFINITY) || (fmaxf(top, now) < 1.0f && mx > -INFINITY);
+            if (__any_sync(kFull, off_unit)) {
+              load_scores<k8>(tS + f * W + 32 * cc, ksc + 32 * cc, masked, vis, sv);
+              if (off_unit) up = weights_in_new_unit(sv, vsc + 32 * cc, cr, ms, ve, top, pk);
+            }
+            if (!off_unit) top = fmaxf(top, now);
+          }
+          if (__any_sync(kFull, alpha != 1.0f || up != 0)) {
+            const float a = alpha * pow2(up / 2), b = pow2(up - up / 2);
             if (i > 1) {
               // O is complete up to the group's tile before: its product was issued before S
-              const float by = cc == 0 ? alpha * unit : alpha;
 #pragma unroll 1
               for (int k = 0; k < D / 32; ++k) {
                 float o[32];
                 tmem_ld32(tOw + 32 * k, o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= by;
+                for (int e = 0; e < 32; ++e) o[e] = k8 ? o[e] * a * b : o[e] * a;
                 tmem_st32(tOw + 32 * k, o);
               }
             }
@@ -863,16 +909,14 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
               tmem_wait_st();
 #pragma unroll 1
               for (int k = 0; k < cc; ++k) {
-                uint32_t pk[16];
-                tmem_ld16(tS + f * (W / 2) + 16 * k, pk);
+                uint32_t old[16];
+                tmem_ld16(tS + f * (W / 2) + 16 * k, old);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) pk[e] = scale_pair<k8>(pk[e], alpha);
-                tmem_st16(tS + f * (W / 2) + 16 * k, pk);
+                for (int e = 0; e < 16; ++e) old[e] = scale_pair<k8>(old[e], a, b);
+                tmem_st16(tS + f * (W / 2) + 16 * k, old);
               }
             }
           }
-          uint32_t pk[16];
-          l += weights<k8>(sv, vsc + 32 * cc, g, cr, m == -INFINITY ? 0.f : m, pk);
           tmem_st16(tS + f * (W / 2) + 16 * cc, pk);
         }
         if constexpr (k8) warp_arrive(&scfree[slot]);

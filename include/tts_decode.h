@@ -570,7 +570,9 @@ tts_status tts_kv_read_rows(const tts_kv_cache* cache, const tts_kv_desc* desc, 
  * Statistics and sums in f32; with f32 q or an f32 cache every product too.  With bf16 q over a
  * bf16 or 8-bit cache (bf16 pages of fewer than 8 rows excepted) the products run on the tensor
  * cores, exact in q and K, with the softmax weights rounded where they meet V: to bf16 over a
- * bf16 cache, to f16 times the row's scale over an 8-bit one.  Results do not depend on timing.
+ * bf16 cache; over an 8-bit one to f16 times the V row's scale, in a unit of each query row's own,
+ * so that what a weight times its scale adds is lost only below 2^-25 of the largest such product
+ * that the row sees.  Results do not depend on timing.
  * ------------------------------------------------------------------------- */
 #define TTS_MAX_TREE_NODES 64
 size_t tts_tree_attn_workspace_size(const tts_kv_desc* desc, int32_t T, int32_t q_dtype);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import draft_ref as R
-from test_draft_gpu import check_tree, ints, run_tree, tts  # noqa: F401
+from test_draft_gpu import check_tree, ints, masks, run_tree, tts  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,73 @@ def test_a_dominant_row_with_small_values(tts, kv, T, n, small):  # noqa: F811
     out, _ = run_tree(tts, c, q.cuda().repeat(B, 1, 1, 1), [n - T] * B, [T] * B, None, T, 1.0)
     ref, mag = attend(c, q[0].double(), n - T, T, None, 1.0)
     check_tree(out, ref[None].expand(B, -1, -1, -1), mag[None].expand(B, -1, -1, -1), [T] * B)
+
+
+# ---------------------------------------------------------------------------
+# Attention: V scales many powers of two apart
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kv", ["e4m3", "i8"])
+@pytest.mark.parametrize("q_dt", ["bf16", "f32"])
+@pytest.mark.parametrize("e", [20, 40, 60, 100, 118])
+@pytest.mark.parametrize("T,past", [(3, 97), (20, 700), (64, 1000), (64, 0)])
+def test_a_large_row_that_is_not_seen(tts, kv, q_dt, e, T, past):  # noqa: F811
+    """A node's row with a V scale 2^e times the others' (finite): the nodes that do not see it
+    give what they would give without it."""
+    hq, hkv, d, big = 4, 2, 128, T // 2
+    c = R.Cache(1, hkv, d, 1100, kv, 0, seed=3)
+    c.vs[0, :, past + big] *= 2.0 ** e
+    c.to_device(tts, hq)
+    g = np.random.default_rng(T)
+    m = masks(1, T, 3, empty=0.0)
+    m[0] |= np.int64(1)
+    for t in range(T):
+        if t % 3:
+            m[0, t] &= ~np.int64(np.uint64(1 << big).astype(np.int64))
+    q = torch.from_numpy(g.standard_normal((1, T, hq, d)).astype(np.float32)).to(R.TORCH[q_dt])
+    out, _ = run_tree(tts, c, q.cuda(), [past], [T], m, T, 0.1)
+    ref, mag = attend(c, q[0].double(), past, T, m[0], 0.1)
+    check_tree(out, ref[None], mag[None], [T])
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "i8"])
+@pytest.mark.parametrize("q_dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 12, 30, 64])
+@pytest.mark.parametrize("at", [3, 130, 700, 1180])
+def test_a_large_row_of_no_weight(tts, kv, q_dt, T, at):  # noqa: F811
+    """A committed row with a V scale 2^60 times the others' and a weight of 2^-90 of theirs."""
+    hq, hkv, d, past = 4, 2, 128, 1190
+    c = R.Cache(1, hkv, d, 1280, kv, 0, seed=4)
+    k = torch.randn(1, hkv, 1280, d, generator=torch.Generator().manual_seed(T)) * 0.3
+    k[0, :, at] = -2.0
+    c.k, c.ks = R.to_cache(k.numpy(), kv)
+    c.vs[0, :, at] *= 2.0 ** 60
+    c.to_device(tts, hq)
+    g = np.random.default_rng(T)
+    q = torch.from_numpy(0.05 * g.standard_normal((1, T, hq, d)).astype(np.float32) + 0.25).to(R.TORCH[q_dt])
+    out, _ = run_tree(tts, c, q.cuda(), [past], [T], None, T, 1.0)
+    ref, mag = attend(c, q[0].double(), past, T, None, 1.0)
+    check_tree(out, ref[None], mag[None], [T])
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "i8"])
+@pytest.mark.parametrize("T", [1, 12, 30, 64])
+@pytest.mark.parametrize("seed", range(4))
+def test_scales_and_scores_that_both_move(tts, kv, T, seed):  # noqa: F811
+    """V scales from 2^-40 to 2^40, by row or in runs, under scores that spread over 2^60: the
+    largest weight, the largest weight times scale, and what was summed before all move."""
+    hq, hkv, d, cap, past = 4, 2, 128, 1500, 1400
+    g = np.random.default_rng(100 * T + seed)
+    c = R.Cache(1, hkv, d, cap, kv, 0, seed=5 + seed)
+    run = (1, 7, 64, 300)[seed]
+    c.vs *= torch.from_numpy(np.exp2(np.repeat(g.integers(-40, 41, cap // run + 1), run)[:cap]).astype(np.float32))
+    c.to_device(tts, hq)
+    # scores of standard deviation about 6: 2^+-30 between the largest and the smallest
+    q = torch.from_numpy(g.standard_normal((1, T, hq, d)).astype(np.float32)).bfloat16()
+    m = masks(1, T, seed, empty=0.0)
+    out, _ = run_tree(tts, c, q.cuda(), [past], [T], m, T, 6.0 * d ** -0.5)
+    ref, mag = attend(c, q[0].double(), past, T, m[0], 6.0 * d ** -0.5)
+    # scores of up to 40 in f32: 2^-24 of a sum of magnitudes of about 60, a few roundings, move a
+    # weight by up to 2e-5 of itself; a weight whose tile's maximum moved later is rounded twice
+    # (f16: 2^-11 each)
+    bound = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 3e-5) * mag + 1e-5 * ref.abs().amax(-1, keepdim=True)
+    assert ((out[0].cpu().double() - ref).abs() <= bound).all()
