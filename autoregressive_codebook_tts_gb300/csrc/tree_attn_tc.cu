@@ -68,7 +68,8 @@ struct TcCfg {
   static constexpr int kOffScale = kOffRawV + kRaw * kRawBytes; // [2][K, V][128] f32: scales of a tile's rows
   static constexpr int kOffQs = kOffScale + (k8 ? 2048 : 0);    // [128] f32: the power of two q was divided by
   static constexpr int kOffBar = kOffQs + (k8 ? 512 : 0);
-  static constexpr size_t kSmem = kOffBar + 320;
+  static constexpr int kOffNf = kOffBar + 320;                  // [D] f32, bf16: a column's non-finite V entries
+  static constexpr size_t kSmem = kOffNf + (k8 ? 0 : D * 4);
 };
 
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -434,6 +435,29 @@ __device__ __forceinline__ float4 bad_v_sum(const CacheView& c, int b, int g, in
   return make_float4(a[0], a[1], a[2], a[3]);
 }
 
+// Adds up the non-finite V entries of the piece's committed rows, by column, into nf [D] (zeros
+// before): by the softmax threads, 16 bytes of a row each.
+template <int D>
+__device__ __forceinline__ void nonfinite_columns(const TreeParams& p, const Piece& it, int tid, float* nf) {
+  constexpr int UR = D / 8, STEP = kSmxThreads / UR;
+  const CacheView& c = p.cache;
+  const int u = tid % UR, end = min(it.t1 * kN, it.w.past);
+  float sum[8] = {};
+#pragma unroll 4
+  for (int j = it.t0 * kN + tid / UR; j < end; j += STEP) {
+    const int page = c.paged ? max(cache_page(c, it.b, j), 0) : 0;
+    const int64_t row = cache_row(c, it.b, it.g, j, page);
+    float x[8];
+    unpack_bf16x8(__ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.v) + row * D) + u), x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if ((__float_as_uint(x[e]) & 0x7f800000u) == 0x7f800000u) sum[e] += x[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (sum[e] != 0.f) atomicAdd(nf + u * 8 + e, sum[e]);   // (infinities and NaN: in any order)
+}
+
 // One tile of K or V into `dst`, by a whole warp: bf16 in the operand layout (boxes of the
 // tensor map), 8-bit as it lies (bulk copies).  Rows past the window are not asked for, but for
 // the rest of a box.  `page` is the lane's entry of the tile's pages (lane pages apart).
@@ -532,6 +556,7 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
   float* stage = reinterpret_cast<float*>(smem);                          // epilogue: [256][32]
   float* s_scale = reinterpret_cast<float*>(smem + C::kOffScale);         // [2][2][128]
   float* s_qs = reinterpret_cast<float*>(smem + C::kOffQs);               // [128]
+  float* s_nf = reinterpret_cast<float*>(smem + C::kOffNf);               // [D]
   uint64_t* fullK = reinterpret_cast<uint64_t*>(smem + C::kOffBar);       // [NS] operand tile written
   uint64_t* emptyK = fullK + NS;                                          // [NS] its product done
   uint64_t* fullV = emptyK + NS;
@@ -1008,42 +1033,65 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
       const int rows = min(RP, it.w.nodes * p.group - first);
       const int wide = rows * 4 <= RP && D == 128 ? 2 : rows * 2 <= RP ? 1 : 0;
       const int per = RP >> wide, units = 8 << wide;
+      // A committed row's infinite V entry leaves NaN in the replicas that hold weights of 0 for it.
+      // bf16: where an output row is not finite, the piece's rows are looked through and the passes
+      // taken again; such a column is then the sum of its infinities and NaN, whose weights are
+      // above 0.  (Columns of other causes stay; 8-bit V operands are finite, or NaN.)
+      bool fine = true;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32 << wide) {
-        float* mine = stage + ((wg * F + f) * per + rr) * (32 << wide);
+      for (bool mend = false;; mend = true) {
 #pragma unroll 1
-        for (int k = 0; k < 1 << wide; ++k) {
-          float o[32];
-          if (had) tmem_ld32(tOw + c0 + 32 * k, o);
-          if (rr < rows) {
+        for (int c0 = 0; c0 < D; c0 += 32 << wide) {
+          float* mine = stage + ((wg * F + f) * per + rr) * (32 << wide);
+#pragma unroll 1
+          for (int k = 0; k < 1 << wide; ++k) {
+            float o[32];
+            if (had) tmem_ld32(tOw + c0 + 32 * k, o);
+            if (rr < rows) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              *reinterpret_cast<float4*>(mine + ((8 * k + (u ^ (rr & 7))) << 2)) =
-                  had ? make_float4(o[4 * u] * wt, o[4 * u + 1] * wt, o[4 * u + 2] * wt, o[4 * u + 3] * wt)
-                      : make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<float4*>(mine + ((8 * k + (u ^ (rr & 7))) << 2)) =
+                    had ? make_float4(o[4 * u] * wt, o[4 * u + 1] * wt, o[4 * u + 2] * wt, o[4 * u + 3] * wt)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+              if (!k8 && mend && had) {
+#pragma unroll 1
+                for (int e = 0; e < 32; ++e) {
+                  const float x = s_nf[c0 + 32 * k + e];
+                  if (x != 0.f)
+                    mine[((8 * k + ((e >> 2) ^ (rr & 7))) << 2) + (e & 3)] =
+                        l != l || wt != wt ? __uint_as_float(0x7fc00000u) : x;
+                }
+              }
+            }
           }
+          smx_sync();
+#pragma unroll 1
+          for (int i = tid; i < rows * units; i += kSmxThreads) {
+            const int row = i >> (3 + wide), u = i & (units - 1), t = (first + row) >> gs, h = (first + row) & (p.group - 1);
+            const float* src = stage + row * (32 << wide) + ((u ^ (row & 7)) << 2);
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < 2 * F; ++x) {
+              const float4 v = *reinterpret_cast<const float4*>(src + x * per * (32 << wide));
+              a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+            }
+            if (!k8) fine = fine && fmaf(a.x, 0.f, fmaf(a.y, 0.f, fmaf(a.z, 0.f, a.w * 0.f))) == 0.f;
+            const int col = c0 + 4 * u;
+            if (bad_v != 0) {
+              const float4 x = bad_v_sum<KvT, D>(p.cache, it.b, it.g, it.w.past, bad_v & seen_nodes(p, it.b, t, it.w.nodes), col);
+              a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+            }
+            if (complete)
+              store_tree_row4(p, it.b, t, it.g * p.group + h, D, col, a, 1.f);
+            else
+              *reinterpret_cast<float4*>(p.part + (slot * RP + row) * D + col) = a;
+          }
+          if (k8 || mend || c0 + (32 << wide) < D) smx_sync();
         }
+        if (k8 || mend || smx_sync_and(fine)) break;
+        if (tid < D) s_nf[tid] = 0.f;
         smx_sync();
-#pragma unroll 1
-        for (int i = tid; i < rows * units; i += kSmxThreads) {
-          const int row = i >> (3 + wide), u = i & (units - 1), t = (first + row) >> gs, h = (first + row) & (p.group - 1);
-          const float* src = stage + row * (32 << wide) + ((u ^ (row & 7)) << 2);
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int x = 0; x < 2 * F; ++x) {
-            const float4 v = *reinterpret_cast<const float4*>(src + x * per * (32 << wide));
-            a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-          }
-          const int col = c0 + 4 * u;
-          if (bad_v != 0) {
-            const float4 x = bad_v_sum<KvT, D>(p.cache, it.b, it.g, it.w.past, bad_v & seen_nodes(p, it.b, t, it.w.nodes), col);
-            a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-          }
-          if (complete)
-            store_tree_row4(p, it.b, t, it.g * p.group + h, D, col, a, 1.f);
-          else
-            *reinterpret_cast<float4*>(p.part + (slot * RP + row) * D + col) = a;
-        }
+        if constexpr (!k8) nonfinite_columns<D>(p, it, tid, s_nf);
         smx_sync();
       }
     }

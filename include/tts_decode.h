@@ -553,7 +553,8 @@ tts_status tts_kv_read_rows(const tts_kv_cache* cache, const tts_kv_desc* desc, 
  *   out[b][t][h] = sum_j softmax_j(scale * q[b][t][h] . K[b][g][j]) V[b][g][j],  g = h / (Hq/Hkv)
  * over the positions it sees; a node that sees none gives 0.  Rows outside what a node sees,
  * whatever they hold, do not affect it; a visible NaN or infinity gives NaN or infinity as the
- * formula does.  T = 1 with a NULL mask is the single-token form: the window [0, n_past + 1).
+ * formula does (NaN for an infinity whose weight is too small for f32, 2^-126 of the largest).
+ * T = 1 with a NULL mask is the single-token form: the window [0, n_past + 1).
  *   q: device rows r = b*T + t of q_dtype (f32 or bf16), q + r*q_stride elements, heads
  *        contiguous, rows 16-byte aligned.  out: q_dtype, dense [B][T][Hq][D]; rows t >= n are
  *        left as they were.  out must not overlap q (q == out is refused), the cache or the

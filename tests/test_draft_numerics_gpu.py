@@ -159,3 +159,34 @@ def test_scales_and_scores_that_both_move(tts, kv, T, seed):  # noqa: F811
     # (f16: 2^-11 each)
     bound = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 3e-5) * mag + 1e-5 * ref.abs().amax(-1, keepdim=True)
     assert ((out[0].cpu().double() - ref).abs() <= bound).all()
+
+
+# ---------------------------------------------------------------------------
+# Attention: infinities in committed rows
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+@pytest.mark.parametrize("q_dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 5, 12, 30, 64])
+@pytest.mark.parametrize("d,page,cap,past", [(128, 0, 512, 400), (64, 16, 768, 600), (128, 16, 4096, 3900), (64, 0, 2048, 1900)])
+def test_infinities_in_committed_rows(tts, kv, q_dt, T, d, page, cap, past):  # noqa: F811
+    """An infinite committed V entry gives that infinity in its column for every node, whatever the
+    number of query rows; infinities of both signs, or a NaN, give NaN; other columns are exact."""
+    hq, hkv, B = 4, 2, 2
+    c = R.Cache(B, hkv, d, cap, kv, page, seed=6, fill=[past + T, past + T])
+    inf = float("inf")
+    for col, puts in ((3, [(7, inf)]), (4, [(past - 1, -inf)]), (9, [(130, inf), (131, inf)]),
+                      (33, [(1, inf), (300, -inf)]), (50, [(64, float("nan"))]), (51, [(200, -inf), (201, float("nan"))])):
+        for pos, x in puts:
+            at, row = c.at(1, pos)
+            c.v[at, :, row, col] = x
+    c.to_device(tts, hq)
+    q = torch.randn(B, T, hq, d, generator=torch.Generator().manual_seed(T)).to(R.TORCH[q_dt])
+    out, ef = run_tree(tts, c, q.cuda(), [past] * B, [T] * B, None, T, 0.1)
+    assert ef == 0
+    ref, mag = (torch.stack(x) for x in zip(*(attend(c, q[b].double(), past, T, None, 0.1, b) for b in range(B))))
+    check_tree(out[:1], ref[:1], mag[:1], [T])
+    o = out[1].cpu().double()
+    assert (o[..., 3] == inf).all() and (o[..., 4] == -inf).all() and (o[..., 9] == inf).all()
+    assert o[..., 33].isnan().all() and o[..., 50].isnan().all() and o[..., 51].isnan().all()
+    fine = [i for i in range(d) if i not in (3, 4, 9, 33, 50, 51)]
+    check_tree(out[1:, ..., fine], ref[1:, ..., fine], mag[1:, ..., fine], [T])
