@@ -197,15 +197,21 @@ def status_str(status: int) -> str:
 # ---------------------------------------------------------------------------
 # Descriptors
 # ---------------------------------------------------------------------------
-_KV_CODES = {"f32": TTS_F32, "bf16": TTS_BF16, "i8": TTS_I8, "e4m3": TTS_E4M3}
+_KV_CODES = {"f32": TTS_F32, "bf16": TTS_BF16, "i8": TTS_I8, "e4m3": TTS_E4M3,
+             "float32": TTS_F32, "bfloat16": TTS_BF16, "int8": TTS_I8, "float8_e4m3fn": TTS_E4M3,
+             torch.float32: TTS_F32, torch.bfloat16: TTS_BF16, torch.int8: TTS_I8,
+             torch.float8_e4m3fn: TTS_E4M3}
 
 
 def kv_desc(B, n_q_heads, n_kv_heads, head_dim, capacity, kv_dtype="f32", window_quantum=256,
             paged=False, page_size=16, n_pages=0, block_table=None, flags=0) -> TtsKvDesc:
+    """A layer's cache.  kv_dtype: "f32", "bf16", "i8" or "e4m3", or the torch dtype (its name)."""
+    if kv_dtype not in _KV_CODES:
+        raise ValueError("kv_dtype must be \"f32\", \"bf16\", \"i8\", \"e4m3\" or the torch dtype")
     d = TtsKvDesc()
     d.B, d.n_q_heads, d.n_kv_heads, d.head_dim, d.capacity = B, n_q_heads, n_kv_heads, head_dim, capacity
     d.window_quantum = window_quantum
-    d.kv_dtype = _KV_CODES.get(kv_dtype, TTS_BF16)
+    d.kv_dtype = _KV_CODES[kv_dtype]
     d.paged = 1 if paged else 0
     d.page_size = page_size if paged else 0
     d.n_pages = n_pages if paged else 0

@@ -227,6 +227,18 @@ def test_binding_refuses_small_flags_and_expanded_workspaces(tts):
         tts.tts_tree_attn(q, c, d, pos, 2, 0.1, torch.empty_like(q), ws)
 
 
+def test_descriptors_name_their_dtype(tts):
+    # (an unknown name once meant bf16: two bytes an entry over a one-byte tensor)
+    for names, code in ((("f32", "float32", torch.float32), tts.TTS_F32), (("bf16", "bfloat16", torch.bfloat16), tts.TTS_BF16),
+                        (("i8", "int8", torch.int8), tts.TTS_I8),
+                        (("e4m3", "float8_e4m3fn", torch.float8_e4m3fn), tts.TTS_E4M3)):
+        for name in names:
+            assert tts.kv_desc(1, 16, 8, 128, 256, name).kv_dtype == code, name
+    for name in ("fp8", "int4", "f16", "", None, torch.float16, torch.uint8, torch.float8_e5m2):
+        with pytest.raises(ValueError, match="kv_dtype"):
+            tts.kv_desc(1, 16, 8, 128, 256, name)
+
+
 # The reference's own quantiser against facts of the formats.
 def test_reference_codes():
     assert R.E4M3.size == 127 and R.E4M3[-1] == 448.0 and R.E4M3[1] == 2.0 ** -9
