@@ -190,3 +190,69 @@ def test_infinities_in_committed_rows(tts, kv, q_dt, T, d, page, cap, past):  # 
     assert o[..., 33].isnan().all() and o[..., 50].isnan().all() and o[..., 51].isnan().all()
     fine = [i for i in range(d) if i not in (3, 4, 9, 33, 50, 51)]
     check_tree(out[1:, ..., fine], ref[1:, ..., fine], mag[1:, ..., fine], [T])
+
+
+# ---------------------------------------------------------------------------
+# Attention: poisoned node rows where windows are cut over CTAs, page sizes of every box
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kv", ["bf16", "i8", "e4m3", "f32"])
+@pytest.mark.parametrize("q_dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [10, 40])
+def test_poisoned_node_rows_in_cut_windows(tts, kv, q_dt, T):  # noqa: F811
+    """A capacity above what one CTA takes whole: noted V rows and scores that are all NaN pass
+    through partial rows and their merge; an empty mask over no committed rows gives 0."""
+    hq, hkv, d, cap, past = 4, 2, 128, 4096, [0, 1500, 3001]
+    B, bad_v, bad_k = 3, 3, 1
+    g = np.random.default_rng(T)
+    c = R.Cache(B, hkv, d, cap, kv, 0, seed=7, fill=[p + T for p in past])
+    m = masks(B, T, 4, empty=0.0)
+    m[:, 4] = 0
+    m[:, 6] = 1 << bad_k                        # with no committed rows: nothing but a NaN score
+    m[:, 8] |= (1 << bad_v) | (1 << bad_k)
+    for b, p in enumerate(past):
+        if kv in R.TOP:
+            c.vs[b, :, p + bad_v] = float("inf")
+            c.ks[b, :, p + bad_k] = float("nan")
+        else:
+            c.v[b, :, p + bad_v, 5] = float("inf")
+            c.v[b, :, p + bad_v, 6] = float("nan")
+            c.k[b, :, p + bad_k, 0] = float("nan")
+    c.to_device(tts, hq)
+    q = torch.from_numpy(g.standard_normal((B, T, hq, d)).astype(np.float32)).to(R.TORCH[q_dt])
+    out, ef = run_tree(tts, c, q.cuda(), past, [T] * B, m, T, 0.1)
+    assert ef == 0
+    ref, mag = R.tree_attn(c, q.double(), past, [T] * B, m, 0.1)
+    o = out.cpu().double()
+    for b in range(B):
+        for t in range(T):
+            got, want = out[b:b + 1, t:t + 1], (ref[b:b + 1, t:t + 1], mag[b:b + 1, t:t + 1])
+            if m[b, t] >> bad_k & 1:
+                assert o[b, t].isnan().all(), (b, t)
+            elif m[b, t] >> bad_v & 1:
+                if kv in R.TOP:
+                    assert not o[b, t].isfinite().any(), (b, t)
+                else:
+                    assert (o[b, t, :, 5] == float("inf")).all() and o[b, t, :, 6].isnan().all(), (b, t)
+                    fine = [i for i in range(d) if i not in (5, 6)]
+                    check_tree(got[..., fine], *(x[..., fine] for x in want), [1])
+            else:
+                check_tree(got, *want, [1])
+    assert (o[0, 4] == 0).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+@pytest.mark.parametrize("page", [2, 8, 32, 128, 256])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [512, 2048])
+def test_pages_of_every_size(tts, kv, page, d, cap):  # noqa: F811
+    hq, hkv, B, T = 4, 2, 3, 9
+    past = [cap - T, 3, cap // 2 - 5]
+    c = R.Cache(B, hkv, d, cap, kv, page, seed=page, fill=[p + T for p in past]).to_device(tts, hq)
+    q = torch.randn(B, T, hq, d, generator=torch.Generator().manual_seed(page)).bfloat16()
+    m = masks(B, T, page)
+    out, ef = run_tree(tts, c, q.cuda(), past, [T] * B, m, T, d ** -0.5)
+    assert ef == 0
+    ref, mag = (torch.stack(x) for x in zip(*(attend(c, q[b].double(), past[b], T, m[b], d ** -0.5, b) for b in range(B))))
+    none = torch.tensor([[not (past[b] or int(m[b, t]) & ((1 << T) - 1)) for t in range(T)] for b in range(B)])
+    ref[none], mag[none] = 0.0, 0.0
+    check_tree(out, ref, mag, [T] * B)
