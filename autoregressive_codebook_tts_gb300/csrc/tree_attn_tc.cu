@@ -1033,66 +1033,79 @@ __global__ void __launch_bounds__(TcCfg<D, KvT>::kThreads, 1)
       const int rows = min(RP, it.w.nodes * p.group - first);
       const int wide = rows * 4 <= RP && D == 128 ? 2 : rows * 2 <= RP ? 1 : 0;
       const int per = RP >> wide, units = 8 << wide;
-      // A committed row's infinite V entry leaves NaN in the replicas that hold weights of 0 for it.
-      // bf16: where an output row is not finite, the piece's rows are looked through and the passes
-      // taken again; such a column is then the sum of its infinities and NaN, whose weights are
-      // above 0.  (Columns of other causes stay; 8-bit V operands are finite, or NaN.)
       bool fine = true;
 #pragma unroll 1
-      for (bool mend = false;; mend = true) {
+      for (int c0 = 0; c0 < D; c0 += 32 << wide) {
+        float* mine = stage + ((wg * F + f) * per + rr) * (32 << wide);
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32 << wide) {
-          float* mine = stage + ((wg * F + f) * per + rr) * (32 << wide);
-#pragma unroll 1
-          for (int k = 0; k < 1 << wide; ++k) {
-            float o[32];
-            if (had) tmem_ld32(tOw + c0 + 32 * k, o);
-            if (rr < rows) {
+        for (int k = 0; k < 1 << wide; ++k) {
+          float o[32];
+          if (had) tmem_ld32(tOw + c0 + 32 * k, o);
+          if (rr < rows) {
 #pragma unroll
-              for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<float4*>(mine + ((8 * k + (u ^ (rr & 7))) << 2)) =
-                    had ? make_float4(o[4 * u] * wt, o[4 * u + 1] * wt, o[4 * u + 2] * wt, o[4 * u + 3] * wt)
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
-              if (!k8 && mend && had) {
+            for (int u = 0; u < 8; ++u)
+              *reinterpret_cast<float4*>(mine + ((8 * k + (u ^ (rr & 7))) << 2)) =
+                  had ? make_float4(o[4 * u] * wt, o[4 * u + 1] * wt, o[4 * u + 2] * wt, o[4 * u + 3] * wt)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+        smx_sync();
 #pragma unroll 1
-                for (int e = 0; e < 32; ++e) {
-                  const float x = s_nf[c0 + 32 * k + e];
-                  if (x != 0.f)
-                    mine[((8 * k + ((e >> 2) ^ (rr & 7))) << 2) + (e & 3)] =
-                        l != l || wt != wt ? __uint_as_float(0x7fc00000u) : x;
-                }
-              }
+        for (int i = tid; i < rows * units; i += kSmxThreads) {
+          const int row = i >> (3 + wide), u = i & (units - 1), t = (first + row) >> gs, h = (first + row) & (p.group - 1);
+          const float* src = stage + row * (32 << wide) + ((u ^ (row & 7)) << 2);
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int x = 0; x < 2 * F; ++x) {
+            const float4 v = *reinterpret_cast<const float4*>(src + x * per * (32 << wide));
+            a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+          }
+          if (!k8) fine = fine && fmaf(a.x, 0.f, fmaf(a.y, 0.f, fmaf(a.z, 0.f, a.w * 0.f))) == 0.f;
+          const int col = c0 + 4 * u;
+          if (bad_v != 0) {
+            const float4 x = bad_v_sum<KvT, D>(p.cache, it.b, it.g, it.w.past, bad_v & seen_nodes(p, it.b, t, it.w.nodes), col);
+            a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+          }
+          if (complete)
+            store_tree_row4(p, it.b, t, it.g * p.group + h, D, col, a, 1.f);
+          else
+            *reinterpret_cast<float4*>(p.part + (slot * RP + row) * D + col) = a;
+        }
+        smx_sync();
+      }
+      // A committed row's infinite V entry leaves NaN in the replicas that hold weights of 0 for it.
+      // bf16: where an output row is not finite, the piece's rows are looked through and such a
+      // column becomes the sum of its infinities and NaN, whose weights are above 0.  (Columns of
+      // other causes stay; 8-bit V operands are finite, or NaN.)
+      if constexpr (!k8) {
+        if (__builtin_expect(!smx_sync_and(fine), false)) {
+          float* s_row = stage;   // [256]: whether the weights of this thread's row are NaN
+          s_row[tid] = had && (l != l || wt != wt) ? 1.f : 0.f;
+          if (tid < D) s_nf[tid] = 0.f;
+          smx_sync();
+          nonfinite_columns<D>(p, it, tid, s_nf);
+          smx_sync();
+#pragma unroll 1
+          for (int i = tid; i < rows * D; i += kSmxThreads) {
+            const int row = i / D, col = i % D, t = (first + row) >> gs, h = (first + row) & (p.group - 1);
+            float a = s_nf[col];
+            if (a == 0.f) continue;
+            float nan = 0.f;
+            for (int x = 0; x < 2 * F; ++x) nan += s_row[(x & 1) * kM + (x >> 1) * RP + row];
+            if (nan != 0.f) a = __uint_as_float(0x7fc00000u);
+            if (bad_v != 0) {
+              const float4 x = bad_v_sum<KvT, D>(p.cache, it.b, it.g, it.w.past, bad_v & seen_nodes(p, it.b, t, it.w.nodes), col & ~3);
+              a += (col & 3) == 0 ? x.x : (col & 3) == 1 ? x.y : (col & 3) == 2 ? x.z : x.w;
+            }
+            if (complete) {
+              const int64_t at = ((static_cast<int64_t>(it.b) * p.T + t) * p.n_q_heads + it.g * p.group + h) * D + col;
+              static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(a);
+            } else {
+              p.part[(slot * RP + row) * D + col] = a;
             }
           }
           smx_sync();
-#pragma unroll 1
-          for (int i = tid; i < rows * units; i += kSmxThreads) {
-            const int row = i >> (3 + wide), u = i & (units - 1), t = (first + row) >> gs, h = (first + row) & (p.group - 1);
-            const float* src = stage + row * (32 << wide) + ((u ^ (row & 7)) << 2);
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int x = 0; x < 2 * F; ++x) {
-              const float4 v = *reinterpret_cast<const float4*>(src + x * per * (32 << wide));
-              a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-            }
-            if (!k8) fine = fine && fmaf(a.x, 0.f, fmaf(a.y, 0.f, fmaf(a.z, 0.f, a.w * 0.f))) == 0.f;
-            const int col = c0 + 4 * u;
-            if (bad_v != 0) {
-              const float4 x = bad_v_sum<KvT, D>(p.cache, it.b, it.g, it.w.past, bad_v & seen_nodes(p, it.b, t, it.w.nodes), col);
-              a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-            }
-            if (complete)
-              store_tree_row4(p, it.b, t, it.g * p.group + h, D, col, a, 1.f);
-            else
-              *reinterpret_cast<float4*>(p.part + (slot * RP + row) * D + col) = a;
-          }
-          if (k8 || mend || c0 + (32 << wide) < D) smx_sync();
         }
-        if (k8 || mend || smx_sync_and(fine)) break;
-        if (tid < D) s_nf[tid] = 0.f;
-        smx_sync();
-        if constexpr (!k8) nonfinite_columns<D>(p, it, tid, s_nf);
-        smx_sync();
       }
     }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
