@@ -161,6 +161,22 @@ def test_scales_and_scores_that_both_move(tts, kv, T, seed):  # noqa: F811
     assert ((out[0].cpu().double() - ref).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("kv", ["e4m3", "i8"])
+@pytest.mark.parametrize("q_dt", ["bf16", "f32"])
+@pytest.mark.parametrize("e", [-90, -40, 40, 60])
+def test_k_scales_and_queries_that_cancel(tts, kv, q_dt, e):  # noqa: F811
+    """K scales times 2^e under queries times 2^-e: the scores are ordinary ones."""
+    hq, hkv, d, past = 4, 2, 128, 900
+    T = 11
+    c = R.Cache(1, hkv, d, 1024, kv, 0, seed=8)
+    c.ks *= 2.0 ** e
+    c.to_device(tts, hq)
+    q = torch.randn(1, T, hq, d, generator=torch.Generator().manual_seed(T)).to(R.TORCH[q_dt]) * 2.0 ** -e
+    out, _ = run_tree(tts, c, q.cuda(), [past], [T], None, T, 0.1)
+    ref, mag = attend(c, q[0].double(), past, T, None, 0.1)
+    check_tree(out, ref[None], mag[None], [T])
+
+
 # ---------------------------------------------------------------------------
 # Attention: infinities in committed rows
 # ---------------------------------------------------------------------------
