@@ -205,9 +205,14 @@ _KV_CODES = {"f32": TTS_F32, "bf16": TTS_BF16, "i8": TTS_I8, "e4m3": TTS_E4M3,
 
 def kv_desc(B, n_q_heads, n_kv_heads, head_dim, capacity, kv_dtype="f32", window_quantum=256,
             paged=False, page_size=16, n_pages=0, block_table=None, flags=0) -> TtsKvDesc:
-    """A layer's cache.  kv_dtype: "f32", "bf16", "i8" or "e4m3", or the torch dtype (its name)."""
+    """A layer's cache.  kv_dtype: "f32", "bf16", "i8" or "e4m3", or the torch dtype (its name).
+    block_table: int32 [B or more rows][pages], entries of a row contiguous."""
     if kv_dtype not in _KV_CODES:
         raise ValueError("kv_dtype must be \"f32\", \"bf16\", \"i8\", \"e4m3\" or the torch dtype")
+    if paged and block_table is not None:
+        if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] < B or \
+                (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+            raise ValueError("block_table must be int32 with a contiguous row of page ids per stream")
     d = TtsKvDesc()
     d.B, d.n_q_heads, d.n_kv_heads, d.head_dim, d.capacity = B, n_q_heads, n_kv_heads, head_dim, capacity
     d.window_quantum = window_quantum
@@ -218,6 +223,7 @@ def kv_desc(B, n_q_heads, n_kv_heads, head_dim, capacity, kv_dtype="f32", window
     d.bt_stride = block_table.stride(0) if (paged and block_table is not None) else 0
     d.flags = flags
     d.block_table = block_table.data_ptr() if (paged and block_table is not None) else None
+    d.table_device = block_table.get_device() if (paged and block_table is not None) else None
     return d
 
 
@@ -507,6 +513,8 @@ def _cache_fits(cache: TtsKvCache, desc: TtsKvDesc):
     if cache.dtype != _KV_TORCH.get(desc.kv_dtype) or cache.shape != rows:
         raise ValueError(f"the descriptor's cache is {_KV_TORCH.get(desc.kv_dtype)} {rows}, "
                          f"the tensors are {cache.dtype} {cache.shape}")
+    if getattr(desc, "table_device", None) not in (None, cache.device_index):
+        raise ValueError("the block table and the cache must be on one device")
 
 
 def tts_rope_table_scaled(cs, max_pos, rot_dim, base, kind="none", factor=1.0, original_max_pos=1,

@@ -239,6 +239,23 @@ def test_descriptors_name_their_dtype(tts):
             tts.kv_desc(1, 16, 8, 128, 256, name)
 
 
+def test_descriptors_check_their_block_table(tts):
+    def desc(bt, B=2):
+        return tts.kv_desc(B, 16, 8, 128, 256, "i8", paged=True, page_size=16, n_pages=40, block_table=bt)
+    bt = torch.arange(32, dtype=torch.int32).reshape(2, 16)
+    assert desc(bt).bt_stride == 16 and desc(torch.zeros(3, 20, dtype=torch.int32)[:, :16]).bt_stride == 20
+    # 64-bit ids (read as pairs), too few rows (read past the end), other strides
+    for bad in (bt.long(), bt[:1], bt[0], bt.reshape(16, 2).t()):
+        with pytest.raises(ValueError, match="block_table"):
+            desc(bad)
+    k, sc = torch.zeros(40, 8, 16, 128, dtype=torch.int8), torch.zeros(40, 8, 16)
+    c, d = tts.kv_cache(k, k, sc, sc), desc(bt)
+    d.table_device = 1
+    rows = torch.zeros(4, 1024)
+    with pytest.raises(ValueError, match="one device"):
+        tts.tts_kv_write_rows(rows, rows, c, d, torch.zeros(2, dtype=torch.int32), 2)
+
+
 # The reference's own quantiser against facts of the formats.
 def test_reference_codes():
     assert R.E4M3.size == 127 and R.E4M3[-1] == 448.0 and R.E4M3[1] == 2.0 ** -9
