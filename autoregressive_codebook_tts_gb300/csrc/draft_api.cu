@@ -64,14 +64,14 @@ TreePlan tree_plan(const tts_kv_desc* d, int T, int q_dtype) {
   t.tile = t.tc ? 128 : 64;
   const int64_t items = static_cast<int64_t>(d->B) * d->n_kv_heads * t.n_rb;
   // Short windows are one CTA's each: the combine launch costs more than cutting them saves.  (Five
-  // nodes, one / eight streams, whole against cut.  Tensor cores, bf16: 250 rows 7.0 / 7.5 against
-  // 12.0 / 13.3 us, 500 rows 9.2 / 9.6 against 12.2 / 14.8, about 1.1 us a tile more.  CUDA cores,
+  // nodes, one / eight streams, whole against cut.  Tensor cores, bf16: 250 rows 7.1 / 7.6 against
+  // 12.2 / 13.5 us, 500 rows 9.2 / 9.8 against 12.4 / 14.9, about 1.1 us a tile more.  CUDA cores,
   // f32: 120 rows 12.9 / 13.0 against 12.4 / 15.6 us, 250 rows 22.8 / 23.0 against 14.5 / 23.3.)
   t.whole = d->capacity <= (t.tc ? 6 : 2) * t.tile;
   // An item's query rows, epilogue and partials in units of a quarter tile: two tiles' time, four
-  // with 128 query rows on the tensor cores.  (32 streams, 63 nodes, e4m3: 8 144 us, 20 136 us;
-  // one node, int8: 8 39.3 us, 14 40.2 us, 20 41.5 us; f32, 16 nodes: 8 126 us, 14 136 us;
-  // int8, 16 nodes, is the exception: 8 80.9 us, 14 77.7 us.)
+  // with 128 query rows on the tensor cores.  (32 streams, 63 nodes, e4m3: 8 146 us, 14 141 us, 18
+  // and 20 138 us; one node, int8: 8 38.3 us, 14 39.8 us, 20 41.0 us; f32, 8 streams of 16 nodes: 8
+  // 126 us, 14 137 us; 16 nodes gain 1 % with 14: int8 77.4 against 76.7 us, bf16 pages 32.5 against 32.2.)
   t.fixed = t.tc && t.rows == 128 ? 18 : 8;
   t.n_cta = t.whole ? static_cast<int>(items) : (t.tc ? 1 : 2) * sm_count();
   if (!t.whole) {

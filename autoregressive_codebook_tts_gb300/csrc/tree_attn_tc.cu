@@ -33,10 +33,10 @@
 // as four and a half with 128 rows.  All roles' loops share the instruction cache: the step
 // that rolled them (with one arrival a warp and elected issue) took int8 from 137 to 98 us.
 // 32 streams of 1500..4000 rows, one node: bf16 66 us (5.4 TB/s, 0.81 of the measured copy rate),
-// int8 71 us; 63 nodes: bf16 94 us, int8 133 us.
+// int8 69 us, e4m3 79 us; 63 nodes: bf16 95 us, int8 133 us, e4m3 137 us.
 //
 // The window is cut over one CTA per SM by cost (tree_plan.cuh).  Non-finite V entries of node
-// rows are handled as in tree_attn.cu.  Every wait is bounded; on expiry TTS_EFLAG_TIMEOUT is
+// rows are handled as in tree_attn.cu, those of committed rows behind the output passes.  Every wait is bounded; on expiry TTS_EFLAG_TIMEOUT is
 // set and the CTA winds down.
 #include <mutex>
 #include <type_traits>
@@ -512,7 +512,7 @@ __device__ __forceinline__ void load_tile(const TreeParams& p, const CUtensorMap
   }
 }
 
-// 128 x D codes of a staged tile to bf16 in the operand layout, by the widening threads: four
+// 128 x D codes of a staged tile to f16 in the operand layout, by the widening threads: four
 // 16-code vectors of a thread at a time.  Which thread takes which vector: a phase's eight lanes
 // read from every bank once, and what they write lies in eight different bank groups (the even
 // units of an even row and the odd places they take in an odd one).

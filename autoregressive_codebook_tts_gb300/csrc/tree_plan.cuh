@@ -55,7 +55,9 @@ __device__ __forceinline__ int cost_of(const TreeParams& p, int b0, int b1) {
   return sum;
 }
 
-// (a CTA's range may end past the axis: the ranges' ends stay below 2^32)
+// (The axis is shorter than 2^30: an item costs at most (capacity + 192) / 2 over its row blocks, and
+// the entry point refuses B * n_kv_heads * (capacity + 192) from 2^31 on.  The last
+// ranges may end past the axis, by fewer than n_cta units: all ends stay below 2^31.)
 __device__ __forceinline__ int cost_per_cta(int total, int n_cta) { return (total + n_cta - 1) / n_cta; }
 
 struct Piece {

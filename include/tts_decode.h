@@ -573,7 +573,9 @@ tts_status tts_kv_read_rows(const tts_kv_cache* cache, const tts_kv_desc* desc, 
  * cores, exact in q and K, with the softmax weights rounded where they meet V: to bf16 over a
  * bf16 cache; over an 8-bit one to f16 times the V row's scale, in a unit of each query row's own,
  * so that what a weight times its scale adds is lost only below 2^-25 of the largest such product
- * that the row sees.  Results do not depend on timing.
+ * that the row sees.  A weight whose row's maximum or unit moves later in the same tile is rounded a
+ * second time.  K's scales are below 2^64 in magnitude there (rows of larger ones may give NaN).
+ * Results do not depend on timing.
  * ------------------------------------------------------------------------- */
 #define TTS_MAX_TREE_NODES 64
 size_t tts_tree_attn_workspace_size(const tts_kv_desc* desc, int32_t T, int32_t q_dtype);
