@@ -1,4 +1,4 @@
-// Cache rows of drafted decoding: rows written into a cache (quantised for the 8-bit
+// Cache rows: rows written into a cache by position or by slot (quantised for the 8-bit
 // dtypes), read back from it, and moved inside it when a tree's path is accepted.
 //
 // All three only move bytes, so they are bound by HBM on long inputs and by launch latency
@@ -13,6 +13,7 @@
 // codes by double division and narrower lanes.
 #include "cache_view.cuh"
 #include "draft_kernels.h"
+#include "serve_kernels.h"
 
 namespace tts {
 namespace {
@@ -143,6 +144,37 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const KvRowsParam
     }
   }
   const int64_t row = cache_row(c, b, g, live ? static_cast<int>(pos) : 0, live ? page : 0);
+  write_head_row<KvT, VE, LPR>(c.k, c.k_scale, row, D, lr, live, xk);
+  write_head_row<KvT, VE, LPR>(c.v, c.v_scale, row, D, lr, live, xv);
+}
+
+// The same by slot: head row i is row i / n_kv_heads of k and v, for cache row slot[r] of kv head
+// i % n_kv_heads.
+template <typename SrcT, typename KvT, int D>
+__global__ void __launch_bounds__(kWarps * 32) kv_slots_kernel(const KvSlotsParams p) {
+  constexpr int VE = Src<SrcT>::kVec, LPR = D / VE, RPW = 32 / LPR;
+  grid_wait();
+  grid_launch_dependents();
+  const CacheView& c = p.cache;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lr = lane % LPR;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * RPW + lane / LPR;
+  const int64_t r = i / c.n_kv_heads;
+  const int g = static_cast<int>(i - r * c.n_kv_heads);
+  int64_t slot = r < p.rows ? __ldcg(p.slot + r) : -1;
+  float xk[VE] = {}, xv[VE] = {};
+  if (slot >= p.n_slots) {
+    if (g == 0 && lr == 0) set_err(p.err, TTS_EFLAG_POS_RANGE);
+    slot = -1;
+  }
+  const bool live = slot >= 0;
+  int64_t row = 0;
+  if (live) {
+    const int64_t src = r * p.row_stride + static_cast<int64_t>(g) * D + lr * VE;
+    Src<SrcT>::load(p.k, src, xk);
+    Src<SrcT>::load(p.v, src, xv);
+    const int64_t page = c.paged ? slot >> c.page_shift : slot / p.page_rows;
+    row = (page * c.n_kv_heads + g) * p.page_rows + (slot - page * p.page_rows);
+  }
   write_head_row<KvT, VE, LPR>(c.k, c.k_scale, row, D, lr, live, xk);
   write_head_row<KvT, VE, LPR>(c.v, c.v_scale, row, D, lr, live, xv);
 }
@@ -294,6 +326,26 @@ cudaError_t launch_write_kv(const KvRowsParams& p, cudaStream_t s) {
   }
 }
 
+template <typename SrcT, typename KvT, int D>
+cudaError_t launch_slots(const KvSlotsParams& p, cudaStream_t s) {
+  constexpr int per = kWarps * (32 / (D / Src<SrcT>::kVec));
+  const int64_t n = static_cast<int64_t>(p.rows) * p.cache.n_kv_heads;
+  return launch_pdl(kv_slots_kernel<SrcT, KvT, D>, dim3(static_cast<unsigned>((n + per - 1) / per)), dim3(kWarps * 32), 0, s, p);
+}
+template <typename SrcT, typename KvT>
+cudaError_t launch_slots_d(const KvSlotsParams& p, cudaStream_t s) {
+  return p.head_dim == 64 ? launch_slots<SrcT, KvT, 64>(p, s) : launch_slots<SrcT, KvT, 128>(p, s);
+}
+template <typename SrcT>
+cudaError_t launch_slots_kv(const KvSlotsParams& p, cudaStream_t s) {
+  switch (p.kv_dtype) {
+    case TTS_F32: return launch_slots_d<SrcT, float>(p, s);
+    case TTS_BF16: return launch_slots_d<SrcT, __nv_bfloat16>(p, s);
+    case TTS_I8: return launch_slots_d<SrcT, CodeI8>(p, s);
+    default: return launch_slots_d<SrcT, CodeE4m3>(p, s);
+  }
+}
+
 template <typename KvT, typename OutT, int D>
 cudaError_t launch_read(const KvRowsParams& p, cudaStream_t s) {
   constexpr int RPW = 32 / (D / LaneRow<KvT>::kVec);
@@ -404,6 +456,10 @@ __global__ void __launch_bounds__(32) commit_kernel(const CommitParams p) {
 
 cudaError_t launch_kv_write(const KvRowsParams& p, cudaStream_t s) {
   return p.row_bf16 ? launch_write_kv<__nv_bfloat16>(p, s) : launch_write_kv<float>(p, s);
+}
+
+cudaError_t launch_kv_slots(const KvSlotsParams& p, cudaStream_t s) {
+  return p.row_bf16 ? launch_slots_kv<__nv_bfloat16>(p, s) : launch_slots_kv<float>(p, s);
 }
 
 cudaError_t launch_kv_read(const KvRowsParams& p, cudaStream_t s) {

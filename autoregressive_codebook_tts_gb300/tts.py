@@ -27,6 +27,7 @@ TTS_F32, TTS_BF16, TTS_Q8_0, TTS_I8, TTS_E4M3 = 0, 1, 2, 3, 4
 Q8_0_BLOCK, Q8_0_BYTES = 32, 34  # entries and bytes of a Q8_0 block
 TTS_MAX_TABLES = 16
 TTS_MAX_TREE_NODES = 64
+TTS_MAX_NORM_WIDTH, TTS_MAX_ADAPTER_RANK, TTS_MAX_PLAN_STREAMS = 16384, 128, 4096
 TTS_KV_PREFETCH_BEFORE_WAIT = 1
 
 EFLAG_ID_RANGE = 1
@@ -57,6 +58,11 @@ EXPORTED = [
     "tts_tree_attn_workspace_size",
     "tts_tree_attn",
     "tts_tree_commit",
+    "tts_add_rms_norm",
+    "tts_project_workspace_size",
+    "tts_project_rows",
+    "tts_page_plan",
+    "tts_kv_write_slots",
 ]
 
 
@@ -92,6 +98,15 @@ class TtsKvCache(ctypes.Structure):
     """Built by kv_cache, which also notes what the tensors behind it are."""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+    def get_device(self):
+        return self.device_index
+
+
+class TtsAdapters(ctypes.Structure):
+    """Built by adapters, which also notes what the tensors behind it are."""
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("rank", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("n_adapters", ctypes.c_int32), ("rank_max", ctypes.c_int32)]
 
     def get_device(self):
         return self.device_index
@@ -144,6 +159,13 @@ _sigs = {
                        _P, _P, _I32, _F, _P, _P, _SZ, _P, _P], _I32),
     "tts_tree_commit": ([ctypes.POINTER(TtsKvCache), ctypes.POINTER(TtsKvDesc), _P, _P, _I64, _P,
                          _I32, _P, _P], _I32),
+    "tts_add_rms_norm": ([_P, _I64, _I32, _P, _I64, _I32, _P, _I64, _P, _F, _I32, _I32, _P, _I64, _I32, _P, _P], _I32),
+    "tts_project_workspace_size": ([_I32, _I32, _I32, _I32, ctypes.POINTER(TtsAdapters)], _SZ),
+    "tts_project_rows": ([_P, _I64, _I32, _P, _P, _P, _I32, _I32, ctypes.POINTER(TtsAdapters), _P, _P, _I32, _I32,
+                          _P, _I64, _I32, _P, _SZ, _P, _P], _I32),
+    "tts_page_plan": ([ctypes.POINTER(TtsKvDesc), _P, _P, _P, _P, _P, _I32, _I32, _P, _P, _P, _P, _P, _P, _P], _I32),
+    "tts_kv_write_slots": ([_P, _P, _I32, _I64, ctypes.POINTER(TtsKvCache), ctypes.POINTER(TtsKvDesc), _P, _I32, _P,
+                            _P], _I32),
 }
 for _name, (_args, _ret) in _sigs.items():
     _fn = getattr(_lib, _name)
@@ -656,6 +678,158 @@ def tts_tree_commit(cache: TtsKvCache, desc: TtsKvDesc, n_past, path, n_accept, 
     _check(_lib.tts_tree_commit(ctypes.byref(cache), ctypes.byref(desc), _p(n_past), _p(path),
                                 path.stride(0) if desc.B > 1 else T, _p(n_accept), T, _p(err_flag), st),
            "tts_tree_commit")
+
+
+# ---------------------------------------------------------------------------
+# One step of many requests
+# ---------------------------------------------------------------------------
+_ROW8_CODES = {torch.float32: TTS_F32, torch.bfloat16: TTS_BF16, torch.float8_e4m3fn: TTS_E4M3}
+_X_CODES = {"bf16": TTS_BF16, "e4m3": TTS_E4M3, torch.bfloat16: TTS_BF16, torch.float8_e4m3fn: TTS_E4M3}
+
+
+def _rows_of(t, what, codes, shape):
+    """Checks a view of `shape` whose rows are contiguous; returns (dtype code, stride)."""
+    code = codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} must be one of {', '.join(str(c) for c in codes if not isinstance(c, str))}")
+    if t.shape != shape or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a [{shape[0]}, {shape[1]}] view of contiguous rows")
+    # one row has no stride of its own: any that keeps it aligned
+    return code, t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
+
+
+def tts_add_rms_norm(x, residual, sum_out, gamma, eps, out, out_scale=None, stream=None):
+    """residual + x into sum_out (None: not stored; may be residual), and the RMS norm of that sum
+    times gamma into out, [rows, n] each: x, residual and sum_out float32 or bfloat16, out
+    float32, bfloat16 or float8_e4m3fn with out_scale [rows].  residual None: the norm of x."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, n]")
+    n, width = x.shape
+    dt, xs = _rows_of(x, "x", _ROW_CODES, x.shape)
+    odt, os_ = _rows_of(out, "out", _ROW8_CODES, x.shape)
+    rdt = rs = ss = 0
+    if residual is not None:
+        rdt, rs = _rows_of(residual, "residual", _ROW_CODES, x.shape)
+        if sum_out is not None:
+            sdt, ss = _rows_of(sum_out, "sum_out", _ROW_CODES, x.shape)
+            if sdt != rdt:
+                raise ValueError("sum_out must be of residual's dtype")
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    if (odt == TTS_E4M3) != (out_scale is not None):
+        raise ValueError("float8_e4m3fn outputs, and only they, take out_scale")
+    _ints(gamma, "gamma", width, torch.float32)
+    _ints(out_scale, "out_scale", n, torch.float32)
+    st = _on_device(stream, x, residual, sum_out, gamma, out, out_scale)
+    _check(_lib.tts_add_rms_norm(_p(x), xs, dt, _p(residual), rs, rdt, _p(sum_out), ss, _p(gamma), float(eps), n, width,
+                                 _p(out), os_, odt, _p(out_scale), st), "tts_add_rms_norm")
+
+
+def adapters(a, b, rank=None, scale=None) -> TtsAdapters:
+    """A pool of low-rank adapters of a projection [n, k]: a [adapters, rank_max, k] and b
+    [adapters, n, rank_max], bfloat16; rank int32 and scale float32 [adapters] (None: rank_max and
+    1 each).  The caller keeps the tensors alive."""
+    for t in (a, b):
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_contiguous():
+            raise ValueError("a and b must be contiguous bfloat16 of three dimensions")
+    if a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+        raise ValueError("a is [adapters, rank_max, k], b [adapters, n, rank_max]")
+    _ints(rank, "rank", a.shape[0])
+    _ints(scale, "scale", a.shape[0], torch.float32)
+    for t in (b, rank, scale):
+        if t is not None and t.device != a.device:
+            raise ValueError("the adapters' tensors must be on one device")
+    p = TtsAdapters(a.data_ptr(), b.data_ptr(), _p(rank), _p(scale), a.shape[0], a.shape[1])
+    p.n, p.k, p.device_index = b.shape[1], a.shape[2], a.get_device()
+    return p
+
+
+def tts_project_workspace_size(rows, n, k, x_dtype, adapters=None) -> int:
+    if x_dtype not in _X_CODES:
+        raise ValueError("x_dtype must be \"bf16\", \"e4m3\" or the torch dtype")
+    ad = None if adapters is None else ctypes.byref(adapters)
+    return int(_lib.tts_project_workspace_size(rows, n, k, _X_CODES[x_dtype], ad))
+
+
+def project_workspace(rows, n, k, x_dtype, adapters=None, device="cuda"):
+    """Allocate (through torch) a workspace for projections of up to `rows` rows."""
+    return torch.empty(max(tts_project_workspace_size(rows, n, k, x_dtype, adapters), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def tts_project_rows(x, w, out, ws, x_scale=None, w_scale=None, adapters=None, stream_adapter=None,
+                     row_stream=None, err_flag=None, stream=None):
+    """out [rows, n] = x [rows, k] times w [n, k] transposed, and to each row its request's
+    adapter: row r is of request row_stream[r] (None: r; negative: the row is left as it was),
+    which has adapter stream_adapter[request] (negative: none).  x and w bfloat16, or
+    float8_e4m3fn with x_scale [rows] and w_scale [n]; out float32 or bfloat16."""
+    if x.dim() != 2 or w.dim() != 2 or not w.is_contiguous() or w.dtype != x.dtype or w.shape[1] != x.shape[1]:
+        raise ValueError("x is [rows, k], w contiguous [n, k], of one dtype")
+    rows, k = x.shape
+    n = w.shape[0]
+    dt, xs = _rows_of(x, "x", _X_CODES, x.shape)
+    odt, os_ = _rows_of(out, "out", _ROW_CODES, (rows, n))
+    if (dt == TTS_E4M3) != (x_scale is not None) or (dt == TTS_E4M3) != (w_scale is not None):
+        raise ValueError("float8_e4m3fn rows and weights, and only they, take x_scale and w_scale")
+    _ints(x_scale, "x_scale", rows, torch.float32)
+    _ints(w_scale, "w_scale", n, torch.float32)
+    _ints(row_stream, "row_stream", rows)
+    n_streams = 0
+    if adapters is not None:
+        if adapters.n != n or adapters.k != k:
+            raise ValueError("the adapters are of another projection")
+        if stream_adapter is None:
+            raise ValueError("adapters need stream_adapter")
+        _ints(stream_adapter, "stream_adapter", rows if row_stream is None else 1)
+        n_streams = stream_adapter.numel()
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    _ints(err_flag, "err_flag", 1)
+    st = _on_device(stream, x, w, out, ws, x_scale, w_scale, adapters, stream_adapter, row_stream, err_flag)
+    _check(_lib.tts_project_rows(_p(x), xs, dt, _p(x_scale), _p(w), _p(w_scale), n, k,
+                                 None if adapters is None else ctypes.byref(adapters), _p(row_stream),
+                                 _p(stream_adapter), n_streams, rows, _p(out), os_, odt, _p(ws),
+                                 0 if ws is None else ws.numel() * ws.element_size(), _p(err_flag), st),
+           "tts_project_rows")
+
+
+def tts_page_plan(desc: TtsKvDesc, block_table, free_pages, n_free, n_past, n_new, n_rows, row_start, row_stream,
+                  row_pos, row_slot, T=0, err_flag=None, stream=None):
+    """Pages and row maps of a step: block_table (desc's own, updated), free_pages [n_pages] and
+    n_free [1] (updated), n_past and n_new [B]; n_rows [B], row_start [B + 1], and row_stream,
+    row_pos and row_slot (int64) of max_rows = row_stream's entries each.  T 0: packed rows,
+    else T rows a stream (include/tts_decode.h states the rules)."""
+    if not desc.paged or block_table.data_ptr() != desc.block_table:
+        raise ValueError("block_table must be the descriptor's own, of a paged cache")
+    for t, what, n in ((free_pages, "free_pages", desc.n_pages), (n_free, "n_free", 1), (n_past, "n_past", desc.B),
+                       (n_new, "n_new", desc.B), (n_rows, "n_rows", desc.B), (row_start, "row_start", desc.B + 1)):
+        _ints(t, what, n)
+    max_rows = row_stream.numel()
+    _ints(row_stream, "row_stream", max_rows)
+    _ints(row_pos, "row_pos", max_rows)
+    _ints(row_slot, "row_slot", max_rows, torch.int64)
+    _ints(err_flag, "err_flag", 1)
+    st = _on_device(stream, block_table, free_pages, n_free, n_past, n_new, n_rows, row_start, row_stream, row_pos,
+                    row_slot, err_flag)
+    _check(_lib.tts_page_plan(ctypes.byref(desc), _p(block_table), _p(free_pages), _p(n_free), _p(n_past), _p(n_new), T,
+                              max_rows, _p(n_rows), _p(row_start), _p(row_stream), _p(row_pos), _p(row_slot),
+                              _p(err_flag), st), "tts_page_plan")
+
+
+def tts_kv_write_slots(k, v, cache: TtsKvCache, desc: TtsKvDesc, row_slot, err_flag=None, stream=None):
+    """k, v [rows, n_kv_heads * head_dim] into the cache at row_slot [rows] (int64; negative: the
+    row is skipped), converted or quantised as by tts_kv_write_rows."""
+    kd = desc.n_kv_heads * desc.head_dim
+    dt, ks = _rows(k, "k", kd)
+    vdt, vs = _rows(v, "v", kd)
+    if vdt != dt or vs != ks or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must share dtype, stride and row count")
+    _cache_fits(cache, desc)
+    _ints(row_slot, "row_slot", k.shape[0], torch.int64)
+    _ints(err_flag, "err_flag", 1)
+    st = _on_device(stream, k, v, cache, row_slot, err_flag)
+    _check(_lib.tts_kv_write_slots(_p(k), _p(v), dt, ks, ctypes.byref(cache), ctypes.byref(desc), _p(row_slot),
+                                   k.shape[0], _p(err_flag), st), "tts_kv_write_slots")
 
 
 def default_scale(head_dim: int) -> float:

@@ -67,8 +67,9 @@ extern "C" {
  * inside the library and returns TTS_OK, or TTS_ERR_ABI for a V below the minimum or
  * above the current version.  (ABI 2 added tts_tables.dtype; ABI 3 added the `draw`
  * argument of tts_sample, tts_abi_check and Q8_0 codebook tables; ABI 4 added the calls
- * from tts_rope_table_scaled on, and changed no earlier one.) */
-#define TTS_ABI_VERSION 4
+ * from tts_rope_table_scaled on, ABI 5 those from tts_add_rms_norm on; both changed no
+ * earlier one.) */
+#define TTS_ABI_VERSION 5
 #define TTS_ABI_MIN_VERSION 3
 int32_t tts_abi_version(void);
 int32_t tts_abi_min_version(void);
@@ -597,6 +598,132 @@ tts_status tts_tree_attn(const void* q, int32_t q_dtype, int64_t q_stride, const
 tts_status tts_tree_commit(const tts_kv_cache* cache, const tts_kv_desc* desc, const int32_t* n_past,
                            const int32_t* path, int64_t path_stride, const int32_t* n_accept, int32_t T,
                            int32_t* err_flag, void* stream);
+
+/* ===========================================================================
+ * One step of many requests: rows of requests of different lengths, each with an adapter of its
+ * own, over a paged cache whose pages come and go.  The paper has no counterpart.  A step is:
+ * tts_page_plan (from the requests' lengths: pages, and every row's request, position and cache
+ * slot), then per layer tts_add_rms_norm, tts_project_rows, tts_rope_rows at row_pos,
+ * tts_kv_write_slots and an attention over the same block table.  Row counts are fixed on the
+ * host and rows without a request are marked on the device, so that a step can be captured.
+ * The conventions above hold (device pointers, stream order, status, err_flag, alignment).
+ * =========================================================================== */
+
+/* ---------------------------------------------------------------------------
+ * The residual's addition and the norm of the sum, row by row:
+ *   h = residual + x  (one f32 addition, rounded to res_dtype: the value that is stored)
+ *   y = h * (mean(h^2) + eps)^(-1/2) * gamma  (f32)
+ * and y as out_dtype: f32; bf16, rounded to nearest even; or E4M3 codes with a scale a row,
+ * s = max|y| * (1 / 448) in f32, code = the code nearest to the exact quotient y / s, ties to
+ * even (s = 0: codes 0; a row with a NaN or an infinity in y: scale NaN, codes 0), as
+ * tts_kv_write_rows rounds a cache row and tts_project_rows takes its rows.
+ *   x: device rows of x_dtype (f32 or bf16), row r at x + r*x_stride elements.
+ *   residual: rows of res_dtype (f32 or bf16), or NULL: h = x, and sum_out must be NULL too.
+ *   sum_out: rows of res_dtype for h, or NULL; may be residual itself (same stride).
+ *   gamma: device f32 [n].  n: a multiple of 8, at most TTS_MAX_NORM_WIDTH.  eps >= 0.
+ *   out: rows of out_dtype; may be x itself (same type and stride).  out_scale: device f32
+ *        [rows] for E4M3, else NULL.  Row strides keep rows 16-byte aligned.  Other overlaps are
+ *        not allowed.
+ * ------------------------------------------------------------------------- */
+#define TTS_MAX_NORM_WIDTH 16384
+tts_status tts_add_rms_norm(const void* x, int64_t x_stride, int32_t x_dtype, const void* residual,
+                            int64_t res_stride, int32_t res_dtype, void* sum_out, int64_t sum_stride,
+                            const float* gamma, float eps, int32_t rows, int32_t n, void* out,
+                            int64_t out_stride, int32_t out_dtype, float* out_scale, void* stream);
+
+/* A pool of low-rank adapters of one projection [n][k].  Adapter i of rank r_i adds
+ * scale[i] * (x A_i^T) B_i^T to a row x: A_i is the first r_i rows of a[i], B_i the first r_i
+ * columns of b[i].  What lies behind them in the pool is never used, whatever it holds. */
+typedef struct {
+  const void* a;        /* device bf16 [n_adapters][rank_max][k] */
+  const void* b;        /* device bf16 [n_adapters][n][rank_max] */
+  const int32_t* rank;  /* device int32 [n_adapters], 0..rank_max; NULL: rank_max each */
+  const float* scale;   /* device f32 [n_adapters]; NULL: 1 each */
+  int32_t n_adapters;   /* >= 1 */
+  int32_t rank_max;     /* a multiple of 8, 8..TTS_MAX_ADAPTER_RANK */
+} tts_adapters;
+#define TTS_MAX_ADAPTER_RANK 128
+
+/* ---------------------------------------------------------------------------
+ * Rows of many requests through one shared projection, with every request's own adapter:
+ *   out[r] = x[r] W^T + scale_a (x[r] A_a^T) B_a^T,   a = stream_adapter[s], s = row_stream[r]
+ * x and W are bf16, or both E4M3 codes with a scale a row (x[r] stands for x_scale[r] * codes,
+ * W's row n for w_scale[n] * codes).  Products accumulate in f32; x A^T is held in f32 (where
+ * many rows share an adapter it meets B_a as three bf16 parts, which hold all its bits); the
+ * sum is rounded to out_dtype once.
+ *   x: device rows of x_dtype, row r at x + r*x_stride elements; w: dense [n][k].
+ *   x_scale [rows], w_scale [n]: device f32 for E4M3, else NULL.
+ *   k: a multiple of 8 (bf16) or 16 (E4M3), at most 65536; n: at most 2^20; rows at most 2^20.
+ *   adapters: NULL for none (then row_stream only marks rows).  b rows of the pool are [n].
+ *   row_stream: device int32 [rows], or NULL: row r is request r's.  A negative entry marks a
+ *        row without a request: its out row is left as it was.  Any order is allowed; rows of a
+ *        request that lie together are the fastest.
+ *   stream_adapter: device int32 [n_streams]; negative: the shared projection alone.
+ *   A request outside [0, n_streams), or an adapter at or above n_adapters, sets
+ *        TTS_EFLAG_ID_RANGE and counts as one without an adapter; a rank outside
+ *        [0, rank_max] is clamped and sets TTS_EFLAG_NVALID.
+ *   out: rows of out_dtype (f32 or bf16), row r at out + r*out_stride elements; must not
+ *        overlap an input.
+ *   workspace: at least tts_project_workspace_size() bytes, 256-byte aligned; needs no
+ *        clearing and holds nothing between calls.  Calls that overlap in time on the GPU must
+ *        not share one.
+ * A NaN or an infinity in a row, or in an adapter, reaches that row, or the rows of that adapter,
+ * alone.  Results do not depend on timing.
+ * ------------------------------------------------------------------------- */
+size_t tts_project_workspace_size(int32_t rows, int32_t n, int32_t k, int32_t x_dtype,
+                                  const tts_adapters* adapters);
+
+tts_status tts_project_rows(const void* x, int64_t x_stride, int32_t x_dtype, const float* x_scale,
+                            const void* w, const float* w_scale, int32_t n, int32_t k,
+                            const tts_adapters* adapters, const int32_t* row_stream,
+                            const int32_t* stream_adapter, int32_t n_streams, int32_t rows, void* out,
+                            int64_t out_stride, int32_t out_dtype, void* workspace, size_t ws_bytes,
+                            int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages and row maps of one step, on the device.  desc is a paged cache of B streams; block_table
+ * is its table, written here.  An entry outside [0, n_pages) holds no page (-1 is written where a
+ * page is taken away).  free_pages[0 .. *n_free) lists the pages that nobody holds.  In order:
+ *   1. streams with n_new[b] < 0 have ended: the pages of their table row, in ascending order of
+ *      streams and entries, go to the end of the list, and the entries become -1;
+ *   2. a stream with n_new[b] > 0 wants rows at positions n_past[b] + t, t < n_new[b].  Entries
+ *      of its table row under them that hold no page need one.  Streams in ascending order are
+ *      granted their rows while the pages they need, summed, are in the list, and (T = 0) while
+ *      their rows, summed, fit max_rows; one that asks for no page needs only its rows to fit.
+ *      What is refused gets no rows and no pages, and sets TTS_EFLAG_PAGE (pages) or
+ *      TTS_EFLAG_NVALID (rows; also n_past < 0, positions past the capacity, and with T > 0
+ *      n_new > T).  The page for the j-th entry in need (ascending streams and entries) is
+ *      the j-th last of the list;
+ *   3. n_rows[b] = the rows granted.  With T = 0 rows are packed: stream b's are
+ *      row_start[b] .. row_start[b + 1).  With T > 0 stream b's are b*T .. b*T + n_rows[b] and
+ *      row_start[b] = b*T (max_rows = B*T).  For each row: row_stream = b, row_pos = its position,
+ *      row_slot = page * page_size + position within the page; a row of no stream has
+ *      row_stream -1, row_pos 0 and row_slot -1.
+ * n_past is read only: add n_rows (or the accepted part) to it afterwards; a stream keeps pages
+ * that it was given, so rows that were not accepted need no new ones in the next step.
+ *   free_pages: device int32 [n_pages]; n_free: device int32 [1], clamped into [0, n_pages] (then
+ *        TTS_EFLAG_NVALID).  A page that the list cannot hold any more is dropped, and a listed
+ *        page outside [0, n_pages) gives rows without a slot (both TTS_EFLAG_PAGE).
+ *   n_past, n_new: device int32 [B].  n_rows: device int32 [B], row_start [B + 1].
+ *   row_stream, row_pos: device int32 [max_rows]; row_slot: device int64 [max_rows].
+ * B at most TTS_MAX_PLAN_STREAMS, max_rows at most 2^24.
+ * ------------------------------------------------------------------------- */
+#define TTS_MAX_PLAN_STREAMS 4096
+tts_status tts_page_plan(const tts_kv_desc* desc, int32_t* block_table, int32_t* free_pages,
+                         int32_t* n_free, const int32_t* n_past, const int32_t* n_new, int32_t T,
+                         int32_t max_rows, int32_t* n_rows, int32_t* row_start, int32_t* row_stream,
+                         int32_t* row_pos, int64_t* row_slot, int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rows into the cache by slot: row r of k and v goes to cache row row_slot[r] of every kv head,
+ * converted or quantised as tts_kv_write_rows does.  Slot s is position s % P of page s / P
+ * (contiguous caches: of stream s / P, P = capacity; block_table is not read).  A negative slot
+ * skips the row; one at or past the cache's end skips it and sets TTS_EFLAG_POS_RANGE.  Two rows
+ * must not have the same slot.  rows at most 2^24; the other arguments as in tts_kv_write_rows.
+ * ------------------------------------------------------------------------- */
+tts_status tts_kv_write_slots(const void* k, const void* v, int32_t dtype, int64_t row_stride,
+                              const tts_kv_cache* cache, const tts_kv_desc* desc, const int64_t* row_slot,
+                              int32_t rows, int32_t* err_flag, void* stream);
 
 #ifdef __cplusplus
 }
