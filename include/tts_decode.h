@@ -648,8 +648,7 @@ typedef struct {
  * Rows of many requests through one shared projection, with every request's own adapter:
  *   out[r] = x[r] W^T + scale_a (x[r] A_a^T) B_a^T,   a = stream_adapter[s], s = row_stream[r]
  * x and W are bf16, or both E4M3 codes with a scale a row (x[r] stands for x_scale[r] * codes,
- * W's row n for w_scale[n] * codes).  Products accumulate in f32; x A^T is held in f32 (where
- * many rows share an adapter it meets B_a as three bf16 parts, which hold all its bits); the
+ * W's row n for w_scale[n] * codes).  Products accumulate in f32 and x A^T is held in f32; the
  * sum is rounded to out_dtype once.
  *   x: device rows of x_dtype, row r at x + r*x_stride elements; w: dense [n][k].
  *   x_scale [rows], w_scale [n]: device f32 for E4M3, else NULL.
@@ -662,8 +661,8 @@ typedef struct {
  *   A request outside [0, n_streams), or an adapter at or above n_adapters, sets
  *        TTS_EFLAG_ID_RANGE and counts as one without an adapter; a rank outside
  *        [0, rank_max] is clamped and sets TTS_EFLAG_NVALID.
- *   out: rows of out_dtype (f32 or bf16), row r at out + r*out_stride elements; must not
- *        overlap an input.
+ *   out: rows of out_dtype (f32 or bf16), row r at out + r*out_stride elements (any stride from n
+ *        on); must not overlap an input.
  *   workspace: at least tts_project_workspace_size() bytes, 256-byte aligned; needs no
  *        clearing and holds nothing between calls.  Calls that overlap in time on the GPU must
  *        not share one.

@@ -71,7 +71,7 @@ def test_project_rows_refuses(tts):
                 dict(os_=44), dict(ns=0), dict(ad=pool(tts, n=0)), dict(ad=pool(tts, r=0)), dict(ad=pool(tts, r=12)),
                 dict(ad=pool(tts, r=136)), dict(ad=pool(tts, n=(1 << 31) - 1))):
         assert call(**bad) == SHAPE, bad
-    for bad in (dict(x=24), dict(w=40), dict(o=72), dict(xs=68), dict(os_=50), dict(k=60), dict(rs=8), dict(sa=8),
+    for bad in (dict(x=24), dict(w=40), dict(o=72), dict(xs=68), dict(k=60), dict(rs=8), dict(sa=8),
                 dict(ad=pool(tts, a=24)), dict(ad=pool(tts, b=24)), dict(ad=pool(tts, rank=8)), dict(ad=pool(tts, scale=8)),
                 dict(dt=4, sx=16, sw=16, k=72, xs=80), dict(dt=4, sx=8, sw=16), dict(dt=4, sx=16, sw=16, xs=72), dict(ws=128)):
         assert call(**bad) == ALIGN, bad
