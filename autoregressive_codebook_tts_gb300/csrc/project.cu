@@ -17,21 +17,13 @@
 //     is never rounded, a request's adapter never meets another request's row, and what lies behind
 //     an adapter's rank is not used.
 #include <map>
-#include <mutex>
 #include <tuple>
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include "cache_view.cuh"
-#include "checks.h"
-#include "serve_kernels.h"
+#include "project_parts.cuh"
 
 namespace tts {
 namespace {
 
-constexpr int kM = 128;               // rows of W a tile
-constexpr int kRowBytes = 128;        // bytes of K a swizzled row holds
 constexpr int kWChunk = kM * kRowBytes;
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;
@@ -39,7 +31,7 @@ constexpr int kThreads = 192;         // warps 0-3 epilogue, 4 copies, 5 product
 constexpr int kEpi = 128;
 constexpr int kTmemCols = 512;
 constexpr int kRedLd = kM + 16;       // floats between the rows of a partial
-constexpr int kRingVecs = 16;         // 16-byte pieces of B a thread has room for
+constexpr int kMaxAhead = 8;           // runs of B rows in flight at most
 
 struct Plan {
   int nb, nbr;          // x rows a tile (a multiple of 16), and that rounded up to 32
@@ -49,173 +41,42 @@ struct Plan {
   int n_rt, n_nt, n_tiles;
   int n_chunks;         // 128-byte columns of K (the last may be short)
   int flat;             // K is not whole columns: one copy each
-  int ring;             // runs of B rows in flight
+  int ring;             // 16-byte pieces of B a thread has room for
+  int parts;            // bf16 parts of v that meet B on the tensor cores (0: none do)
   int v_off, b_off, bar_off, smem;
   int vec_out;          // out rows take 16-byte (f32) or 8-byte (bf16) stores
 };
 
-// ---------------------------------------------------------------------------
-// The adapter of row r: -1 none, -2 the row is of no request.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ int row_adapter(const ProjectParams& p, int r, int* bad) {
-  const int s = p.row_stream == nullptr ? r : __ldcg(p.row_stream + r);
-  if (s < 0) return -2;
-  if (p.ad.n_adapters == 0) return -1;
-  if (s >= p.n_streams) {
-    *bad |= TTS_EFLAG_ID_RANGE;
-    return -1;
-  }
-  const int a = __ldcg(p.stream_adapter + s);
-  if (a >= p.ad.n_adapters) {
-    *bad |= TTS_EFLAG_ID_RANGE;
-    return -1;
-  }
-  return a < 0 ? -1 : a;
-}
-__device__ __forceinline__ int adapter_rank(const ProjectParams& p, int a, int* bad) {
-  const int r = p.ad.rank == nullptr ? p.ad.rank_max : __ldcg(p.ad.rank + a);
-  if (r < 0 || r > p.ad.rank_max) *bad |= TTS_EFLAG_NVALID;
-  return min(max(r, 0), p.ad.rank_max);
-}
-
-// ---------------------------------------------------------------------------
-// v[r][j] = scale_a x_scale[r] sum_k x[r][k] A_a[j][k], a warp a rank of a row; zeros from the rank
-// to the next multiple of eight, up to where the epilogue reads.
-// ---------------------------------------------------------------------------
-constexpr int kShrinkWarps = 8;
-
-// eight entries of a row
-__device__ __forceinline__ void entries8(const uint8_t* x, int64_t i, float (&f)[8]) {
-  const uint2 v = __ldg(reinterpret_cast<const uint2*>(x + i));
-  float a[4], b[4];
-  E4m3Code::values(v.x, a);
-  E4m3Code::values(v.y, b);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[e] = a[e];
-    f[4 + e] = b[e];
+// All but the newest n copy groups of this thread have landed.
+__device__ __forceinline__ void cp_async_wait(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
   }
 }
-__device__ __forceinline__ void entries8(const __nv_bfloat16* x, int64_t i, float (&f)[8]) {
-  unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(x + i)), f);
+// Neighbouring blocks of 16 rows that share an adapter.
+struct BlockRun {
+  int ad, first, count;   // blocks [first, first + count) of the tile
+};
+// The next run of blocks from `at` on with one adapter; lane b of the warp holds block b's adapter
+// (negative: none, or several).  Converged warp; false when there is none.
+__device__ __forceinline__ bool next_run(int mine, int blocks, int at, BlockRun& run) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t some = __ballot_sync(kFull, mine >= 0 && lane >= at && lane < blocks);
+  if (some == 0) return false;
+  run.first = __ffs(static_cast<int>(some)) - 1;
+  run.ad = __shfl_sync(kFull, mine, run.first);
+  const uint32_t other = __ballot_sync(kFull, (mine != run.ad || lane >= blocks) && lane > run.first);
+  run.count = (other != 0 ? __ffs(static_cast<int>(other)) - 1 : 32) - run.first;
+  return true;
 }
 
-template <typename X>
-__global__ void __launch_bounds__(kShrinkWarps * 32) shrink_kernel(const ProjectParams p) {
-  grid_wait();
-  grid_launch_dependents();
-  const int r = blockIdx.x, lane = threadIdx.x & 31, j = blockIdx.y * kShrinkWarps + (threadIdx.x >> 5);
-  int bad = 0;
-  const int a = row_adapter(p, r, &bad);
-  const int rank = a >= 0 ? adapter_rank(p, a, &bad) : 0;
-  if (blockIdx.y == 0 && threadIdx.x == 0 && bad != 0) set_err(p.err, bad);
-  if (j >= ((rank + 7) & ~7)) return;
-  float acc = 0.f;
-  if (j < rank) {
-    const X* x = static_cast<const X*>(p.x) + r * p.x_stride;
-    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.ad.a) + (static_cast<int64_t>(a) * p.ad.rank_max + j) * p.k;
-#pragma unroll 4
-    for (int k = lane * 8; k < p.k; k += 256) {
-      float f[8], g[8];
-      entries8(x, k, f);
-      entries8(w, k, g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc = fmaf(f[e], g[e], acc);
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
-    if (sizeof(X) == 1) acc *= __ldcg(p.x_scale + r);
-    if (p.ad.scale != nullptr) acc *= __ldcg(p.ad.scale + a);
-  }
-  if (lane == 0) p.v[static_cast<int64_t>(r) * p.ad.rank_max + j] = acc;
-}
-
-// ---------------------------------------------------------------------------
-// Tensor-core pieces
-// ---------------------------------------------------------------------------
-// Shared-memory matrix descriptor: K-major rows of 128 bytes in the 128-byte swizzle (mode 2),
-// 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
-  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(1) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// Issued by one elected lane of a converged warp.
-template <bool E4M3>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  if (E4M3)
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
-      ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(kFull, mbar_wait(bar, parity));
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr) : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Box {one 128-byte column, rows, columns} of a matrix seen as [K columns][rows][128 bytes].
-__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the newest n groups of this thread have landed; n + 1 = 1, 2, 4 or 8.
-__device__ __forceinline__ void cp_async_wait(int ring) {
-  if (ring == 8) asm volatile("cp.async.wait_group 7;" ::: "memory");
-  else if (ring == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-  else if (ring == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
-// A barrier of the epilogue's threads that also makes an outcome common to them.
-__device__ __forceinline__ bool epilogue_all(bool v) {
-  uint32_t out;
-  asm volatile(
-      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\t"
-      "bar.red.and.pred po, 1, 128, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
-      : "=r"(out) : "r"(static_cast<uint32_t>(v)) : "memory");
-  return out != 0;
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ void store_out(const ProjectParams& p, int64_t at, float y) {
   if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
   else static_cast<float*>(p.out)[at] = y;
@@ -226,6 +87,7 @@ struct TileInfo {
   int rank[256];
   float sx[256];
   int run[256];      // rows that share an adapter: first | length << 16, within 32 rows each
+  bool one[256];     // the row's block of 16 shares one adapter
   int n_runs;
 };
 
@@ -247,16 +109,24 @@ __device__ __forceinline__ void v_pairs(const float* v, float2& a, float2& b) {
   b = make_float2(x.z, x.w);
 }
 
+// Block `lane` of a tile: the adapter its rows share, negative for none, several or no such block.
+__device__ __forceinline__ int tile_block(const ProjectParams& p, const Plan& q, int rt, int lane) {
+  const int r = rt * q.nb + lane * 16;
+  return lane < q.nb / 16 && r < p.rows ? __ldcg(p.block_ad + r / 16) : -1;
+}
+
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_constant__ CUtensorMap wmap,
                                                               const __grid_constant__ CUtensorMap xmap,
+                                                              const __grid_constant__ CUtensorMap bmap,
+                                                              const __grid_constant__ CUtensorMap vmap,
                                                               const ProjectParams p, const Plan q) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ TileInfo s_tile;
   const int stage_bytes = q.ch * (kWChunk + q.nb * kRowBytes);
   float* s_v = reinterpret_cast<float*>(smem + q.v_off);          // [2][32][rank_max]
-  unsigned char* s_b = smem + q.b_off;                            // [kRingVecs][128] 16-byte pieces
+  unsigned char* s_b = smem + q.b_off;                            // [ring][128] 16-byte pieces
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + q.bar_off);
   uint64_t* empty = full + kMaxStages;
   uint64_t* acc_full = empty + kMaxStages;
@@ -299,18 +169,21 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
 
   if (warp == 4) {
     // ------------------------------------------------------------------ copies
-    if (lane == 0) {
-      const int cols = kRowBytes / (E4M3 ? 1 : 2);
-      bool ok = true;
-      int it = 0;
-      for (int tile = blockIdx.x; tile < q.n_tiles && ok; tile += gridDim.x) {
-        const int rt = tile % q.n_rt, nt = tile / q.n_rt;
-        for (int i = 0; i < nst; ++i, ++it) {
+    const int cols = kRowBytes / (E4M3 ? 1 : 2);
+    bool ok = true, waited = false;
+    int it = 0;
+    // a free stage, once its last products have read it
+    auto next_stage = [&]() {
+      const int s = it % q.stages;
+      return it < q.stages || warp_wait(&empty[s], static_cast<uint32_t>(it / q.stages - 1) & 1u);
+    };
+    for (int tile = blockIdx.x; tile < q.n_tiles && ok; tile += gridDim.x) {
+      const int rt = tile % q.n_rt, nt = tile / q.n_rt;
+      for (int i = 0; i < nst; ++i, ++it) {
+        ok = next_stage();
+        if (!ok) break;
+        if (lane == 0) {
           const int s = it % q.stages;
-          if (it >= q.stages && !mbar_wait(&empty[s], static_cast<uint32_t>(it / q.stages - 1) & 1u)) {
-            ok = false;
-            break;
-          }
           unsigned char* w = smem + s * stage_bytes;
           unsigned char* x = w + q.ch * kWChunk;
           const int c0 = (st0 + i) * q.ch;
@@ -325,11 +198,35 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
             tma_load(x, &xmap, 0, rt * q.nb, c0, &full[s]);
           }
         }
+        __syncwarp();
       }
-      if (!ok) set_err(p.err, TTS_EFLAG_TIMEOUT);
-      // no copy may still be landing when the CTA leaves
-      for (int t = max(0, it - q.stages); t < it; ++t) mbar_wait(&full[t % q.stages], static_cast<uint32_t>(t / q.stages) & 1u);
+      if (q.parts == 0 || rank != 0 || !ok) continue;
+      // B rows and parts of v for blocks that share an adapter, 64 ranks a stage
+      if (!waited) grid_wait();
+      waited = true;
+      const int mine = tile_block(p, q, rt, lane);
+      BlockRun run;
+      for (int at = 0; ok && next_run(mine, q.nb / 16, at, run); at = run.first + run.count) {
+        int bad = 0;
+        const int ranks = adapter_rank(p, run.ad, &bad);
+        for (int j = 0; j < ranks && ok; j += 64)
+          for (int h = 0; h < q.parts; ++h, ++it) {
+            ok = next_stage();
+            if (!ok) break;
+            if (lane == 0) {
+              const int s = it % q.stages;
+              unsigned char* w = smem + s * stage_bytes;
+              mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(kWChunk + q.nb * kRowBytes));
+              tma_load(w, &bmap, j, run.ad * p.n + nt * kM, 0, &full[s]);
+              tma_load(w + q.ch * kWChunk, &vmap, j, rt * q.nb, h, &full[s]);
+            }
+            __syncwarp();
+          }
+      }
     }
+    if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
+    // no copy may still be landing when the CTA leaves
+    for (int t = max(0, it - q.stages); t < it; ++t) warp_wait(&full[t % q.stages], static_cast<uint32_t>(t / q.stages) & 1u);
     __syncwarp();
   } else if (warp == 5) {
     // ---------------------------------------------------------------- products
@@ -337,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
     // both K-major; N >> 3 at bit 17, M >> 4 at bit 24
     const uint32_t idesc = (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | (static_cast<uint32_t>(q.nb >> 3) << 17) |
                            (static_cast<uint32_t>(kM >> 4) << 24);
-    bool ok = true;
+    bool ok = true, waited = false;
     int it = 0, i = 0;
     for (int tile = blockIdx.x; tile < q.n_tiles && ok; tile += gridDim.x, ++i) {
       const int buf = i % q.n_acc, use = i / q.n_acc;
@@ -363,6 +260,47 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
         }
         mma_commit(&empty[s]);   // the stage is free once these products have read it
       }
+      if (q.parts > 0 && rank == 0 && ok) {
+        // z of blocks that share an adapter, beside the accumulators; the last tile's z has to be
+        // read first
+        if (!waited) grid_wait();
+        waited = true;
+        if (i > 0 && !warp_wait(&acc_empty[(i - 1) % q.n_acc], static_cast<uint32_t>((i - 1) / q.n_acc) & 1u)) ok = false;
+        tc_fence_after();
+        const int mine = tile_block(p, q, tile % q.n_rt, lane);
+        const uint32_t zd = tmem + static_cast<uint32_t>(q.n_acc * q.nbr);
+        BlockRun run;
+        for (int at = 0; ok && next_run(mine, q.nb / 16, at, run); at = run.first + run.count) {
+          int bad = 0;
+          const int ranks = adapter_rank(p, run.ad, &bad);
+          const uint32_t zi = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(run.count * 2) << 17) |
+                              (static_cast<uint32_t>(kM >> 4) << 24);
+          for (int j = 0; j < ranks && ok; j += 64)
+            for (int h = 0; h < q.parts; ++h, ++it) {
+              const int s = it % q.stages;
+              if (!warp_wait(&full[s], static_cast<uint32_t>(it / q.stages) & 1u)) {
+                ok = false;
+                break;
+              }
+              unsigned char* b = smem + s * stage_bytes;
+              const int left = min(64, ranks - j);
+              if (left % 16 != 0) {
+                // what lies behind the rank is not this adapter's: zeros up to the instruction's 16
+                for (int m = lane; m < kM; m += 32)
+                  for (int e = left; e < ((left + 15) & ~15); ++e)
+                    *reinterpret_cast<uint16_t*>(b + m * kRowBytes + (((e >> 3) ^ (m & 7)) << 4) + (e & 7) * 2) = 0;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+              }
+              tc_fence_after();
+              const uint64_t ad = smem_desc(smem_u32(b));
+              const uint64_t bd = smem_desc(smem_u32(b) + q.ch * kWChunk + run.first * 16 * kRowBytes);
+              for (int k = 0; k < (left + 15) / 16; ++k)
+                mma<false>(zd + run.first * 16, ad + 2 * k, bd + 2 * k, zi, j > 0 || h > 0 || k > 0);
+              mma_commit(&empty[s]);
+            }
+        }
+      }
       mma_commit(&acc_full[buf]);
     }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
@@ -372,7 +310,6 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t zcol = tmem + static_cast<uint32_t>(q.n_acc * q.nbr) + lane_off;
     const int m = tid, rm = p.ad.rank_max;
-    const int per_run = kRingVecs / q.ring;   // 16-byte pieces of a row of B
     const bool with = p.ad.n_adapters > 0;
     const int lo = q.nb * rank / S, hi = q.nb * (rank + 1) / S;   // rows whose adapters this CTA adds
     bool ok = true;
@@ -397,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
       named_barrier(1, kEpi);
       int n_runs = 0;
       if (with) {
-        const int c_lo = lo / 32, c_hi = (hi + 31) / 32;
+        const int c_lo = q.parts > 0 ? 0 : lo / 32, c_hi = q.parts > 0 ? q.nbr / 32 : (hi + 31) / 32;
         auto ask_v = [&](int c, uint32_t seq) {   // 32 rows of v
           const int r = r0 + c * 32, cnt = min(32, p.rows - r);
           const uint32_t bytes = static_cast<uint32_t>(cnt * rm) * 4u;
@@ -408,7 +345,20 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
           int base = 0;
           for (int c = c_lo; c < c_hi; ++c) {
             const int t = c * 32 + lane;
-            const int a = t >= lo && t < hi ? s_tile.ad[t] : -3;
+            int a = t >= lo && t < hi ? s_tile.ad[t] : -3;
+            if (q.parts > 0) {
+              // blocks that share an adapter are the tensor cores'
+              const int all = s_tile.ad[t];
+              int top = all, low = all >= 0 ? all : 0x7fffffff;
+#pragma unroll
+              for (int o = 8; o >= 1; o >>= 1) {
+                top = max(top, __shfl_xor_sync(kFull, top, o));
+                low = min(low, __shfl_xor_sync(kFull, low, o));
+              }
+              const bool one = top >= 0 && top == low;
+              s_tile.one[t] = one;
+              if (one) a = -3;
+            }
             const int prev = __shfl_up_sync(kFull, a, 1);
             const uint32_t edge = __ballot_sync(kFull, lane == 0 || a != prev);
             const uint32_t first = __ballot_sync(kFull, a >= 0 && (edge >> lane & 1u));
@@ -424,17 +374,27 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
         named_barrier(1, kEpi);
         n_runs = s_tile.n_runs;
         const unsigned char* brow = static_cast<const unsigned char*>(p.ad.b) + static_cast<int64_t>(n) * rm * 2;
-        auto ask_b = [&](int k) {
-          if (k < n_runs && n < p.n) {
-            const int t = s_tile.run[k] & 0xffff;
-            const unsigned char* src = brow + static_cast<int64_t>(s_tile.ad[t]) * p.n * rm * 2;
-            const int have = (s_tile.rank[t] + 7) / 8;
-            unsigned char* dst = s_b + (k % q.ring) * per_run * (kEpi * 16) + tid * 16;
-            for (int v = 0; v < have; ++v) cp_async16(dst + v * (kEpi * 16), src + v * 16);
+        // B rows go round a ring of 16-byte pieces, as many runs ahead as fit it
+        int ahead = 0, put = 0, room = q.ring, get = 0;
+        auto ask_b = [&](int done) {
+          while (ahead < n_runs && ahead - done < kMaxAhead) {
+            const int t = s_tile.run[ahead] & 0xffff, have = (s_tile.rank[t] + 7) / 8;
+            if (have > room) break;
+            if (n < p.n) {
+              const unsigned char* src = brow + static_cast<int64_t>(s_tile.ad[t]) * p.n * rm * 2;
+              for (int v = 0, at = put; v < have; ++v) {
+                cp_async16(s_b + (at * kEpi + tid) * 16, src + v * 16);
+                at = at + 1 == q.ring ? 0 : at + 1;
+              }
+            }
+            cp_async_commit();
+            put += have;
+            if (put >= q.ring) put -= q.ring;
+            room -= have;
+            ++ahead;
           }
-          cp_async_commit();
         };
-        for (int k = 0; k < q.ring; ++k) ask_b(k);
+        ask_b(0);
         int cur = -1, c_next = c_lo;   // the chunk of v in use (copy cur_seq), the next to ask for
         uint32_t cur_seq = 0, seq = vq;
         // (thread 0 asks; all threads count along)
@@ -461,50 +421,29 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
             cur_seq = seq0 + static_cast<uint32_t>(cur - c_lo);
             ok = mbar_wait(&v_full[cur_seq & 1], (cur_seq >> 1) & 1u) && ok;
           }
-          cp_async_wait(q.ring);
+          cp_async_wait(ahead - k - 1);
           const float* v = s_v + (cur_seq & 1) * 32 * rm;
-          const unsigned char* b = s_b + (k % q.ring) * per_run * (kEpi * 16) + tid * 16;
           const int have = (a_rank + 7) / 8;
-          if (len >= 8) {
-            float2 z[32];
-#pragma unroll
-            for (int t = 0; t < 32; ++t) z[t] = make_float2(0.f, 0.f);
-            for (int e = 0; e < have; ++e) {
-              float2 bp[4];
-              b_pairs(lds128(b + e * (kEpi * 16)), a_rank - 8 * e, bp);
-#pragma unroll
-              for (int t = 0; t < 32; ++t) {
-                float2 v0, v1, v2, v3;
-                v_pairs(v + t * rm + e * 8, v0, v1);
-                v_pairs(v + t * rm + e * 8 + 4, v2, v3);
-                z[t] = __ffma2_rn(v0, bp[0], z[t]);
-                z[t] = __ffma2_rn(v1, bp[1], z[t]);
-                z[t] = __ffma2_rn(v2, bp[2], z[t]);
-                z[t] = __ffma2_rn(v3, bp[3], z[t]);
-              }
+          for (int t = t0; t < t0 + len; ++t) {
+            float2 z = make_float2(0.f, 0.f), y = z;
+            const float* vt = v + (t - c * 32) * rm;
+            for (int e = 0, at = get; e < have; ++e) {
+              float2 bp[4], v0, v1, v2, v3;
+              b_pairs(lds128(s_b + (at * kEpi + tid) * 16), a_rank - 8 * e, bp);
+              at = at + 1 == q.ring ? 0 : at + 1;
+              v_pairs(vt + e * 8, v0, v1);
+              v_pairs(vt + e * 8 + 4, v2, v3);
+              z = __ffma2_rn(v0, bp[0], z);
+              y = __ffma2_rn(v1, bp[1], y);
+              z = __ffma2_rn(v2, bp[2], z);
+              y = __ffma2_rn(v3, bp[3], y);
             }
-            const int first = t0 - c * 32;
-#pragma unroll
-            for (int t = 0; t < 32; ++t)
-              if (t >= first && t < first + len) tmem_st1(zcol + static_cast<uint32_t>(c * 32 + t), z[t].x + z[t].y);
-          } else {
-            for (int t = t0; t < t0 + len; ++t) {
-              float2 z = make_float2(0.f, 0.f), y = z;
-              for (int e = 0; e < have; ++e) {
-                float2 bp[4], v0, v1, v2, v3;
-                b_pairs(lds128(b + e * (kEpi * 16)), a_rank - 8 * e, bp);
-                const float* vt = v + (t - c * 32) * rm + e * 8;
-                v_pairs(vt, v0, v1);
-                v_pairs(vt + 4, v2, v3);
-                z = __ffma2_rn(v0, bp[0], z);
-                y = __ffma2_rn(v1, bp[1], y);
-                z = __ffma2_rn(v2, bp[2], z);
-                y = __ffma2_rn(v3, bp[3], y);
-              }
-              tmem_st1(zcol + static_cast<uint32_t>(t), (z.x + z.y) + (y.x + y.y));
-            }
+            tmem_st1(zcol + static_cast<uint32_t>(t), (z.x + z.y) + (y.x + y.y));
           }
-          ask_b(k + q.ring);
+          get += have;
+          if (get >= q.ring) get -= q.ring;
+          room += have;
+          ask_b(k + 1);
         }
         // copies of chunks that no run needed: waited for, so that every phase is used once
         for (uint32_t w = cur < 0 ? seq0 : cur_seq + 1; w != seq; ++w) ok = mbar_wait(&v_full[w & 1], (w >> 1) & 1u) && ok;
@@ -529,7 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
         const int a = s_tile.ad[c * 32 + lane];
         const int t = c * 32 + lane;
         const uint32_t live = __ballot_sync(kFull, a != -2);
-        const uint32_t has = __ballot_sync(kFull, a >= 0 && t >= lo && t < hi);
+        // (z of a block that shares an adapter is with the cluster's first CTA)
+        const bool one = q.parts > 0 && s_tile.one[t];
+        const uint32_t has = __ballot_sync(kFull, a >= 0 && (one ? rank == 0 : t >= lo && t < hi));
         if (has != 0) tmem_ld32(zcol + c * 32, z);
         if (E4M3) {
 #pragma unroll
@@ -615,39 +556,6 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
   }
 }
 
-// cuTensorMapEncodeTiled, looked up once through the runtime (no link against the driver)
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static std::mutex mtx;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::lock_guard<std::mutex> lock(mtx);
-  if (fn == nullptr) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) == cudaSuccess &&
-        r == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    else
-      cudaGetLastError();
-  }
-  return fn;
-}
-
-// A row-major matrix of 1- or 2-byte entries as [K columns][rows][128 bytes] (whole columns), or
-// as [1][rows][K] (flat), boxes of `box_rows` rows.
-bool encode(CUtensorMap* map, const void* base, int es, int64_t stride, int k, int rows, int box_rows, int ch, bool flat) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (enc == nullptr) return false;
-  const cuuint64_t cols = kRowBytes / es, pitch = static_cast<cuuint64_t>(stride) * es;
-  cuuint64_t dims[3] = {flat ? static_cast<cuuint64_t>(k) : cols, static_cast<cuuint64_t>(rows),
-                        flat ? 1 : static_cast<cuuint64_t>(k) / cols};
-  cuuint64_t strides[2] = {pitch, flat ? pitch : kRowBytes};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(box_rows), flat ? 1u : static_cast<cuuint32_t>(ch)};
-  cuuint32_t es3[3] = {1, 1, 1};
-  return enc(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-             strides, box, es3, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 constexpr int kBarBytes = (2 * kMaxStages + 6) * 8 + 16;
 
 // The dynamic shared memory a CTA of the kernel may take on device `dev`, set as its limit once
@@ -679,22 +587,7 @@ int max_active_clusters(int dev, int S, int smem) {
   std::lock_guard<std::mutex> lock(mtx);
   const auto it = cache.find(key);
   if (it != cache.end()) return it->second;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1, S);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = static_cast<unsigned>(S);
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, project_kernel<E4M3>, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    n = 0;
-  }
+  const int n = active_clusters(project_kernel<E4M3>, S, kThreads, smem);
   cache[key] = n;
   return n;
 }
@@ -702,8 +595,8 @@ int max_active_clusters(int dev, int S, int smem) {
 // Shared memory of a plan: the ring, two chunks of v, the ring of B rows, barriers.
 void lay_out(Plan& q, int rank_max, size_t budget) {
   const int stage = q.ch * (kWChunk + q.nb * kRowBytes);
-  q.ring = rank_max == 0 ? 1 : rank_max <= 16 ? 8 : rank_max <= 32 ? 4 : rank_max <= 64 ? 2 : 1;
-  const int v = 2 * 32 * rank_max * 4, b = rank_max == 0 ? 0 : kRingVecs * kEpi * 16;
+  q.ring = rank_max == 0 ? 0 : 16;
+  const int v = 2 * 32 * rank_max * 4, b = q.ring * kEpi * 16;
   const int fixed = 1024 + v + b + kBarBytes;
   int st = static_cast<int>((budget - fixed) / stage);
   const int per_cta = (q.n_chunks + q.ch - 1) / q.ch;
@@ -761,39 +654,45 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
   if (static_cast<size_t>(q.smem) > budget) return cudaErrorInvalidConfiguration;
   const int quantum = p.out_bf16 ? 8 : 16;
   q.vec_out = p.out_stride * (p.out_bf16 ? 2 : 4) % quantum == 0;
-  CUtensorMap wmap, xmap;
+  // bf16 outputs keep eight bits: two parts, sixteen bits of v, are plenty; f32 outputs get all
+  q.parts = !p.tc ? 0 : p.out_bf16 ? 2 : 3;
+  CUtensorMap wmap, xmap, bmap, vmap;
   if (!encode(&wmap, p.w, es, p.k, p.k, p.n, kM, q.ch, q.flat) ||
       !encode(&xmap, p.x, es, p.x_stride, p.k, p.rows, q.nb, q.ch, q.flat))
     return cudaErrorInvalidValue;
+  bmap = vmap = wmap;
+  if (q.parts > 0 && (!encode(&bmap, p.ad.b, 2, rm, rm, p.ad.n_adapters * p.n, kM, 1, true) ||
+                      !encode(&vmap, p.v_parts, 2, rm, rm, p.rows, q.nb, 1, true, 0, 3)))
+    return cudaErrorInvalidValue;
   if (rm > 0) {
-    using X = typename std::conditional<E4M3, uint8_t, __nv_bfloat16>::type;
-    e = launch_pdl(shrink_kernel<X>, dim3(p.rows, (rm + kShrinkWarps - 1) / kShrinkWarps), dim3(kShrinkWarps * 32), 0, s, p);
+    e = launch_shrink(p, s);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = q.split > 1 ? dim3(q.n_tiles, q.split) : dim3(q.n_tiles < n_sm ? q.n_tiles : n_sm);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = q.smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1;
-  attr[1].val.clusterDim.y = static_cast<unsigned>(q.split);
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, project_kernel<E4M3>, wmap, xmap, p, q);
+  const dim3 grid = q.split > 1 ? dim3(q.n_tiles, q.split) : dim3(q.n_tiles < n_sm ? q.n_tiles : n_sm);
+  return launch_clustered(project_kernel<E4M3>, grid, kThreads, q.smem, q.split, s, wmap, xmap, bmap, vmap, p, q);
 }
 
 }  // namespace
 
-size_t project_workspace(int rows, int n, int k, bool x_e4m3, int rank_max) {
-  return static_cast<size_t>(rows) * rank_max * sizeof(float);
+// From this many rows on the adapters' products run on the tensor cores.
+bool project_tc(int rows) { return rows >= 128; }
+
+size_t project_workspace(int rows, int rank_max) {
+  const size_t v = static_cast<size_t>(rows) * rank_max;
+  return project_tc(rows) ? round256(v * 4) + round256(v * 2 * 3) + round256((static_cast<size_t>(rows) + 15) / 16 * 4)
+                          : round256(v * 4);
 }
 
-cudaError_t launch_project(const ProjectParams& p, cudaStream_t s) {
+cudaError_t launch_project(const ProjectParams& given, void* workspace, cudaStream_t s) {
+  ProjectParams p = given;
+  p.tc = p.ad.n_adapters > 0 && project_tc(p.rows);
+  if (p.ad.n_adapters > 0) {
+    const size_t v = static_cast<size_t>(p.rows) * p.ad.rank_max;
+    unsigned char* at = static_cast<unsigned char*>(workspace);
+    p.v = reinterpret_cast<float*>(at);
+    p.v_parts = reinterpret_cast<__nv_bfloat16*>(at + round256(v * 4));
+    p.block_ad = reinterpret_cast<int32_t*>(at + round256(v * 4) + round256(v * 2 * 3));
+  }
   return p.x_e4m3 ? launch_t<true>(p, s) : launch_t<false>(p, s);
 }
 

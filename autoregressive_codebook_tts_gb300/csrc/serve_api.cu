@@ -80,7 +80,7 @@ tts_status tts_add_rms_norm(const void* x, int64_t x_stride, int32_t x_dtype, co
 
 size_t tts_project_workspace_size(int32_t rows, int32_t n, int32_t k, int32_t x_dtype, const tts_adapters* ad) {
   if (check_project(rows, n, k, x_dtype, ad) != TTS_OK || ad == nullptr) return 0;
-  return round256(project_workspace(rows, n, k, x_dtype == TTS_E4M3, ad->rank_max));
+  return project_workspace(rows, ad->rank_max);
 }
 
 tts_status tts_project_rows(const void* x, int64_t x_stride, int32_t x_dtype, const float* x_scale, const void* w,
@@ -103,7 +103,6 @@ tts_status tts_project_rows(const void* x, int64_t x_stride, int32_t x_dtype, co
     if (workspace == nullptr || ws_bytes < tts_project_workspace_size(rows, n, k, x_dtype, ad)) return TTS_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return TTS_ERR_ALIGN;
     p.ad = *ad;
-    p.v = static_cast<float*>(workspace);
   }
   // an input row is read by many CTAs, some after others have written out
   if (out == x || out == w) return TTS_ERR_LAYOUT;
@@ -123,7 +122,7 @@ tts_status tts_project_rows(const void* x, int64_t x_stride, int32_t x_dtype, co
   p.out_stride = out_stride;
   p.out_bf16 = out_dtype == TTS_BF16;
   p.err = err_flag;
-  return from_cuda(launch_project(p, as_stream(stream)));
+  return from_cuda(launch_project(p, workspace, as_stream(stream)));
 }
 
 tts_status tts_page_plan(const tts_kv_desc* d, int32_t* block_table, int32_t* free_pages, int32_t* n_free,

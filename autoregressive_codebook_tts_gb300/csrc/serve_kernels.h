@@ -70,14 +70,21 @@ struct ProjectParams {
   void* out;
   int64_t out_stride;
   int out_bf16;
-  float* v;                     // workspace: x A^T, [rows][rank_max]
+  // workspace: scale x A^T in f32 [rows][rank_max]; with tc also as three bf16 parts
+  // [3][rows][rank_max], and each 16 rows' adapter (-1 none, -2 several)
+  float* v;
+  __nv_bfloat16* v_parts;
+  int32_t* block_ad;
+  int tc;                       // the adapters' products on the tensor cores too
   int32_t* err;
 };
 
 cudaError_t launch_add_norm(const AddNormParams& p, cudaStream_t s);
 cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t s);
 cudaError_t launch_kv_slots(const KvSlotsParams& p, cudaStream_t s);
-size_t project_workspace(int rows, int n, int k, bool x_e4m3, int rank_max);
-cudaError_t launch_project(const ProjectParams& p, cudaStream_t s);
+bool project_tc(int rows);
+size_t project_workspace(int rows, int rank_max);
+cudaError_t launch_shrink(const ProjectParams& p, cudaStream_t s);
+cudaError_t launch_project(const ProjectParams& p, void* workspace, cudaStream_t s);
 
 }  // namespace tts
