@@ -91,24 +91,6 @@ struct TileInfo {
   int n_runs;
 };
 
-// Eight entries of B as four pairs, zero from the rank on.
-__device__ __forceinline__ void b_pairs(const uint4 w, int left, float2 (&b)[4]) {
-  float f[8];
-  unpack_bf16x8(w, f);
-  if (left < 8) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = e < left ? f[e] : 0.f;
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) b[e] = make_float2(f[2 * e], f[2 * e + 1]);
-}
-// four entries of v at once, the same address for the whole warp
-__device__ __forceinline__ void v_pairs(const float* v, float2& a, float2& b) {
-  const float4 x = *reinterpret_cast<const float4*>(v);
-  a = make_float2(x.x, x.y);
-  b = make_float2(x.z, x.w);
-}
-
 // Block `lane` of a tile: the adapter its rows share, negative for none, several or no such block.
 __device__ __forceinline__ int tile_block(const ProjectParams& p, const Plan& q, int rt, int lane) {
   const int r = rt * q.nb + lane * 16;
@@ -693,6 +675,7 @@ cudaError_t launch_project(const ProjectParams& given, void* workspace, cudaStre
     p.v_parts = reinterpret_cast<__nv_bfloat16*>(at + round256(v * 4));
     p.block_ad = reinterpret_cast<int32_t*>(at + round256(v * 4) + round256(v * 2 * 3));
   }
+  if (project_is_many(p.rows, p.n)) return launch_project_many(p, s);
   return p.x_e4m3 ? launch_t<true>(p, s) : launch_t<false>(p, s);
 }
 

@@ -119,6 +119,24 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
+// Eight entries of B as four pairs, zero from the rank on.
+__device__ __forceinline__ void b_pairs(const uint4 w, int left, float2 (&b)[4]) {
+  float f[8];
+  unpack_bf16x8(w, f);
+  if (left < 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = e < left ? f[e] : 0.f;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = make_float2(f[2 * e], f[2 * e + 1]);
+}
+// four entries of v at once, the same address for the whole warp
+__device__ __forceinline__ void v_pairs(const float* v, float2& a, float2& b) {
+  const float4 x = *reinterpret_cast<const float4*>(v);
+  a = make_float2(x.x, x.y);
+  b = make_float2(x.z, x.w);
+}
+
 // cuTensorMapEncodeTiled, looked up once through the runtime (no link against the driver)
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::mutex mtx;
@@ -188,6 +206,26 @@ cudaError_t launch_clustered(Kernel kern, dim3 grid, int threads, int smem, int 
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = static_cast<unsigned>(S);
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// The same in clusters of two along x: pairs of CTAs.
+template <typename Kernel, typename... Args>
+cudaError_t launch_pairs(Kernel kern, int grid, int threads, int smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;

@@ -235,6 +235,51 @@ def test_segments_of_requests(tts, lengths, dead, xdt, odt, rank_max):
     assert ef.item() == 0
 
 
+# enough tiles for the pairs of SMs: lengths of the requests, rows without one, n, k
+MANY = [([700], 0, 4096, 512), ([1999], 1, 2100, 272), ([160] * 6, 0, 3080, 64), ([64, 96, 160, 33, 127, 31, 1, 200, 90], 30, 3800, 80),
+        ([100, 60, 150, 10, 7, 153, 300, 20, 5, 5, 5, 5, 140], 0, 4096, 336), ([1] * 170 + [2, 3, 9, 8, 7] * 20, 9, 5200, 128),
+        ([31, 33] * 14, 0, 3400, 2064), ([480, 0, 0, 480], 64, 3088, 192)]
+
+
+@pytest.mark.parametrize("lengths,dead,n,k", MANY)
+@pytest.mark.parametrize("xdt,odt,rank_max", [("bf16", "f32", 16), ("e4m3", "bf16", 64), ("bf16", "bf16", 128), ("e4m3", "f32", 40),
+                                              ("bf16", "bf16", None), ("e4m3", "f32", None)])
+def test_many_rows(tts, lengths, dead, n, k, xdt, odt, rank_max):
+    rows, pool = sum(lengths) + dead, 7
+    c = project_case(rows + n, rows, n, k, xdt, None if rank_max is None else pool, rank_max)
+    of = torch.cat([torch.repeat_interleave(torch.arange(len(lengths)), torch.tensor(lengths)), torch.full((dead,), -1)])
+    sa = torch.tensor([(3 * i) % (pool + 1) - 1 for i in range(len(lengths))], dtype=I32)
+    if rank_max is None:
+        sa[:] = -1
+    adapter = torch.where(of >= 0, sa[of.clamp(min=0)], -1)
+    ef = flag()
+    out = run_project(tts, c, row_stream=of.to("cuda", I32), stream_adapter=None if rank_max is None else sa.cuda(), odt=odt, ef=ef,
+                      pad=3)
+    check_project(c, out, adapter, dead=(of < 0).cuda(), odt=odt)
+    assert ef.item() == 0
+    assert torch.equal(out, run_project(tts, c, row_stream=of.to("cuda", I32), stream_adapter=None if rank_max is None else sa.cuda(),
+                                        odt=odt, pad=3))
+
+
+def test_many_rows_each_its_own_adapter_and_a_bad_one(tts):
+    c = project_case(33, 900, 4000, 128, "bf16", 6, 16)
+    c["a"], c["b"] = c["a"].nan_to_num(0.5), c["b"].nan_to_num(0.25)
+    c["rank"][:] = ints([16, 13, 7, 1, 8, 16])
+    adapter = torch.randint(-1, 6, (900,), generator=gen(34), device="cuda", dtype=I32)
+    check_project(c, run_project(tts, c, adapter), adapter)
+    runs = torch.repeat_interleave(ints([0, 1, 2, 3, 0, 4, 5, 1]), torch.tensor([200, 100, 57, 43, 160, 40, 200, 100], device="cuda"))
+    for of in (adapter, runs):
+        d = dict(c, a=c["a"].clone(), b=c["b"].clone())
+        d["b"][1, 5, 0] = float("inf")
+        d["b"][1, 3000, 0] = float("nan")
+        d["a"][4, 0, 3] = float("nan")
+        got, clean = run_project(tts, d, of), run_project(tts, c, of)
+        good = (of != 1) & (of != 4)
+        assert torch.equal(got[good], clean[good]) and got[of == 4].isnan().all()
+        one = got[of == 1]
+        assert not one[:, 5].isfinite().any() and one[:, 3000].isnan().all() and (~one.isfinite()).sum() == 2 * one.shape[0]
+
+
 @pytest.mark.parametrize("rows", [40, 300])
 def test_requests_in_any_order_with_dead_rows_between(tts, rows):
     c = project_case(9, rows, 260, 192, "bf16", 5, 32)
@@ -325,16 +370,16 @@ def test_a_workspace_is_enough_for_fewer_rows_and_holds_nothing(tts):
     assert torch.equal(run_project(tts, c, adapter, ws=ws), first)
 
 
-@pytest.mark.parametrize("rows", [1, 32, 100, 700])
+@pytest.mark.parametrize("rows,n", [(1, 520), (32, 520), (100, 520), (700, 520), (1000, 3100)])
 @pytest.mark.parametrize("xdt", ["bf16", "e4m3"])
-def test_projection_replayed_and_on_two_streams(tts, rows, xdt):
-    c = project_case(20, rows, 520, 1024, xdt, 4, 32)
+def test_projection_replayed_and_on_two_streams(tts, rows, n, xdt):
+    c = project_case(20, rows, n, 1024, xdt, 4, 32)
     adapter = torch.randint(-1, 4, (rows,), generator=gen(21), device="cuda", dtype=I32)
     eager = run_project(tts, c, adapter)
     check_project(c, eager, adapter)
     pool = tts.adapters(c["a"], c["b"], rank=c["rank"], scale=c["scale"])
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
-    spaces = [tts.project_workspace(rows, 520, 1024, xdt, pool) for _ in streams]
+    spaces = [tts.project_workspace(rows, n, 1024, xdt, pool) for _ in streams]
     outs = [torch.zeros_like(eager) for _ in streams]
     graph = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
