@@ -675,7 +675,7 @@ cudaError_t launch_project(const ProjectParams& given, void* workspace, cudaStre
     p.v_parts = reinterpret_cast<__nv_bfloat16*>(at + round256(v * 4));
     p.block_ad = reinterpret_cast<int32_t*>(at + round256(v * 4) + round256(v * 2 * 3));
   }
-  if (project_is_many(p.rows, p.n)) return launch_project_many(p, s);
+  if (project_is_many(p)) return launch_project_many(p, s);
   return p.x_e4m3 ? launch_t<true>(p, s) : launch_t<false>(p, s);
 }
 

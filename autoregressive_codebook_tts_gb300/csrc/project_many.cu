@@ -1,37 +1,35 @@
 // The shared projection of many rows, with the adapters' wide products beside it, on pairs of SMs.
 //
 // Many rows bound the product by the tensor cores, and those by the operands that have to reach
-// them.  Two CTAs therefore share a tile of 256 rows of W by up to 160 rows of x (cta_group::2): each
-// brings its own 128 rows of W and half the rows of x, 26 bytes a kiloflop instead of the 36 of a
-// CTA by itself.  The accumulator is double, so that a tile's products run under the epilogue of
-// the last one; what is left of tensor memory holds z = v B_a^T.
+// them: an SM takes 64 bytes a clock from L2.  Two CTAs therefore share a tile of 256 rows of W by up
+// to 224 rows of x (cta_group::2): each brings its own 128 rows of W and half the rows of x, which is
+// 480 clocks of L2 for 448 of products a column of 128 bytes (a CTA by itself with 160 rows: 576
+// for 320).  Accumulator and z together take all of tensor memory, so a tile's epilogue first moves
+// both into registers (eight warps, half the columns each), which frees them for the next tile's
+// products, and stores from there.
 //
-// z: rows of a tile that lie together and share an adapter are a run.  A run has columns of its own
-// (its rows, up to a multiple of 32), so its product meets no other adapter's rows, and what the
-// columns behind it hold is not read.  v comes as bf16 parts (two for bf16 outputs, all three for
-// f32 ones).  Entries of B behind the adapter's rank are overwritten with zeros in shared memory
-// before the product reads them.  Runs that find no room are added on the CUDA cores in the
-// epilogue.
+// z = v B_a^T: rows of a tile that lie together and share an adapter are a run.  A run has columns of
+// its own (its rows, up to a multiple of 32), so its product meets no other adapter's rows, and what
+// the columns behind it hold is not read.  v comes as bf16 parts (two for bf16 outputs, all three
+// for f32 ones).  Entries of B behind the adapter's rank are overwritten with zeros in shared memory
+// before the product reads them.  Runs that find no room are added on the CUDA cores in the epilogue.
 //
-// Warps: 0-3 epilogue, 4 copies, 5 products (of the pair's first CTA), 6 notes (each row's
-// adapter, runs and their columns, a tile ahead), 7 the zeros behind the ranks.
-#include <map>
-#include <tuple>
+// Warps: 0-7 epilogue, 8 copies, 9 products (of the pair's first CTA), 10 notes (each row's
+// adapter, runs and their columns, a tile ahead), 11 the zeros behind the ranks.
+#include <cstdint>
 
 #include "project_parts.cuh"
 
 namespace tts {
 namespace {
 
-constexpr int kMaxNb = 160;
+constexpr int kMaxNb = 224;
 constexpr int kMaxRuns = 16;
-constexpr int kThreads = 256;
-constexpr int kEpi = 128;
+constexpr int kThreads = 384;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kNoteWarp = 10, kZeroWarp = 11;
 constexpr int kMaxStages = 8;
 constexpr int kTmemCols = 512;
 constexpr int kWChunk = kM * kRowBytes;
-constexpr int kRing = 16;             // 16-byte pieces of B a thread of the epilogue has room for
-constexpr int kMaxAhead = 8;
 
 struct ManyPlan {
   int nb;                   // rows of x a tile, a multiple of 32
@@ -39,7 +37,7 @@ struct ManyPlan {
   int n_rt, n_nt, n_tiles;
   int n_chunks, flat;
   int parts;                // 0: no adapters
-  int v_off, b_off, z_off, bar_off, smem;
+  int bar_off, smem;
 };
 
 struct Notes {
@@ -80,86 +78,70 @@ __device__ __forceinline__ void tma_load2(void* dst, const CUtensorMap* map, int
       ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
+// Arrives at a barrier of either CTA; what it tells of was read, not written.
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity) {
   return __all_sync(kFull, mbar_wait_cluster(bar, parity, kWaitLimitCycles));
 }
-__device__ __forceinline__ void tmem_ld1(uint32_t taddr, float& v) {
+// (the values may be used after tmem_wait_ld)
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
   uint32_t r;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-  v = __uint_as_float(r);
-}
-__device__ __forceinline__ void cp_async_wait(int n) {
-  switch (n) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-    case 7: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 8;" ::: "memory"); break;
-  }
+  tmem_wait_ld();
+  return __uint_as_float(r);
 }
 
-// z of the rows `todo` of a chunk of 32 on the CUDA cores, into s_z[row][thread]: thread m streams
-// its row of each B_a through a ring of 16-byte pieces.
-__device__ __noinline__ void z_on_cuda_cores(const ProjectParams& p, const Notes& note, int c, int r0, int n, uint32_t todo,
-                                             float* s_v, unsigned char* s_b, float* s_z) {
-  const int tid = threadIdx.x, rm = p.ad.rank_max;
-  named_barrier(1, kEpi);   // the last chunk's rows of v have been read
-  for (int i = tid; i < 32 * rm / 4; i += kEpi) {
-    const int t = i / (rm / 4), r = r0 + c * 32 + t;
-    if (todo >> t & 1u) cp_async16(s_v + i * 4, p.v + static_cast<int64_t>(r) * rm + (i - t * (rm / 4)) * 4);
+// z of four rows of the tile (row[u] < 0: none) for output column n, on the CUDA cores.
+__device__ __forceinline__ void z_of_rows(const ProjectParams& p, const Notes& note, int t0, int r0, int n, const int (&row)[4],
+                                          float (&z)[4]) {
+  const int rm = p.ad.rank_max;
+  int rank[4], most = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    rank[u] = row[u] >= 0 && n < p.n ? note.rank[t0 + row[u]] : 0;
+    most = max(most, rank[u]);
   }
-  cp_async_commit();
-  uint32_t next = todo;
-  int ahead = 0, put = 0, room = kRing, get = 0;
-  auto ask = [&](int done) {
-    while (next != 0 && ahead - done < kMaxAhead) {
-      const int t = c * 32 + __ffs(static_cast<int>(next)) - 1, have = (note.rank[t] + 7) / 8;
-      if (have > room) break;
-      if (n < p.n) {
-        const unsigned char* src = static_cast<const unsigned char*>(p.ad.b) + (static_cast<int64_t>(note.ad[t]) * p.n + n) * rm * 2;
-        for (int v = 0, at = put; v < have; ++v) {
-          cp_async16(s_b + (at * kEpi + tid) * 16, src + v * 16);
-          at = at + 1 == kRing ? 0 : at + 1;
-        }
+  for (int e = 0; e < most; e += 8) {
+    uint4 w[4];
+    float4 va[4], vb[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (e < rank[u]) {
+        const int a = note.ad[t0 + row[u]];
+        w[u] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.ad.b) +
+                                                     (static_cast<int64_t>(a) * p.n + n) * rm + e));
+        const float4* v = reinterpret_cast<const float4*>(p.v + static_cast<int64_t>(r0 + row[u]) * rm + e);
+        va[u] = __ldcg(v);
+        vb[u] = __ldcg(v + 1);
       }
-      cp_async_commit();
-      put = put + have >= kRing ? put + have - kRing : put + have;
-      room -= have;
-      ++ahead;
-      next &= next - 1;
-    }
-  };
-  ask(0);
-  cp_async_wait(ahead);     // v
-  named_barrier(1, kEpi);
-  int k = 0;
-  for (uint32_t left = todo; left != 0; left &= left - 1, ++k) {
-    const int j = __ffs(static_cast<int>(left)) - 1, rank = note.rank[c * 32 + j], have = (rank + 7) / 8;
-    cp_async_wait(ahead - k - 1);
-    const float* vt = s_v + j * rm;
-    float2 z = make_float2(0.f, 0.f), y = z;
-    for (int e = 0, at = get; e < have; ++e) {
-      float2 bp[4], v0, v1, v2, v3;
-      b_pairs(lds128(s_b + (at * kEpi + tid) * 16), rank - 8 * e, bp);
-      at = at + 1 == kRing ? 0 : at + 1;
-      v_pairs(vt + e * 8, v0, v1);
-      v_pairs(vt + e * 8 + 4, v2, v3);
-      z = __ffma2_rn(v0, bp[0], z);
-      y = __ffma2_rn(v1, bp[1], y);
-      z = __ffma2_rn(v2, bp[2], z);
-      y = __ffma2_rn(v3, bp[3], y);
-    }
-    s_z[j * kEpi + tid] = (z.x + z.y) + (y.x + y.y);
-    get = get + have >= kRing ? get + have - kRing : get + have;
-    room += have;
-    ask(k + 1);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (e < rank[u]) {
+        float2 bp[4];
+        b_pairs(w[u], rank[u] - e, bp);
+        z[u] = fmaf(va[u].x, bp[0].x, z[u]);
+        z[u] = fmaf(va[u].y, bp[0].y, z[u]);
+        z[u] = fmaf(va[u].z, bp[1].x, z[u]);
+        z[u] = fmaf(va[u].w, bp[1].y, z[u]);
+        z[u] = fmaf(vb[u].x, bp[2].x, z[u]);
+        z[u] = fmaf(vb[u].y, bp[2].y, z[u]);
+        z[u] = fmaf(vb[u].z, bp[3].x, z[u]);
+        z[u] = fmaf(vb[u].w, bp[3].y, z[u]);
+      }
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <bool E4M3>
@@ -174,15 +156,13 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
   __shared__ Notes s_note[2];
   const int half = q.nb / 2, x_chunk = half * kRowBytes;
   const int stage_bytes = q.ch * (kWChunk + x_chunk);
-  float* s_v = reinterpret_cast<float*>(smem + q.v_off);
-  unsigned char* s_b = smem + q.b_off;
-  float* s_z = reinterpret_cast<float*>(smem + q.z_off);          // [32][128]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + q.bar_off);  // (the first CTA's)
   uint64_t* zl = full + kMaxStages;                                // B and v parts have landed here
-  uint64_t* empty = zl + kMaxStages;
+  uint64_t* zr = zl + kMaxStages;                                  // (the first CTA's) ... in the second CTA
+  uint64_t* empty = zr + kMaxStages;
   uint64_t* acc_full = empty + kMaxStages;
-  uint64_t* acc_empty = acc_full + 2;                              // (the first CTA's)
-  uint64_t* note_full = acc_empty + 2;
+  uint64_t* acc_empty = acc_full + 1;                              // (the first CTA's)
+  uint64_t* note_full = acc_empty + 1;
   uint64_t* note_empty = note_full + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(note_empty + 2);
 
@@ -193,19 +173,20 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
 
   if (tid == 0) {
     for (int i = 0; i < q.stages; ++i) {
-      mbar_init(&full[i], 2);
+      mbar_init(&full[i], 1);
       mbar_init(&zl[i], 1);
+      mbar_init(&zr[i], 1);
       mbar_init(&empty[i], 1);
     }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 16);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);
       mbar_init(&note_full[i], 1);
-      mbar_init(&note_empty[i], q.parts > 0 ? 7 : 4);   // epilogue 4; copies, products, zeros
+      mbar_init(&note_empty[i], q.parts > 0 ? 11 : 8);   // epilogue 8; copies, products, zeros
     }
     mbar_init_fence();
   }
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                  ::"r"(smem_u32(s_tmem)), "n"(kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -217,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
   if (p.ad.n_adapters == 0) grid_wait();   // (else the narrow products' kernel has waited)
   grid_launch_dependents();
 
-  const uint32_t zbase = static_cast<uint32_t>(2 * q.nb);
+  const uint32_t zbase = static_cast<uint32_t>(q.nb);
   // a tile's notes: the i-th tile of this CTA, to be given back with note_done
   auto note_wait = [&](int i) { return warp_wait(&note_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u); };
   auto note_done = [&](int i) {
@@ -225,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
     if (lane == 0) mbar_arrive(&note_empty[i & 1]);
   };
 
-  if (warp == 4) {
+  if (warp == kCopyWarp) {
     // ------------------------------------------------------------------ copies
     const int cols = kRowBytes / (E4M3 ? 1 : 2);
     bool ok = true;
@@ -247,7 +228,6 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
           const uint32_t bar = map_shared_rank(&full[s], 0);
           // the first CTA's barrier counts the bytes of both
           if (rank == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(2 * stage_bytes));
-          else mbar_arrive_remote(bar);
           const int c0 = st * q.ch;
           if (q.flat) {
             for (int c = 0; c < q.ch; ++c) {
@@ -287,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
     // no copy may still be landing, and no product reading, when the CTA leaves
     for (int t = max(0, it - q.stages); t < it; ++t) warp_wait(&empty[t % q.stages], static_cast<uint32_t>(t / q.stages) & 1u);
-  } else if (warp == 5) {
+  } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
     bool ok = true;
     int it = 0, i = 0;
@@ -301,16 +281,15 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
         }
         continue;
       }
-      const int buf = i & 1;
-      if (i > 1 && !warp_wait_cluster(&acc_empty[buf], static_cast<uint32_t>(i / 2 - 1) & 1u)) {
+      // the last tile's accumulator and z are in registers
+      if (i > 0 && !warp_wait_cluster(acc_empty, static_cast<uint32_t>(i - 1) & 1u)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t d = tmem + static_cast<uint32_t>(buf * q.nb);
       for (int st = 0; st < nst; ++st, ++it) {
         const int s = it % q.stages;
-        if (!warp_wait_cluster(&full[s], static_cast<uint32_t>(it / q.stages) & 1u)) {
+        if (!warp_wait(&full[s], static_cast<uint32_t>(it / q.stages) & 1u)) {
           ok = false;
           break;
         }
@@ -319,16 +298,13 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
         for (int c = 0; c < q.ch; ++c) {
           const uint64_t ad = smem_desc(w + c * kWChunk), bd = smem_desc(x + c * x_chunk);
 #pragma unroll
-          for (int k = 0; k < kRowBytes / 32; ++k) mma2<E4M3>(d, ad + 2 * k, bd + 2 * k, idesc, st > 0 || c > 0 || k > 0);
+          for (int k = 0; k < kRowBytes / 32; ++k) mma2<E4M3>(tmem, ad + 2 * k, bd + 2 * k, idesc, st > 0 || c > 0 || k > 0);
         }
         commit2(&empty[s]);
       }
       if (q.parts > 0 && ok) {
         ok = note_wait(i);
-        // the last tile's z has to be read first
-        if (i > 0 && !warp_wait_cluster(&acc_empty[(i - 1) & 1], static_cast<uint32_t>((i - 1) / 2) & 1u)) ok = false;
-        tc_fence_after();
-        const Notes& note = s_note[buf];
+        const Notes& note = s_note[i & 1];
         const int runs = ok ? note.n_runs : 0;
         for (int k = 0; k < runs && ok; ++k) {
           const uint32_t zi = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(note.run_n[k] >> 3) << 17) |
@@ -352,15 +328,15 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
         }
         note_done(i);
       }
-      commit2(&acc_full[buf]);
+      commit2(acc_full);
     }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
-  } else if (warp == 6) {
+  } else if (warp == kNoteWarp) {
     // ------------------------------------------------------------------- notes
     bool ok = true;
     int i = 0;
     constexpr int kC = kMaxNb / 32;
-    const int zcols = kTmemCols - 2 * q.nb;
+    const int zcols = kTmemCols - q.nb;
     for (int tile = pair; tile < q.n_tiles && ok; tile += pairs, ++i) {
       if (i > 1 && !warp_wait(&note_empty[i & 1], static_cast<uint32_t>(i / 2 - 1) & 1u)) {
         ok = false;
@@ -438,11 +414,11 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
       if (lane == 0) mbar_arrive(&note_full[i & 1]);
     }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
-  } else if (warp == 7) {
+  } else if (warp == kZeroWarp) {
     // ------------------------------------------------- zeros behind the ranks
     bool ok = true;
     int it = 0, i = 0;
-    uint32_t phase = 0;   // of each stage's zl
+    uint32_t phase = 0;   // of each stage's zl (and zr)
     if (q.parts > 0)
       for (int tile = pair; tile < q.n_tiles && ok; tile += pairs, ++i) {
         it += nst;
@@ -458,7 +434,6 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
                 ok = false;
                 break;
               }
-              phase ^= 1u << s;
               const int left = min(64, ranks - j);
               if (left % 16 != 0) {
                 unsigned char* b = smem + s * stage_bytes;
@@ -468,7 +443,17 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
               }
               __syncwarp();
-              if (lane == 0) mbar_arrive_remote(map_shared_rank(&full[s], 0));
+              if (rank == 0) {
+                // both CTAs' operands: the products may read them
+                if (!warp_wait_cluster(&zr[s], phase >> s & 1u)) {
+                  ok = false;
+                  break;
+                }
+                if (lane == 0) mbar_arrive(&full[s]);
+              } else if (lane == 0) {
+                mbar_arrive_remote(map_shared_rank(&zr[s], 0));
+              }
+              phase ^= 1u << s;
             }
         }
         note_done(i);
@@ -477,93 +462,120 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
   } else {
     // ---------------------------------------------------------------- epilogue
     grid_wait();
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int t0 = warp < 4 ? 0 : half, chunks = half / 16;   // this warp's columns
     bool ok = true;
     int i = 0;
     for (int tile = pair; tile < q.n_tiles && ok; tile += pairs, ++i) {
-      const int rt = tile % q.n_rt, nt = tile / q.n_rt, r0 = rt * q.nb, buf = i & 1;
-      const int n = nt * 2 * kM + rank * kM + tid;
+      const int rt = tile % q.n_rt, nt = tile / q.n_rt, r0 = rt * q.nb + t0;
+      const int n = nt * 2 * kM + rank * kM + (warp & 3) * 32 + lane;
       const float sw = E4M3 && n < p.n ? __ldcg(p.w_scale + n) : 0.f;
-      ok = mbar_wait(&note_full[buf], static_cast<uint32_t>(i >> 1) & 1u);
-      ok = mbar_wait(&acc_full[buf], static_cast<uint32_t>(i >> 1) & 1u) && ok;
-      ok = epilogue_all(ok);
+      const Notes& note = s_note[i & 1];
+      ok = note_wait(i);
+      ok = warp_wait(acc_full, static_cast<uint32_t>(i) & 1u) && ok;
       if (!ok) {
-        if (tid == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
+        if (lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
         break;
       }
       tc_fence_after();
-      const Notes& note = s_note[buf];
-      const uint32_t dcol = tmem + static_cast<uint32_t>(buf * q.nb) + lane_off;
-      for (int c = 0; c < q.nb / 32; ++c) {
-        float acc[32];
-        tmem_ld32(dcol + c * 32, acc);
-        const int a = note.ad[c * 32 + lane], zc = note.zcol[c * 32 + lane];
-        const uint32_t live = __ballot_sync(kFull, a != -2);
-        const uint32_t on_tc = __ballot_sync(kFull, zc >= 0), on_cc = __ballot_sync(kFull, a >= 0 && zc < 0 && q.parts > 0);
-        if (E4M3) {
+      float acc[kMaxNb / 2];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) acc[j] *= note.sx[c * 32 + j] * sw;
-        }
-        if (on_tc != 0) {
-          // one run: its columns lie together
-          const int f = __ffs(static_cast<int>(on_tc)) - 1, base = __shfl_sync(kFull, zc, f) - f;
-          const bool one = __all_sync(kFull, zc < 0 || zc - lane == base) && static_cast<int>(zbase) + base + 32 <= kTmemCols;
-          if (one) {
-            float z[32];
-            tmem_ld32(tmem + static_cast<uint32_t>(static_cast<int>(zbase) + base) + lane_off, z);
+      for (int c = 0; c < kMaxNb / 32; ++c)
+        if (c < chunks) tmem_ld16(tmem + static_cast<uint32_t>(t0 + c * 16) + lane_off, acc + c * 16);
+      tmem_wait_ld();
+      uint32_t live[kMaxNb / 32];   // rows of requests
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (on_tc >> j & 1u) acc[j] += z[j];
-          } else {
-            for (uint32_t left = on_tc; left != 0; left &= left - 1) {
-              const int j = __ffs(static_cast<int>(left)) - 1;
-              float z;
-              tmem_ld1(tmem + zbase + static_cast<uint32_t>(__shfl_sync(kFull, zc, j)) + lane_off, z);
-              s_z[j * kEpi + tid] = z;
-            }
+      for (int c = 0; c < kMaxNb / 32; ++c) {
+        live[c] = 0;
+        if (c < chunks) {
+          const int t = t0 + c * 16 + (lane & 15);
+          const int a = note.ad[t], zc = note.zcol[t];
+          live[c] = __ballot_sync(kFull, a != -2) & 0xffffu;
+          const uint32_t z_of = __ballot_sync(kFull, zc >= 0) & 0xffffu;
+          if (E4M3) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (on_tc >> j & 1u) acc[j] += s_z[j * kEpi + tid];
+            for (int j = 0; j < 16; ++j) acc[c * 16 + j] *= note.sx[t0 + c * 16 + j] * sw;
           }
-        }
-        if (on_cc != 0) {
-          z_on_cuda_cores(p, note, c, r0, n, on_cc, s_v, s_b, s_z);
+          if (z_of != 0) {
+            // one run: its columns lie together
+            const int f = __ffs(static_cast<int>(z_of)) - 1, base = __shfl_sync(kFull, zc, f) - f;
+            const bool one = __all_sync(kFull, zc < 0 || zc - (lane & 15) == base) &&
+                             static_cast<int>(zbase) + base + 16 <= kTmemCols;
+            if (one) {
+              float z[16];
+              tmem_ld16(tmem + static_cast<uint32_t>(static_cast<int>(zbase) + base) + lane_off, z);
+              tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (on_cc >> j & 1u) acc[j] += s_z[j * kEpi + tid];
-        }
-        if (n < p.n) {
-          const int64_t at = static_cast<int64_t>(r0 + c * 32) * p.out_stride + n;
-          if (p.out_bf16) {
+              for (int j = 0; j < 16; ++j)
+                if (z_of >> j & 1u) acc[c * 16 + j] += z[j];
+            } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (live >> j & 1u) static_cast<__nv_bfloat16*>(p.out)[at + j * p.out_stride] = __float2bfloat16_rn(acc[j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (live >> j & 1u) static_cast<float*>(p.out)[at + j * p.out_stride] = acc[j];
+              for (int j = 0; j < 16; ++j)
+                if (z_of >> j & 1u)
+                  acc[c * 16 + j] += tmem_ld1(tmem + zbase + static_cast<uint32_t>(__shfl_sync(kFull, zc, j)) + lane_off);
+            }
           }
         }
       }
+      // accumulator and z may be overwritten
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive_remote(map_shared_rank(&acc_empty[buf], 0));
-        mbar_arrive(&note_empty[buf]);
+      if (lane == 0) arrive_relaxed(map_shared_rank(acc_empty, 0));
+      if (q.parts > 0) {
+        // rows whose runs found no columns, four at a time
+        for (int c = 0; c < chunks; ++c) {
+          const int t = t0 + c * 16 + (lane & 15);
+          uint32_t left = __ballot_sync(kFull, note.ad[t] >= 0 && note.zcol[t] < 0) & 0xffffu;
+          while (left != 0) {
+            int row[4];
+            float z[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              row[u] = __ffs(static_cast<int>(left)) - 1;   // -1: none left
+              left &= left - 1;
+              z[u] = 0.f;
+            }
+            z_of_rows(p, note, t0 + c * 16, r0 + c * 16, n, row, z);
+#pragma unroll
+            for (int j = 0; j < kMaxNb / 2; ++j)
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (row[u] >= 0 && c * 16 + row[u] == j) acc[j] += z[u];
+          }
+        }
       }
+#pragma unroll
+      for (int c = 0; c < kMaxNb / 32; ++c) {
+        if (c < chunks) {
+          if (n < p.n) {
+            const int64_t at = static_cast<int64_t>(r0 + c * 16) * p.out_stride + n;
+            if (p.out_bf16) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (live[c] >> j & 1u)
+                  static_cast<__nv_bfloat16*>(p.out)[at + j * p.out_stride] = __float2bfloat16_rn(acc[c * 16 + j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (live[c] >> j & 1u) static_cast<float*>(p.out)[at + j * p.out_stride] = acc[c * 16 + j];
+            }
+          }
+        }
+      }
+      note_done(i);
     }
   }
   __syncwarp();
   tc_fence_before();
   // no CTA leaves while the other may still signal it, read its operands or land in its memory
   cluster_sync_all();
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
   }
 }
 
-constexpr int kBars = (3 * kMaxStages + 8) * 8 + 16;
+constexpr int kBars = (4 * kMaxStages + 6) * 8 + 16;
 
 template <bool E4M3>
 size_t configure(int dev) {
@@ -600,24 +612,26 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
   q.n_nt = (p.n + 2 * kM - 1) / (2 * kM);
   q.n_chunks = (p.k * es + kRowBytes - 1) / kRowBytes;
   q.flat = p.k * es % kRowBytes != 0;
-  q.n_rt = (p.rows + kMaxNb - 1) / kMaxNb;
-  q.nb = ((p.rows + q.n_rt - 1) / q.n_rt + 31) / 32 * 32;
+  // The rows a tile that make the least of waves times a tile's time: products (2 nb clocks a column
+  // of 128 bytes) or L2 (256 + nb), and about 1500 clocks of a tile's ends.
+  int64_t best = INT64_MAX;
+  for (int nb = 96; nb <= kMaxNb; nb += 32) {
+    const int64_t tiles = static_cast<int64_t>(q.n_nt) * ((p.rows + nb - 1) / nb);
+    const int64_t cost = (tiles + n_pairs - 1) / n_pairs * (static_cast<int64_t>(q.n_chunks) * (2 * nb > 256 + nb ? 2 * nb : 256 + nb) + 1500);
+    if (cost <= best) {
+      best = cost;
+      q.nb = nb;
+    }
+  }
   q.n_rt = (p.rows + q.nb - 1) / q.nb;
   q.n_tiles = q.n_nt * q.n_rt;
   q.parts = rm == 0 ? 0 : p.out_bf16 ? 2 : 3;
-  const int v = 32 * rm * 4, b = rm > 0 ? kRing * kEpi * 16 : 0, z = rm > 0 ? 32 * kEpi * 4 : 0;
-  const int left = static_cast<int>(budget) - 1024 - v - b - z - kBars;
-  // larger copies stream faster: two columns of K a stage where three such stages fit
-  for (q.ch = 2; q.ch >= 1; --q.ch) {
-    const int stage = q.ch * (kWChunk + q.nb / 2 * kRowBytes);
-    q.stages = left / stage > kMaxStages ? kMaxStages : left / stage;
-    q.v_off = q.stages * stage;
-    if (q.stages >= 3) break;
-  }
-  if (q.ch < 1) return cudaErrorInvalidConfiguration;
-  q.b_off = q.v_off + v;
-  q.z_off = q.b_off + b;
-  q.bar_off = q.z_off + z;
+  const int left = static_cast<int>(budget) - 1024 - kBars;
+  // larger copies stream faster: two columns of K a stage
+  q.ch = 2;
+  const int stage = q.ch * (kWChunk + q.nb / 2 * kRowBytes);
+  q.stages = left / stage > kMaxStages ? kMaxStages : left / stage;
+  q.bar_off = q.stages * stage;
   q.smem = 1024 + q.bar_off + kBars;
   CUtensorMap wmap, xmap, bmap, vmap;
   if (!encode(&wmap, p.w, es, p.k, p.k, p.n, kM, q.ch, q.flat) ||
@@ -637,11 +651,12 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// Whether the pairs' tiles fill the device: fewer leave SMs idle, which smaller tiles split over K
-// do not.
-bool project_is_many(int rows, int n) {
-  const int64_t tiles = static_cast<int64_t>((n + 2 * kM - 1) / (2 * kM)) * ((rows + kMaxNb - 1) / kMaxNb);
-  return rows > kMaxNb && tiles >= sm_count() / 2;
+// Whether the pairs' tiles of 160 rows would fill the device, which smaller tiles split over K do
+// for fewer rows; and whether requests have 32 rows and more, as runs need.
+bool project_is_many(const ProjectParams& p) {
+  const int64_t tiles = static_cast<int64_t>((p.n + 2 * kM - 1) / (2 * kM)) * ((p.rows + 159) / 160);
+  return p.rows > 256 && tiles >= sm_count() / 2 &&
+         (p.ad.n_adapters == 0 || (p.row_stream != nullptr && p.n_streams <= p.rows / 32));
 }
 
 cudaError_t launch_project_many(const ProjectParams& p, cudaStream_t s) {

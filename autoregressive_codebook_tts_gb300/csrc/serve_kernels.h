@@ -85,7 +85,7 @@ cudaError_t launch_kv_slots(const KvSlotsParams& p, cudaStream_t s);
 bool project_tc(int rows);
 size_t project_workspace(int rows, int rank_max);
 cudaError_t launch_shrink(const ProjectParams& p, cudaStream_t s);
-bool project_is_many(int rows, int n);
+bool project_is_many(const ProjectParams& p);
 cudaError_t launch_project_many(const ProjectParams& p, cudaStream_t s);
 cudaError_t launch_project(const ProjectParams& p, void* workspace, cudaStream_t s);
 
