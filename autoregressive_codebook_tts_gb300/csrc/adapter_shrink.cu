@@ -88,9 +88,9 @@ struct ShrinkPlan {
 struct RowNotes {
   int ad[kM];
   int rank[kM];
-  int slot[kM];        // which of the tile's adapters
-  int slot_ad[kM];
-  int first[4];        // adapters first seen in each warp's rows
+  int run_ad[kM];      // adapters of the tile's runs of rows, in order
+  int slot_ad[kM];     // and each of them once
+  int first[4], leads[4];   // how many of them each warp's threads hold
 };
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) shrink_tc_kernel(const __grid_con
 
   if (tid == 0) {
     for (int i = 0; i < q.stages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 2);   // x, and the adapters' rows
       mbar_init(&wide[i], 4);
       mbar_init(&empty[i], 1);
     }
@@ -158,7 +158,6 @@ __global__ void __launch_bounds__(kThreads, 1) shrink_tc_kernel(const __grid_con
   grid_launch_dependents();
 
   // ---- the rows' adapters, and the tile's list of them
-  int n_slots = 0;
   if (warp < 4) {
     const int r = r0 + tid;
     int bad = 0, a = -2, k = 0;
@@ -178,25 +177,39 @@ __global__ void __launch_bounds__(kThreads, 1) shrink_tc_kernel(const __grid_con
       low = min(low, __shfl_xor_sync(kFull, low, o));
     }
     if (rank == 0 && (lane & 15) == 0 && r < p.rows) p.block_ad[r / 16] = top < 0 ? -1 : top == low ? top : -2;
-    named_barrier(1, kRows);
-    // first of its adapter among the tile's rows: only the first of a run has to look
+    // the runs' adapters in order, then those among them that no earlier run has
     const int prev = __shfl_up_sync(kFull, a, 1);
-    bool leads = a >= 0 && (lane == 0 || prev != a);
-    if (leads)
-      for (int u = 0; u < tid; ++u)
-        if (s_row.ad[u] == a) {
-          leads = false;
-          break;
-        }
+    const bool edge = a >= 0 && (lane == 0 || prev != a);
+    const uint32_t e = __ballot_sync(kFull, edge);
+    if (lane == 0) s_row.first[warp] = __popc(e);
+    named_barrier(1, kRows);
+    int at = __popc(e & ((1u << lane) - 1)), edges = 0;
+    for (int w = 0; w < 4; ++w) {
+      at += w < warp ? s_row.first[w] : 0;
+      edges += s_row.first[w];
+    }
+    if (edge) s_row.run_ad[at] = a;
+    named_barrier(1, kRows);
+    const int mine = tid < edges ? s_row.run_ad[tid] : -1;
+    bool leads = mine >= 0;
+    for (int u = 0; u < tid && leads; ++u) leads = s_row.run_ad[u] != mine;
     const uint32_t m = __ballot_sync(kFull, leads);
-    if (lane == 0) s_row.first[warp] = __popc(m);
+    if (lane == 0) s_row.leads[warp] = __popc(m);
     named_barrier(1, kRows);
     int base = 0;
-    for (int w = 0; w < warp; ++w) base += s_row.first[w];
-    if (leads) s_row.slot_ad[base + __popc(m & ((1u << lane) - 1))] = a;
+    for (int w = 0; w < warp; ++w) base += s_row.leads[w];
+    if (leads) s_row.slot_ad[base + __popc(m & ((1u << lane) - 1))] = mine;
+  } else if (warp == 4 && lane == 0) {
+    // rows of x need no notes
+    const int n = nc < q.stages ? nc : q.stages;
+    for (int i = 0; i < n; ++i) {
+      unsigned char* x = smem + i * kStage;
+      mbar_arrive_expect_tx(&full[i], static_cast<uint32_t>(E4M3 ? kRawBytes : kXBytes));
+      tma_load(E4M3 ? x + kXBytes + kStackBytes : x, &xmap, (c0 + i) * 64, r0, 0, &full[i]);
+    }
   }
   __syncthreads();
-  n_slots = s_row.first[0] + s_row.first[1] + s_row.first[2] + s_row.first[3];
+  const int n_slots = s_row.leads[0] + s_row.leads[1] + s_row.leads[2] + s_row.leads[3];
   const int passes = (n_slots + q.per_pass - 1) / q.per_pass;
 
   if (warp == 4) {
@@ -214,14 +227,19 @@ __global__ void __launch_bounds__(kThreads, 1) shrink_tc_kernel(const __grid_con
           }
           unsigned char* x = smem + s * kStage;
           unsigned char* st = x + kXBytes;
-          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>((E4M3 ? kRawBytes : kXBytes) + cnt * rm * kRowBytes));
-          tma_load(E4M3 ? st + kStackBytes : x, &xmap, (c0 + i) * 64, r0, 0, &full[s]);
+          if (it >= min(nc, q.stages)) {   // (the first were asked for above)
+            mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(E4M3 ? kRawBytes : kXBytes));
+            tma_load(E4M3 ? st + kStackBytes : x, &xmap, (c0 + i) * 64, r0, 0, &full[s]);
+          }
+          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(cnt * rm * kRowBytes));
           for (int k = 0; k < cnt; ++k)
             tma_load(st + k * rm * kRowBytes, &amap, (c0 + i) * 64, s_row.slot_ad[ps * q.per_pass + k] * rm, 0, &full[s]);
         }
       }
       if (!ok) set_err(p.err, TTS_EFLAG_TIMEOUT);
       // no copy may still be landing when the CTA leaves
+      if (passes == 0)   // (rows of x that nothing reads: their second arrivals are missing)
+        for (; it < min(nc, q.stages); ++it) mbar_arrive(&full[it]);
       for (int t = max(0, it - q.stages); t < it; ++t) mbar_wait(&full[t % q.stages], static_cast<uint32_t>(t / q.stages) & 1u);
     }
     __syncwarp();

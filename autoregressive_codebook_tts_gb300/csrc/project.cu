@@ -77,11 +77,6 @@ __device__ __forceinline__ bool next_run(int mine, int blocks, int at, BlockRun&
   return true;
 }
 
-__device__ __forceinline__ void store_out(const ProjectParams& p, int64_t at, float y) {
-  if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
-  else static_cast<float*>(p.out)[at] = y;
-}
-
 struct TileInfo {
   int ad[256];       // adapter of the tile's rows: -1 none, -2 no request
   int rank[256];

@@ -44,9 +44,13 @@ struct Notes {
   int ad[kMaxNb];           // -1 none, -2 no request
   int rank[kMaxNb];
   int zcol[kMaxNb];         // the row's column of z, -1 none
-  float sx[kMaxNb];
+  __align__(16) float sx[kMaxNb];
   int run_ad[kMaxRuns], run_rank[kMaxRuns], run_first[kMaxRuns], run_n[kMaxRuns], run_col[kMaxRuns];
   int n_runs;
+  // of each 16 rows: those of requests and not on the CUDA cores, those that have columns of z, and
+  // the first one's column (-1: the columns do not lie together), those on the CUDA cores
+  uint32_t live[kMaxNb / 16], z_of[kMaxNb / 16], cores[kMaxNb / 16];
+  int z_at[kMaxNb / 16];
 };
 
 // ---- pairs of CTAs
@@ -218,6 +222,41 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
     for (int tile = pair; tile < q.n_tiles && ok; tile += pairs, ++i) {
       const int rt = tile % q.n_rt, nt = tile / q.n_rt;
       const int w0 = nt * 2 * kM + rank * kM, x0 = rt * q.nb + rank * half;
+      if (q.parts > 0) {
+        // B rows and v's parts of the tile's runs, 64 ranks a stage, ahead of the shared operands:
+        // they arrive while the last tile is finished
+        if (i == 0) grid_wait();
+        ok = note_wait(i);
+        const Notes& note = s_note[i & 1];
+        const int runs = ok ? note.n_runs : 0;
+        for (int k = 0; k < runs && ok; ++k) {
+          const int n2 = note.run_n[k] / 2, bytes = kWChunk + q.parts * n2 * kRowBytes;
+          for (int j = 0; j < note.run_rank[k]; j += 64, ++it) {
+            ok = next_stage();
+            if (!ok) break;
+            if (lane == 0) {
+              const int s = it % q.stages;
+              unsigned char* w = smem + s * stage_bytes;
+              // where zeros have to be written first the stage is announced here, else with the pair's
+              uint32_t bar = smem_u32(&zl[s]);
+              if (min(64, note.run_rank[k] - j) % 16 == 0) {
+                bar = map_shared_rank(&full[s], 0);
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(2 * bytes));
+              } else {
+                mbar_arrive_expect_tx(&zl[s], static_cast<uint32_t>(bytes));
+              }
+              tma_load2(w, &bmap, j, note.run_ad[k] * p.n + w0, 0, bar);
+              for (int h = 0; h < q.parts; ++h)
+                for (int t = 0; t < n2; t += 16)
+                  tma_load2(w + kWChunk + h * x_chunk + t * kRowBytes, &vmap, j,
+                            rt * q.nb + note.run_first[k] + rank * n2 + t, h, bar);
+            }
+            __syncwarp();
+          }
+        }
+        note_done(i);
+        if (!ok) break;
+      }
       for (int st = 0; st < nst; ++st, ++it) {
         ok = next_stage();
         if (!ok) break;
@@ -241,28 +280,6 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
         }
         __syncwarp();
       }
-      if (q.parts == 0 || !ok) continue;
-      if (i == 0) grid_wait();   // v's parts
-      ok = note_wait(i);
-      const Notes& note = s_note[i & 1];
-      const int runs = ok ? note.n_runs : 0;
-      for (int k = 0; k < runs && ok; ++k)
-        for (int j = 0; j < note.run_rank[k] && ok; j += 64)
-          for (int h = 0; h < q.parts; ++h, ++it) {
-            ok = next_stage();
-            if (!ok) break;
-            if (lane == 0) {
-              const int s = it % q.stages, n2 = note.run_n[k] / 2;
-              unsigned char* w = smem + s * stage_bytes;
-              unsigned char* x = w + q.ch * kWChunk;
-              mbar_arrive_expect_tx(&zl[s], static_cast<uint32_t>(kWChunk + n2 * kRowBytes));
-              tma_load(w, &bmap, j, note.run_ad[k] * p.n + w0, 0, &zl[s]);
-              for (int t = 0; t < n2; t += 16)
-                tma_load(x + t * kRowBytes, &vmap, j, rt * q.nb + note.run_first[k] + rank * n2 + t, h, &zl[s]);
-            }
-            __syncwarp();
-          }
-      note_done(i);
     }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
     // no copy may still be landing, and no product reading, when the CTA leaves
@@ -287,6 +304,33 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
         break;
       }
       tc_fence_after();
+      if (q.parts > 0) {
+        ok = note_wait(i);
+        const Notes& note = s_note[i & 1];
+        const int runs = ok ? note.n_runs : 0;
+        for (int k = 0; k < runs && ok; ++k) {
+          const uint32_t zi = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(note.run_n[k] >> 3) << 17) |
+                              (static_cast<uint32_t>(2 * kM >> 4) << 24);
+          const int ranks = note.run_rank[k];
+          const uint32_t zd = tmem + zbase + static_cast<uint32_t>(note.run_col[k]);
+          for (int j = 0; j < ranks; j += 64, ++it) {
+            const int s = it % q.stages;
+            if (!warp_wait(&full[s], static_cast<uint32_t>(it / q.stages) & 1u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t w = smem_u32(smem + s * stage_bytes);
+            const int steps = (min(64, ranks - j) + 15) / 16;
+            for (int h = 0; h < q.parts; ++h) {
+              const uint64_t ad = smem_desc(w), bd = smem_desc(w + static_cast<uint32_t>(kWChunk + h * x_chunk));
+              for (int e = 0; e < steps; ++e) mma2<false>(zd, ad + 2 * e, bd + 2 * e, zi, j > 0 || h > 0 || e > 0);
+            }
+            commit2(&empty[s]);
+          }
+        }
+        note_done(i);
+      }
       for (int st = 0; st < nst; ++st, ++it) {
         const int s = it % q.stages;
         if (!warp_wait(&full[s], static_cast<uint32_t>(it / q.stages) & 1u)) {
@@ -301,32 +345,6 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
           for (int k = 0; k < kRowBytes / 32; ++k) mma2<E4M3>(tmem, ad + 2 * k, bd + 2 * k, idesc, st > 0 || c > 0 || k > 0);
         }
         commit2(&empty[s]);
-      }
-      if (q.parts > 0 && ok) {
-        ok = note_wait(i);
-        const Notes& note = s_note[i & 1];
-        const int runs = ok ? note.n_runs : 0;
-        for (int k = 0; k < runs && ok; ++k) {
-          const uint32_t zi = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(note.run_n[k] >> 3) << 17) |
-                              (static_cast<uint32_t>(2 * kM >> 4) << 24);
-          const int ranks = note.run_rank[k];
-          const uint32_t zd = tmem + zbase + static_cast<uint32_t>(note.run_col[k]);
-          for (int j = 0; j < ranks && ok; j += 64)
-            for (int h = 0; h < q.parts; ++h, ++it) {
-              const int s = it % q.stages;
-              if (!warp_wait_cluster(&full[s], static_cast<uint32_t>(it / q.stages) & 1u)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t w = smem_u32(smem + s * stage_bytes);
-              const uint64_t ad = smem_desc(w), bd = smem_desc(w + static_cast<uint32_t>(q.ch * kWChunk));
-              const int steps = (min(64, ranks - j) + 15) / 16;
-              for (int e = 0; e < steps; ++e) mma2<false>(zd, ad + 2 * e, bd + 2 * e, zi, j > 0 || h > 0 || e > 0);
-              commit2(&empty[s]);
-            }
-        }
-        note_done(i);
       }
       commit2(acc_full);
     }
@@ -409,6 +427,21 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
             first = end;
           }
         }
+      __syncwarp();
+      for (int c = 0; c < q.nb / 16; ++c) {
+        const int t = c * 16 + (lane & 15), a = note.ad[t], zc = note.zcol[t];
+        const uint32_t with = __ballot_sync(kFull, zc >= 0) & 0xffffu;
+        const uint32_t cores = q.parts > 0 ? __ballot_sync(kFull, a >= 0 && zc < 0) & 0xffffu : 0u;
+        const uint32_t live = __ballot_sync(kFull, a != -2) & 0xffffu & ~cores;
+        const int f = with != 0 ? __ffs(static_cast<int>(with)) - 1 : 0, base = __shfl_sync(kFull, zc, f) - f + static_cast<int>(zbase);
+        const bool one = __all_sync(kFull, zc < 0 || zc - (lane & 15) + static_cast<int>(zbase) == base);
+        if (lane == 0) {
+          note.live[c] = live;
+          note.z_of[c] = with;
+          note.cores[c] = cores;
+          note.z_at[c] = one && base + 16 <= kTmemCols ? base : -1;
+        }
+      }
       if (lane == 0) note.n_runs = n_runs;
       __syncwarp();
       if (lane == 0) mbar_arrive(&note_full[i & 1]);
@@ -421,41 +454,38 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
     uint32_t phase = 0;   // of each stage's zl (and zr)
     if (q.parts > 0)
       for (int tile = pair; tile < q.n_tiles && ok; tile += pairs, ++i) {
-        it += nst;
         ok = note_wait(i);
         const Notes& note = s_note[i & 1];
         const int runs = ok ? note.n_runs : 0;
         for (int k = 0; k < runs && ok; ++k) {
           const int ranks = note.run_rank[k];
-          for (int j = 0; j < ranks && ok; j += 64)
-            for (int h = 0; h < q.parts; ++h, ++it) {
-              const int s = it % q.stages;
-              if (!warp_wait(&zl[s], phase >> s & 1u)) {
+          for (int j = 0; j < ranks; j += 64, ++it) {
+            const int s = it % q.stages, left = min(64, ranks - j);
+            if (left % 16 == 0) continue;
+            if (!warp_wait(&zl[s], phase >> s & 1u)) {
+              ok = false;
+              break;
+            }
+            unsigned char* b = smem + s * stage_bytes;
+            for (int m = lane; m < kM; m += 32)
+              for (int e = left; e < ((left + 15) & ~15); ++e)
+                *reinterpret_cast<uint16_t*>(b + m * kRowBytes + (((e >> 3) ^ (m & 7)) << 4) + (e & 7) * 2) = 0;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (rank == 0) {
+              // both CTAs' operands: the products may read them
+              if (!warp_wait_cluster(&zr[s], phase >> s & 1u)) {
                 ok = false;
                 break;
               }
-              const int left = min(64, ranks - j);
-              if (left % 16 != 0) {
-                unsigned char* b = smem + s * stage_bytes;
-                for (int m = lane; m < kM; m += 32)
-                  for (int e = left; e < ((left + 15) & ~15); ++e)
-                    *reinterpret_cast<uint16_t*>(b + m * kRowBytes + (((e >> 3) ^ (m & 7)) << 4) + (e & 7) * 2) = 0;
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              }
-              __syncwarp();
-              if (rank == 0) {
-                // both CTAs' operands: the products may read them
-                if (!warp_wait_cluster(&zr[s], phase >> s & 1u)) {
-                  ok = false;
-                  break;
-                }
-                if (lane == 0) mbar_arrive(&full[s]);
-              } else if (lane == 0) {
-                mbar_arrive_remote(map_shared_rank(&zr[s], 0));
-              }
-              phase ^= 1u << s;
+              if (lane == 0) mbar_arrive(&full[s]);
+            } else if (lane == 0) {
+              mbar_arrive_remote(map_shared_rank(&zr[s], 0));
             }
+            phase ^= 1u << s;
+          }
         }
+        it += nst;
         note_done(i);
       }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
@@ -478,37 +508,56 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
         break;
       }
       tc_fence_after();
+      // rows whose runs found no columns, four at a time, finished by themselves
+      for (int c = 0; c < chunks; ++c) {
+        for (uint32_t left = note.cores[t0 / 16 + c]; left != 0;) {
+          int row[4];
+          float z[4] = {};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            row[u] = __ffs(static_cast<int>(left)) - 1;   // -1: none left
+            left &= left - 1;
+          }
+          z_of_rows(p, note, t0 + c * 16, r0 + c * 16, n, row, z);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (row[u] >= 0) {
+              float y = tmem_ld1(tmem + static_cast<uint32_t>(t0 + c * 16 + row[u]) + lane_off);
+              if (E4M3) y *= note.sx[t0 + c * 16 + row[u]] * sw;
+              if (n < p.n) store_out(p, static_cast<int64_t>(r0 + c * 16 + row[u]) * p.out_stride + n, y + z[u]);
+            }
+        }
+      }
       float acc[kMaxNb / 2];
 #pragma unroll
       for (int c = 0; c < kMaxNb / 32; ++c)
         if (c < chunks) tmem_ld16(tmem + static_cast<uint32_t>(t0 + c * 16) + lane_off, acc + c * 16);
       tmem_wait_ld();
-      uint32_t live[kMaxNb / 32];   // rows of requests
 #pragma unroll
       for (int c = 0; c < kMaxNb / 32; ++c) {
-        live[c] = 0;
         if (c < chunks) {
-          const int t = t0 + c * 16 + (lane & 15);
-          const int a = note.ad[t], zc = note.zcol[t];
-          live[c] = __ballot_sync(kFull, a != -2) & 0xffffu;
-          const uint32_t z_of = __ballot_sync(kFull, zc >= 0) & 0xffffu;
+          const uint32_t z_of = note.z_of[t0 / 16 + c];
+          const int z_at = note.z_at[t0 / 16 + c];
           if (E4M3) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[c * 16 + j] *= note.sx[t0 + c * 16 + j] * sw;
+            for (int j = 0; j < 16; j += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&note.sx[t0 + c * 16 + j]);
+              acc[c * 16 + j] *= f.x * sw;
+              acc[c * 16 + j + 1] *= f.y * sw;
+              acc[c * 16 + j + 2] *= f.z * sw;
+              acc[c * 16 + j + 3] *= f.w * sw;
+            }
           }
           if (z_of != 0) {
-            // one run: its columns lie together
-            const int f = __ffs(static_cast<int>(z_of)) - 1, base = __shfl_sync(kFull, zc, f) - f;
-            const bool one = __all_sync(kFull, zc < 0 || zc - (lane & 15) == base) &&
-                             static_cast<int>(zbase) + base + 16 <= kTmemCols;
-            if (one) {
+            if (z_at >= 0) {
               float z[16];
-              tmem_ld16(tmem + static_cast<uint32_t>(static_cast<int>(zbase) + base) + lane_off, z);
+              tmem_ld16(tmem + static_cast<uint32_t>(z_at) + lane_off, z);
               tmem_wait_ld();
 #pragma unroll
               for (int j = 0; j < 16; ++j)
                 if (z_of >> j & 1u) acc[c * 16 + j] += z[j];
             } else {
+              const int zc = note.zcol[t0 + c * 16 + (lane & 15)];
 #pragma unroll
               for (int j = 0; j < 16; ++j)
                 if (z_of >> j & 1u)
@@ -521,43 +570,21 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_relaxed(map_shared_rank(acc_empty, 0));
-      if (q.parts > 0) {
-        // rows whose runs found no columns, four at a time
-        for (int c = 0; c < chunks; ++c) {
-          const int t = t0 + c * 16 + (lane & 15);
-          uint32_t left = __ballot_sync(kFull, note.ad[t] >= 0 && note.zcol[t] < 0) & 0xffffu;
-          while (left != 0) {
-            int row[4];
-            float z[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              row[u] = __ffs(static_cast<int>(left)) - 1;   // -1: none left
-              left &= left - 1;
-              z[u] = 0.f;
-            }
-            z_of_rows(p, note, t0 + c * 16, r0 + c * 16, n, row, z);
-#pragma unroll
-            for (int j = 0; j < kMaxNb / 2; ++j)
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (row[u] >= 0 && c * 16 + row[u] == j) acc[j] += z[u];
-          }
-        }
-      }
 #pragma unroll
       for (int c = 0; c < kMaxNb / 32; ++c) {
         if (c < chunks) {
+          const uint32_t live = note.live[t0 / 16 + c];
           if (n < p.n) {
             const int64_t at = static_cast<int64_t>(r0 + c * 16) * p.out_stride + n;
             if (p.out_bf16) {
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                if (live[c] >> j & 1u)
+                if (live >> j & 1u)
                   static_cast<__nv_bfloat16*>(p.out)[at + j * p.out_stride] = __float2bfloat16_rn(acc[c * 16 + j]);
             } else {
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                if (live[c] >> j & 1u) static_cast<float*>(p.out)[at + j * p.out_stride] = acc[c * 16 + j];
+                if (live >> j & 1u) static_cast<float*>(p.out)[at + j * p.out_stride] = acc[c * 16 + j];
             }
           }
         }

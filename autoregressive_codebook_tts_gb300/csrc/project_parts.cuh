@@ -119,6 +119,11 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ void store_out(const ProjectParams& p, int64_t at, float y) {
+  if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+  else static_cast<float*>(p.out)[at] = y;
+}
+
 // Eight entries of B as four pairs, zero from the rank on.
 __device__ __forceinline__ void b_pairs(const uint4 w, int left, float2 (&b)[4]) {
   float f[8];
