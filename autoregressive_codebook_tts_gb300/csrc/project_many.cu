@@ -4,9 +4,11 @@
 // them: an SM takes 64 bytes a clock from L2.  Two CTAs therefore share a tile of 256 rows of W by up
 // to 224 rows of x (cta_group::2): each brings its own 128 rows of W and half the rows of x, which is
 // 480 clocks of L2 for 448 of products a column of 128 bytes (a CTA by itself with 160 rows: 576
-// for 320).  Accumulator and z together take all of tensor memory, so a tile's epilogue first moves
-// both into registers (eight warps, half the columns each), which frees them for the next tile's
-// products, and stores from there.
+// for 320).  Accumulator and z together take all of tensor memory, so the next tile's products wait
+// for the epilogue, which is kept short: eight warps, half the columns each, in a rolled loop (held
+// in registers by an unrolled one it took three times as long: its code outgrew the instruction
+// cache), bf16 rows stored in pairs.  A pair walks neighbouring tiles of the same rows of x, whose
+// notes it takes once.
 //
 // z = v B_a^T: rows of a tile that lie together and share an adapter are a run.  A run has columns of
 // its own (its rows, up to a multiple of 32), so its product meets no other adapter's rows, and what
@@ -38,6 +40,7 @@ struct ManyPlan {
   int n_chunks, flat;
   int parts;                // 0: no adapters
   int bar_off, smem;
+  int pair_out;             // bf16 rows start at even entries: stores of two entries
 };
 
 struct Notes {
@@ -172,7 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_rank());
+  // this pair's tiles, neighbours along W first
   const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const int tile0 = static_cast<int>(static_cast<int64_t>(pair) * q.n_tiles / pairs);
+  const int tile1 = static_cast<int>(static_cast<int64_t>(pair + 1) * q.n_tiles / pairs);
   const int nst = (q.n_chunks + q.ch - 1) / q.ch;
 
   if (tid == 0) {
@@ -219,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
       const int s = it % q.stages;
       return it < q.stages || warp_wait(&empty[s], static_cast<uint32_t>(it / q.stages - 1) & 1u);
     };
-    for (int tile = pair; tile < q.n_tiles && ok; tile += pairs, ++i) {
-      const int rt = tile % q.n_rt, nt = tile / q.n_rt;
+    for (int tile = tile0; tile < tile1 && ok; ++tile, ++i) {
+      const int rt = tile / q.n_nt, nt = tile - rt * q.n_nt;
       const int w0 = nt * 2 * kM + rank * kM, x0 = rt * q.nb + rank * half;
       if (q.parts > 0) {
         // B rows and v's parts of the tile's runs, 64 ranks a stage, ahead of the shared operands:
@@ -290,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
     int it = 0, i = 0;
     const uint32_t idesc = (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | (static_cast<uint32_t>(q.nb >> 3) << 17) |
                            (static_cast<uint32_t>(2 * kM >> 4) << 24);
-    for (int tile = pair; tile < q.n_tiles && ok; tile += pairs, ++i) {
+    for (int tile = tile0; tile < tile1 && ok; ++tile, ++i) {
       if (rank != 0) {   // the first CTA issues for both
         if (q.parts > 0) {
           ok = note_wait(i);
@@ -355,13 +361,17 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
     int i = 0;
     constexpr int kC = kMaxNb / 32;
     const int zcols = kTmemCols - q.nb;
-    for (int tile = pair; tile < q.n_tiles && ok; tile += pairs, ++i) {
+    for (int tile = tile0; tile < tile1 && ok; ++tile, ++i) {
       if (i > 1 && !warp_wait(&note_empty[i & 1], static_cast<uint32_t>(i / 2 - 1) & 1u)) {
         ok = false;
         break;
       }
       Notes& note = s_note[i & 1];
-      const int r0 = (tile % q.n_rt) * q.nb;
+      if (i > 1 && tile / q.n_nt == (tile - 2) / q.n_nt) {   // the same rows
+        if (lane == 0) mbar_arrive(&note_full[i & 1]);
+        continue;
+      }
+      const int r0 = tile / q.n_nt * q.nb;
       int ad[kC], k[kC];
       float sx[kC];
 #pragma unroll
@@ -453,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
     int it = 0, i = 0;
     uint32_t phase = 0;   // of each stage's zl (and zr)
     if (q.parts > 0)
-      for (int tile = pair; tile < q.n_tiles && ok; tile += pairs, ++i) {
+      for (int tile = tile0; tile < tile1 && ok; ++tile, ++i) {
         ok = note_wait(i);
         const Notes& note = s_note[i & 1];
         const int runs = ok ? note.n_runs : 0;
@@ -496,10 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
     const int t0 = warp < 4 ? 0 : half, chunks = half / 16;   // this warp's columns
     bool ok = true;
     int i = 0;
-    for (int tile = pair; tile < q.n_tiles && ok; tile += pairs, ++i) {
-      const int rt = tile % q.n_rt, nt = tile / q.n_rt, r0 = rt * q.nb + t0;
+    for (int tile = tile0; tile < tile1 && ok; ++tile, ++i) {
+      const int rt = tile / q.n_nt, nt = tile - rt * q.n_nt, r0 = rt * q.nb + t0;
       const int n = nt * 2 * kM + rank * kM + (warp & 3) * 32 + lane;
       const float sw = E4M3 && n < p.n ? __ldcg(p.w_scale + n) : 0.f;
+      const bool whole = __all_sync(kFull, n < p.n);
       const Notes& note = s_note[i & 1];
       ok = note_wait(i);
       ok = warp_wait(acc_full, static_cast<uint32_t>(i) & 1u) && ok;
@@ -528,65 +539,83 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
             }
         }
       }
-      float acc[kMaxNb / 2];
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        float acc[16];
+        const uint32_t z_of = note.z_of[t0 / 16 + c], live = note.live[t0 / 16 + c];
+        const int z_at = note.z_at[t0 / 16 + c];
+        tmem_ld16(tmem + static_cast<uint32_t>(t0 + c * 16) + lane_off, acc);
+        float z[16];
+        if (z_of != 0 && z_at >= 0) tmem_ld16(tmem + static_cast<uint32_t>(z_at) + lane_off, z);
+        tmem_wait_ld();
+        if (c == chunks - 1 && (z_of == 0 || z_at >= 0)) {
+          // accumulator and z may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_relaxed(map_shared_rank(acc_empty, 0));
+        }
+        if (E4M3) {
+          const float2 w2 = make_float2(sw, sw);
 #pragma unroll
-      for (int c = 0; c < kMaxNb / 32; ++c)
-        if (c < chunks) tmem_ld16(tmem + static_cast<uint32_t>(t0 + c * 16) + lane_off, acc + c * 16);
-      tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < kMaxNb / 32; ++c) {
-        if (c < chunks) {
-          const uint32_t z_of = note.z_of[t0 / 16 + c];
-          const int z_at = note.z_at[t0 / 16 + c];
-          if (E4M3) {
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&note.sx[t0 + c * 16 + j]);
-              acc[c * 16 + j] *= f.x * sw;
-              acc[c * 16 + j + 1] *= f.y * sw;
-              acc[c * 16 + j + 2] *= f.z * sw;
-              acc[c * 16 + j + 3] *= f.w * sw;
-            }
-          }
-          if (z_of != 0) {
-            if (z_at >= 0) {
-              float z[16];
-              tmem_ld16(tmem + static_cast<uint32_t>(z_at) + lane_off, z);
-              tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (z_of >> j & 1u) acc[c * 16 + j] += z[j];
-            } else {
-              const int zc = note.zcol[t0 + c * 16 + (lane & 15)];
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (z_of >> j & 1u)
-                  acc[c * 16 + j] += tmem_ld1(tmem + zbase + static_cast<uint32_t>(__shfl_sync(kFull, zc, j)) + lane_off);
-            }
+          for (int j = 0; j < 16; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&note.sx[t0 + c * 16 + j]);
+            const float2 u = __fmul2_rn(make_float2(acc[j], acc[j + 1]), __fmul2_rn(make_float2(f.x, f.y), w2));
+            const float2 v = __fmul2_rn(make_float2(acc[j + 2], acc[j + 3]), __fmul2_rn(make_float2(f.z, f.w), w2));
+            acc[j] = u.x;
+            acc[j + 1] = u.y;
+            acc[j + 2] = v.x;
+            acc[j + 3] = v.y;
           }
         }
-      }
-      // accumulator and z may be overwritten
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_relaxed(map_shared_rank(acc_empty, 0));
+        if (z_of != 0) {
+          if (z_at < 0) {
+            // two runs meet in these rows
+            const int zc = note.zcol[t0 + c * 16 + (lane & 15)];
 #pragma unroll
-      for (int c = 0; c < kMaxNb / 32; ++c) {
-        if (c < chunks) {
-          const uint32_t live = note.live[t0 / 16 + c];
-          if (n < p.n) {
-            const int64_t at = static_cast<int64_t>(r0 + c * 16) * p.out_stride + n;
-            if (p.out_bf16) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (live >> j & 1u)
-                  static_cast<__nv_bfloat16*>(p.out)[at + j * p.out_stride] = __float2bfloat16_rn(acc[c * 16 + j]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (live >> j & 1u) static_cast<float*>(p.out)[at + j * p.out_stride] = acc[c * 16 + j];
+            for (int j = 0; j < 16; ++j)
+              z[j] = z_of >> j & 1u ? tmem_ld1(tmem + zbase + static_cast<uint32_t>(__shfl_sync(kFull, zc, j)) + lane_off) : 0.f;
+            if (c == chunks - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) arrive_relaxed(map_shared_rank(acc_empty, 0));
             }
+          } else if (z_of != 0xffffu) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) z[j] = z_of >> j & 1u ? z[j] : 0.f;
           }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[j] += z[j];
+        }
+        const int64_t row = static_cast<int64_t>(r0 + c * 16) * p.out_stride;
+        if (live == 0xffffu && whole) {
+          if (q.pair_out) {
+            // of two rows a lane stores two neighbouring columns of one: even lanes the first row's
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + row + (lane & 1 ? p.out_stride : 0) + (n & ~1);
+            const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
+            uint32_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * j], acc[2 * j + 1]);
+              v[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = __shfl_xor_sync(kFull, v[j], 1);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) *reinterpret_cast<uint32_t*>(to + 2 * j * p.out_stride) = __byte_perm(v[j], o[j], sel);
+          } else if (p.out_bf16) {
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + row + n;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) to[j * p.out_stride] = __float2bfloat16_rn(acc[j]);
+          } else {
+            float* to = static_cast<float*>(p.out) + row + n;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) to[j * p.out_stride] = acc[j];
+          }
+        } else if (n < p.n) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (live >> j & 1u) store_out(p, row + j * p.out_stride + n, acc[j]);
         }
       }
       note_done(i);
@@ -652,6 +681,7 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
   }
   q.n_rt = (p.rows + q.nb - 1) / q.nb;
   q.n_tiles = q.n_nt * q.n_rt;
+  q.pair_out = p.out_bf16 && p.out_stride % 2 == 0;
   q.parts = rm == 0 ? 0 : p.out_bf16 ? 2 : 3;
   const int left = static_cast<int>(budget) - 1024 - kBars;
   // larger copies stream faster: two columns of K a stage
