@@ -2,13 +2,12 @@
 //
 // Many rows bound the product by the tensor cores, and those by the operands that have to reach
 // them: an SM takes 64 bytes a clock from L2.  Two CTAs therefore share a tile of 256 rows of W by up
-// to 224 rows of x (cta_group::2): each brings its own 128 rows of W and half the rows of x, which is
-// 480 clocks of L2 for 448 of products a column of 128 bytes (a CTA by itself with 160 rows: 576
-// for 320).  Accumulator and z together take all of tensor memory, so the next tile's products wait
-// for the epilogue, which is kept short: eight warps, half the columns each, in a rolled loop (held
-// in registers by an unrolled one it took three times as long: its code outgrew the instruction
-// cache), bf16 rows stored in pairs.  A pair walks neighbouring tiles of the same rows of x, whose
-// notes it takes once.
+// to 256 rows of x (cta_group::2): each brings its own 128 rows of W and half the rows of x.  The
+// accumulator is double, so that a tile's products run under the epilogue of the last one (some 6000
+// clocks, as long as the products of a tile of e4m3); with adapters that leaves room for 160 rows a
+// tile, 416 clocks of L2 for 320 of products a column of 128 bytes (224 rows and one accumulator, 480
+// for 448 with the epilogue in between, came to 71 and 197 us on the cases below).  A pair walks
+// neighbouring tiles of the same rows of x, whose notes it takes once.
 //
 // z = v B_a^T: rows of a tile that lie together and share an adapter are a run.  A run has columns of
 // its own (its rows, up to a multiple of 32), so its product meets no other adapter's rows, and what
@@ -25,13 +24,15 @@
 namespace tts {
 namespace {
 
-constexpr int kMaxNb = 224;
+constexpr int kMaxNb = 256;
 constexpr int kMaxRuns = 16;
 constexpr int kThreads = 384;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kNoteWarp = 10, kZeroWarp = 11;
 constexpr int kMaxStages = 8;
 constexpr int kTmemCols = 512;
 constexpr int kWChunk = kM * kRowBytes;
+
+constexpr int kNoZ = -1, kByRow = -2;
 
 struct ManyPlan {
   int nb;                   // rows of x a tile, a multiple of 32
@@ -40,7 +41,6 @@ struct ManyPlan {
   int n_chunks, flat;
   int parts;                // 0: no adapters
   int bar_off, smem;
-  int pair_out;             // bf16 rows start at even entries: stores of two entries
 };
 
 struct Notes {
@@ -50,9 +50,9 @@ struct Notes {
   __align__(16) float sx[kMaxNb];
   int run_ad[kMaxRuns], run_rank[kMaxRuns], run_first[kMaxRuns], run_n[kMaxRuns], run_col[kMaxRuns];
   int n_runs;
-  // of each 16 rows: those of requests and not on the CUDA cores, those that have columns of z, and
-  // the first one's column (-1: the columns do not lie together), those on the CUDA cores
-  uint32_t live[kMaxNb / 16], z_of[kMaxNb / 16], cores[kMaxNb / 16];
+  // of each 16 rows: those of requests; where z of all of them begins (kNoZ: none has any; kByRow: some
+  // have, or not in one piece, or some rows are of no request)
+  uint32_t live[kMaxNb / 16];
   int z_at[kMaxNb / 16];
 };
 
@@ -92,23 +92,26 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity) {
   return __all_sync(kFull, mbar_wait_cluster(bar, parity, kWaitLimitCycles));
 }
-// (the values may be used after tmem_wait_ld)
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
-  uint32_t r[16];
+// 16 columns of this thread's lane; to be used after a wait that names them.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(taddr) : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
-  tmem_wait_ld();
-  return __uint_as_float(r);
+__device__ __forceinline__ void tmem_wait16(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               ::"memory");
+}
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, float& v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_wait(float (&a)[4], float (&b)[4]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(a[0]), "+f"(a[1]), "+f"(a[2]), "+f"(a[3]), "+f"(b[0]), "+f"(b[1]), "+f"(b[2]), "+f"(b[3])::"memory");
 }
 
 // z of four rows of the tile (row[u] < 0: none) for output column n, on the CUDA cores.
@@ -168,8 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
   uint64_t* zr = zl + kMaxStages;                                  // (the first CTA's) ... in the second CTA
   uint64_t* empty = zr + kMaxStages;
   uint64_t* acc_full = empty + kMaxStages;
-  uint64_t* acc_empty = acc_full + 1;                              // (the first CTA's)
-  uint64_t* note_full = acc_empty + 1;
+  uint64_t* acc_empty = acc_full + 2;                              // (the first CTA's)
+  uint64_t* note_full = acc_empty + 2;
   uint64_t* note_empty = note_full + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(note_empty + 2);
 
@@ -188,9 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
       mbar_init(&zr[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 16);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 16);
       mbar_init(&note_full[i], 1);
       mbar_init(&note_empty[i], q.parts > 0 ? 11 : 8);   // epilogue 8; copies, products, zeros
     }
@@ -208,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
   if (p.ad.n_adapters == 0) grid_wait();   // (else the narrow products' kernel has waited)
   grid_launch_dependents();
 
-  const uint32_t zbase = static_cast<uint32_t>(q.nb);
+  const uint32_t zbase = static_cast<uint32_t>(2 * q.nb);
   // a tile's notes: the i-th tile of this CTA, to be given back with note_done
   auto note_wait = [&](int i) { return warp_wait(&note_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u); };
   auto note_done = [&](int i) {
@@ -228,10 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
     for (int tile = tile0; tile < tile1 && ok; ++tile, ++i) {
       const int rt = tile / q.n_nt, nt = tile - rt * q.n_nt;
       const int w0 = nt * 2 * kM + rank * kM, x0 = rt * q.nb + rank * half;
-      if (q.parts > 0) {
-        // B rows and v's parts of the tile's runs, 64 ranks a stage, ahead of the shared operands:
-        // they arrive while the last tile is finished
-        if (i == 0) grid_wait();
+      // B rows and v's parts of the tile's runs, 64 ranks a stage
+      auto copy_z = [&]() {
+        if (i == 0) grid_wait();   // (v)
         ok = note_wait(i);
         const Notes& note = s_note[i & 1];
         const int runs = ok ? note.n_runs : 0;
@@ -261,9 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
           }
         }
         note_done(i);
-        if (!ok) break;
-      }
-      for (int st = 0; st < nst; ++st, ++it) {
+      };
+      for (int st = 0; st < nst && ok; ++st, ++it) {
         ok = next_stage();
         if (!ok) break;
         if (lane == 0) {
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
         }
         __syncwarp();
       }
+      if (q.parts > 0 && ok) copy_z();
     }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
     // no copy may still be landing, and no product reading, when the CTA leaves
@@ -304,14 +306,18 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
         }
         continue;
       }
-      // the last tile's accumulator and z are in registers
-      if (i > 0 && !warp_wait_cluster(acc_empty, static_cast<uint32_t>(i - 1) & 1u)) {
+      const int buf = i & 1;
+      if (i > 1 && !warp_wait_cluster(&acc_empty[buf], static_cast<uint32_t>(i / 2 - 1) & 1u)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      if (q.parts > 0) {
+      const uint32_t d = tmem + static_cast<uint32_t>(buf * q.nb);
+      auto mma_z = [&]() {
         ok = note_wait(i);
+        // the last tile's z has to be read first
+        if (i > 0 && !warp_wait_cluster(&acc_empty[buf ^ 1], static_cast<uint32_t>((i - 1) / 2) & 1u)) ok = false;
+        tc_fence_after();
         const Notes& note = s_note[i & 1];
         const int runs = ok ? note.n_runs : 0;
         for (int k = 0; k < runs && ok; ++k) {
@@ -336,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
           }
         }
         note_done(i);
-      }
-      for (int st = 0; st < nst; ++st, ++it) {
+      };
+      for (int st = 0; st < nst && ok; ++st, ++it) {
         const int s = it % q.stages;
         if (!warp_wait(&full[s], static_cast<uint32_t>(it / q.stages) & 1u)) {
           ok = false;
@@ -348,11 +354,12 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
         for (int c = 0; c < q.ch; ++c) {
           const uint64_t ad = smem_desc(w + c * kWChunk), bd = smem_desc(x + c * x_chunk);
 #pragma unroll
-          for (int k = 0; k < kRowBytes / 32; ++k) mma2<E4M3>(tmem, ad + 2 * k, bd + 2 * k, idesc, st > 0 || c > 0 || k > 0);
+          for (int k = 0; k < kRowBytes / 32; ++k) mma2<E4M3>(d, ad + 2 * k, bd + 2 * k, idesc, st > 0 || c > 0 || k > 0);
         }
         commit2(&empty[s]);
       }
-      commit2(acc_full);
+      if (q.parts > 0 && ok) mma_z();
+      commit2(&acc_full[buf]);
     }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
   } else if (warp == kNoteWarp) {
@@ -360,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
     bool ok = true;
     int i = 0;
     constexpr int kC = kMaxNb / 32;
-    const int zcols = kTmemCols - q.nb;
+    const int zcols = kTmemCols - 2 * q.nb;
     for (int tile = tile0; tile < tile1 && ok; ++tile, ++i) {
       if (i > 1 && !warp_wait(&note_empty[i & 1], static_cast<uint32_t>(i / 2 - 1) & 1u)) {
         ok = false;
@@ -440,16 +447,12 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
       __syncwarp();
       for (int c = 0; c < q.nb / 16; ++c) {
         const int t = c * 16 + (lane & 15), a = note.ad[t], zc = note.zcol[t];
-        const uint32_t with = __ballot_sync(kFull, zc >= 0) & 0xffffu;
-        const uint32_t cores = q.parts > 0 ? __ballot_sync(kFull, a >= 0 && zc < 0) & 0xffffu : 0u;
-        const uint32_t live = __ballot_sync(kFull, a != -2) & 0xffffu & ~cores;
-        const int f = with != 0 ? __ffs(static_cast<int>(with)) - 1 : 0, base = __shfl_sync(kFull, zc, f) - f + static_cast<int>(zbase);
-        const bool one = __all_sync(kFull, zc < 0 || zc - (lane & 15) + static_cast<int>(zbase) == base);
+        const uint32_t live = __ballot_sync(kFull, a != -2) & 0xffffu;
+        const int base = __shfl_sync(kFull, zc, 0);
+        const bool none = __all_sync(kFull, a == -1 || q.parts == 0), all = __all_sync(kFull, zc >= 0 && zc - (lane & 15) == base);
         if (lane == 0) {
           note.live[c] = live;
-          note.z_of[c] = with;
-          note.cores[c] = cores;
-          note.z_at[c] = one && base + 16 <= kTmemCols ? base : -1;
+          note.z_at[c] = live != 0xffffu ? kByRow : none ? kNoZ : all ? static_cast<int>(zbase) + base : kByRow;
         }
       }
       if (lane == 0) note.n_runs = n_runs;
@@ -464,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
     uint32_t phase = 0;   // of each stage's zl (and zr)
     if (q.parts > 0)
       for (int tile = tile0; tile < tile1 && ok; ++tile, ++i) {
+        it += nst;   // (they come behind the shared operands)
         ok = note_wait(i);
         const Notes& note = s_note[i & 1];
         const int runs = ok ? note.n_runs : 0;
@@ -495,7 +499,6 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
             phase ^= 1u << s;
           }
         }
-        it += nst;
         note_done(i);
       }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
@@ -510,112 +513,102 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
       const int rt = tile / q.n_nt, nt = tile - rt * q.n_nt, r0 = rt * q.nb + t0;
       const int n = nt * 2 * kM + rank * kM + (warp & 3) * 32 + lane;
       const float sw = E4M3 && n < p.n ? __ldcg(p.w_scale + n) : 0.f;
-      const bool whole = __all_sync(kFull, n < p.n);
       const Notes& note = s_note[i & 1];
       ok = note_wait(i);
-      ok = warp_wait(acc_full, static_cast<uint32_t>(i) & 1u) && ok;
+      // (16 rows each) those taken by rows
+      const uint32_t by_row = __ballot_sync(kFull, lane < chunks && note.z_at[t0 / 16 + (lane < chunks ? lane : 0)] == kByRow);
+      ok = warp_wait(&acc_full[i & 1], static_cast<uint32_t>(i / 2) & 1u) && ok;
       if (!ok) {
         if (lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
         break;
       }
       tc_fence_after();
-      // rows whose runs found no columns, four at a time, finished by themselves
-      for (int c = 0; c < chunks; ++c) {
-        for (uint32_t left = note.cores[t0 / 16 + c]; left != 0;) {
-          int row[4];
-          float z[4] = {};
+      const uint32_t dcol = tmem + static_cast<uint32_t>((i & 1) * q.nb) + lane_off;
+      const int64_t row0 = static_cast<int64_t>(r0) * p.out_stride + n;
+      // Rows where runs meet or end, four at a time; those whose run found no columns get z here.
+#pragma unroll 1
+      for (uint32_t some = by_row; some != 0; some &= some - 1) {
+        const int c = __ffs(static_cast<int>(some)) - 1;
+#pragma unroll 1
+        for (uint32_t left = note.live[t0 / 16 + c]; left != 0;) {
+          int row[4], alone[4];
+          float y[4], z[4], zs[4] = {};
+          bool any = false;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             row[u] = __ffs(static_cast<int>(left)) - 1;   // -1: none left
             left &= left - 1;
+            const int t = t0 + c * 16 + max(row[u], 0), zc = note.zcol[t];
+            tmem_ld1(dcol + static_cast<uint32_t>(t), y[u]);
+            // (a row without z has no column there: any of the accumulator's instead)
+            tmem_ld1(zc >= 0 ? tmem + zbase + static_cast<uint32_t>(zc) + lane_off : dcol + static_cast<uint32_t>(t), z[u]);
+            alone[u] = q.parts > 0 && row[u] >= 0 && note.ad[t] >= 0 && zc < 0 ? row[u] : -1;
+            any = any || alone[u] >= 0;
           }
-          z_of_rows(p, note, t0 + c * 16, r0 + c * 16, n, row, z);
+          tmem_wait(y, z);
+          if (any) z_of_rows(p, note, t0 + c * 16, r0 + c * 16, n, alone, zs);
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             if (row[u] >= 0) {
-              float y = tmem_ld1(tmem + static_cast<uint32_t>(t0 + c * 16 + row[u]) + lane_off);
-              if (E4M3) y *= note.sx[t0 + c * 16 + row[u]] * sw;
-              if (n < p.n) store_out(p, static_cast<int64_t>(r0 + c * 16 + row[u]) * p.out_stride + n, y + z[u]);
+              const int t = t0 + c * 16 + row[u];
+              if (E4M3) y[u] *= note.sx[t] * sw;
+              y[u] += note.zcol[t] >= 0 ? z[u] : zs[u];
+              if (n < p.n) store_out(p, row0 + (c * 16 + row[u]) * p.out_stride, y[u]);
             }
         }
       }
+      // The others 16 columns at a time; the next ones' loads are in flight while these are stored.
+      float acc[16], z[16];
+      auto load = [&](int c) {
+        const int z_at = note.z_at[t0 / 16 + c];
+        if (z_at != kByRow) tmem_ld16(dcol + static_cast<uint32_t>(t0 + c * 16), acc);
+        if (z_at >= 0) tmem_ld16(tmem + static_cast<uint32_t>(z_at) + lane_off, z);
+      };
+      load(0);
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
-        float acc[16];
-        const uint32_t z_of = note.z_of[t0 / 16 + c], live = note.live[t0 / 16 + c];
         const int z_at = note.z_at[t0 / 16 + c];
-        tmem_ld16(tmem + static_cast<uint32_t>(t0 + c * 16) + lane_off, acc);
-        float z[16];
-        if (z_of != 0 && z_at >= 0) tmem_ld16(tmem + static_cast<uint32_t>(z_at) + lane_off, z);
-        tmem_wait_ld();
-        if (c == chunks - 1 && (z_of == 0 || z_at >= 0)) {
-          // accumulator and z may be overwritten
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_relaxed(map_shared_rank(acc_empty, 0));
-        }
+        tmem_wait16(acc);
+        tmem_wait16(z);
+        float y[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] = acc[j];
         if (E4M3) {
           const float2 w2 = make_float2(sw, sw);
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(&note.sx[t0 + c * 16 + j]);
-            const float2 u = __fmul2_rn(make_float2(acc[j], acc[j + 1]), __fmul2_rn(make_float2(f.x, f.y), w2));
-            const float2 v = __fmul2_rn(make_float2(acc[j + 2], acc[j + 3]), __fmul2_rn(make_float2(f.z, f.w), w2));
-            acc[j] = u.x;
-            acc[j + 1] = u.y;
-            acc[j + 2] = v.x;
-            acc[j + 3] = v.y;
+            const float2 u = __fmul2_rn(make_float2(y[j], y[j + 1]), __fmul2_rn(make_float2(f.x, f.y), w2));
+            const float2 v = __fmul2_rn(make_float2(y[j + 2], y[j + 3]), __fmul2_rn(make_float2(f.z, f.w), w2));
+            y[j] = u.x;
+            y[j + 1] = u.y;
+            y[j + 2] = v.x;
+            y[j + 3] = v.y;
           }
         }
-        if (z_of != 0) {
-          if (z_at < 0) {
-            // two runs meet in these rows
-            const int zc = note.zcol[t0 + c * 16 + (lane & 15)];
+        if (z_at >= 0) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              z[j] = z_of >> j & 1u ? tmem_ld1(tmem + zbase + static_cast<uint32_t>(__shfl_sync(kFull, zc, j)) + lane_off) : 0.f;
-            if (c == chunks - 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) arrive_relaxed(map_shared_rank(acc_empty, 0));
-            }
-          } else if (z_of != 0xffffu) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) z[j] = z_of >> j & 1u ? z[j] : 0.f;
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[j] += z[j];
+          for (int j = 0; j < 16; ++j) y[j] += z[j];
         }
-        const int64_t row = static_cast<int64_t>(r0 + c * 16) * p.out_stride;
-        if (live == 0xffffu && whole) {
-          if (q.pair_out) {
-            // of two rows a lane stores two neighbouring columns of one: even lanes the first row's
-            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + row + (lane & 1 ? p.out_stride : 0) + (n & ~1);
-            const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
-            uint32_t v[8];
+        if (c + 1 < chunks) {
+          load(c + 1);
+        } else {
+          // accumulator and z may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_relaxed(map_shared_rank(&acc_empty[i & 1], 0));
+        }
+        if (z_at != kByRow && n < p.n) {
+          const int64_t at = row0 + c * 16 * p.out_stride;
+          if (p.out_bf16) {
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + at;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * j], acc[2 * j + 1]);
-              v[j] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            uint32_t o[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = __shfl_xor_sync(kFull, v[j], 1);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) *reinterpret_cast<uint32_t*>(to + 2 * j * p.out_stride) = __byte_perm(v[j], o[j], sel);
-          } else if (p.out_bf16) {
-            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + row + n;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) to[j * p.out_stride] = __float2bfloat16_rn(acc[j]);
+            for (int j = 0; j < 16; ++j) to[j * p.out_stride] = __float2bfloat16_rn(y[j]);
           } else {
-            float* to = static_cast<float*>(p.out) + row + n;
+            float* to = static_cast<float*>(p.out) + at;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) to[j * p.out_stride] = acc[j];
+            for (int j = 0; j < 16; ++j) to[j * p.out_stride] = y[j];
           }
-        } else if (n < p.n) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (live >> j & 1u) store_out(p, row + j * p.out_stride + n, acc[j]);
         }
       }
       note_done(i);
@@ -631,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
   }
 }
 
-constexpr int kBars = (4 * kMaxStages + 6) * 8 + 16;
+constexpr int kBars = (4 * kMaxStages + 8) * 8 + 16;
 
 template <bool E4M3>
 size_t configure(int dev) {
@@ -669,11 +662,11 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
   q.n_chunks = (p.k * es + kRowBytes - 1) / kRowBytes;
   q.flat = p.k * es % kRowBytes != 0;
   // The rows a tile that make the least of waves times a tile's time: products (2 nb clocks a column
-  // of 128 bytes) or L2 (256 + nb), and about 1500 clocks of a tile's ends.
+  // of 128 bytes) or L2 (256 + nb).  With adapters two accumulators and z share tensor memory.
   int64_t best = INT64_MAX;
-  for (int nb = 96; nb <= kMaxNb; nb += 32) {
+  for (int nb = 96; nb <= (rm > 0 ? 160 : kMaxNb); nb += 32) {
     const int64_t tiles = static_cast<int64_t>(q.n_nt) * ((p.rows + nb - 1) / nb);
-    const int64_t cost = (tiles + n_pairs - 1) / n_pairs * (static_cast<int64_t>(q.n_chunks) * (2 * nb > 256 + nb ? 2 * nb : 256 + nb) + 1500);
+    const int64_t cost = (tiles + n_pairs - 1) / n_pairs * (2 * nb > 256 + nb ? 2 * nb : 256 + nb);
     if (cost <= best) {
       best = cost;
       q.nb = nb;
@@ -681,7 +674,6 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
   }
   q.n_rt = (p.rows + q.nb - 1) / q.nb;
   q.n_tiles = q.n_nt * q.n_rt;
-  q.pair_out = p.out_bf16 && p.out_stride % 2 == 0;
   q.parts = rm == 0 ? 0 : p.out_bf16 ? 2 : 3;
   const int left = static_cast<int>(budget) - 1024 - kBars;
   // larger copies stream faster: two columns of K a stage
