@@ -16,7 +16,9 @@
 // before the product reads them.  Runs that find no room are added on the CUDA cores in the epilogue.
 //
 // Warps: 0-7 epilogue, 8 copies, 9 products (of the pair's first CTA), 10 notes (each row's
-// adapter, runs and their columns, a tile ahead), 11 the zeros behind the ranks.
+// adapter, runs and their columns, a tile ahead), 11 the zeros behind the ranks, 12 copies of B and v,
+// which have stages of their own, as narrow as the ranks allow: they come while the tile's shared
+// products run.
 #include <cstdint>
 
 #include "project_parts.cuh"
@@ -26,8 +28,9 @@ namespace {
 
 constexpr int kMaxNb = 256;
 constexpr int kMaxRuns = 16;
-constexpr int kThreads = 384;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kNoteWarp = 10, kZeroWarp = 11;
+constexpr int kThreads = 416;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kNoteWarp = 10, kZeroWarp = 11, kZCopyWarp = 12;
+constexpr int kMaxZSlots = 4;         // stages of B and v
 constexpr int kMaxStages = 8;
 constexpr int kTmemCols = 512;
 constexpr int kWChunk = kM * kRowBytes;
@@ -40,7 +43,8 @@ struct ManyPlan {
   int n_rt, n_nt, n_tiles;
   int n_chunks, flat;
   int parts;                // 0: no adapters
-  int bar_off, smem;
+  int zw, z_slots;          // ranks a stage of B and v holds (16, 32 or 64), such stages
+  int z_off, bar_off, smem;
 };
 
 struct Notes {
@@ -114,6 +118,20 @@ __device__ __forceinline__ void tmem_wait(float (&a)[4], float (&b)[4]) {
                : "+f"(a[0]), "+f"(a[1]), "+f"(a[2]), "+f"(a[3]), "+f"(b[0]), "+f"(b[1]), "+f"(b[2]), "+f"(b[3])::"memory");
 }
 
+// Where byte i of rows of 2 zw bytes lies in their swizzle: the 16-byte pieces of 128 bytes trade
+// places with each other (rows of 128, 64, 32 bytes).
+__device__ __forceinline__ int swizzled(int i, int zw) {
+  const int mask = zw == 64 ? 0x70 : zw == 32 ? 0x30 : 0x10;
+  return i ^ ((i >> 3) & mask);
+}
+// Descriptor of K-major rows of 2 zw bytes in that swizzle (modes 2, 4, 6), 8-row groups one after
+// the other.
+__device__ __forceinline__ uint64_t z_desc(uint32_t addr, int zw) {
+  const uint64_t mode = zw == 64 ? 2 : zw == 32 ? 4 : 6;
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>(zw) << 32) | (static_cast<uint64_t>(1) << 46) | (mode << 61);
+}
+
 // z of four rows of the tile (row[u] < 0: none) for output column n, on the CUDA cores.
 __device__ __forceinline__ void z_of_rows(const ProjectParams& p, const Notes& note, int t0, int r0, int n, const int (&row)[4],
                                           float (&z)[4]) {
@@ -165,12 +183,15 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ Notes s_note[2];
   const int half = q.nb / 2, x_chunk = half * kRowBytes;
-  const int stage_bytes = q.ch * (kWChunk + x_chunk);
+  const int stage_bytes = q.ch * (kWChunk + x_chunk), z_row = q.zw * 2;
+  const int z_bytes = (kM + q.parts * half) * z_row;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + q.bar_off);  // (the first CTA's)
-  uint64_t* zl = full + kMaxStages;                                // B and v parts have landed here
-  uint64_t* zr = zl + kMaxStages;                                  // (the first CTA's) ... in the second CTA
-  uint64_t* empty = zr + kMaxStages;
-  uint64_t* acc_full = empty + kMaxStages;
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* z_full = empty + kMaxStages;                           // (the first CTA's)
+  uint64_t* zl = z_full + kMaxZSlots;                                 // B and v have landed here,
+  uint64_t* zr = zl + kMaxZSlots;                                     // (the first CTA's) and in the second CTA
+  uint64_t* z_empty = zr + kMaxZSlots;
+  uint64_t* acc_full = z_empty + kMaxZSlots;
   uint64_t* acc_empty = acc_full + 2;                              // (the first CTA's)
   uint64_t* note_full = acc_empty + 2;
   uint64_t* note_empty = note_full + 2;
@@ -187,9 +208,13 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
   if (tid == 0) {
     for (int i = 0; i < q.stages; ++i) {
       mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < q.z_slots; ++i) {
+      mbar_init(&z_full[i], 1);
       mbar_init(&zl[i], 1);
       mbar_init(&zr[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&z_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -231,39 +256,6 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
     for (int tile = tile0; tile < tile1 && ok; ++tile, ++i) {
       const int rt = tile / q.n_nt, nt = tile - rt * q.n_nt;
       const int w0 = nt * 2 * kM + rank * kM, x0 = rt * q.nb + rank * half;
-      // B rows and v's parts of the tile's runs, 64 ranks a stage
-      auto copy_z = [&]() {
-        if (i == 0) grid_wait();   // (v)
-        ok = note_wait(i);
-        const Notes& note = s_note[i & 1];
-        const int runs = ok ? note.n_runs : 0;
-        for (int k = 0; k < runs && ok; ++k) {
-          const int n2 = note.run_n[k] / 2, bytes = kWChunk + q.parts * n2 * kRowBytes;
-          for (int j = 0; j < note.run_rank[k]; j += 64, ++it) {
-            ok = next_stage();
-            if (!ok) break;
-            if (lane == 0) {
-              const int s = it % q.stages;
-              unsigned char* w = smem + s * stage_bytes;
-              // where zeros have to be written first the stage is announced here, else with the pair's
-              uint32_t bar = smem_u32(&zl[s]);
-              if (min(64, note.run_rank[k] - j) % 16 == 0) {
-                bar = map_shared_rank(&full[s], 0);
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(2 * bytes));
-              } else {
-                mbar_arrive_expect_tx(&zl[s], static_cast<uint32_t>(bytes));
-              }
-              tma_load2(w, &bmap, j, note.run_ad[k] * p.n + w0, 0, bar);
-              for (int h = 0; h < q.parts; ++h)
-                for (int t = 0; t < n2; t += 16)
-                  tma_load2(w + kWChunk + h * x_chunk + t * kRowBytes, &vmap, j,
-                            rt * q.nb + note.run_first[k] + rank * n2 + t, h, bar);
-            }
-            __syncwarp();
-          }
-        }
-        note_done(i);
-      };
       for (int st = 0; st < nst && ok; ++st, ++it) {
         ok = next_stage();
         if (!ok) break;
@@ -287,7 +279,6 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
         }
         __syncwarp();
       }
-      if (q.parts > 0 && ok) copy_z();
     }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
     // no copy may still be landing, and no product reading, when the CTA leaves
@@ -295,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
     bool ok = true;
-    int it = 0, i = 0;
+    int it = 0, iz = 0, i = 0;
     const uint32_t idesc = (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | (static_cast<uint32_t>(q.nb >> 3) << 17) |
                            (static_cast<uint32_t>(2 * kM >> 4) << 24);
     for (int tile = tile0; tile < tile1 && ok; ++tile, ++i) {
@@ -313,36 +304,6 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
       }
       tc_fence_after();
       const uint32_t d = tmem + static_cast<uint32_t>(buf * q.nb);
-      auto mma_z = [&]() {
-        ok = note_wait(i);
-        // the last tile's z has to be read first
-        if (i > 0 && !warp_wait_cluster(&acc_empty[buf ^ 1], static_cast<uint32_t>((i - 1) / 2) & 1u)) ok = false;
-        tc_fence_after();
-        const Notes& note = s_note[i & 1];
-        const int runs = ok ? note.n_runs : 0;
-        for (int k = 0; k < runs && ok; ++k) {
-          const uint32_t zi = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(note.run_n[k] >> 3) << 17) |
-                              (static_cast<uint32_t>(2 * kM >> 4) << 24);
-          const int ranks = note.run_rank[k];
-          const uint32_t zd = tmem + zbase + static_cast<uint32_t>(note.run_col[k]);
-          for (int j = 0; j < ranks; j += 64, ++it) {
-            const int s = it % q.stages;
-            if (!warp_wait(&full[s], static_cast<uint32_t>(it / q.stages) & 1u)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t w = smem_u32(smem + s * stage_bytes);
-            const int steps = (min(64, ranks - j) + 15) / 16;
-            for (int h = 0; h < q.parts; ++h) {
-              const uint64_t ad = smem_desc(w), bd = smem_desc(w + static_cast<uint32_t>(kWChunk + h * x_chunk));
-              for (int e = 0; e < steps; ++e) mma2<false>(zd, ad + 2 * e, bd + 2 * e, zi, j > 0 || h > 0 || e > 0);
-            }
-            commit2(&empty[s]);
-          }
-        }
-        note_done(i);
-      };
       for (int st = 0; st < nst && ok; ++st, ++it) {
         const int s = it % q.stages;
         if (!warp_wait(&full[s], static_cast<uint32_t>(it / q.stages) & 1u)) {
@@ -358,7 +319,35 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
         }
         commit2(&empty[s]);
       }
-      if (q.parts > 0 && ok) mma_z();
+      if (q.parts > 0) {
+        // z's products, 16 to 64 ranks at a time, behind the shared ones (asked for in between, they
+        // cost those more than they saved); the last tile's z has to be read first
+        ok = note_wait(i) && ok;
+        const Notes& note = s_note[buf];
+        const int runs = ok ? note.n_runs : 0;
+        if (i > 0 && runs > 0) ok = warp_wait_cluster(&acc_empty[buf ^ 1], static_cast<uint32_t>((i - 1) / 2) & 1u);
+        tc_fence_after();
+        for (int k = 0; k < runs && ok; ++k) {
+          const uint32_t zi = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(note.run_n[k] >> 3) << 17) |
+                              (static_cast<uint32_t>(2 * kM >> 4) << 24);
+          const int ranks = note.run_rank[k];
+          const uint32_t zd = tmem + zbase + static_cast<uint32_t>(note.run_col[k]);
+          for (int j = 0; j < ranks; j += q.zw, ++iz) {
+            const int s = iz % q.z_slots;
+            ok = warp_wait(&z_full[s], static_cast<uint32_t>(iz / q.z_slots) & 1u);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t w = smem_u32(smem + q.z_off + s * z_bytes);
+            const int steps = (min(q.zw, ranks - j) + 15) / 16;
+            for (int h = 0; h < q.parts; ++h) {
+              const uint64_t ad = z_desc(w, q.zw), bd = z_desc(w + static_cast<uint32_t>((kM + h * half) * z_row), q.zw);
+              for (int e = 0; e < steps; ++e) mma2<false>(zd, ad + 2 * e, bd + 2 * e, zi, j > 0 || h > 0 || e > 0);
+            }
+            commit2(&z_empty[s]);
+          }
+        }
+        note_done(i);
+      }
       commit2(&acc_full[buf]);
     }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
@@ -463,27 +452,26 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
   } else if (warp == kZeroWarp) {
     // ------------------------------------------------- zeros behind the ranks
     bool ok = true;
-    int it = 0, i = 0;
-    uint32_t phase = 0;   // of each stage's zl (and zr)
+    int iz = 0, i = 0;
+    uint32_t phase = 0;   // of each slot's zl and zr
     if (q.parts > 0)
       for (int tile = tile0; tile < tile1 && ok; ++tile, ++i) {
-        it += nst;   // (they come behind the shared operands)
         ok = note_wait(i);
         const Notes& note = s_note[i & 1];
         const int runs = ok ? note.n_runs : 0;
         for (int k = 0; k < runs && ok; ++k) {
           const int ranks = note.run_rank[k];
-          for (int j = 0; j < ranks; j += 64, ++it) {
-            const int s = it % q.stages, left = min(64, ranks - j);
+          for (int j = 0; j < ranks; j += q.zw, ++iz) {
+            const int s = iz % q.z_slots, left = min(q.zw, ranks - j);
             if (left % 16 == 0) continue;
             if (!warp_wait(&zl[s], phase >> s & 1u)) {
               ok = false;
               break;
             }
-            unsigned char* b = smem + s * stage_bytes;
+            unsigned char* b = smem + q.z_off + s * z_bytes;
             for (int m = lane; m < kM; m += 32)
               for (int e = left; e < ((left + 15) & ~15); ++e)
-                *reinterpret_cast<uint16_t*>(b + m * kRowBytes + (((e >> 3) ^ (m & 7)) << 4) + (e & 7) * 2) = 0;
+                *reinterpret_cast<uint16_t*>(b + swizzled(m * z_row + e * 2, q.zw)) = 0;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (rank == 0) {
@@ -492,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
                 ok = false;
                 break;
               }
-              if (lane == 0) mbar_arrive(&full[s]);
+              if (lane == 0) mbar_arrive(&z_full[s]);
             } else if (lane == 0) {
               mbar_arrive_remote(map_shared_rank(&zr[s], 0));
             }
@@ -501,6 +489,50 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
         }
         note_done(i);
       }
+    if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
+  } else if (warp == kZCopyWarp) {
+    // ------------------------------ B rows and v's parts of runs, 64 ranks a stage
+    bool ok = true;
+    int iz = 0, i = 0;
+    if (q.parts > 0) {
+      grid_wait();   // (v)
+      for (int tile = tile0; tile < tile1 && ok; ++tile, ++i) {
+        const int rt = tile / q.n_nt, nt = tile - rt * q.n_nt, w0 = nt * 2 * kM + rank * kM;
+        ok = note_wait(i);
+        const Notes& note = s_note[i & 1];
+        const int runs = ok ? note.n_runs : 0;
+        for (int k = 0; k < runs && ok; ++k) {
+          const int n2 = note.run_n[k] / 2, bytes = (kM + q.parts * n2) * z_row;
+          for (int j = 0; j < note.run_rank[k]; j += q.zw, ++iz) {
+            const int s = iz % q.z_slots;
+            if (iz >= q.z_slots && !warp_wait(&z_empty[s], static_cast<uint32_t>(iz / q.z_slots - 1) & 1u)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              unsigned char* b = smem + q.z_off + s * z_bytes;
+              // where zeros have to be written first the stage is announced here, else with the pair's
+              uint32_t bar = smem_u32(&zl[s]);
+              if (min(q.zw, note.run_rank[k] - j) % 16 == 0) {
+                bar = map_shared_rank(&z_full[s], 0);
+                if (rank == 0) mbar_arrive_expect_tx(&z_full[s], static_cast<uint32_t>(2 * bytes));
+              } else {
+                mbar_arrive_expect_tx(&zl[s], static_cast<uint32_t>(bytes));
+              }
+              tma_load2(b, &bmap, j, note.run_ad[k] * p.n + w0, 0, bar);
+              for (int h = 0; h < q.parts; ++h)
+                for (int t = 0; t < n2; t += 16)
+                  tma_load2(b + (kM + h * half + t) * z_row, &vmap, j,
+                            rt * q.nb + note.run_first[k] + rank * n2 + t, h, bar);
+            }
+            __syncwarp();
+          }
+        }
+        note_done(i);
+      }
+      // no copy may still be landing, and no product reading, when the CTA leaves
+      for (int t = max(0, iz - q.z_slots); t < iz; ++t) warp_wait(&z_empty[t % q.z_slots], static_cast<uint32_t>(t / q.z_slots) & 1u);
+    }
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
   } else {
     // ---------------------------------------------------------------- epilogue
@@ -624,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
   }
 }
 
-constexpr int kBars = (4 * kMaxStages + 8) * 8 + 16;
+constexpr int kBars = (2 * kMaxStages + 4 * kMaxZSlots + 8) * 8 + 16;
 
 template <bool E4M3>
 size_t configure(int dev) {
@@ -664,7 +696,9 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
   // The rows a tile that make the least of waves times a tile's time: products (2 nb clocks a column
   // of 128 bytes) or L2 (256 + nb).  With adapters two accumulators and z share tensor memory.
   int64_t best = INT64_MAX;
-  for (int nb = 96; nb <= (rm > 0 ? 160 : kMaxNb); nb += 32) {
+  // 160 rows leave columns for two runs a tile, 128 for five.
+  const int widest = rm == 0 ? kMaxNb : p.n_streams <= p.rows / 320 ? 160 : 128;
+  for (int nb = 96; nb <= widest; nb += 32) {
     const int64_t tiles = static_cast<int64_t>(q.n_nt) * ((p.rows + nb - 1) / nb);
     const int64_t cost = (tiles + n_pairs - 1) / n_pairs * (2 * nb > 256 + nb ? 2 * nb : 256 + nb);
     if (cost <= best) {
@@ -675,20 +709,27 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
   q.n_rt = (p.rows + q.nb - 1) / q.nb;
   q.n_tiles = q.n_nt * q.n_rt;
   q.parts = rm == 0 ? 0 : p.out_bf16 ? 2 : 3;
-  const int left = static_cast<int>(budget) - 1024 - kBars;
-  // larger copies stream faster: two columns of K a stage
-  q.ch = 2;
-  const int stage = q.ch * (kWChunk + q.nb / 2 * kRowBytes);
-  q.stages = left / stage > kMaxStages ? kMaxStages : left / stage;
-  q.bar_off = q.stages * stage;
+  // Larger copies stream faster: two columns of K a stage and three such stages, and as many of B and
+  // v as then fit (one at least).
+  const int chunk = kWChunk + q.nb / 2 * kRowBytes, room = static_cast<int>(budget) - 1024 - kBars;
+  q.zw = rm <= 16 ? 16 : rm <= 32 ? 32 : 64;
+  const int z_bytes = q.parts == 0 ? 0 : (kM + q.parts * (q.nb / 2)) * q.zw * 2;
+  q.z_slots = z_bytes == 0 ? 0 : (room - 6 * chunk) / z_bytes;
+  q.z_slots = q.z_slots > kMaxZSlots ? kMaxZSlots : z_bytes > 0 && q.z_slots < 1 ? 1 : q.z_slots;
+  const int z = q.z_slots * z_bytes;
+  q.ch = (room - z) / (2 * chunk) >= 3 ? 2 : 1;
+  q.stages = (room - z) / (q.ch * chunk);
+  q.stages = q.stages > kMaxStages ? kMaxStages : q.stages;
+  q.z_off = q.stages * q.ch * chunk;
+  q.bar_off = q.z_off + z;
   q.smem = 1024 + q.bar_off + kBars;
   CUtensorMap wmap, xmap, bmap, vmap;
   if (!encode(&wmap, p.w, es, p.k, p.k, p.n, kM, q.ch, q.flat) ||
       !encode(&xmap, p.x, es, p.x_stride, p.k, p.rows, q.nb / 2, q.ch, q.flat))
     return cudaErrorInvalidValue;
   bmap = vmap = wmap;
-  if (q.parts > 0 && (!encode(&bmap, p.ad.b, 2, rm, rm, p.ad.n_adapters * p.n, kM, 1, true) ||
-                      !encode(&vmap, p.v_parts, 2, rm, rm, p.rows, 16, 1, true, 0, 3)))
+  if (q.parts > 0 && (!encode(&bmap, p.ad.b, 2, rm, rm, p.ad.n_adapters * p.n, kM, 1, true, 0, 1, q.zw) ||
+                      !encode(&vmap, p.v_parts, 2, rm, rm, p.rows, 16, 1, true, 0, 3, q.zw)))
     return cudaErrorInvalidValue;
   if (rm > 0) {
     e = launch_shrink(p, s);

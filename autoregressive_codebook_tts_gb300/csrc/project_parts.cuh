@@ -161,19 +161,20 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 // A row-major matrix of 1- or 2-byte entries as [K columns][rows][128 bytes] (whole columns), or
 // as [1][rows][K] (flat), boxes of `box_rows` rows; raw > 0: boxes of that many columns,
-// unswizzled; planes: that many such matrices, one after the other (flat).
+// unswizzled; planes: that many such matrices, one after the other (flat); swizzled: boxes of that many
+// 2-byte columns, 16, 32 or 64, in the swizzle of their width.
 bool encode(CUtensorMap* map, const void* base, int es, int64_t stride, int k, int rows, int box_rows, int ch, bool flat,
-            int raw = 0, int planes = 1) {
+            int raw = 0, int planes = 1, int swizzled = 0) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   const cuuint64_t cols = kRowBytes / es, pitch = static_cast<cuuint64_t>(stride) * es;
   cuuint64_t dims[3] = {flat ? static_cast<cuuint64_t>(k) : cols, static_cast<cuuint64_t>(rows),
                         flat ? static_cast<cuuint64_t>(planes) : static_cast<cuuint64_t>(k) / cols};
   cuuint64_t strides[2] = {pitch, flat ? pitch * rows : kRowBytes};
-  cuuint32_t box[3] = {raw > 0 ? static_cast<cuuint32_t>(raw) : static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(box_rows), flat ? 1u : static_cast<cuuint32_t>(ch)};
+  cuuint32_t box[3] = {raw > 0 || swizzled > 0 ? static_cast<cuuint32_t>(raw + swizzled) : static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(box_rows), flat ? 1u : static_cast<cuuint32_t>(ch)};
   cuuint32_t es3[3] = {1, 1, 1};
   return enc(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-             strides, box, es3, CU_TENSOR_MAP_INTERLEAVE_NONE, raw > 0 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             strides, box, es3, CU_TENSOR_MAP_INTERLEAVE_NONE, raw > 0 ? CU_TENSOR_MAP_SWIZZLE_NONE : swizzled == 16 ? CU_TENSOR_MAP_SWIZZLE_32B : swizzled == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
