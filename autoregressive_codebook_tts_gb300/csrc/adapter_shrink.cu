@@ -22,26 +22,47 @@ namespace {
 constexpr int kShrinkWarps = 8;
 
 // eight entries of a row
-__device__ __forceinline__ void entries8(const uint8_t* x, int64_t i, float (&f)[8]) {
-  const uint2 v = __ldg(reinterpret_cast<const uint2*>(x + i));
-  float a[4], b[4];
-  E4m3Code::values(v.x, a);
-  E4m3Code::values(v.y, b);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[e] = a[e];
-    f[4 + e] = b[e];
+template <typename X> struct Raw;
+template <> struct Raw<uint8_t> {
+  uint2 v;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + i));
   }
-}
-__device__ __forceinline__ void entries8(const __nv_bfloat16* x, int64_t i, float (&f)[8]) {
-  unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(x + i)), f);
-}
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+    float a[4], b[4];
+    E4m3Code::values(v.x, a);
+    E4m3Code::values(v.y, b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] = a[e];
+      f[4 + e] = b[e];
+    }
+  }
+};
+template <> struct Raw<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i));
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const { unpack_bf16x8(v, f); }
+};
 
+// The row's entries are asked for while its adapter is looked up (three dependent loads), then the
+// adapter's, 2048 of K at a time.
 template <typename X>
 __global__ void __launch_bounds__(kShrinkWarps * 32) shrink_kernel(const ProjectParams p) {
+  constexpr int U = 8;
   grid_wait();
   grid_launch_dependents();
   const int r = blockIdx.x, lane = threadIdx.x & 31, j = blockIdx.y * kShrinkWarps + (threadIdx.x >> 5);
+  Raw<X> x[U];
+  Raw<__nv_bfloat16> w[U];
+  const int64_t row = r * p.x_stride;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int k = u * 256 + lane * 8;
+    if (k < p.k) x[u].load(p.x, row + k);
+  }
   int bad = 0;
   const int a = row_adapter(p, r, &bad);
   const int rank = a >= 0 ? adapter_rank(p, a, &bad) : 0;
@@ -49,15 +70,26 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) shrink_kernel(const Project
   if (j >= ((rank + 7) & ~7)) return;
   float acc = 0.f;
   if (j < rank) {
-    const X* x = static_cast<const X*>(p.x) + r * p.x_stride;
-    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.ad.a) + (static_cast<int64_t>(a) * p.ad.rank_max + j) * p.k;
-#pragma unroll 4
-    for (int k = lane * 8; k < p.k; k += 256) {
-      float f[8], g[8];
-      entries8(x, k, f);
-      entries8(w, k, g);
+    const int64_t at = (static_cast<int64_t>(a) * p.ad.rank_max + j) * p.k;
+    for (int k0 = 0; k0 < p.k; k0 += U * 256) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc = fmaf(f[e], g[e], acc);
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * 256 + lane * 8;
+        if (k < p.k) {
+          if (k0 > 0) x[u].load(p.x, row + k);
+          w[u].load(p.ad.a, at + k);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k0 + u * 256 + lane * 8 < p.k) {
+          float f[8], g[8];
+          x[u].values(f);
+          w[u].values(g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc = fmaf(f[e], g[e], acc);
+        }
+      }
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
@@ -304,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) shrink_tc_kernel(const __grid_con
         }
       }
       ok = mbar_wait(acc_full, static_cast<uint32_t>(ps) & 1u) && ok;
-      ok = epilogue_all(ok);
+      ok = epilogue_all(ok, kRows);
       if (!ok) {
         if (tid == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
         break;

@@ -11,11 +11,13 @@
 //   * few tiles: the K range is split over a cluster, whose partial sums meet in rank order through
 //     distributed shared memory.  Many tiles: CTAs walk them, and with up to 160 rows a tile the
 //     accumulator is double, so the products of the next tile run under the epilogue;
-//   * the epilogue's threads take z = v B_a^T on the CUDA cores, in f32, while the tensor cores work:
-//     thread m reads row n = 128 tile + m of B_a through a private ring of asynchronous copies, v
-//     comes by bulk copies of 32 rows, and z waits in tensor memory beside the accumulator.  So x A^T
-//     is never rounded, a request's adapter never meets another request's row, and what lies behind
-//     an adapter's rank is not used.
+//   * the epilogue's warps take z = v B_a^T on the CUDA cores, in f32, while the tensor cores work: a
+//     group of four warps covers the 128 columns, a lane streams its own row of each B_a through a ring
+//     of asynchronous copies (no lane waits for another's), v comes by one bulk copy, and z waits in
+//     tensor memory beside the accumulator.  So x A^T is never rounded, a request's adapter never meets
+//     another request's row, and what lies behind an adapter's rank is not used.  One group waits on
+//     its own copies most of the time (96 requests with adapters of up to 64 ranks, 12288 columns: 84
+//     us), so where a CTA has more than 16 rows to add three groups share them.
 #include <map>
 #include <tuple>
 
@@ -27,11 +29,12 @@ namespace {
 constexpr int kWChunk = kM * kRowBytes;
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;
-constexpr int kThreads = 192;         // warps 0-3 epilogue, 4 copies, 5 products
-constexpr int kEpi = 128;
+constexpr int kMaxGroups = 3;         // groups of four epilogue warps; then a warp for copies, one for products
+constexpr int kMaxThreads = kMaxGroups * 128 + 64;
 constexpr int kTmemCols = 512;
 constexpr int kRedLd = kM + 16;       // floats between the rows of a partial
-constexpr int kMaxAhead = 8;           // runs of B rows in flight at most
+constexpr int kMaxAhead = 8;          // runs of B rows in flight at most, a warp
+constexpr int kMaxV = 48 * 1024;      // bytes of v held in shared memory; more is read where it is
 
 struct Plan {
   int nb, nbr;          // x rows a tile (a multiple of 16), and that rounded up to 32
@@ -41,7 +44,9 @@ struct Plan {
   int n_rt, n_nt, n_tiles;
   int n_chunks;         // 128-byte columns of K (the last may be short)
   int flat;             // K is not whole columns: one copy each
-  int ring;             // 16-byte pieces of B a thread has room for
+  int groups;           // of epilogue warps
+  int ring;             // 16-byte pieces of B a lane has room for
+  int v_rows;           // rows of v in shared memory (0: none)
   int parts;            // bf16 parts of v that meet B on the tensor cores (0: none do)
   int v_off, b_off, bar_off, smem;
   int vec_out;          // out rows take 16-byte (f32) or 8-byte (bf16) stores
@@ -81,9 +86,7 @@ struct TileInfo {
   int ad[256];       // adapter of the tile's rows: -1 none, -2 no request
   int rank[256];
   float sx[256];
-  int run[256];      // rows that share an adapter: first | length << 16, within 32 rows each
   bool one[256];     // the row's block of 16 shares one adapter
-  int n_runs;
 };
 
 // Block `lane` of a tile: the adapter its rows share, negative for none, several or no such block.
@@ -93,7 +96,7 @@ __device__ __forceinline__ int tile_block(const ProjectParams& p, const Plan& q,
 }
 
 template <bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_constant__ CUtensorMap wmap,
+__global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_constant__ CUtensorMap wmap,
                                                               const __grid_constant__ CUtensorMap xmap,
                                                               const __grid_constant__ CUtensorMap bmap,
                                                               const __grid_constant__ CUtensorMap vmap,
@@ -102,14 +105,13 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ TileInfo s_tile;
   const int stage_bytes = q.ch * (kWChunk + q.nb * kRowBytes);
-  float* s_v = reinterpret_cast<float*>(smem + q.v_off);          // [2][32][rank_max]
-  unsigned char* s_b = smem + q.b_off;                            // [ring][128] 16-byte pieces
+  float* s_v = reinterpret_cast<float*>(smem + q.v_off);          // [v_rows][rank_max]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + q.bar_off);
   uint64_t* empty = full + kMaxStages;
   uint64_t* acc_full = empty + kMaxStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* v_full = acc_empty + 2;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(v_full + 2);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(v_full + 1);
   float* red = reinterpret_cast<float*>(smem);   // partial sums, over the ring once it is drained
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -125,12 +127,13 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
-      mbar_init(&v_full[i], 1);
+      mbar_init(&acc_empty[i], 4 * q.groups);
     }
+    mbar_init(v_full, 1);
     mbar_init_fence();
   }
-  if (warp == 5) {
+  const int copy_warp = 4 * q.groups, mma_warp = copy_warp + 1;
+  if (warp == mma_warp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  ::"r"(smem_u32(s_tmem)), "n"(kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
   if (p.ad.n_adapters == 0) grid_wait();
   grid_launch_dependents();
 
-  if (warp == 4) {
+  if (warp == copy_warp) {
     // ------------------------------------------------------------------ copies
     const int cols = kRowBytes / (E4M3 ? 1 : 2);
     bool ok = true, waited = false;
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
     // no copy may still be landing when the CTA leaves
     for (int t = max(0, it - q.stages); t < it; ++t) warp_wait(&full[t % q.stages], static_cast<uint32_t>(t / q.stages) & 1u);
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == mma_warp) {
     // ---------------------------------------------------------------- products
     // f32 accumulator (bits 4-5 = 1); bf16 operands are 1 at bits 7-9 and 10-12, e4m3 ones 0;
     // both K-major; N >> 3 at bit 17, M >> 4 at bit 24
@@ -283,19 +286,20 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
     if (!ok && lane == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
   } else {
     // ---------------------------------------------------------------- epilogue
-    grid_wait();   // v, and whoever read or wrote out before
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const int group = warp >> 2, quad = warp & 3, n_epi = 128 * q.groups;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t zcol = tmem + static_cast<uint32_t>(q.n_acc * q.nbr) + lane_off;
-    const int m = tid, rm = p.ad.rank_max;
+    const int m = quad * 32 + lane, rm = p.ad.rank_max;
     const bool with = p.ad.n_adapters > 0;
-    const int lo = q.nb * rank / S, hi = q.nb * (rank + 1) / S;   // rows whose adapters this CTA adds
-    bool ok = true;
-    uint32_t vq = 0;   // chunks of v asked for so far
+    const int lo = q.nb * rank / S, hi = q.nb * (rank + 1) / S;   // rows whose adapters this CTA adds,
+    const int glo = lo + (hi - lo) * group / q.groups, ghi = lo + (hi - lo) * (group + 1) / q.groups;   // and this group
+    unsigned char* s_b = smem + q.b_off + warp * (q.ring * 512) + lane * 16;   // this lane's pieces, 512 bytes apart
+    bool ok = true, waited = !with;
     int i = 0;
     for (int tile = blockIdx.x; tile < q.n_tiles && ok; tile += gridDim.x, ++i) {
       const int rt = tile % q.n_rt, nt = tile / q.n_rt, r0 = rt * q.nb;
       const int n = nt * kM + m;
-      for (int t = tid; t < q.nbr; t += kEpi) {
+      for (int t = tid; t < q.nbr; t += n_epi) {
         const int r = r0 + t;
         int a = -2, k = 0, bad = 0;
         float sx = 0.f;
@@ -308,130 +312,110 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
         s_tile.rank[t] = k;
         s_tile.sx[t] = sx;
       }
-      named_barrier(1, kEpi);
-      int n_runs = 0;
-      if (with) {
-        const int c_lo = q.parts > 0 ? 0 : lo / 32, c_hi = q.parts > 0 ? q.nbr / 32 : (hi + 31) / 32;
-        auto ask_v = [&](int c, uint32_t seq) {   // 32 rows of v
-          const int r = r0 + c * 32, cnt = min(32, p.rows - r);
-          const uint32_t bytes = static_cast<uint32_t>(cnt * rm) * 4u;
-          mbar_arrive_expect_tx(&v_full[seq & 1], bytes);
-          bulk_g2s_plain(s_v + (seq & 1) * 32 * rm, p.v + static_cast<int64_t>(r) * rm, bytes, &v_full[seq & 1]);
-        };
-        if (warp == 0) {
-          int base = 0;
-          for (int c = c_lo; c < c_hi; ++c) {
-            const int t = c * 32 + lane;
-            int a = t >= lo && t < hi ? s_tile.ad[t] : -3;
-            if (q.parts > 0) {
-              // blocks that share an adapter are the tensor cores'
-              const int all = s_tile.ad[t];
-              int top = all, low = all >= 0 ? all : 0x7fffffff;
+      epilogue_all(true, n_epi);
+      if (q.parts > 0) {
+        // blocks that share an adapter are the tensor cores'
+        for (int c = warp; c < q.nbr / 32; c += 4 * q.groups) {
+          const int a = s_tile.ad[c * 32 + lane];
+          int top = a, low = a >= 0 ? a : 0x7fffffff;
 #pragma unroll
-              for (int o = 8; o >= 1; o >>= 1) {
-                top = max(top, __shfl_xor_sync(kFull, top, o));
-                low = min(low, __shfl_xor_sync(kFull, low, o));
-              }
-              const bool one = top >= 0 && top == low;
-              s_tile.one[t] = one;
-              if (one) a = -3;
-            }
-            const int prev = __shfl_up_sync(kFull, a, 1);
-            const uint32_t edge = __ballot_sync(kFull, lane == 0 || a != prev);
-            const uint32_t first = __ballot_sync(kFull, a >= 0 && (edge >> lane & 1u));
-            if (first >> lane & 1u) {
-              const uint32_t later = lane == 31 ? 0u : edge >> (lane + 1);
-              const int len = later != 0 ? __ffs(static_cast<int>(later)) : 32 - lane;
-              s_tile.run[base + __popc(first & ((1u << lane) - 1))] = t | (len << 16);
-            }
-            base += __popc(first);
+          for (int o = 8; o >= 1; o >>= 1) {
+            top = max(top, __shfl_xor_sync(kFull, top, o));
+            low = min(low, __shfl_xor_sync(kFull, low, o));
           }
-          if (lane == 0) s_tile.n_runs = base;
+          s_tile.one[c * 32 + lane] = top >= 0 && top == low;
         }
-        named_barrier(1, kEpi);
-        n_runs = s_tile.n_runs;
+        epilogue_all(true, n_epi);
+      }
+      if (with) {
         const unsigned char* brow = static_cast<const unsigned char*>(p.ad.b) + static_cast<int64_t>(n) * rm * 2;
-        // B rows go round a ring of 16-byte pieces, as many runs ahead as fit it
-        int ahead = 0, put = 0, room = q.ring, get = 0;
-        auto ask_b = [&](int done) {
-          while (ahead < n_runs && ahead - done < kMaxAhead) {
-            const int t = s_tile.run[ahead] & 0xffff, have = (s_tile.rank[t] + 7) / 8;
-            if (have > room) break;
-            if (n < p.n) {
-              const unsigned char* src = brow + static_cast<int64_t>(s_tile.ad[t]) * p.n * rm * 2;
-              for (int v = 0, at = put; v < have; ++v) {
-                cp_async16(s_b + (at * kEpi + tid) * 16, src + v * 16);
-                at = at + 1 == q.ring ? 0 : at + 1;
+        const float* v0 = q.v_rows > 0 ? s_v - lo * rm : p.v + static_cast<int64_t>(r0) * rm;
+        bool v_here = q.v_rows == 0;
+        for (int base = glo; base < ghi; base += 32) {
+          // runs of rows that share an adapter
+          const int t = base + lane;
+          const int a = t < ghi && !(q.parts > 0 && s_tile.one[t]) ? max(s_tile.ad[t], -1) : -1;
+          const int k = a >= 0 ? s_tile.rank[t] : 0, prev = __shfl_up_sync(kFull, a, 1);
+          const uint32_t edge = __ballot_sync(kFull, lane == 0 || a != prev);
+          const uint32_t first = __ballot_sync(kFull, a >= 0 && (lane == 0 || a != prev));
+          // B rows go round the ring, as many runs ahead as fit it
+          uint32_t next = first;
+          int ahead = 0, done = 0, put = 0, room = q.ring, get = 0;
+          auto ask_b = [&]() {
+            while (next != 0 && ahead - done < kMaxAhead) {
+              const int l = __ffs(static_cast<int>(next)) - 1, of = __shfl_sync(kFull, a, l);
+              const int have = (__shfl_sync(kFull, k, l) + 7) / 8;
+              if (have > room) break;
+              if (n < p.n) {
+                const unsigned char* src = brow + static_cast<int64_t>(of) * p.n * rm * 2;
+                for (int e = 0, at = put; e < have; ++e) {
+                  cp_async16(s_b + at * 512, src + e * 16);
+                  at = at + 1 == q.ring ? 0 : at + 1;
+                }
+              }
+              cp_async_commit();
+              put = put + have >= q.ring ? put + have - q.ring : put + have;
+              room -= have;
+              ++ahead;
+              next &= next - 1;
+            }
+          };
+          ask_b();
+          if (!waited) {
+            grid_wait();   // v, and whoever read or wrote out before
+            waited = true;
+          }
+          if (!v_here) {
+            if (tid == 0) {
+              const int cnt = min(hi, p.rows - r0) - lo;
+              if (cnt > 0) {
+                mbar_arrive_expect_tx(v_full, static_cast<uint32_t>(cnt * rm) * 4u);
+                bulk_g2s_plain(s_v, p.v + static_cast<int64_t>(r0 + lo) * rm, static_cast<uint32_t>(cnt * rm) * 4u, v_full);
+              } else {
+                mbar_arrive(v_full);
               }
             }
-            cp_async_commit();
-            put += have;
-            if (put >= q.ring) put -= q.ring;
-            room -= have;
-            ++ahead;
+            ok = mbar_wait(v_full, static_cast<uint32_t>(i) & 1u) && ok;
+            v_here = true;
           }
-        };
-        ask_b(0);
-        int cur = -1, c_next = c_lo;   // the chunk of v in use (copy cur_seq), the next to ask for
-        uint32_t cur_seq = 0, seq = vq;
-        // (thread 0 asks; all threads count along)
-        auto ask_next = [&]() {
-          if (c_next < c_hi && r0 + c_next * 32 < p.rows) {
-            if (tid == 0) ask_v(c_next, seq);
-            ++seq;
-          }
-          ++c_next;
-        };
-        const uint32_t seq0 = seq;
-        ask_next();
-        ask_next();
-        for (int k = 0; k < n_runs; ++k) {
-          const int run = s_tile.run[k], t0 = run & 0xffff, len = run >> 16, a_rank = s_tile.rank[t0];
-          const int c = t0 / 32;
-          while (cur < c) {
-            // the next chunk of v: its buffer's last readers have passed this barrier
-            cur = cur < 0 ? c_lo : cur + 1;
-            if (cur > c_lo) {
-              named_barrier(1, kEpi);
-              ask_next();
+          for (uint32_t left = first; left != 0; left &= left - 1) {
+            const int l = __ffs(static_cast<int>(left)) - 1, ranks = __shfl_sync(kFull, k, l), have = (ranks + 7) / 8;
+            const uint32_t later = l == 31 ? 0u : edge >> (l + 1);
+            const int end = base + (later != 0 ? l + __ffs(static_cast<int>(later)) : 32);
+            cp_async_wait(ahead - done - 1);
+            for (int t = base + l; t < end; ++t) {
+              float2 z = make_float2(0.f, 0.f), y = z;
+              const float* vt = v0 + static_cast<int64_t>(t) * rm;
+#pragma unroll 2
+              for (int e = 0; e < have; ++e) {
+                float2 bp[4], va, vb, vc, vd;
+                const int at = get + e >= q.ring ? get + e - q.ring : get + e;
+                v_pairs(vt + e * 8, va, vb);
+                v_pairs(vt + e * 8 + 4, vc, vd);
+                b_pairs(lds128(s_b + at * 512), ranks - 8 * e, bp);
+                z = __ffma2_rn(va, bp[0], z);
+                y = __ffma2_rn(vb, bp[1], y);
+                z = __ffma2_rn(vc, bp[2], z);
+                y = __ffma2_rn(vd, bp[3], y);
+              }
+              tmem_st1(zcol + static_cast<uint32_t>(t), (z.x + z.y) + (y.x + y.y));
             }
-            cur_seq = seq0 + static_cast<uint32_t>(cur - c_lo);
-            ok = mbar_wait(&v_full[cur_seq & 1], (cur_seq >> 1) & 1u) && ok;
+            get = get + have >= q.ring ? get + have - q.ring : get + have;
+            room += have;
+            ++done;
+            ask_b();
           }
-          cp_async_wait(ahead - k - 1);
-          const float* v = s_v + (cur_seq & 1) * 32 * rm;
-          const int have = (a_rank + 7) / 8;
-          for (int t = t0; t < t0 + len; ++t) {
-            float2 z = make_float2(0.f, 0.f), y = z;
-            const float* vt = v + (t - c * 32) * rm;
-            for (int e = 0, at = get; e < have; ++e) {
-              float2 bp[4], v0, v1, v2, v3;
-              b_pairs(lds128(s_b + (at * kEpi + tid) * 16), a_rank - 8 * e, bp);
-              at = at + 1 == q.ring ? 0 : at + 1;
-              v_pairs(vt + e * 8, v0, v1);
-              v_pairs(vt + e * 8 + 4, v2, v3);
-              z = __ffma2_rn(v0, bp[0], z);
-              y = __ffma2_rn(v1, bp[1], y);
-              z = __ffma2_rn(v2, bp[2], z);
-              y = __ffma2_rn(v3, bp[3], y);
-            }
-            tmem_st1(zcol + static_cast<uint32_t>(t), (z.x + z.y) + (y.x + y.y));
-          }
-          get += have;
-          if (get >= q.ring) get -= q.ring;
-          room += have;
-          ask_b(k + 1);
         }
-        // copies of chunks that no run needed: waited for, so that every phase is used once
-        for (uint32_t w = cur < 0 ? seq0 : cur_seq + 1; w != seq; ++w) ok = mbar_wait(&v_full[w & 1], (w >> 1) & 1u) && ok;
-        vq = seq;
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (!waited) grid_wait();
+        waited = true;
+        if (!v_here && tid == 0) mbar_arrive(v_full);   // (no row here has an adapter: the phase is used all the same)
         tmem_wait_st();
+        tc_fence_before();
       }
       // ---- the accumulator
       const int buf = i % q.n_acc, use = i / q.n_acc;
       ok = mbar_wait(&acc_full[buf], static_cast<uint32_t>(use) & 1u) && ok;
-      ok = epilogue_all(ok);
+      ok = epilogue_all(ok, n_epi);
       if (!ok) {
         if (tid == 0) set_err(p.err, TTS_EFLAG_TIMEOUT);
         break;
@@ -439,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
       tc_fence_after();
       const uint32_t dcol = tmem + static_cast<uint32_t>(buf * q.nbr) + lane_off;
       const float sw = E4M3 && n < p.n ? __ldcg(p.w_scale + n) : 0.f;
-      for (int c = 0; c < q.nbr / 32; ++c) {
+      for (int c = group; c < q.nbr / 32; c += q.groups) {
         float acc[32], z[32];
         tmem_ld32(dcol + c * 32, acc);
         const int a = s_tile.ad[c * 32 + lane];
@@ -475,21 +459,21 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[buf]);
-      named_barrier(1, kEpi);   // the tile's notes may change
+      epilogue_all(true, n_epi);   // the tile's notes and v may change
     }
   }
   if (S > 1) {
     __syncwarp();
     tc_fence_before();
     cluster_sync_all();   // every CTA's partial is in its shared memory
-    if (warp < 4) {
+    if (warp < copy_warp) {
       const int rt = static_cast<int>(blockIdx.x) % q.n_rt, nt = static_cast<int>(blockIdx.x) / q.n_rt;
       const int lo = q.nb * rank / S, hi = q.nb * (rank + 1) / S;
       uint32_t peer[kMaxCluster];
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) peer[r] = r < S ? map_shared_rank(red, r) : 0u;
       const int n = nt * kM + lane * 4;
-      for (int t = lo + warp; t < hi; t += 4) {
+      for (int t = lo + warp; t < hi; t += copy_warp) {
         if (s_tile.ad[t] == -2) continue;
         const uint32_t off = static_cast<uint32_t>((t * kRedLd + lane * 4) * 4);
         float4 part[kMaxCluster];
@@ -527,13 +511,13 @@ __global__ void __launch_bounds__(kThreads, 1) project_kernel(const __grid_const
     tc_fence_before();
     __syncthreads();
   }
-  if (warp == 5) {
+  if (warp == mma_warp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
   }
 }
 
-constexpr int kBarBytes = (2 * kMaxStages + 6) * 8 + 16;
+constexpr int kBarBytes = (2 * kMaxStages + 5) * 8 + 16;
 
 // The dynamic shared memory a CTA of the kernel may take on device `dev`, set as its limit once
 // per device; 0 on failure.
@@ -564,16 +548,21 @@ int max_active_clusters(int dev, int S, int smem) {
   std::lock_guard<std::mutex> lock(mtx);
   const auto it = cache.find(key);
   if (it != cache.end()) return it->second;
-  const int n = active_clusters(project_kernel<E4M3>, S, kThreads, smem);
+  const int n = active_clusters(project_kernel<E4M3>, S, kMaxThreads, smem);
   cache[key] = n;
   return n;
 }
 
-// Shared memory of a plan: the ring, two chunks of v, the ring of B rows, barriers.
+// Shared memory of a plan: the ring of operands, v, the rings of B rows, barriers.
 void lay_out(Plan& q, int rank_max, size_t budget) {
+  const int rows = (q.nb + q.split - 1) / q.split;   // whose adapters a CTA adds
+  q.groups = rank_max > 0 && rows > 16 ? kMaxGroups : 1;
+  q.ring = rank_max == 0 ? 0 : rank_max <= 16 && q.groups > 1 ? 8 : 16;
+  q.v_rows = rows * rank_max * 4 <= kMaxV ? rows : 0;
+  const int v = (q.v_rows * rank_max * 4 + 127) / 128 * 128, b = q.groups * 4 * q.ring * 512;
+  // (beside three groups' rings stages of two columns would be too few)
+  if (q.groups > 1 && q.ch > 1 && rank_max > 16) q.ch = 1;
   const int stage = q.ch * (kWChunk + q.nb * kRowBytes);
-  q.ring = rank_max == 0 ? 0 : 16;
-  const int v = 2 * 32 * rank_max * 4, b = q.ring * kEpi * 16;
   const int fixed = 1024 + v + b + kBarBytes;
   int st = static_cast<int>((budget - fixed) / stage);
   const int per_cta = (q.n_chunks + q.ch - 1) / q.ch;
@@ -646,7 +635,7 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   const dim3 grid = q.split > 1 ? dim3(q.n_tiles, q.split) : dim3(q.n_tiles < n_sm ? q.n_tiles : n_sm);
-  return launch_clustered(project_kernel<E4M3>, grid, kThreads, q.smem, q.split, s, wmap, xmap, bmap, vmap, p, q);
+  return launch_clustered(project_kernel<E4M3>, grid, 128 * q.groups + 64, q.smem, q.split, s, wmap, xmap, bmap, vmap, p, q);
 }
 
 }  // namespace

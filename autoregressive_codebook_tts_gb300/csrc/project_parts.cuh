@@ -105,12 +105,12 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // A barrier of the epilogue's threads that also makes an outcome common to them.
-__device__ __forceinline__ bool epilogue_all(bool v) {
+__device__ __forceinline__ bool epilogue_all(bool v, int threads) {
   uint32_t out;
   asm volatile(
       "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\t"
-      "bar.red.and.pred po, 1, 128, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
-      : "=r"(out) : "r"(static_cast<uint32_t>(v)) : "memory");
+      "bar.red.and.pred po, 1, %2, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(out) : "r"(static_cast<uint32_t>(v)), "r"(threads) : "memory");
   return out != 0;
 }
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
