@@ -15,9 +15,10 @@
 //     group of four warps covers the 128 columns, a lane streams its own row of each B_a through a ring
 //     of asynchronous copies (no lane waits for another's), v comes by one bulk copy, and z waits in
 //     tensor memory beside the accumulator.  So x A^T is never rounded, a request's adapter never meets
-//     another request's row, and what lies behind an adapter's rank is not used.  One group waits on
-//     its own copies most of the time (96 requests with adapters of up to 64 ranks, 12288 columns: 84
-//     us), so where a CTA has more than 16 rows to add three groups share them.
+//     another request's row, and what lies behind an adapter's rank is not used.  The copies and
+//     products of a row are a few hundred instructions that wait on each other, so a group has about four
+//     rows, as far as six groups go (96 requests with adapters of up to 64 ranks, 12288 columns: 84 us
+//     with one group, 51 with three; neighbouring lanes taking neighbouring pieces of a row: no gain).
 #include <map>
 #include <tuple>
 
@@ -29,7 +30,7 @@ namespace {
 constexpr int kWChunk = kM * kRowBytes;
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxGroups = 3;         // groups of four epilogue warps; then a warp for copies, one for products
+constexpr int kMaxGroups = 6;         // groups of four epilogue warps; then a warp for copies, one for products
 constexpr int kMaxThreads = kMaxGroups * 128 + 64;
 constexpr int kTmemCols = 512;
 constexpr int kRedLd = kM + 16;       // floats between the rows of a partial
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
     const bool with = p.ad.n_adapters > 0;
     const int lo = q.nb * rank / S, hi = q.nb * (rank + 1) / S;   // rows whose adapters this CTA adds,
     const int glo = lo + (hi - lo) * group / q.groups, ghi = lo + (hi - lo) * (group + 1) / q.groups;   // and this group
-    unsigned char* s_b = smem + q.b_off + warp * (q.ring * 512) + lane * 16;   // this lane's pieces, 512 bytes apart
+    unsigned char* s_b = smem + q.b_off + warp * (q.ring * 512) + lane * 16;   // this lane's ring, pieces 512 bytes apart
     bool ok = true, waited = !with;
     int i = 0;
     for (int tile = blockIdx.x; tile < q.n_tiles && ok; tile += gridDim.x, ++i) {
@@ -348,13 +349,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
               if (have > room) break;
               if (n < p.n) {
                 const unsigned char* src = brow + static_cast<int64_t>(of) * p.n * rm * 2;
-                for (int e = 0, at = put; e < have; ++e) {
-                  cp_async16(s_b + at * 512, src + e * 16);
-                  at = at + 1 == q.ring ? 0 : at + 1;
-                }
+                for (int e = 0; e < have; ++e) cp_async16(s_b + ((put + e) & (q.ring - 1)) * 512, src + e * 16);
               }
               cp_async_commit();
-              put = put + have >= q.ring ? put + have - q.ring : put + have;
+              put += have;
               room -= have;
               ++ahead;
               next &= next - 1;
@@ -389,10 +387,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
 #pragma unroll 2
               for (int e = 0; e < have; ++e) {
                 float2 bp[4], va, vb, vc, vd;
-                const int at = get + e >= q.ring ? get + e - q.ring : get + e;
+                const int at = ((get + e) & (q.ring - 1)) * 512;
                 v_pairs(vt + e * 8, va, vb);
                 v_pairs(vt + e * 8 + 4, vc, vd);
-                b_pairs(lds128(s_b + at * 512), ranks - 8 * e, bp);
+                b_pairs(lds128(s_b + at), ranks - 8 * e, bp);
                 z = __ffma2_rn(va, bp[0], z);
                 y = __ffma2_rn(vb, bp[1], y);
                 z = __ffma2_rn(vc, bp[2], z);
@@ -400,7 +398,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
               }
               tmem_st1(zcol + static_cast<uint32_t>(t), (z.x + z.y) + (y.x + y.y));
             }
-            get = get + have >= q.ring ? get + have - q.ring : get + have;
+            get += have;
             room += have;
             ++done;
             ask_b();
@@ -423,37 +421,35 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
       tc_fence_after();
       const uint32_t dcol = tmem + static_cast<uint32_t>(buf * q.nbr) + lane_off;
       const float sw = E4M3 && n < p.n ? __ldcg(p.w_scale + n) : 0.f;
-      for (int c = group; c < q.nbr / 32; c += q.groups) {
-        float acc[32], z[32];
-        tmem_ld32(dcol + c * 32, acc);
-        const int a = s_tile.ad[c * 32 + lane];
-        const int t = c * 32 + lane;
+      for (int c = group; c < q.nbr / 16; c += q.groups) {
+        float acc[16], z[16];
+        tmem_ld16(dcol + c * 16, acc);
+        const int t = c * 16 + (lane & 15), a = s_tile.ad[t];
         const uint32_t live = __ballot_sync(kFull, a != -2);
         // (z of a block that shares an adapter is with the cluster's first CTA)
         const bool one = q.parts > 0 && s_tile.one[t];
         const uint32_t has = __ballot_sync(kFull, a >= 0 && (one ? rank == 0 : t >= lo && t < hi));
-        if (has != 0) tmem_ld32(zcol + c * 32, z);
+        if (has != 0) tmem_ld16(zcol + c * 16, z);
         if (E4M3) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) acc[j] *= s_tile.sx[c * 32 + j] * sw;
+          for (int j = 0; j < 16; ++j) acc[j] *= s_tile.sx[c * 16 + j] * sw;
         }
         if (has != 0) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
+          for (int j = 0; j < 16; ++j)
             if (has >> j & 1u) acc[j] += z[j];
         }
         if (S == 1) {
           if (n < p.n) {
-            const int64_t at = static_cast<int64_t>(r0 + c * 32) * p.out_stride + n;
+            const int64_t at = static_cast<int64_t>(r0 + c * 16) * p.out_stride + n;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 16; ++j)
               if (live >> j & 1u) store_out(p, at + j * p.out_stride, acc[j]);
           }
-        } else {
+        } else if (c * 16 < q.nb) {
           // (every MMA of this CTA has read the ring)
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c * 32 + j < q.nb) red[(c * 32 + j) * kRedLd + m] = acc[j];
+          for (int j = 0; j < 16; ++j) red[(c * 16 + j) * kRedLd + m] = acc[j];
         }
       }
       tc_fence_before();
@@ -556,12 +552,13 @@ int max_active_clusters(int dev, int S, int smem) {
 // Shared memory of a plan: the ring of operands, v, the rings of B rows, barriers.
 void lay_out(Plan& q, int rank_max, size_t budget) {
   const int rows = (q.nb + q.split - 1) / q.split;   // whose adapters a CTA adds
-  q.groups = rank_max > 0 && rows > 16 ? kMaxGroups : 1;
-  q.ring = rank_max == 0 ? 0 : rank_max <= 16 && q.groups > 1 ? 8 : 16;
+  const int want = (rows + 3) / 4, most = rank_max > 64 ? kMaxGroups / 2 : kMaxGroups;
+  q.groups = rank_max == 0 ? 1 : want < most ? want : most;
+  q.ring = rank_max == 0 ? 0 : rank_max > 64 ? 16 : 8;   // (a power of two that holds a row of B)
   q.v_rows = rows * rank_max * 4 <= kMaxV ? rows : 0;
   const int v = (q.v_rows * rank_max * 4 + 127) / 128 * 128, b = q.groups * 4 * q.ring * 512;
-  // (beside three groups' rings stages of two columns would be too few)
-  if (q.groups > 1 && q.ch > 1 && rank_max > 16) q.ch = 1;
+  // (beside many groups' rings stages of two columns would be too few)
+  if (q.groups > 3 && q.ch > 1) q.ch = 1;
   const int stage = q.ch * (kWChunk + q.nb * kRowBytes);
   const int fixed = 1024 + v + b + kBarBytes;
   int st = static_cast<int>((budget - fixed) / stage);

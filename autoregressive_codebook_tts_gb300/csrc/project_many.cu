@@ -97,7 +97,7 @@ __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity
   return __all_sync(kFull, mbar_wait_cluster(bar, parity, kWaitLimitCycles));
 }
 // 16 columns of this thread's lane; to be used after a wait that names them.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+__device__ __forceinline__ void tmem_ask16(uint32_t taddr, float (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
@@ -593,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
       float acc[16], z[16];
       auto load = [&](int c) {
         const int z_at = note.z_at[t0 / 16 + c];
-        if (z_at != kByRow) tmem_ld16(dcol + static_cast<uint32_t>(t0 + c * 16), acc);
-        if (z_at >= 0) tmem_ld16(tmem + static_cast<uint32_t>(z_at) + lane_off, z);
+        if (z_at != kByRow) tmem_ask16(dcol + static_cast<uint32_t>(t0 + c * 16), acc);
+        if (z_at >= 0) tmem_ask16(tmem + static_cast<uint32_t>(z_at) + lane_off, z);
       };
       load(0);
 #pragma unroll 1
