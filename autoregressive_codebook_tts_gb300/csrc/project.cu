@@ -34,7 +34,7 @@ constexpr int kMaxGroups = 6;         // groups of four epilogue warps; then a w
 constexpr int kMaxThreads = kMaxGroups * 128 + 64;
 constexpr int kTmemCols = 512;
 constexpr int kRedLd = kM + 16;       // floats between the rows of a partial
-constexpr int kMaxAhead = 8;          // runs of B rows in flight at most, a warp
+constexpr int kMaxAhead = 4;          // runs of B rows in flight at most, a warp
 constexpr int kMaxV = 48 * 1024;      // bytes of v held in shared memory; more is read where it is
 
 struct Plan {
@@ -53,18 +53,12 @@ struct Plan {
   int vec_out;          // out rows take 16-byte (f32) or 8-byte (bf16) stores
 };
 
-// All but the newest n copy groups of this thread have landed.
+// All but the newest n copy groups of this thread have landed, n < kMaxAhead.
 __device__ __forceinline__ void cp_async_wait(int n) {
-  switch (n) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-  }
+  if (n >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 // Neighbouring blocks of 16 rows that share an adapter.
 struct BlockRun {
@@ -330,6 +324,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
       }
       if (with) {
         const unsigned char* brow = static_cast<const unsigned char*>(p.ad.b) + static_cast<int64_t>(n) * rm * 2;
+        const uint32_t pool_step = static_cast<uint32_t>(p.n) * rm * 2;   // (at most 2^28)
         const float* v0 = q.v_rows > 0 ? s_v - lo * rm : p.v + static_cast<int64_t>(r0) * rm;
         bool v_here = q.v_rows == 0;
         for (int base = glo; base < ghi; base += 32) {
@@ -339,21 +334,30 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
           const int k = a >= 0 ? s_tile.rank[t] : 0, prev = __shfl_up_sync(kFull, a, 1);
           const uint32_t edge = __ballot_sync(kFull, lane == 0 || a != prev);
           const uint32_t first = __ballot_sync(kFull, a >= 0 && (lane == 0 || a != prev));
-          // B rows go round the ring, as many runs ahead as fit it
+          // B rows go round the ring, as many runs ahead as fit it; a run's pieces lie together
           uint32_t next = first;
           int ahead = 0, done = 0, put = 0, room = q.ring, get = 0;
           auto ask_b = [&]() {
             while (next != 0 && ahead - done < kMaxAhead) {
               const int l = __ffs(static_cast<int>(next)) - 1, of = __shfl_sync(kFull, a, l);
-              const int have = (__shfl_sync(kFull, k, l) + 7) / 8;
-              if (have > room) break;
+              const int have = (__shfl_sync(kFull, k, l) + 7) >> 3;
+              if (ahead == done) {   // (an empty ring begins again)
+                put = get = 0;
+                room = q.ring;
+              }
+              const bool wrap = put + have > q.ring;
+              const int cost = have + (wrap ? q.ring - put : 0);
+              if (cost > room) break;
+              room -= cost;
+              if (wrap) put = 0;
               if (n < p.n) {
-                const unsigned char* src = brow + static_cast<int64_t>(of) * p.n * rm * 2;
-                for (int e = 0; e < have; ++e) cp_async16(s_b + ((put + e) & (q.ring - 1)) * 512, src + e * 16);
+                const unsigned char* src = brow + static_cast<uint64_t>(static_cast<uint32_t>(of)) * pool_step;
+                unsigned char* dst = s_b + put * 512;
+#pragma unroll 4
+                for (int e = 0; e < have; ++e) cp_async16(dst + e * 512, src + e * 16);
               }
               cp_async_commit();
               put += have;
-              room -= have;
               ++ahead;
               next &= next - 1;
             }
@@ -377,29 +381,42 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
             v_here = true;
           }
           for (uint32_t left = first; left != 0; left &= left - 1) {
-            const int l = __ffs(static_cast<int>(left)) - 1, ranks = __shfl_sync(kFull, k, l), have = (ranks + 7) / 8;
-            const uint32_t later = l == 31 ? 0u : edge >> (l + 1);
+            const int l = __ffs(static_cast<int>(left)) - 1, ranks = __shfl_sync(kFull, k, l), have = (ranks + 7) >> 3;
+            const uint32_t later = edge >> l >> 1;
             const int end = base + (later != 0 ? l + __ffs(static_cast<int>(later)) : 32);
+            const bool wrap = get + have > q.ring;
+            const int cost = have + (wrap ? q.ring - get : 0);
+            if (wrap) get = 0;
+            unsigned char* b = s_b + get * 512;
             cp_async_wait(ahead - done - 1);
+            if (ranks & 7) {
+              // zeros behind the rank, where v's are
+              unsigned char* tail = b + (have - 1) * 512;
+              const uint4 w = lds128(tail);
+              const int keep = ranks & 7;
+              const uint32_t odd = keep & 1 ? 0xffffu : 0u;   // of the word in which the rank ends
+              *reinterpret_cast<uint4*>(tail) =
+                  make_uint4(keep > 1 ? w.x : w.x & odd, keep > 3 ? w.y : keep > 1 ? w.y & odd : 0u,
+                             keep > 5 ? w.z : keep > 3 ? w.z & odd : 0u, keep > 5 ? w.w & odd : 0u);
+            }
             for (int t = base + l; t < end; ++t) {
               float2 z = make_float2(0.f, 0.f), y = z;
               const float* vt = v0 + static_cast<int64_t>(t) * rm;
-#pragma unroll 2
+#pragma unroll 4
               for (int e = 0; e < have; ++e) {
-                float2 bp[4], va, vb, vc, vd;
-                const int at = ((get + e) & (q.ring - 1)) * 512;
+                float2 va, vb, vc, vd;
+                const uint4 w = lds128(b + e * 512);
                 v_pairs(vt + e * 8, va, vb);
                 v_pairs(vt + e * 8 + 4, vc, vd);
-                b_pairs(lds128(s_b + at), ranks - 8 * e, bp);
-                z = __ffma2_rn(va, bp[0], z);
-                y = __ffma2_rn(vb, bp[1], y);
-                z = __ffma2_rn(vc, bp[2], z);
-                y = __ffma2_rn(vd, bp[3], y);
+                z = __ffma2_rn(va, bf16_pair_f32(w.x), z);
+                y = __ffma2_rn(vb, bf16_pair_f32(w.y), y);
+                z = __ffma2_rn(vc, bf16_pair_f32(w.z), z);
+                y = __ffma2_rn(vd, bf16_pair_f32(w.w), y);
               }
               tmem_st1(zcol + static_cast<uint32_t>(t), (z.x + z.y) + (y.x + y.y));
             }
             get += have;
-            room += have;
+            room += cost;
             ++done;
             ask_b();
           }

@@ -118,6 +118,9 @@ __device__ __forceinline__ void store_out(const ProjectParams& p, int64_t at, fl
   else static_cast<float*>(p.out)[at] = y;
 }
 
+__device__ __forceinline__ float2 bf16_pair_f32(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 // Eight entries of B as four pairs, zero from the rank on.
 __device__ __forceinline__ void b_pairs(const uint4 w, int left, float2 (&b)[4]) {
   float f[8];
