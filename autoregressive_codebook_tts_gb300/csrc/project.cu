@@ -12,13 +12,12 @@
 //     distributed shared memory.  Many tiles: CTAs walk them, and with up to 160 rows a tile the
 //     accumulator is double, so the products of the next tile run under the epilogue;
 //   * the epilogue's warps take z = v B_a^T on the CUDA cores, in f32, while the tensor cores work: a
-//     group of four warps covers the 128 columns, a lane streams its own row of each B_a through a ring
-//     of asynchronous copies (no lane waits for another's), v comes by one bulk copy, and z waits in
-//     tensor memory beside the accumulator.  So x A^T is never rounded, a request's adapter never meets
-//     another request's row, and what lies behind an adapter's rank is not used.  The copies and
-//     products of a row are a few hundred instructions that wait on each other, so a group has about four
-//     rows, as far as six groups go (96 requests with adapters of up to 64 ranks, 12288 columns: 84 us
-//     with one group, 51 with three; neighbouring lanes taking neighbouring pieces of a row: no gain).
+//     group of four warps covers the 128 columns, a warp streams 32 rows of each B_a through a ring of
+//     asynchronous copies of its own, v comes by one bulk copy, and z waits in tensor memory beside the
+//     accumulator.  So x A^T is never rounded, a request's adapter never meets another request's row,
+//     and what lies behind an adapter's rank is not used.  The copies and products of a row are a few
+//     hundred instructions that wait on each other, so a group has about four rows, as far as six
+//     groups go.
 #include <map>
 #include <tuple>
 
@@ -35,7 +34,7 @@ constexpr int kMaxThreads = kMaxGroups * 128 + 64;
 constexpr int kTmemCols = 512;
 constexpr int kRedLd = kM + 16;       // floats between the rows of a partial
 constexpr int kMaxAhead = 4;          // runs of B rows in flight at most, a warp
-constexpr int kMaxV = 48 * 1024;      // bytes of v held in shared memory; more is read where it is
+constexpr int kMaxV = 64 * 1024;      // bytes of v a CTA holds at most
 
 struct Plan {
   int nb, nbr;          // x rows a tile (a multiple of 16), and that rounded up to 32
@@ -47,7 +46,6 @@ struct Plan {
   int flat;             // K is not whole columns: one copy each
   int groups;           // of epilogue warps
   int ring;             // 16-byte pieces of B a lane has room for
-  int v_rows;           // rows of v in shared memory (0: none)
   int parts;            // bf16 parts of v that meet B on the tensor cores (0: none do)
   int v_off, b_off, bar_off, smem;
   int vec_out;          // out rows take 16-byte (f32) or 8-byte (bf16) stores
@@ -288,7 +286,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
     const bool with = p.ad.n_adapters > 0;
     const int lo = q.nb * rank / S, hi = q.nb * (rank + 1) / S;   // rows whose adapters this CTA adds,
     const int glo = lo + (hi - lo) * group / q.groups, ghi = lo + (hi - lo) * (group + 1) / q.groups;   // and this group
-    unsigned char* s_b = smem + q.b_off + warp * (q.ring * 512) + lane * 16;   // this lane's ring, pieces 512 bytes apart
+    const uint32_t s_b = smem_u32(smem + q.b_off) + warp * (q.ring * 512);   // this warp's ring: 16-byte pieces of 32 rows
     bool ok = true, waited = !with;
     int i = 0;
     for (int tile = blockIdx.x; tile < q.n_tiles && ok; tile += gridDim.x, ++i) {
@@ -323,10 +321,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
         epilogue_all(true, n_epi);
       }
       if (with) {
-        const unsigned char* brow = static_cast<const unsigned char*>(p.ad.b) + static_cast<int64_t>(n) * rm * 2;
+        const unsigned char* brow = static_cast<const unsigned char*>(p.ad.b) + static_cast<int64_t>(n - lane) * rm * 2;
+        const int rows_in = min(32, p.n - (n - lane));   // of this warp's 32
         const uint32_t pool_step = static_cast<uint32_t>(p.n) * rm * 2;   // (at most 2^28)
-        const float* v0 = q.v_rows > 0 ? s_v - lo * rm : p.v + static_cast<int64_t>(r0) * rm;
-        bool v_here = q.v_rows == 0;
+        bool v_here = false;
         for (int base = glo; base < ghi; base += 32) {
           // runs of rows that share an adapter
           const int t = base + lane;
@@ -350,11 +348,20 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
               if (cost > room) break;
               room -= cost;
               if (wrap) put = 0;
-              if (n < p.n) {
-                const unsigned char* src = brow + static_cast<uint64_t>(static_cast<uint32_t>(of)) * pool_step;
-                unsigned char* dst = s_b + put * 512;
+              // Neighbouring lanes take neighbouring pieces of a row (a row a lane touched 32 lines an
+              // instruction); piece e of row l lies at place l ^ (e & mix) of the piece's 512 bytes, so
+              // that neither a row's pieces as they come nor the rows' as they are read meet in a bank.
+              const int sh = have > 8 ? 4 : have > 4 ? 3 : have > 2 ? 2 : have - 1, step = 32 >> sh;
+              const int e = lane & ((1 << sh) - 1), row = lane >> sh;
+              if (e < have) {
+                const unsigned char* src = brow + static_cast<uint64_t>(static_cast<uint32_t>(of)) * pool_step + row * rm * 2 + e * 16;
+                uint32_t dst = s_b + (put + e) * 512 + ((row ^ (e & min(7, step - 1))) << 4);
 #pragma unroll 4
-                for (int e = 0; e < have; ++e) cp_async16(dst + e * 512, src + e * 16);
+                for (int l = row; l < rows_in; l += step) {
+                  cp_async16(dst, src);
+                  src += step * rm * 2;
+                  dst += step * 16;
+                }
               }
               cp_async_commit();
               put += have;
@@ -387,27 +394,28 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
             const bool wrap = get + have > q.ring;
             const int cost = have + (wrap ? q.ring - get : 0);
             if (wrap) get = 0;
-            unsigned char* b = s_b + get * 512;
+            const uint32_t b = s_b + get * 512;
+            const int mix = have > 8 ? 1 : have > 4 ? 3 : 7;   // (as they were put)
             cp_async_wait(ahead - done - 1);
+            __syncwarp();
             if (ranks & 7) {
               // zeros behind the rank, where v's are
-              unsigned char* tail = b + (have - 1) * 512;
-              const uint4 w = lds128(tail);
+              const uint32_t tail = b + (have - 1) * 512 + ((lane ^ ((have - 1) & mix)) << 4);
+              const uint4 w = lds16(tail);
               const int keep = ranks & 7;
               const uint32_t odd = keep & 1 ? 0xffffu : 0u;   // of the word in which the rank ends
-              *reinterpret_cast<uint4*>(tail) =
-                  make_uint4(keep > 1 ? w.x : w.x & odd, keep > 3 ? w.y : keep > 1 ? w.y & odd : 0u,
-                             keep > 5 ? w.z : keep > 3 ? w.z & odd : 0u, keep > 5 ? w.w & odd : 0u);
+              sts16(tail, make_uint4(keep > 1 ? w.x : w.x & odd, keep > 3 ? w.y : keep > 1 ? w.y & odd : 0u,
+                                     keep > 5 ? w.z : keep > 3 ? w.z & odd : 0u, keep > 5 ? w.w & odd : 0u));
             }
             for (int t = base + l; t < end; ++t) {
               float2 z = make_float2(0.f, 0.f), y = z;
-              const float* vt = v0 + static_cast<int64_t>(t) * rm;
+              const uint32_t vt = smem_u32(s_v) + (t - lo) * rm * 4;
 #pragma unroll 4
               for (int e = 0; e < have; ++e) {
                 float2 va, vb, vc, vd;
-                const uint4 w = lds128(b + e * 512);
-                v_pairs(vt + e * 8, va, vb);
-                v_pairs(vt + e * 8 + 4, vc, vd);
+                const uint4 w = lds16(b + e * 512 + ((lane ^ (e & mix)) << 4));
+                v_pairs(vt + e * 32, va, vb);
+                v_pairs(vt + e * 32 + 16, vc, vd);
                 z = __ffma2_rn(va, bf16_pair_f32(w.x), z);
                 y = __ffma2_rn(vb, bf16_pair_f32(w.y), y);
                 z = __ffma2_rn(vc, bf16_pair_f32(w.z), z);
@@ -418,6 +426,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
             get += have;
             room += cost;
             ++done;
+            __syncwarp();   // (read by all lanes)
             ask_b();
           }
         }
@@ -569,15 +578,15 @@ int max_active_clusters(int dev, int S, int smem) {
 // Shared memory of a plan: the ring of operands, v, the rings of B rows, barriers.
 void lay_out(Plan& q, int rank_max, size_t budget) {
   const int rows = (q.nb + q.split - 1) / q.split;   // whose adapters a CTA adds
-  const int want = (rows + 3) / 4, most = rank_max > 64 ? kMaxGroups / 2 : kMaxGroups;
+  const int v = (rows * rank_max * 4 + 127) / 128 * 128;
+  const int want = (rows + 3) / 4, most = rank_max > 64 || v > kMaxV / 2 ? kMaxGroups / 2 : kMaxGroups;
   q.groups = rank_max == 0 ? 1 : want < most ? want : most;
   q.ring = rank_max == 0 ? 0 : rank_max > 64 ? 16 : 8;   // (a power of two that holds a row of B)
-  q.v_rows = rows * rank_max * 4 <= kMaxV ? rows : 0;
-  const int v = (q.v_rows * rank_max * 4 + 127) / 128 * 128, b = q.groups * 4 * q.ring * 512;
-  // (beside many groups' rings stages of two columns would be too few)
-  if (q.groups > 3 && q.ch > 1) q.ch = 1;
-  const int stage = q.ch * (kWChunk + q.nb * kRowBytes);
-  const int fixed = 1024 + v + b + kBarBytes;
+  const int b = q.groups * 4 * q.ring * 512;
+  const int fixed = 1024 + v + b + kBarBytes, chunk = kWChunk + q.nb * kRowBytes;
+  // two stages at least, where one column of K a stage leaves room for them
+  while (q.ch > 1 && static_cast<int>(budget) - fixed < 2 * q.ch * chunk) q.ch /= 2;
+  const int stage = q.ch * chunk;
   int st = static_cast<int>((budget - fixed) / stage);
   const int per_cta = (q.n_chunks + q.ch - 1) / q.ch;
   st = st > kMaxStages ? kMaxStages : st;
@@ -611,7 +620,8 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
   q.flat = p.k * es % kRowBytes != 0;
   // Up to 256 rows are one tile where that leaves every CTA one tile at most; else tiles of up to
   // 160 rows, of which two accumulators and z fit tensor memory.
-  const int most = p.rows <= 256 && q.n_nt <= n_sm ? 256 : 160;
+  int most = p.rows <= 256 && q.n_nt <= n_sm ? 256 : 160;
+  if (most * rm * 4 > kMaxV) most = 128;   // (whose v fits)
   q.n_rt = (p.rows + most - 1) / most;
   q.nb = ((p.rows + q.n_rt - 1) / q.n_rt + 15) / 16 * 16;
   q.n_rt = (p.rows + q.nb - 1) / q.nb;
@@ -654,7 +664,7 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// From this many rows on the adapters' products run on the tensor cores.
+// From this many rows on the adapters' products may run on the tensor cores.
 bool project_tc(int rows) { return rows >= 128; }
 
 size_t project_workspace(int rows, int rank_max) {
@@ -665,7 +675,8 @@ size_t project_workspace(int rows, int rank_max) {
 
 cudaError_t launch_project(const ProjectParams& given, void* workspace, cudaStream_t s) {
   ProjectParams p = given;
-  p.tc = p.ad.n_adapters > 0 && project_tc(p.rows);
+  // on the tensor cores where requests have eight rows and more
+  p.tc = p.ad.n_adapters > 0 && project_tc(p.rows) && p.row_stream != nullptr && p.n_streams <= p.rows / 8;
   if (p.ad.n_adapters > 0) {
     const size_t v = static_cast<size_t>(p.rows) * p.ad.rank_max;
     unsigned char* at = static_cast<unsigned char*>(workspace);

@@ -94,8 +94,17 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
       ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes at a shared-memory address
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, const uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // A barrier of the epilogue's threads that also makes an outcome common to them.
@@ -133,10 +142,10 @@ __device__ __forceinline__ void b_pairs(const uint4 w, int left, float2 (&b)[4])
   for (int e = 0; e < 4; ++e) b[e] = make_float2(f[2 * e], f[2 * e + 1]);
 }
 // four entries of v at once, the same address for the whole warp
-__device__ __forceinline__ void v_pairs(const float* v, float2& a, float2& b) {
-  const float4 x = *reinterpret_cast<const float4*>(v);
-  a = make_float2(x.x, x.y);
-  b = make_float2(x.z, x.w);
+__device__ __forceinline__ void v_pairs(uint32_t v, float2& a, float2& b) {
+  const uint4 x = lds16(v);
+  a = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+  b = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
 }
 
 // cuTensorMapEncodeTiled, looked up once through the runtime (no link against the driver)
