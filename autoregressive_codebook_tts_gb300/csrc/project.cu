@@ -12,12 +12,13 @@
 //     distributed shared memory.  Many tiles: CTAs walk them, and with up to 160 rows a tile the
 //     accumulator is double, so the products of the next tile run under the epilogue;
 //   * the epilogue's warps take z = v B_a^T on the CUDA cores, in f32, while the tensor cores work: a
-//     group of four warps covers the 128 columns, a warp streams 32 rows of each B_a through a ring of
-//     asynchronous copies of its own, v comes by one bulk copy, and z waits in tensor memory beside the
-//     accumulator.  So x A^T is never rounded, a request's adapter never meets another request's row,
-//     and what lies behind an adapter's rank is not used.  The copies and products of a row are a few
-//     hundred instructions that wait on each other, so a group has about four rows, as far as six
-//     groups go.
+//     group of four warps covers the 128 columns; a warp loads 32 rows of a B_a into registers while it
+//     works on the last ones, and lays them out in shared memory; v comes by one bulk copy, and z waits
+//     in tensor memory beside the accumulator.  So x A^T is never rounded, a request's adapter never
+//     meets another request's row, and what lies behind an adapter's rank is not used.  (Asynchronous
+//     copies to shared memory took a wavefront a lane, however the lanes shared the rows, 16 bytes a
+//     clock; TMA boxes of 32 rows no less: 35 us of the 57 that 96 requests with adapters of up to 64
+//     ranks, 12288 columns, took either way.)  A group has about four rows, as far as four groups go.
 #include <map>
 #include <tuple>
 
@@ -29,11 +30,11 @@ namespace {
 constexpr int kWChunk = kM * kRowBytes;
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxGroups = 6;         // groups of four epilogue warps; then a warp for copies, one for products
-constexpr int kMaxThreads = kMaxGroups * 128 + 64;
+// Groups of four epilogue warps; then a warp for copies, one for products.  WIDE: ranks over 64.
+constexpr int max_groups(bool wide) { return wide ? 3 : 4; }
+constexpr int max_threads(bool wide) { return max_groups(wide) * 128 + 64; }
 constexpr int kTmemCols = 512;
 constexpr int kRedLd = kM + 16;       // floats between the rows of a partial
-constexpr int kMaxAhead = 4;          // runs of B rows in flight at most, a warp
 constexpr int kMaxV = 64 * 1024;      // bytes of v a CTA holds at most
 
 struct Plan {
@@ -45,19 +46,12 @@ struct Plan {
   int n_chunks;         // 128-byte columns of K (the last may be short)
   int flat;             // K is not whole columns: one copy each
   int groups;           // of epilogue warps
-  int ring;             // 16-byte pieces of B a lane has room for
+  int pieces;           // 16-byte pieces of a row of B a warp has room for
   int parts;            // bf16 parts of v that meet B on the tensor cores (0: none do)
   int v_off, b_off, bar_off, smem;
   int vec_out;          // out rows take 16-byte (f32) or 8-byte (bf16) stores
 };
 
-// All but the newest n copy groups of this thread have landed, n < kMaxAhead.
-__device__ __forceinline__ void cp_async_wait(int n) {
-  if (n >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
-  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
 // Neighbouring blocks of 16 rows that share an adapter.
 struct BlockRun {
   int ad, first, count;   // blocks [first, first + count) of the tile
@@ -88,8 +82,8 @@ __device__ __forceinline__ int tile_block(const ProjectParams& p, const Plan& q,
   return lane < q.nb / 16 && r < p.rows ? __ldcg(p.block_ad + r / 16) : -1;
 }
 
-template <bool E4M3>
-__global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_constant__ CUtensorMap wmap,
+template <bool E4M3, bool WIDE>
+__global__ void __launch_bounds__(max_threads(WIDE), 1) project_kernel(const __grid_constant__ CUtensorMap wmap,
                                                               const __grid_constant__ CUtensorMap xmap,
                                                               const __grid_constant__ CUtensorMap bmap,
                                                               const __grid_constant__ CUtensorMap vmap,
@@ -286,7 +280,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
     const bool with = p.ad.n_adapters > 0;
     const int lo = q.nb * rank / S, hi = q.nb * (rank + 1) / S;   // rows whose adapters this CTA adds,
     const int glo = lo + (hi - lo) * group / q.groups, ghi = lo + (hi - lo) * (group + 1) / q.groups;   // and this group
-    const uint32_t s_b = smem_u32(smem + q.b_off) + warp * (q.ring * 512);   // this warp's ring: 16-byte pieces of 32 rows
+    const uint32_t s_b = smem_u32(smem + q.b_off) + warp * (q.pieces * 512);   // this warp's 32 rows of B, piece by piece
     bool ok = true, waited = !with;
     int i = 0;
     for (int tile = blockIdx.x; tile < q.n_tiles && ok; tile += gridDim.x, ++i) {
@@ -332,44 +326,22 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
           const int k = a >= 0 ? s_tile.rank[t] : 0, prev = __shfl_up_sync(kFull, a, 1);
           const uint32_t edge = __ballot_sync(kFull, lane == 0 || a != prev);
           const uint32_t first = __ballot_sync(kFull, a >= 0 && (lane == 0 || a != prev));
-          // B rows go round the ring, as many runs ahead as fit it; a run's pieces lie together
-          uint32_t next = first;
-          int ahead = 0, done = 0, put = 0, room = q.ring, get = 0;
-          auto ask_b = [&]() {
-            while (next != 0 && ahead - done < kMaxAhead) {
-              const int l = __ffs(static_cast<int>(next)) - 1, of = __shfl_sync(kFull, a, l);
-              const int have = (__shfl_sync(kFull, k, l) + 7) >> 3;
-              if (ahead == done) {   // (an empty ring begins again)
-                put = get = 0;
-                room = q.ring;
-              }
-              const bool wrap = put + have > q.ring;
-              const int cost = have + (wrap ? q.ring - put : 0);
-              if (cost > room) break;
-              room -= cost;
-              if (wrap) put = 0;
-              // Neighbouring lanes take neighbouring pieces of a row (a row a lane touched 32 lines an
-              // instruction); piece e of row l lies at place l ^ (e & mix) of the piece's 512 bytes, so
-              // that neither a row's pieces as they come nor the rows' as they are read meet in a bank.
-              const int sh = have > 8 ? 4 : have > 4 ? 3 : have > 2 ? 2 : have - 1, step = 32 >> sh;
-              const int e = lane & ((1 << sh) - 1), row = lane >> sh;
-              if (e < have) {
-                const unsigned char* src = brow + static_cast<uint64_t>(static_cast<uint32_t>(of)) * pool_step + row * rm * 2 + e * 16;
-                uint32_t dst = s_b + (put + e) * 512 + ((row ^ (e & min(7, step - 1))) << 4);
-#pragma unroll 4
-                for (int l = row; l < rows_in; l += step) {
-                  cp_async16(dst, src);
-                  src += step * rm * 2;
-                  dst += step * 16;
-                }
-              }
-              cp_async_commit();
-              put += have;
-              ++ahead;
-              next &= next - 1;
-            }
+          // A run's B rows, into registers: neighbouring lanes take neighbouring pieces of a row.  Piece e
+          // of row l then lies at place l ^ (e & mix) of the piece's 512 bytes, so that neither a row's
+          // pieces as they are stored nor the rows' as they are read meet in a bank.
+          constexpr int kPieces = WIDE ? 16 : 8;
+          uint4 w[kPieces];
+          auto shift_of = [](int have) { return have > 8 ? 4 : have > 4 ? 3 : have > 2 ? 2 : have - 1; };
+          auto ask_b = [&](int l) {
+            const int of = __shfl_sync(kFull, a, l), have = (__shfl_sync(kFull, k, l) + 7) >> 3;
+            const int sh = shift_of(have), step = 32 >> sh, e = lane & ((1 << sh) - 1), row = lane >> sh;
+            const unsigned char* src = brow + static_cast<uint64_t>(static_cast<uint32_t>(of)) * pool_step + row * rm * 2 + e * 16;
+#pragma unroll
+            for (int c = 0; c < kPieces; ++c)
+              if (c < 1 << sh && e < have && row + c * step < rows_in)
+                w[c] = __ldcg(reinterpret_cast<const uint4*>(src + c * step * rm * 2));
           };
-          ask_b();
+          if (first != 0) ask_b(__ffs(static_cast<int>(first)) - 1);
           if (!waited) {
             grid_wait();   // v, and whoever read or wrote out before
             waited = true;
@@ -391,13 +363,18 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
             const int l = __ffs(static_cast<int>(left)) - 1, ranks = __shfl_sync(kFull, k, l), have = (ranks + 7) >> 3;
             const uint32_t later = edge >> l >> 1;
             const int end = base + (later != 0 ? l + __ffs(static_cast<int>(later)) : 32);
-            const bool wrap = get + have > q.ring;
-            const int cost = have + (wrap ? q.ring - get : 0);
-            if (wrap) get = 0;
-            const uint32_t b = s_b + get * 512;
-            const int mix = have > 8 ? 1 : have > 4 ? 3 : 7;   // (as they were put)
-            cp_async_wait(ahead - done - 1);
+            const int sh = shift_of(have), step = 32 >> sh, mix = min(7, step - 1);
+            __syncwarp();   // (the last run has been read)
+            {
+              const int e = lane & ((1 << sh) - 1), row = lane >> sh;
+              const uint32_t dst = s_b + e * 512 + ((row ^ (e & mix)) << 4);
+#pragma unroll
+              for (int c = 0; c < kPieces; ++c)
+                if (c < 1 << sh && e < have) sts16(dst + c * step * 16, w[c]);
+            }
             __syncwarp();
+            if (left & (left - 1)) ask_b(__ffs(static_cast<int>(left & (left - 1))) - 1);
+            const uint32_t b = s_b;
             if (ranks & 7) {
               // zeros behind the rank, where v's are
               const uint32_t tail = b + (have - 1) * 512 + ((lane ^ ((have - 1) & mix)) << 4);
@@ -423,11 +400,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) project_kernel(const __grid_co
               }
               tmem_st1(zcol + static_cast<uint32_t>(t), (z.x + z.y) + (y.x + y.y));
             }
-            get += have;
-            room += cost;
-            ++done;
-            __syncwarp();   // (read by all lanes)
-            ask_b();
           }
         }
         if (!waited) grid_wait();
@@ -543,7 +515,7 @@ constexpr int kBarBytes = (2 * kMaxStages + 5) * 8 + 16;
 
 // The dynamic shared memory a CTA of the kernel may take on device `dev`, set as its limit once
 // per device; 0 on failure.
-template <bool E4M3>
+template <bool E4M3, bool WIDE>
 size_t configure(int dev) {
   static std::mutex mtx;
   static size_t budget[64] = {};
@@ -552,17 +524,17 @@ size_t configure(int dev) {
   int optin = 0;
   cudaFuncAttributes fa;
   if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-      cudaFuncGetAttributes(&fa, project_kernel<E4M3>) != cudaSuccess || static_cast<size_t>(optin) <= fa.sharedSizeBytes)
+      cudaFuncGetAttributes(&fa, project_kernel<E4M3, WIDE>) != cudaSuccess || static_cast<size_t>(optin) <= fa.sharedSizeBytes)
     return 0;
   const size_t b = static_cast<size_t>(optin) - fa.sharedSizeBytes;
-  if (cudaFuncSetAttribute(project_kernel<E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(b)) != cudaSuccess)
+  if (cudaFuncSetAttribute(project_kernel<E4M3, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(b)) != cudaSuccess)
     return 0;
   budget[dev] = b;
   return b;
 }
 
 // Clusters of S CTAs that the device keeps resident at once (cached).
-template <bool E4M3>
+template <bool E4M3, bool WIDE>
 int max_active_clusters(int dev, int S, int smem) {
   static std::mutex mtx;
   static std::map<std::tuple<int, int, int>, int> cache;
@@ -570,7 +542,7 @@ int max_active_clusters(int dev, int S, int smem) {
   std::lock_guard<std::mutex> lock(mtx);
   const auto it = cache.find(key);
   if (it != cache.end()) return it->second;
-  const int n = active_clusters(project_kernel<E4M3>, S, kMaxThreads, smem);
+  const int n = active_clusters(project_kernel<E4M3, WIDE>, S, max_threads(WIDE), smem);
   cache[key] = n;
   return n;
 }
@@ -579,10 +551,10 @@ int max_active_clusters(int dev, int S, int smem) {
 void lay_out(Plan& q, int rank_max, size_t budget) {
   const int rows = (q.nb + q.split - 1) / q.split;   // whose adapters a CTA adds
   const int v = (rows * rank_max * 4 + 127) / 128 * 128;
-  const int want = (rows + 3) / 4, most = rank_max > 64 || v > kMaxV / 2 ? kMaxGroups / 2 : kMaxGroups;
+  const int want = (rows + 3) / 4, most = rank_max > 64 || v > kMaxV / 2 ? max_groups(true) : max_groups(false);
   q.groups = rank_max == 0 ? 1 : want < most ? want : most;
-  q.ring = rank_max == 0 ? 0 : rank_max > 64 ? 16 : 8;   // (a power of two that holds a row of B)
-  const int b = q.groups * 4 * q.ring * 512;
+  q.pieces = rank_max == 0 ? 0 : rank_max <= 16 ? 2 : rank_max <= 32 ? 4 : rank_max <= 64 ? 8 : 16;
+  const int b = q.groups * 4 * q.pieces * 512;
   const int fixed = 1024 + v + b + kBarBytes, chunk = kWChunk + q.nb * kRowBytes;
   // two stages at least, where one column of K a stage leaves room for them
   while (q.ch > 1 && static_cast<int>(budget) - fixed < 2 * q.ch * chunk) q.ch /= 2;
@@ -602,13 +574,13 @@ void lay_out(Plan& q, int rank_max, size_t budget) {
   q.smem = 1024 + q.bar_off + kBarBytes;
 }
 
-template <bool E4M3>
+template <bool E4M3, bool WIDE>
 cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  const size_t budget = configure<E4M3>(dev);
+  const size_t budget = configure<E4M3, WIDE>(dev);
   if (budget == 0) {
     const cudaError_t le = cudaGetLastError();
     return le != cudaSuccess ? le : cudaErrorInvalidValue;
@@ -637,7 +609,7 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
       Plan t = q;
       t.split = c;
       lay_out(t, rm, budget);
-      if (static_cast<size_t>(t.smem) <= budget && q.n_tiles <= max_active_clusters<E4M3>(dev, c, t.smem)) q.split = c;
+      if (static_cast<size_t>(t.smem) <= budget && q.n_tiles <= max_active_clusters<E4M3, WIDE>(dev, c, t.smem)) q.split = c;
     }
   }
   lay_out(q, rm, budget);
@@ -659,7 +631,7 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   const dim3 grid = q.split > 1 ? dim3(q.n_tiles, q.split) : dim3(q.n_tiles < n_sm ? q.n_tiles : n_sm);
-  return launch_clustered(project_kernel<E4M3>, grid, 128 * q.groups + 64, q.smem, q.split, s, wmap, xmap, bmap, vmap, p, q);
+  return launch_clustered(project_kernel<E4M3, WIDE>, grid, 128 * q.groups + 64, q.smem, q.split, s, wmap, xmap, bmap, vmap, p, q);
 }
 
 }  // namespace
@@ -685,7 +657,9 @@ cudaError_t launch_project(const ProjectParams& given, void* workspace, cudaStre
     p.block_ad = reinterpret_cast<int32_t*>(at + round256(v * 4) + round256(v * 2 * 3));
   }
   if (project_is_many(p)) return launch_project_many(p, s);
-  return p.x_e4m3 ? launch_t<true>(p, s) : launch_t<false>(p, s);
+  const bool wide = p.ad.n_adapters > 0 && p.ad.rank_max > 64;
+  if (p.x_e4m3) return wide ? launch_t<true, true>(p, s) : launch_t<true, false>(p, s);
+  return wide ? launch_t<false, true>(p, s) : launch_t<false, false>(p, s);
 }
 
 }  // namespace tts
