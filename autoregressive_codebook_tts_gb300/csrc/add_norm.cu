@@ -1,17 +1,19 @@
 // The residual's addition and the RMS norm of the sum, to f32, bf16 or e4m3 rows with a scale.
 //
 // A row is read once and held in registers (eight entries a vector): the sum is stored, its mean
-// square is reduced by shuffles (and through shared memory where a row has several warps), and y
-// leaves in the output's type; for e4m3 the row's largest |y| is reduced in the same way.  Sums and
-// statistics are in f32.  Nothing is read twice, so the kernel is bound by HBM on many rows and by
-// the launch and one round trip to memory on few.
+// square is reduced by shuffles and through shared memory, and y
+// leaves in the output's type.  Sums and statistics are in f32.  Nothing is read twice, so the kernel
+// is bound by HBM on many rows and by the launch and one round trip to memory on few.
+//
+// e4m3: the root is common to a row's entries and their largest, so the code of entry i is that
+// nearest to 448 h_i g_i / max |h g|, with no rounding of y in between.  A quotient of f32 values
+// decides it unless it lies within a few last places of a border (an entry in some 10^5); those are
+// decided by the products in double, which holds them exactly.
 #include "cache_view.cuh"
 #include "serve_kernels.h"
 
 namespace tts {
 namespace {
-
-constexpr int kRowsPerBlock = 4;   // where a warp has a row of its own
 
 __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
   const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
@@ -31,119 +33,167 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
 }
+__device__ __forceinline__ void gamma8(const float* p, float (&g)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w; g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
+}
 // an f32 value rounded to the residual's type
 __device__ __forceinline__ float as_stored(float x, const float*) { return x; }
 __device__ __forceinline__ float as_stored(float x, const __nv_bfloat16*) { return __bfloat162float(__float2bfloat16_rn(x)); }
 
-// V vectors a thread.  WARP: a warp has a row of its own, else a block has.
-template <typename X, typename R, typename O, int V, bool WARP>
-__global__ void __launch_bounds__(WARP ? kRowsPerBlock * 32 : (V == 1 ? 512 : 1024)) add_norm_kernel(const AddNormParams p) {
+// Codes of the quotients x * inv of eight entries; whether one of them lies within a few last places of
+// a border.  20 mantissa bits are dropped from a normal code, a border has them at 0x80000; below 2^-6
+// the codes are 2^-9 apart.  (x, inv and the product are off by two units in the last place together.)
+__device__ __forceinline__ bool codes_near(const float (&x)[8], float inv, uint2& w) {
+  uint32_t border = ~0u;
+  float off = 0.f;
+  uint32_t c[4];
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float a = __fmul_rn(x[e], inv), b = __fmul_rn(x[e + 1], inv);
+    border = min(border, min((__float_as_uint(a) & 0xfffffu) - 0x7fff8u, (__float_as_uint(b) & 0xfffffu) - 0x7fff8u));
+    // quotient / 2^-9 off its nearest integer (1.5 2^23 added and taken away leaves that)
+    const float da = fmaf(a, 512.f, -__fsub_rn(fmaf(a, 512.f, 12582912.f), 12582912.f));
+    const float db = fmaf(b, 512.f, -__fsub_rn(fmaf(b, 512.f, 12582912.f), 12582912.f));
+    off = fmaxf(off, fmaxf(fabsf(a) < 0.015625f ? fabsf(da) : 0.f, fabsf(b) < 0.015625f ? fabsf(db) : 0.f));
+    c[e / 2] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  }
+  w = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+  return border <= 16u || off > 0.49999f;
+}
+// The same from the exact products of h and gamma, against the largest of the row.
+__device__ __noinline__ uint2 codes_exact(float4 a, float4 b, const float* gamma, double most) {
+  const float4 g = __ldg(reinterpret_cast<const float4*>(gamma)), k = __ldg(reinterpret_cast<const float4*>(gamma) + 1);
+  auto code = [&](float h, float c) {
+    return static_cast<uint32_t>(
+        __nv_cvt_double_to_fp8(E4m3Code::kTop * (static_cast<double>(h) * static_cast<double>(c)) / most, __NV_SATFINITE, __NV_E4M3));
+  };
+  return make_uint2(code(a.x, g.x) | code(a.y, g.y) << 8 | code(a.z, g.z) << 16 | code(a.w, g.w) << 24,
+                    code(b.x, k.x) | code(b.y, k.y) << 8 | code(b.z, k.z) << 16 | code(b.w, k.w) << 24);
+}
+
+// A block a row, V vectors a thread.  (A warp a row with eight vectors a lane has fewer loads in flight
+// an SM for its registers: 6001 rows of 2048, bf16 to bf16 25.2 us against 19.2.)
+template <typename X, typename R, typename O, int V>
+__global__ void __launch_bounds__(V == 1 ? 512 : 1024) add_norm_kernel(const AddNormParams p) {
   constexpr bool kCodes = sizeof(O) == 1;
   __shared__ float s_sum[32];
   __shared__ uint32_t s_top[32];
+  __shared__ int s_rest;   // what the largest product is above its rounded value, as an ordered integer
   grid_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = WARP ? lane : static_cast<int>(threadIdx.x), nt = WARP ? 32 : static_cast<int>(blockDim.x);
-  const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + warp : blockIdx.x;
-  if (row >= p.rows) return;   // (a whole warp; no block barrier follows for WARP)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = threadIdx.x, nt = blockDim.x;
+  const int64_t row = blockIdx.x;
   const X* x = static_cast<const X*>(p.x) + row * p.x_stride;
   const R* res = static_cast<const R*>(p.res) + row * p.res_stride;
-  float h[V][8];
-  float ss = 0.f;
+  float h[V][8], g[V][8];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int at = (j * nt + t) * 8;
-    if (at < p.n) load8(x + at, h[j]);
-    else
+    if (at < p.n) {
+      load8(x + at, h[j]);
+      float q[8];
+      if (p.res != nullptr) load8(res + at, q);
+      gamma8(p.gamma + at, g[j]);
+      if (p.res != nullptr) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[j][e] = 0.f;
-  }
-  if (p.res != nullptr) {
-    float q[V][8];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int at = (j * nt + t) * 8;
-      if (at < p.n) load8(res + at, q[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int at = (j * nt + t) * 8;
-      if (at < p.n) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[j][e] = as_stored(q[j][e] + h[j][e], static_cast<const R*>(nullptr));
+        for (int e = 0; e < 8; ++e) h[j][e] = as_stored(q[e] + h[j][e], static_cast<const R*>(nullptr));
         if (p.sum != nullptr) store8(static_cast<R*>(p.sum) + row * p.sum_stride + at, h[j]);
       }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[j][e] = 0.f;
     }
   }
+  float ss = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(h[j][e], h[j][e], ss);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-  if (!WARP) {
-    if (lane == 0) s_sum[warp] = ss;
-    __syncthreads();
-    ss = lane < nt / 32 ? s_sum[lane] : 0.f;
+  if (lane == 0) s_sum[warp] = ss;
+  if (kCodes && t == 0) s_rest = static_cast<int>(0x80000000u);
+  __syncthreads();
+  ss = lane < nt / 32 ? s_sum[lane] : 0.f;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-  }
+  for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
   const float r = 1.0f / sqrtf(ss / static_cast<float>(p.n) + p.eps);
-  // magnitudes order as their bits do; infinities and NaN are the largest
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int at = (j * nt + t) * 8;
-    if (at < p.n) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(p.gamma + at));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(p.gamma + at) + 1);
-      const float g[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[j][e] = h[j][e] * r * g[e];
-        if (kCodes) top = max(top, __float_as_uint(h[j][e]) & 0x7fffffffu);
-      }
-      if constexpr (!kCodes) store8(static_cast<O*>(p.out) + row * p.out_stride + at, h[j]);
-    }
-  }
-  if constexpr (kCodes) {
-    top = __reduce_max_sync(kFull, top);
-    if (!WARP) {
-      if (lane == 0) s_top[warp] = top;
-      __syncthreads();
-      top = __reduce_max_sync(kFull, lane < nt / 32 ? s_top[lane] : 0u);
-    }
-    const bool bad = top >= 0x7f800000u;
-    const float s = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) * (1.0f / E4m3Code::kTop);
-    if (t == 0) p.out_scale[row] = s;
+  if constexpr (!kCodes) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int at = (j * nt + t) * 8;
       if (at < p.n) {
-        uint32_t w[2] = {};
-        if (!bad && s != 0.f) codes<E4m3Code>(h[j], s, w);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * p.out_stride + at) = make_uint2(w[0], w[1]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[j][e] = h[j][e] * r * g[j][e];
+        store8(static_cast<O*>(p.out) + row * p.out_stride + at, h[j]);
       }
+    }
+  } else {
+    // by the power of two below the root (exact), so that the products are as large as y
+    const float u = __uint_as_float(__float_as_uint(r) & 0x7f800000u);
+    // magnitudes order as their bits do; infinities and NaN are the largest
+    uint32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if ((j * nt + t) * 8 < p.n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          h[j][e] *= u;
+          mine = max(mine, __float_as_uint(h[j][e] * g[j][e]) & 0x7fffffffu);
+        }
+      }
+    uint32_t top = __reduce_max_sync(kFull, mine);
+    if (lane == 0) s_top[warp] = top;
+    __syncthreads();
+    top = __reduce_max_sync(kFull, lane < nt / 32 ? s_top[lane] : 0u);
+    const bool bad = top >= 0x7f800000u, plain = bad || top == 0;   // plain: codes 0
+    const float largest = __uint_as_float(top), inv = E4m3Code::kTop / largest;
+    if (t == 0) p.out_scale[row] = bad ? __uint_as_float(0x7fc00000u) : top == 0 ? 0.f : largest * (r / u) * (1.0f / E4m3Code::kTop);
+    uint2 w[V];
+    bool near = false;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      w[j] = make_uint2(0, 0);
+      if ((j * nt + t) * 8 < p.n && !plain) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = h[j][e] * g[j][e];
+        near = codes_near(y, inv, w[j]) || near;
+        if (mine == top) {
+          // one of the products that round to the largest may be it
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if ((__float_as_uint(y[e]) & 0x7fffffffu) == top) {
+              const int rest = __float_as_int(copysignf(1.f, y[e]) * fmaf(h[j][e], g[j][e], -y[e]));
+              atomicMax(&s_rest, rest ^ ((rest >> 31) & 0x7fffffff));
+            }
+        }
+      }
+    }
+    if (__syncthreads_or(near) && near) {
+      const int rest = s_rest;
+      const double most = static_cast<double>(largest) + static_cast<double>(__int_as_float(rest ^ ((rest >> 31) & 0x7fffffff)));
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if ((j * nt + t) * 8 < p.n)
+          w[j] = codes_exact(make_float4(h[j][0], h[j][1], h[j][2], h[j][3]), make_float4(h[j][4], h[j][5], h[j][6], h[j][7]),
+                             p.gamma + (j * nt + t) * 8, most);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int at = (j * nt + t) * 8;
+      if (at < p.n) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * p.out_stride + at) = w[j];
     }
   }
 }
 
 template <typename X, typename R, typename O>
 cudaError_t launch(const AddNormParams& p, cudaStream_t s) {
-  const int vecs = p.n / 8;
-  // A warp a row needs no block barrier, and its lanes have several loads in flight; with few rows
-  // a block a row has more of them.
-  if (vecs <= 256 && p.rows >= 4 * p.n_sm) {
-    const dim3 grid((p.rows + kRowsPerBlock - 1) / kRowsPerBlock), block(kRowsPerBlock * 32);
-    if (vecs <= 64) return launch_pdl(add_norm_kernel<X, R, O, 2, true>, grid, block, 0, s, p);
-    if (vecs <= 128) return launch_pdl(add_norm_kernel<X, R, O, 4, true>, grid, block, 0, s, p);
-    return launch_pdl(add_norm_kernel<X, R, O, 8, true>, grid, block, 0, s, p);
-  }
-  const int v = vecs <= 512 ? 1 : 2;
+  const int vecs = p.n / 8, v = vecs <= 512 ? 1 : 2;
   const dim3 grid(p.rows), block(((vecs + v - 1) / v + 31) / 32 * 32);
-  return v == 1 ? launch_pdl(add_norm_kernel<X, R, O, 1, false>, grid, block, 0, s, p)
-                : launch_pdl(add_norm_kernel<X, R, O, 2, false>, grid, block, 0, s, p);
+  return v == 1 ? launch_pdl(add_norm_kernel<X, R, O, 1>, grid, block, 0, s, p)
+                : launch_pdl(add_norm_kernel<X, R, O, 2>, grid, block, 0, s, p);
 }
 template <typename X, typename R>
 cudaError_t launch_out(const AddNormParams& p, cudaStream_t s) {

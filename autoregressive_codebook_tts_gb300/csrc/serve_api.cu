@@ -74,7 +74,6 @@ tts_status tts_add_rms_norm(const void* x, int64_t x_stride, int32_t x_dtype, co
   p.x_bf16 = x_dtype == TTS_BF16;
   p.res_bf16 = with_res && res_dtype == TTS_BF16;
   p.out_dtype = out_dtype;
-  p.n_sm = sm_count();
   return from_cuda(launch_add_norm(p, as_stream(stream)));
 }
 

@@ -22,7 +22,6 @@ struct AddNormParams {
   float eps;
   int rows, n;
   int x_bf16, res_bf16, out_dtype;
-  int n_sm;
 };
 
 struct PagePlanParams {

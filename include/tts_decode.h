@@ -613,10 +613,10 @@ tts_status tts_tree_commit(const tts_kv_cache* cache, const tts_kv_desc* desc, c
  * The residual's addition and the norm of the sum, row by row:
  *   h = residual + x  (one f32 addition, rounded to res_dtype: the value that is stored)
  *   y = h * (mean(h^2) + eps)^(-1/2) * gamma  (f32)
- * and y as out_dtype: f32; bf16, rounded to nearest even; or E4M3 codes with a scale a row,
- * s = max|y| * (1 / 448) in f32, code = the code nearest to the exact quotient y / s, ties to
- * even (s = 0: codes 0; a row with a NaN or an infinity in y: scale NaN, codes 0), as
- * tts_kv_write_rows rounds a cache row and tts_project_rows takes its rows.
+ * and y as out_dtype: f32; bf16, rounded to nearest even; or E4M3 codes with a scale a row, as
+ * tts_project_rows takes its rows: s = max|y| / 448 in f32, and the code of entry i is the one
+ * nearest to 448 h_i gamma_i / max|h gamma| (the root is common to both; products and quotient
+ * exact), ties to even.  s = 0: codes 0; a row with a NaN or an infinity in y: scale NaN, codes 0.
  *   x: device rows of x_dtype (f32 or bf16), row r at x + r*x_stride elements.
  *   residual: rows of res_dtype (f32 or bf16), or NULL: h = x, and sum_out must be NULL too.
  *   sum_out: rows of res_dtype for h, or NULL; may be residual itself (same stride).
