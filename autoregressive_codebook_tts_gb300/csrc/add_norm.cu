@@ -41,27 +41,7 @@ __device__ __forceinline__ void gamma8(const float* p, float (&g)[8]) {
 __device__ __forceinline__ float as_stored(float x, const float*) { return x; }
 __device__ __forceinline__ float as_stored(float x, const __nv_bfloat16*) { return __bfloat162float(__float2bfloat16_rn(x)); }
 
-// Codes of the quotients x * inv of eight entries; whether one of them lies within a few last places of
-// a border.  20 mantissa bits are dropped from a normal code, a border has them at 0x80000; below 2^-6
-// the codes are 2^-9 apart.  (x, inv and the product are off by two units in the last place together.)
-__device__ __forceinline__ bool codes_near(const float (&x)[8], float inv, uint2& w) {
-  uint32_t border = ~0u;
-  float off = 0.f;
-  uint32_t c[4];
-#pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    const float a = __fmul_rn(x[e], inv), b = __fmul_rn(x[e + 1], inv);
-    border = min(border, min((__float_as_uint(a) & 0xfffffu) - 0x7fff8u, (__float_as_uint(b) & 0xfffffu) - 0x7fff8u));
-    // quotient / 2^-9 off its nearest integer (1.5 2^23 added and taken away leaves that)
-    const float da = fmaf(a, 512.f, -__fsub_rn(fmaf(a, 512.f, 12582912.f), 12582912.f));
-    const float db = fmaf(b, 512.f, -__fsub_rn(fmaf(b, 512.f, 12582912.f), 12582912.f));
-    off = fmaxf(off, fmaxf(fabsf(a) < 0.015625f ? fabsf(da) : 0.f, fabsf(b) < 0.015625f ? fabsf(db) : 0.f));
-    c[e / 2] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  }
-  w = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-  return border <= 16u || off > 0.49999f;
-}
-// The same from the exact products of h and gamma, against the largest of the row.
+// Codes of eight entries from the exact products of h and gamma, against the largest of the row.
 __device__ __noinline__ uint2 codes_exact(float4 a, float4 b, const float* gamma, double most) {
   const float4 g = __ldg(reinterpret_cast<const float4*>(gamma)), k = __ldg(reinterpret_cast<const float4*>(gamma) + 1);
   auto code = [&](float h, float c) {
@@ -133,16 +113,16 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) add_norm_kernel(const Add
     // by the power of two below the root (exact), so that the products are as large as y
     const float u = __uint_as_float(__float_as_uint(r) & 0x7f800000u);
     // magnitudes order as their bits do; infinities and NaN are the largest
-    uint32_t mine = 0;
+    float most = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if ((j * nt + t) * 8 < p.n) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          h[j][e] *= u;
-          mine = max(mine, __float_as_uint(h[j][e] * g[j][e]) & 0x7fffffffu);
-        }
+        for (int e = 0; e < 8; ++e) h[j][e] *= u;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) most = max_abs(most, h[j][e] * g[j][e], h[j][e + 1] * g[j][e + 1]);
       }
+    const uint32_t mine = __float_as_uint(most) & 0x7fffffffu;
     uint32_t top = __reduce_max_sync(kFull, mine);
     if (lane == 0) s_top[warp] = top;
     __syncthreads();
@@ -159,7 +139,10 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) add_norm_kernel(const Add
         float y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = h[j][e] * g[j][e];
-        near = codes_near(y, inv, w[j]) || near;
+        // (roundings: the product, the largest, its quotient, the quotient of the two)
+        uint32_t c[2];
+        near = E4m3Code::fast<5>(y, inv, c) || near;
+        w[j] = make_uint2(c[0], c[1]);
         if (mine == top) {
           // one of the products that round to the largest may be it
 #pragma unroll
@@ -173,12 +156,12 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) add_norm_kernel(const Add
     }
     if (__syncthreads_or(near) && near) {
       const int rest = s_rest;
-      const double most = static_cast<double>(largest) + static_cast<double>(__int_as_float(rest ^ ((rest >> 31) & 0x7fffffff)));
+      const double exact = static_cast<double>(largest) + static_cast<double>(__int_as_float(rest ^ ((rest >> 31) & 0x7fffffff)));
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if ((j * nt + t) * 8 < p.n)
           w[j] = codes_exact(make_float4(h[j][0], h[j][1], h[j][2], h[j][3]), make_float4(h[j][4], h[j][5], h[j][6], h[j][7]),
-                             p.gamma + (j * nt + t) * 8, most);
+                             p.gamma + (j * nt + t) * 8, exact);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {

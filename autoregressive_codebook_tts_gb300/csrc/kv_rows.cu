@@ -85,9 +85,10 @@ __device__ __forceinline__ void write_head_row(void* cache, float* scale, int64_
   const int64_t at = row * D + lr * VE;
   if constexpr (CacheElem<KvT>::kScaled) {
     // magnitudes order as their bits do; infinities and NaN are the largest
-    uint32_t top = 0;
+    float most = 0.f;
 #pragma unroll
-    for (int e = 0; e < VE; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+    for (int e = 0; e < VE; e += 2) most = max_abs(most, x[e], x[e + 1]);
+    uint32_t top = __float_as_uint(most) & 0x7fffffffu;
 #pragma unroll
     for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
     if (!live) return;
@@ -157,11 +158,17 @@ __global__ void __launch_bounds__(kWarps * 32) kv_slots_kernel(const KvSlotsPara
   grid_launch_dependents();
   const CacheView& c = p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lr = lane % LPR;
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * RPW + lane / LPR;
-  const int64_t r = i / c.n_kv_heads;
-  const int g = static_cast<int>(i - r * c.n_kv_heads);
-  int64_t slot = r < p.rows ? __ldcg(p.slot + r) : -1;
+  const uint32_t i = (blockIdx.x * kWarps + warp) * RPW + lane / LPR;   // (head rows are below 2^31)
+  const int r = static_cast<int>(i / static_cast<uint32_t>(c.n_kv_heads)), g = static_cast<int>(i) - r * c.n_kv_heads;
+  int64_t slot = -1;
   float xk[VE] = {}, xv[VE] = {};
+  if (r < p.rows) {
+    // a skipped row is read too, rather than all rows only after their slots
+    const int64_t src = r * p.row_stride + static_cast<int64_t>(g) * D + lr * VE;
+    slot = __ldcg(p.slot + r);
+    Src<SrcT>::load(p.k, src, xk);
+    Src<SrcT>::load(p.v, src, xv);
+  }
   if (slot >= p.n_slots) {
     if (g == 0 && lr == 0) set_err(p.err, TTS_EFLAG_POS_RANGE);
     slot = -1;
@@ -169,9 +176,6 @@ __global__ void __launch_bounds__(kWarps * 32) kv_slots_kernel(const KvSlotsPara
   const bool live = slot >= 0;
   int64_t row = 0;
   if (live) {
-    const int64_t src = r * p.row_stride + static_cast<int64_t>(g) * D + lr * VE;
-    Src<SrcT>::load(p.k, src, xk);
-    Src<SrcT>::load(p.v, src, xv);
     const int64_t page = c.paged ? slot >> c.page_shift : slot / p.page_rows;
     row = (page * c.n_kv_heads + g) * p.page_rows + (slot - page * p.page_rows);
   }
