@@ -41,15 +41,10 @@ __device__ __forceinline__ void gamma8(const float* p, float (&g)[8]) {
 __device__ __forceinline__ float as_stored(float x, const float*) { return x; }
 __device__ __forceinline__ float as_stored(float x, const __nv_bfloat16*) { return __bfloat162float(__float2bfloat16_rn(x)); }
 
-// Codes of eight entries from the exact products of h and gamma, against the largest of the row.
-__device__ __noinline__ uint2 codes_exact(float4 a, float4 b, const float* gamma, double most) {
-  const float4 g = __ldg(reinterpret_cast<const float4*>(gamma)), k = __ldg(reinterpret_cast<const float4*>(gamma) + 1);
-  auto code = [&](float h, float c) {
-    return static_cast<uint32_t>(
-        __nv_cvt_double_to_fp8(E4m3Code::kTop * (static_cast<double>(h) * static_cast<double>(c)) / most, __NV_SATFINITE, __NV_E4M3));
-  };
-  return make_uint2(code(a.x, g.x) | code(a.y, g.y) << 8 | code(a.z, g.z) << 16 | code(a.w, g.w) << 24,
-                    code(b.x, k.x) | code(b.y, k.y) << 8 | code(b.z, k.z) << 16 | code(b.w, k.w) << 24);
+// The code of an entry from its exact product, against the largest of the row.
+__device__ __noinline__ uint32_t code_exact(float h, float gamma, double most) {
+  return __nv_cvt_double_to_fp8(E4m3Code::kTop * (static_cast<double>(h) * static_cast<double>(gamma)) / most, __NV_SATFINITE,
+                                __NV_E4M3);
 }
 
 // A block a row, V vectors a thread.  (A warp a row with eight vectors a lane has fewer loads in flight
@@ -130,19 +125,17 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) add_norm_kernel(const Add
     const bool bad = top >= 0x7f800000u, plain = bad || top == 0;   // plain: codes 0
     const float largest = __uint_as_float(top), inv = E4m3Code::kTop / largest;
     if (t == 0) p.out_scale[row] = bad ? __uint_as_float(0x7fc00000u) : top == 0 ? 0.f : largest * (r / u) * (1.0f / E4m3Code::kTop);
-    uint2 w[V];
+    uint32_t w[V][2], d[V][2];
     bool near = false;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      w[j] = make_uint2(0, 0);
+      w[j][0] = w[j][1] = d[j][0] = d[j][1] = 0;
       if ((j * nt + t) * 8 < p.n && !plain) {
         float y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = h[j][e] * g[j][e];
         // (roundings: the product, the largest, its quotient, the quotient of the two)
-        uint32_t c[2];
-        near = E4m3Code::fast<5>(y, inv, c) || near;
-        w[j] = make_uint2(c[0], c[1]);
+        near = fast_codes<E4m3Code>(y, inv, 5, w[j], d[j]) || near;
         if (mine == top) {
           // one of the products that round to the largest may be it
 #pragma unroll
@@ -159,14 +152,12 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) add_norm_kernel(const Add
       const double exact = static_cast<double>(largest) + static_cast<double>(__int_as_float(rest ^ ((rest >> 31) & 0x7fffffff)));
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        if ((j * nt + t) * 8 < p.n)
-          w[j] = codes_exact(make_float4(h[j][0], h[j][1], h[j][2], h[j][3]), make_float4(h[j][4], h[j][5], h[j][6], h[j][7]),
-                             p.gamma + (j * nt + t) * 8, exact);
+        each_marked(d[j], h[j], w[j], [&](float x, int e) { return code_exact(x, __ldg(p.gamma + (j * nt + t) * 8 + e), exact); });
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int at = (j * nt + t) * 8;
-      if (at < p.n) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * p.out_stride + at) = w[j];
+      if (at < p.n) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * p.out_stride + at) = make_uint2(w[j][0], w[j][1]);
     }
   }
 }

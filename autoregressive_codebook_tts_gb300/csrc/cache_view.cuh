@@ -42,61 +42,75 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
   return d;
 }
 
+// Puts fix(x[e], e) as entry e's code into w, for each e whose byte in d is not 0.
+template <int N, typename Fix>
+__device__ __forceinline__ void each_marked(uint32_t (&d)[N / 4], const float (&x)[N], uint32_t (&w)[N / 4], Fix fix) {
+#pragma unroll
+  for (int e = 0; e < N; e += 4)
+    while (d[e / 4] != 0) {
+      const int at = (__ffs(d[e / 4]) - 1) & 24;
+      const float y = at < 16 ? (at == 0 ? x[e] : x[e + 1]) : (at == 16 ? x[e + 2] : x[e + 3]);
+      w[e / 4] = (w[e / 4] & ~(0xffu << at)) | fix(y, e + (at >> 3)) << at;
+      d[e / 4] &= ~(0xffu << at);
+    }
+}
+
 // Codes of the 8-bit caches: kTop is the largest; codes() the codes nearest to the exact
 // quotients x / s of N entries, four to a word.
 //
 // x * (1 / s) is off x / s by at most two units in the last place (one rounding of 1 / s, one
-// of the product), so it decides the code unless it lies that close to a border between two
-// codes.  If any of a lane's entries does (about one in 10^4), all of them are decided by the
-// exact remainder x - q s, which one fused multiply-add gives with its right sign.  (No entry
-// is that far below s that the remainder could underflow: tiny rows are scaled up first.)
+// of the product).  Codes rise with the quotient: where a product with a value just below 1 / s and one
+// with a value just above it have the same code, x / s has it too.  (fast_codes() takes those `steps` last
+// places of inv away.  A step is at least 2^-24 of inv, and a rounding on the way to the product at
+// most that, so steps is one more than the roundings.)  The other entries are decided by the exact
+// remainder x - q s, which one fused multiply-add gives with its right sign; one at a time, for half a
+// percent of the entries of a bf16 row are on a border or beside it (none of an f32 row's), which leaves
+// most warps with a few.  (No entry is that far below s that the remainder could underflow: tiny rows
+// are scaled up first.)
+template <typename Code, int N>
+__device__ __forceinline__ bool fast_codes(const float (&x)[N], float inv, int steps, uint32_t (&w)[N / 4], uint32_t (&d)[N / 4]) {
+  const float below = __uint_as_float(__float_as_uint(inv) - steps), above = __uint_as_float(__float_as_uint(inv) + steps);
+  uint32_t any = 0;
+#pragma unroll
+  for (int e = 0; e < N / 4; ++e) {
+    w[e] = Code::four(x + 4 * e, below);
+    d[e] = w[e] ^ Code::four(x + 4 * e, above);
+    any |= d[e];
+  }
+  return any != 0;
+}
 template <typename Code, int N>
 __device__ __forceinline__ void codes(const float (&x)[N], float s, uint32_t (&w)[N / 4]) {
   const bool tiny = s < 1e-27f;
   const float inv = 1.0f / s;
-  if (Code::fast(x, inv, w) || tiny) {
+  uint32_t d[N / 4];
+  if (fast_codes<Code>(x, inv, 3, w, d) || tiny) {
     const float up = tiny ? 1.152921504606846976e18f : 1.0f;   // 2^60
     const float su = s * up, iu = 1.0f / su;
+    if (tiny) {
 #pragma unroll
-    for (int e = 0; e < N / 4; ++e) {
-      w[e] = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[e] |= Code::nearest(x[4 * e + k] * up, su, iu) << (8 * k);
+      for (int e = 0; e < N / 4; ++e) d[e] = ~0u;
     }
+    each_marked(d, x, w, [&](float y, int) { return Code::nearest(y * up, su, iu); });
   }
 }
 
 struct I8Code {
   static constexpr float kTop = 127.f;
   static __device__ __forceinline__ uint32_t nearest(float x, float s, float inv) {
-    const float t = x * inv;
-    float c = rintf(t);
+    // (1.5 2^23 + an integer has it in its low bits: no conversions, which are slow)
+    const float t = x * inv, r = __fadd_rn(t, 12582912.f), c = __fsub_rn(r, 12582912.f);
     // the border beyond c on the quotient's side: is the quotient past it, or on it?
     const float side = copysignf(1.f, t - c), past = side * fmaf(-(c + 0.5f * side), s, x);
-    if (past > 0.f || (past == 0.f && (static_cast<int>(c) & 1) != 0)) c += side;
-    return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(c, -127.f), 127.f))) & 0xffu;
+    const float to = past > 0.f || (past == 0.f && (__float_as_uint(r) & 1u) != 0) ? side : 0.f;
+    return __float_as_uint(fminf(fmaxf(r + to, 12582785.f), 12583039.f)) & 0xffu;
   }
-  // t + 1.5 2^23 has the nearest integer in its low bits; whether one of the quotients is near
-  // a border
-  template <int N>
-  static __device__ __forceinline__ bool fast(const float (&x)[N], float inv, uint32_t (&w)[N / 4]) {
-    float off = 0.f;
-    const float2 i2 = make_float2(inv, inv), magic = make_float2(12582912.f, 12582912.f),
-                 back = make_float2(-12582912.f, -12582912.f), one = make_float2(-1.f, -1.f);
-#pragma unroll
-    for (int e = 0; e < N; e += 4) {
-      uint32_t b[4];
-#pragma unroll
-      for (int k = 0; k < 4; k += 2) {
-        const float2 t = __fmul2_rn(make_float2(x[e + k], x[e + k + 1]), i2), r = __fadd2_rn(t, magic);
-        const float2 d = __ffma2_rn(__fadd2_rn(r, back), one, t);
-        off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
-        b[k] = __float_as_uint(r.x);
-        b[k + 1] = __float_as_uint(r.y);
-      }
-      w[e / 4] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    }
-    return !(off < 0.49995f);
+  // t + 1.5 2^23 has the nearest integer in its low bits
+  static __device__ __forceinline__ uint32_t four(const float* x, float inv) {
+    const float2 i2 = make_float2(inv, inv), magic = make_float2(12582912.f, 12582912.f);
+    const float2 a = __ffma2_rn(make_float2(x[0], x[1]), i2, magic), b = __ffma2_rn(make_float2(x[2], x[3]), i2, magic);
+    return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                       __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
   }
   // the values of a word's codes: code + 128 in the low bits of 2^23
   static __device__ __forceinline__ void values(uint32_t w, float (&f)[4]) {
@@ -124,24 +138,12 @@ struct E4m3Code {
     }
     return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
   }
-  // Codes rise with the quotient: where one just below it and one just above it have the same code,
-  // it has that code.  (A step of inv's last place is at least 2^-24 of it; each rounding on the way
-  // to a product is at most that, so kSteps is one more than the roundings.)  16 x 1024 rows of 8
-  // heads from bf16: 37 us with tests of the mantissas' dropped bits.
-  template <int kSteps = 3, int N>
-  static __device__ __forceinline__ bool fast(const float (&x)[N], float inv, uint32_t (&w)[N / 4]) {
-    const float below = __uint_as_float(__float_as_uint(inv) - kSteps), above = __uint_as_float(__float_as_uint(inv) + kSteps);
-    const float2 lo = make_float2(below, below), hi = make_float2(above, above);
-    uint32_t differ = 0;
-#pragma unroll
-    for (int e = 0; e < N; e += 4) {
-      const float2 a = make_float2(x[e], x[e + 1]), b = make_float2(x[e + 2], x[e + 3]);
-      w[e / 4] = pair(__fmul2_rn(a, lo)) | pair(__fmul2_rn(b, lo)) << 16;
-      differ |= w[e / 4] ^ (pair(__fmul2_rn(a, hi)) | pair(__fmul2_rn(b, hi)) << 16);
-    }
-    return differ != 0;
+  static __device__ __forceinline__ uint32_t four(const float* x, float inv) {
+    const float2 i2 = make_float2(inv, inv);
+    const float2 a = __fmul2_rn(make_float2(x[0], x[1]), i2), b = __fmul2_rn(make_float2(x[2], x[3]), i2);
+    return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3)) |
+           static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3)) << 16;
   }
-  static __device__ __forceinline__ uint32_t pair(float2 t) { return __nv_cvt_float2_to_fp8x2(t, __NV_SATFINITE, __NV_E4M3); }
   static __device__ __forceinline__ void values(uint32_t w, float (&f)[4]) {
     const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
     const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
