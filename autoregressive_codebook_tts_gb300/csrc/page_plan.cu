@@ -47,11 +47,12 @@ __device__ __forceinline__ void block_scan(uint32_t& a, uint32_t& b, uint32_t ca
 }
 
 // The map entries of row r, which is of stream b (or of none: b < 0).
-__device__ __forceinline__ void map_row(const PagePlanParams& p, int r, int b, int t) {
+template <typename Past>
+__device__ __forceinline__ void map_row(const PagePlanParams& p, int r, int b, int t, Past past) {
   int pos = 0;
   int64_t slot = -1;
   if (b >= 0) {
-    pos = __ldcg(p.n_past + b) + t;
+    pos = past(b) + t;
     const int page = __ldcg(p.table + static_cast<int64_t>(b) * p.bt_stride + (pos >> p.page_shift));
     if (page >= 0 && page < p.n_pages)
       slot = (static_cast<int64_t>(page) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
@@ -75,18 +76,18 @@ __device__ __forceinline__ int stream_of(Start start, int B, int r) {
   return lo;
 }
 
-template <typename Start, typename Rows>
-__device__ __forceinline__ void fill_maps(const PagePlanParams& p, int first, int step, Start start, Rows rows) {
+template <typename Start, typename Rows, typename Past>
+__device__ __forceinline__ void fill_maps(const PagePlanParams& p, int first, int step, Start start, Rows rows, Past past) {
   const int total = p.T > 0 ? 0 : start(p.B);
   for (int r = first; r < p.max_rows; r += step) {
     if (p.T > 0) {
       const int b = r / p.T, t = r - b * p.T;
-      map_row(p, r, t < rows(b) ? b : -1, t);
+      map_row(p, r, t < rows(b) ? b : -1, t, past);
     } else if (r < total) {
       const int b = stream_of(start, p.B, r);
-      map_row(p, r, b, r - start(b));
+      map_row(p, r, b, r - start(b), past);
     } else {
-      map_row(p, r, -1, 0);
+      map_row(p, r, -1, 0, past);
     }
   }
 }
@@ -98,6 +99,8 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlanParam
   uint32_t* s_from = s_dyn + 2 * p.B;   // [B] pages needed before it
   int* s_rows = reinterpret_cast<int*>(s_dyn + 3 * p.B);    // [B] rows granted
   int* s_start = reinterpret_cast<int*>(s_dyn + 4 * p.B);   // [B + 1]
+  int* s_new = reinterpret_cast<int*>(s_dyn + 5 * p.B + 1);   // [B] n_new and n_past: asked for once
+  int* s_past = s_new + p.B;
   __shared__ uint2 s_warp[kPlanWarps];
   __shared__ uint2 s_carry;
   __shared__ uint32_t s_used;
@@ -108,6 +111,11 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlanParam
   const int gw = warp * kCtas + rank;   // this warp among the cluster's
   const int per = p.capacity >> p.page_shift;
   const int listed = __ldcg(p.n_free);
+  for (int b = tid; b < p.B; b += kThreads) {
+    const int fresh = __ldcg(p.n_new + b), past = __ldcg(p.n_past + b);
+    s_new[b] = fresh;
+    s_past[b] = past;
+  }
   const int n_free = min(max(listed, 0), p.n_pages);
   int flags = n_free != listed ? TTS_EFLAG_NVALID : 0;
   auto wants = [&](int past, int fresh) {
@@ -120,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlanParam
   const uint32_t need_at = map_shared_rank(s_need, lane & (kCtas - 1));
   cluster_sync_all();   // every CTA of the cluster has begun: its shared memory may be written
   for (int b = gw; b < p.B; b += kAllWarps) {
-    const int fresh = __ldcg(p.n_new + b), past = __ldcg(p.n_past + b);
+    const int fresh = s_new[b], past = s_past[b];
     const int32_t* row = p.table + static_cast<int64_t>(b) * p.bt_stride;
     const bool ended = fresh < 0;
     uint32_t give = 0, need = 0;
@@ -174,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlanParam
     uint32_t need = 0, upto = 0;
     int rows = 0;
     if (b < p.B) {
-      const int fresh = __ldcg(p.n_new + b), past = __ldcg(p.n_past + b);
+      const int fresh = s_new[b], past = s_past[b];
       need = s_need[b];
       upto = s_from[b];
       if (wants(past, fresh)) {
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlanParam
 
   // 4. pages of ended streams to the list
   for (int b = gw; b < p.B; b += kAllWarps) {
-    if (__ldcg(p.n_new + b) >= 0) continue;
+    if (s_new[b] >= 0 || freed == 0) continue;
     int32_t* row = p.table + static_cast<int64_t>(b) * p.bt_stride;
     uint32_t at = n_free + s_give[b];
     for (int i0 = 0; i0 < per; i0 += 32) {
@@ -242,11 +250,11 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlanParam
       at += __popc(m);
     }
   }
-  cluster_sync_all();
+  if (freed != 0) cluster_sync_all();   // (the same in every CTA)
   // 5. pages from the list's end to the entries in need
   for (int b = gw; b < p.B; b += kAllWarps) {
     if (s_rows[b] == 0 || s_need[b] == 0) continue;
-    const int past = __ldcg(p.n_past + b);
+    const int past = s_past[b];
     int32_t* row = p.table + static_cast<int64_t>(b) * p.bt_stride;
     const int lo = past >> p.page_shift, hi = ((past + s_rows[b] - 1) >> p.page_shift) + 1;
     uint32_t from = s_from[b];
@@ -259,9 +267,9 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlanParam
     }
   }
   if (fill) {
-    cluster_sync_all();
+    if (used != 0) cluster_sync_all();
     fill_maps(p, rank * kThreads + tid, kCtas * kThreads, [&](int b) { return s_start[b]; },
-              [&](int b) { return s_rows[b]; });
+              [&](int b) { return s_rows[b]; }, [&](int b) { return s_past[b]; });
   }
 }
 
@@ -274,18 +282,18 @@ __global__ void __launch_bounds__(kFillThreads) page_fill_kernel(const PagePlanP
     __syncthreads();
   }
   fill_maps(p, blockIdx.x * kFillThreads + threadIdx.x, gridDim.x * kFillThreads, [&](int b) { return s_begin[b]; },
-            [&](int b) { return __ldcg(p.n_rows + b); });
+            [&](int b) { return __ldcg(p.n_rows + b); }, [&](int b) { return __ldcg(p.n_past + b); });
 }
 
 }  // namespace
 
 cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t s) {
-  const size_t smem = (5 * static_cast<size_t>(p.B) + 1) * sizeof(uint32_t);
+  const size_t smem = (7 * static_cast<size_t>(p.B) + 1) * sizeof(uint32_t);
   const bool fill = p.max_rows <= kOneLaunchRows;
   cudaError_t e = cudaSuccess;
   if (smem > 40 * 1024)
     e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (5 * TTS_MAX_PLAN_STREAMS + 1) * sizeof(uint32_t));
+                             (7 * TTS_MAX_PLAN_STREAMS + 1) * sizeof(uint32_t));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCtas);

@@ -34,6 +34,12 @@ tts_status check_project(int32_t rows, int32_t n, int32_t k, int32_t x_dtype, co
 
 }  // namespace
 
+namespace {
+// Maps and counts may be slices that begin at any entry.
+template <typename T>
+bool own_size(const T* p) { return reinterpret_cast<uintptr_t>(p) % sizeof(T) == 0; }
+}  // namespace
+
 extern "C" {
 
 tts_status tts_add_rms_norm(const void* x, int64_t x_stride, int32_t x_dtype, const void* residual, int64_t res_stride,
@@ -95,7 +101,7 @@ tts_status tts_project_rows(const void* x, int64_t x_stride, int32_t x_dtype, co
   if (!is_row_dtype(out_dtype)) return TTS_ERR_DTYPE;
   if (x_stride < k || out_stride < n || (ad != nullptr && n_streams < 1)) return TTS_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(w) || !aligned16(out) || !aligned16(x_scale) || !aligned16(w_scale) ||
-      !aligned16(row_stream) || !aligned16(stream_adapter) || !stride_ok(x_stride, x_dtype))
+      !own_size(row_stream) || !own_size(stream_adapter) || !stride_ok(x_stride, x_dtype))
     return TTS_ERR_ALIGN;
   ProjectParams p = {};
   if (ad != nullptr) {
@@ -138,8 +144,8 @@ tts_status tts_page_plan(const tts_kv_desc* d, int32_t* block_table, int32_t* fr
   if (d->B > TTS_MAX_PLAN_STREAMS || d->n_pages > (1 << 30) || T < 0 || max_rows < 1 || max_rows > (1 << 24) ||
       (T > 0 && static_cast<int64_t>(d->B) * T != max_rows))
     return TTS_ERR_SHAPE;
-  if (!aligned16(block_table) || !aligned16(free_pages) || !aligned16(n_free) || !aligned16(n_past) || !aligned16(n_new) ||
-      !aligned16(n_rows) || !aligned16(row_start) || !aligned16(row_stream) || !aligned16(row_pos) || !aligned16(row_slot))
+  if (!own_size(block_table) || !own_size(free_pages) || !own_size(n_free) || !own_size(n_past) || !own_size(n_new) ||
+      !own_size(n_rows) || !own_size(row_start) || !own_size(row_stream) || !own_size(row_pos) || !own_size(row_slot))
     return TTS_ERR_ALIGN;
   PagePlanParams p = {};
   p.table = block_table;
@@ -177,7 +183,7 @@ tts_status tts_kv_write_slots(const void* k, const void* v, int32_t dtype, int64
       row_stride < static_cast<int64_t>(d->n_kv_heads) * d->head_dim)
     return TTS_ERR_SHAPE;
   if (!aligned16(c->k) || !aligned16(c->v) || (scaled && (!aligned16(c->k_scale) || !aligned16(c->v_scale))) ||
-      !aligned16(k) || !aligned16(v) || !aligned16(row_slot) || !stride_ok(row_stride, dtype))
+      !aligned16(k) || !aligned16(v) || !own_size(row_slot) || !stride_ok(row_stride, dtype))
     return TTS_ERR_ALIGN;
   KvSlotsParams p = {};
   p.k = k;

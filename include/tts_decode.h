@@ -606,7 +606,9 @@ tts_status tts_tree_commit(const tts_kv_cache* cache, const tts_kv_desc* desc, c
  * slot), then per layer tts_add_rms_norm, tts_project_rows, tts_rope_rows at row_pos,
  * tts_kv_write_slots and an attention over the same block table.  Row counts are fixed on the
  * host and rows without a request are marked on the device, so that a step can be captured.
- * The conventions above hold (device pointers, stream order, status, err_flag, alignment).
+ * The conventions above hold (device pointers, stream order, status, err_flag, alignment); the
+ * int32 and int64 arrays of tts_page_plan, row_stream, stream_adapter and row_slot need only the
+ * alignment of their entries.
  * =========================================================================== */
 
 /* ---------------------------------------------------------------------------

@@ -505,6 +505,17 @@ def test_plan_with_a_damaged_list(tts):
     pool.step([0, 0], [0, 1])
 
 
+def test_plan_arrays_may_begin_at_any_entry(tts):
+    pool = Pool(tts, 5, 64, 16, 20, 40)
+    for key in ("free", "n_free", "n_rows", "row_start", "row_stream", "row_pos", "row_slot"):
+        t = getattr(pool, key)
+        setattr(pool, key, torch.cat([t[:1], t])[1:])
+    call = pool.call
+    pool.call = lambda past, new, ef: call(torch.cat([past[:1], past])[1:], torch.cat([new[:1], new])[1:], ef)
+    pool.step([0] * 5, [17, 1, 0, -1, 20])
+    pool.step([17, 1, 0, 0, 20], [-1, 16, 3, 5, 1])
+
+
 @pytest.mark.parametrize("max_rows", [900, 20000])
 def test_plan_replayed(tts, max_rows):
     a, b = (Pool(tts, 40, 512, 16, 2000, max_rows, seed=3) for _ in range(2))
