@@ -54,8 +54,9 @@ tts_status tts_add_rms_norm(const void* x, int64_t x_stride, int32_t x_dtype, co
   if (rows < 1 || rows > (1 << 24) || n < 8 || n > TTS_MAX_NORM_WIDTH || n % 8 != 0 || !(eps >= 0.f) || x_stride < n ||
       out_stride < n || (with_res && res_stride < n) || (sum_out != nullptr && sum_stride < n))
     return TTS_ERR_SHAPE;
-  if (!aligned16(x) || !aligned16(residual) || !aligned16(sum_out) || !aligned16(gamma) || !aligned16(out) ||
-      !aligned16(out_scale) || !stride_ok(x_stride, x_dtype) || !stride_ok(out_stride, out_dtype) ||
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(sum_out) || !aligned16(gamma) ||
+      !(codes ? reinterpret_cast<uintptr_t>(out) % 8 == 0 && out_stride % 8 == 0 : aligned16(out) && stride_ok(out_stride, out_dtype)) ||
+      !aligned16(out_scale) || !stride_ok(x_stride, x_dtype) ||
       (with_res && !stride_ok(res_stride, res_dtype)) || (sum_out != nullptr && !stride_ok(sum_stride, res_dtype)))
     return TTS_ERR_ALIGN;
   // in place means the same rows: same type and stride

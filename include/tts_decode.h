@@ -624,8 +624,8 @@ tts_status tts_tree_commit(const tts_kv_cache* cache, const tts_kv_desc* desc, c
  *   sum_out: rows of res_dtype for h, or NULL; may be residual itself (same stride).
  *   gamma: device f32 [n].  n: a multiple of 8, at most TTS_MAX_NORM_WIDTH.  eps >= 0.
  *   out: rows of out_dtype; may be x itself (same type and stride).  out_scale: device f32
- *        [rows] for E4M3, else NULL.  Row strides keep rows 16-byte aligned.  Other overlaps are
- *        not allowed.
+ *        [rows] for E4M3, else NULL.  Row strides keep rows 16-byte aligned (E4M3 rows here:
+ *        8-byte).  Other overlaps are not allowed.
  * ------------------------------------------------------------------------- */
 #define TTS_MAX_NORM_WIDTH 16384
 tts_status tts_add_rms_norm(const void* x, int64_t x_stride, int32_t x_dtype, const void* residual,

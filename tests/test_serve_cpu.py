@@ -44,7 +44,7 @@ def test_add_rms_norm_refuses(tts):
                 dict(eps=-1.0), dict(eps=float("nan")), dict(xs=60), dict(rs=60), dict(ss=60), dict(os_=60)):
         assert call(**bad) == SHAPE, bad
     for bad in (dict(x=24), dict(r=40), dict(s=56), dict(g=8), dict(o=72), dict(od=4, sc=8), dict(xs=66), dict(xd=1, xs=68),
-                dict(od=4, sc=16, os_=72), dict(rd=1, rs=68), dict(rd=1, ss=68)):
+                dict(od=4, sc=16, os_=68), dict(od=4, sc=16, o=68), dict(rd=1, rs=68), dict(rd=1, ss=68)):
         assert call(**bad) == ALIGN, bad
     # in place with another type or stride, or over another operand
     for bad in (dict(o=16, od=1), dict(o=16, os_=68), dict(s=32, ss=68), dict(o=32), dict(o=48), dict(s=16)):

@@ -79,7 +79,7 @@ def test_norm(tts, rows, n, xdt, rdt, odt):
     x = randn(g, rows, n + pad, dt=xdt)[:, :n]
     res = None if rdt is None else (randn(g, rows, n + 2 * pad) * torch.exp(randn(g, n + 2 * pad))).to(R.TORCH[rdt])[:, :n]
     gamma = torch.rand(n, generator=g, device="cuda") + 0.5
-    wide = torch.full((rows + 1, n + (n % 16) + pad), float("nan"), device="cuda").to(R.TORCH[odt])
+    wide = torch.full((rows + 1, n + pad), float("nan"), device="cuda").to(R.TORCH[odt])
     raw, step = wide.view(torch.uint8).clone(), wide.element_size()
     out = wide[:rows, :n]
     total = None if rdt is None else torch.full((rows, n + pad), 7.0, device="cuda").to(R.TORCH[rdt])
@@ -91,6 +91,17 @@ def test_norm(tts, rows, n, xdt, rdt, odt):
     now = wide.view(torch.uint8)
     assert torch.equal(now[:rows, n * step:], raw[:rows, n * step:]) and torch.equal(now[rows], raw[rows])
     assert scale is None or scale[rows] == 7.0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_norm_codes_on_the_border(tts, dt):
+    """bf16 entries and a norm weight of ones: one in 200 quotients is exactly between two codes."""
+    x = randn(gen(3), 400, 520, dt="bf16").to(R.TORCH[dt])
+    x[:64] = torch.randint(-56, 57, (64, 520), device="cuda").to(x.dtype) / 32   # mostly ties: the largest is 56 / 32
+    out, scale = torch.empty(400, 520, device="cuda", dtype=torch.float8_e4m3fn), torch.empty(400, device="cuda")
+    gamma = torch.ones(520, device="cuda")
+    tts.tts_add_rms_norm(x, None, None, gamma, 1e-6, out, out_scale=scale)
+    check_norm(x, None, gamma, "f32", out, scale, "e4m3")
 
 
 @pytest.mark.parametrize("rows", [5, 700])
