@@ -7,6 +7,9 @@
 // memory on the way, exactly.  Beside v in f32 the second form leaves v as three bf16 parts, whose
 // sum is v, and notes which blocks of 16 rows share one adapter: there the wide product can run on
 // the tensor cores too.
+//
+// K 2048: 32 rows of rank 16 5 us, 96 rows of up to 64 ranks 8 (a round trip for the row's adapter, one
+// for its entries); 4093 rows of rank 32 12.5 us, 6000 rows of e4m3 17 (the widening), read from a launch list.
 #include <map>
 #include <tuple>
 

@@ -1,16 +1,18 @@
 // Cache rows: rows written into a cache by position or by slot (quantised for the 8-bit
 // dtypes), read back from it, and moved inside it when a tree's path is accepted.
 //
-// All three only move bytes, so they are bound by HBM on long inputs and by launch latency
+// They only move bytes, so they are bound by HBM on long inputs and by launch latency
 // on one decode step.  A row of head_dim entries is held by the lanes of an eighth to half a
 // warp, so a row's largest magnitude is a few shuffles and nothing goes through shared memory.
 // K and V of a row go through the same lane (two loads in flight at least); many rows to read
 // are read two a lane.
 //
-// 16 x 1024 rows of 8 heads, bf16 into int8: 37 us (2.7 TB/s; 0.68 of the issue slots, the quantiser's);
-// 36.8 k rows back to bf16: 47 us (4.8 TB/s, 0.73 of the measured copy rate; waits on loads).  One row
-// of 32 streams: 2.4 and 1.8 us, a launch.  Both of the first took 208 us with
-// codes by double division and narrower lanes.
+// 16001 rows of 8 heads by slot, bf16 into e4m3 and int8: 24.5 us (4.0 TB/s, the quantiser's issue slots),
+// into bf16 22 (6.0 TB/s); f32 into either 8-bit type 27 (6.1 TB/s, 0.90 of the measured copy rate).
+// (35 us with the borders' test on each mantissa and a whole lane's entries decided again where one
+// was near; 8 entries a lane for bf16: 30 for 28 in e4m3, 32 for 36 in int8 before that went.)  36.8 k rows back to
+// bf16: 47 us (4.8 TB/s, 0.73 of the measured copy rate; waits on loads).  One row of 32 streams: 2.4 and 1.8 us, 64
+// rows by slot 2.05: a launch.
 #include "cache_view.cuh"
 #include "draft_kernels.h"
 #include "serve_kernels.h"

@@ -94,9 +94,6 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
       ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 // 16 bytes at a shared-memory address
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
@@ -106,7 +103,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 __device__ __forceinline__ void sts16(uint32_t a, const uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // A barrier of the epilogue's threads that also makes an outcome common to them.
 __device__ __forceinline__ bool epilogue_all(bool v, int threads) {
   uint32_t out;
