@@ -595,6 +595,23 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
   int most = p.rows <= 256 && q.n_nt <= n_sm ? 256 : 160;
   if (most * rm * 4 > kMaxV) most = 128;   // (whose v fits)
   q.n_rt = (p.rows + most - 1) / most;
+  // Adapters on the CUDA cores take a tile's time row by row, W's stream some 16 rows': where a cluster
+  // cannot share a tile, the cut that makes the least of waves times that.  96 requests x 12288 columns (96 tiles,
+  // or 288 of 32 rows): 51.9 us whole, 47.6 in three; 200 requests 60 and 57; 24000 columns 58 and 50 in two;
+  // but 16384 columns (128 tiles) 38.8 whole, 41 in two.
+  if (rm > 0 && !p.tc && 2 * q.n_nt * q.n_rt > n_sm) {
+    int64_t best = INT64_MAX;
+    int cut = q.n_rt;
+    for (int c = q.n_rt; c <= 4 * q.n_rt; ++c) {
+      const int nb = ((p.rows + c - 1) / c + 15) / 16 * 16;
+      const int64_t tiles = static_cast<int64_t>(q.n_nt) * ((p.rows + nb - 1) / nb), cost = (tiles + n_sm - 1) / n_sm * (nb + 16);
+      if (cost < best) {
+        best = cost;
+        cut = c;
+      }
+    }
+    q.n_rt = cut;
+  }
   q.nb = ((p.rows + q.n_rt - 1) / q.n_rt + 15) / 16 * 16;
   q.n_rt = (p.rows + q.nb - 1) / q.nb;
   q.nbr = (q.nb + 31) / 32 * 32;

@@ -618,7 +618,8 @@ tts_status tts_tree_commit(const tts_kv_cache* cache, const tts_kv_desc* desc, c
  * and y as out_dtype: f32; bf16, rounded to nearest even; or E4M3 codes with a scale a row, as
  * tts_project_rows takes its rows: s = max|y| / 448 in f32, and the code of entry i is the one
  * nearest to 448 h_i gamma_i / max|h gamma| (the root is common to both; products and quotient
- * exact), ties to even.  s = 0: codes 0; a row with a NaN or an infinity in y: scale NaN, codes 0.
+ * exact where max|y| is 2^-60 or more), ties to even.  s = 0: codes 0; a row with a NaN or an
+ * infinity in y: scale NaN, codes 0.
  *   x: device rows of x_dtype (f32 or bf16), row r at x + r*x_stride elements.
  *   residual: rows of res_dtype (f32 or bf16), or NULL: h = x, and sum_out must be NULL too.
  *   sum_out: rows of res_dtype for h, or NULL; may be residual itself (same stride).
