@@ -384,10 +384,11 @@ __global__ void __launch_bounds__(kThreads, 1) project_many_kernel(const __grid_
       }
 #pragma unroll
       for (int c = 0; c < kC; ++c)
-        ad[c] = ad[c] < 0 ? -2 : p.ad.n_adapters == 0 || ad[c] >= p.n_streams ? -1 : __ldcg(p.stream_adapter + ad[c]);
+        // (any negative adapter is none; -2 is for rows of no request)
+        ad[c] = ad[c] < 0 ? -2 : p.ad.n_adapters == 0 || ad[c] >= p.n_streams ? -1 : max(__ldcg(p.stream_adapter + ad[c]), -1);
 #pragma unroll
       for (int c = 0; c < kC; ++c) {
-        if (ad[c] >= p.ad.n_adapters || ad[c] == -1 || ad[c] < -2) ad[c] = -1;
+        if (ad[c] >= p.ad.n_adapters) ad[c] = -1;
         k[c] = ad[c] < 0 ? 0 : p.ad.rank == nullptr ? p.ad.rank_max : __ldcg(p.ad.rank + ad[c]);
       }
       uint32_t edge[kC];
