@@ -633,8 +633,8 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
   if (static_cast<size_t>(q.smem) > budget) return cudaErrorInvalidConfiguration;
   const int quantum = p.out_bf16 ? 8 : 16;
   q.vec_out = p.out_stride * (p.out_bf16 ? 2 : 4) % quantum == 0;
-  // bf16 outputs keep eight bits: two parts, sixteen bits of v, are plenty; f32 outputs get all
-  q.parts = !p.tc ? 0 : p.out_bf16 ? 2 : 3;
+  // (bf16 outputs too need all three: terms of z may cancel)
+  q.parts = p.tc ? 3 : 0;
   CUtensorMap wmap, xmap, bmap, vmap;
   if (!encode(&wmap, p.w, es, p.k, p.k, p.n, kM, q.ch, q.flat) ||
       !encode(&xmap, p.x, es, p.x_stride, p.k, p.rows, q.nb, q.ch, q.flat))

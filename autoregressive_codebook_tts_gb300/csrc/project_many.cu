@@ -9,16 +9,17 @@
 // the same rows of x, whose notes it takes once.
 //
 // K 2048, us: without adapters 4096 rows x 4096 columns in bf16 40.2 (1.71 PFLOP/s; the library's
-// product 36.5), 6000 x 12288 in e4m3 92.7; 4093 rows of 7 requests x 4096, rank 32, bf16 76; 6000 rows x
-// 12288 in e4m3, rank 16, of 5 requests 171, of 40 256.  With 224 rows and one accumulator those three took 79, 202
-// and 247, 4093 rows of 40 requests with rank 64 124 against 105, 1000 rows of ten 90 against 72: runs then
-// have more room, but each epilogue stands between two tiles' products.
+// product 36.5), 6000 x 12288 in e4m3 92.7; 4093 rows of 7 requests x 4096, rank 32, bf16 77; 6000 rows x
+// 12288 in e4m3, rank 16, of 40 requests 277.  (With two parts of v for bf16 outputs 76 and 256, and 171
+// with 5 requests; of that form 224 rows and one accumulator took 79, 247 and 202, 4093 rows of 40 requests
+// with rank 64 124 against 105, 1000 rows of ten 90 against 72: runs then have more room, but each epilogue
+// stands between two tiles' products.)
 //
 // z = v B_a^T: rows of a tile that lie together and share an adapter are a run.  A run has columns of
 // its own (its rows, up to a multiple of 32), so its product meets no other adapter's rows, and what
-// the columns behind it hold is not read.  v comes as bf16 parts (two for bf16 outputs, all three
-// for f32 ones).  Entries of B behind the adapter's rank are overwritten with zeros in shared memory
-// before the product reads them.  Runs that find no room are added on the CUDA cores in the epilogue.
+// the columns behind it hold is not read.  v comes as its three bf16 parts.  Entries of B behind the
+// adapter's rank are overwritten with zeros in shared memory before the product reads them.  Runs that
+// find no room are added on the CUDA cores in the epilogue.
 //
 // Warps: 0-7 epilogue, 8 copies, 9 products (of the pair's first CTA), 10 notes (each row's
 // adapter, runs and their columns, a tile ahead), 11 the zeros behind the ranks, 12 copies of B and v,
@@ -714,7 +715,7 @@ cudaError_t launch_t(const ProjectParams& p, cudaStream_t s) {
   }
   q.n_rt = (p.rows + q.nb - 1) / q.nb;
   q.n_tiles = q.n_nt * q.n_rt;
-  q.parts = rm == 0 ? 0 : p.out_bf16 ? 2 : 3;
+  q.parts = rm == 0 ? 0 : 3;   // (bf16 outputs too need all: terms of z may cancel)
   // Larger copies stream faster: two columns of K a stage and three such stages, and as many of B and
   // v as then fit (one at least).
   const int chunk = kWChunk + q.nb / 2 * kRowBytes, room = static_cast<int>(budget) - 1024 - kBars;
