@@ -141,6 +141,24 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// v as three bf16 values of its own sign whose sum it is: eight bits each of the 24, cut off rather than
+// rounded, so that none is larger than v.  None is 0 unless v is (a part that would be shares the one
+// before it), and an infinity is three: so an infinite entry of B meets what it would have met in v,
+// 0 times infinity only where v is 0.  (The parts are exact down to 2^-100; of a smaller v they may
+// drop what is below bf16's range.)
+__device__ __forceinline__ void parts_of(float v, float (&h)[3]) {
+  auto top = [](float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); };
+  h[0] = top(v);
+  const float rest = v - h[0];
+  h[1] = top(rest);
+  h[2] = rest - h[1];
+  if (!(fabsf(rest) > 0.f)) {   // eight bits, an infinity or NaN
+    h[0] = 0.5f * v;
+    h[1] = h[2] = 0.25f * v;
+  } else if (h[2] == 0.f) {
+    h[1] = h[2] = 0.5f * rest;
+  }
+}
 // 16 codes as bf16, exactly
 __device__ __forceinline__ void widen16(const uint4 w, uint4& lo, uint4& hi) {
   float f[16];
@@ -397,12 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1) shrink_tc_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         v[e] = e < left ? v[e] * xs * as : 0.f;
-        // three parts of eight bits each hold the 24 of v (an infinity is its first part)
-        h[0][e] = __bfloat162float(__float2bfloat16_rn(v[e]));
-        const bool fin = fabsf(h[0][e]) < __uint_as_float(0x7f800000u);
-        const float left1 = fin ? v[e] - h[0][e] : 0.f;
-        h[1][e] = __bfloat162float(__float2bfloat16_rn(left1));
-        h[2][e] = left1 - h[1][e];
+        float part[3];
+        parts_of(v[e], part);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) h[i][e] = part[i];
       }
       const int64_t at = static_cast<int64_t>(r) * rm + j, all = static_cast<int64_t>(p.rows) * rm;
       *reinterpret_cast<float4*>(p.v + at) = make_float4(v[0], v[1], v[2], v[3]);

@@ -71,3 +71,80 @@ def test_narrow_products_that_cancel_keep_their_last_bits(tts, path, xdt, odt): 
     out = run_project(tts, c, row_stream=of, stream_adapter=sa, odt=odt)
     want = torch.where(adapter >= 0, c["scale"][adapter.clamp(min=0).long()], 0.0)[:, None] * t[:, None] * col * 2.0 ** -18
     assert torch.equal(out[of >= 0].double(), want[of >= 0].double())
+
+
+def close(out, y, mass, k, rank_max, odt):
+    """Within check_project's bound of the float64 values."""
+    bound = (k / 8 + rank_max + 24) * 2.0 ** -23 * mass + 1e-30
+    if odt == "bf16":
+        bound = bound + R.HALF["bf16"] * y.abs() * (1 + 2.0 ** -8)
+    return ((out.double() - y).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("path", list(PATHS))
+@pytest.mark.parametrize("xdt,odt", [("bf16", "f32"), ("e4m3", "bf16")])
+def test_infinities_of_an_adapter_are_those_of_the_formula(tts, path, xdt, odt):  # noqa: F811
+    """x A^T of small whole numbers (few bits each) against infinite entries of B of either sign, and
+    an infinite scale: an infinity of the products' sign where all agree, NaN where they do not or
+    where 0 meets an infinity."""
+    rows, n, k, streams = PATHS[path]
+    c = project_case(rows + 1, rows, n, k, xdt, 4, 16)
+    g = gen(rows)
+    whole = lambda *s: torch.randint(-1, 2, s, generator=g, device="cuda").float()  # noqa: E731
+    c["x"] = whole(rows, k).to(c["x"].dtype)
+    if xdt == "e4m3":
+        c["x_scale"].fill_(1.0)
+    c["rank"][:] = ints([16, 13, 1, 9])
+    c["scale"][:] = torch.tensor([1.0, 0.5, float("inf"), -1.0], device="cuda")
+    live = torch.arange(16, device="cuda") < c["rank"][:, None]
+    c["a"] = torch.where(live[..., None], whole(4, 16, k), float("nan")).bfloat16()
+    b = randn(g, 4, n, 16, dt="bf16", std=0.2).float()
+    b[0, 5, 3], b[0, 6, 2], b[0, 6, 7] = float("inf"), float("inf"), float("-inf")
+    b[1, 7], b[2, 9, 0], b[3, n - 1, 8] = float("inf"), float("-inf"), float("-inf")
+    c["b"] = torch.where(live[:, None], b, float("nan")).bfloat16()
+    of = segments(path)
+    sa = ints([(3 * i) % 5 - 1 for i in range(streams)])
+    adapter = torch.where(of >= 0, sa[of.clamp(min=0).long()], -1)
+    out = run_project(tts, c, row_stream=of, stream_adapter=sa, odt=odt)
+    for i in range(4):
+        at = (adapter == i).nonzero()[:, 0]
+        r = int(c["rank"][i])
+        bi = c["b"][i, :, :r].double()
+        v = (c["x"][at].double() @ c["a"][i, :r].double().T) * c["scale"][i].double()
+        odd = (~bi.isfinite()).any(1) if i != 2 else torch.ones(n, dtype=torch.bool, device="cuda")
+        assert at.numel() > 0 and odd.any()
+        for col in odd.nonzero()[:, 0].tolist():
+            want = (v * bi[col]).sum(1)     # (elementwise: an infinity for each that the formula has)
+            got = out[at, col].double()
+            assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isposinf(), want.isposinf())
+            assert torch.equal(got.isneginf(), want.isneginf())
+        if i != 2:
+            d = dict(c, x=c["x"][at][:, :], b=c["b"].float().nan_to_num(0.0, 0.0, 0.0).bfloat16())
+            y, mass = R.project(d["x"], d["w"], d["a"], d["b"], d["rank"], d["scale"], torch.full((at.numel(),), i),
+                                None if xdt == "bf16" else c["x_scale"][at], c["w_scale"])
+            assert close(out[at][:, ~odd], y[:, ~odd], mass[:, ~odd], k, 16, odt)
+
+
+@pytest.mark.parametrize("path", list(PATHS))
+@pytest.mark.parametrize("xdt,odt", [("bf16", "f32"), ("e4m3", "bf16")])
+def test_narrow_products_near_the_largest_f32_stay_finite(tts, path, xdt, odt):  # noqa: F811
+    """x A^T of 3.4e38, past bf16's largest value, against a small B."""
+    rows, n, k, streams = PATHS[path]
+    c = project_case(rows + 2, rows, n, k, xdt, 4, 16)
+    x = torch.zeros(rows, k, device="cuda")
+    x[:, 0] = 1 - 2 * (torch.arange(rows, device="cuda") % 2)
+    c["x"] = x.to(c["x"].dtype)
+    if xdt == "e4m3":
+        c["x_scale"].fill_(1.0)
+    c["w"].zero_()
+    c["rank"][:] = 3
+    c["scale"][:] = torch.tensor([3.4e38, -3.4e38, 3.4028234e38, 3.39e38], device="cuda")
+    c["a"].zero_()
+    c["a"][:, :3, 0] = 1.0
+    c["b"] = (randn(gen(3), 4, n, 16) * 2.0 ** -120).bfloat16()
+    of = segments(path)
+    sa = ints([(3 * i) % 5 - 1 for i in range(streams)])
+    adapter = torch.where(of >= 0, sa[of.clamp(min=0).long()], -1)
+    out = run_project(tts, c, row_stream=of, stream_adapter=sa, odt=odt)
+    y, mass = R.project(c["x"], c["w"], c["a"], c["b"], c["rank"], c["scale"], adapter.cpu(), c["x_scale"], c["w_scale"])
+    assert close(out[of >= 0], y[of >= 0], mass[of >= 0], k, 16, odt)
