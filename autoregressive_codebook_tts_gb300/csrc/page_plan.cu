@@ -30,9 +30,12 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
 }
 
 // Inclusive sums over the block of two values a thread, each held at its cap (so that 32 bits hold
-// them; the caps are at most 2^30 + 1).
-__device__ __forceinline__ void block_scan(uint32_t& a, uint32_t& b, uint32_t cap_a, uint32_t cap_b, uint2* s_warp) {
+// them; the caps are at most 2^30 + 1); returns the sum of a before this thread.  (Held at the cap
+// too: the inclusive sum less the thread's own would be too small there.)
+__device__ __forceinline__ uint32_t block_scan(uint32_t& a, uint32_t& b, uint32_t cap_a, uint32_t cap_b, uint2* s_warp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  a = min(a, cap_a);
+  b = min(b, cap_b);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t x = __shfl_up_sync(kFull, a, o), y = __shfl_up_sync(kFull, b, o);
@@ -42,12 +45,16 @@ __device__ __forceinline__ void block_scan(uint32_t& a, uint32_t& b, uint32_t ca
     }
   }
   if (lane == 31) s_warp[warp] = make_uint2(a, b);
+  uint32_t before = __shfl_up_sync(kFull, a, 1);
+  if (lane == 0) before = 0;
   __syncthreads();
   for (int w = 0; w < warp; ++w) {
     a = min(a + s_warp[w].x, cap_a);
     b = min(b + s_warp[w].y, cap_b);
+    before = min(before + s_warp[w].x, cap_a);
   }
   __syncthreads();
+  return before;
 }
 
 // The map entries of row r, which is of stream b (or of none: b < 0).
@@ -160,10 +167,10 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PagePlanParam
     const int b = b0 + tid;
     const uint32_t give = b < p.B ? s_give[b] : 0, need = b < p.B ? s_need[b] : 0;
     uint32_t x = give, y = need;
-    block_scan(x, y, cap, cap, s_warp);
+    const uint32_t ahead = block_scan(x, y, cap, cap, s_warp);
     if (tid == kThreads - 1) s_carry = make_uint2(x, y);
     if (b < p.B) {
-      s_give[b] = min(freed + x, cap) - min(give, x);
+      s_give[b] = min(freed + ahead, cap);
       s_from[b] = min(asked + y, cap);   // (with its own for now)
     }
     __syncthreads();

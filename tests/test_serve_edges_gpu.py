@@ -1,5 +1,6 @@
 """Inputs of the calls that serve many requests at once that the contract allows and that are easily
-missed: adapters named by any negative number, on each of the projection's kernels.
+missed: adapters named by any negative number, infinities, terms that cancel, on each of the
+projection's kernels; tables that hold more pages than there are.
 
 Tolerances are those of test_serve_gpu (check_project); what is compared with equality is exact
 in f32.
@@ -8,7 +9,7 @@ import pytest
 import torch
 
 import serve_ref as R
-from test_serve_gpu import I32, check_project, flag, gen, ints, project_case, randn, run_project, tts  # noqa: F401
+from test_serve_gpu import I32, Pool, check_project, flag, gen, ints, project_case, randn, run_project, tts  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +149,21 @@ def test_narrow_products_near_the_largest_f32_stay_finite(tts, path, xdt, odt): 
     out = run_project(tts, c, row_stream=of, stream_adapter=sa, odt=odt)
     y, mass = R.project(c["x"], c["w"], c["a"], c["b"], c["rank"], c["scale"], adapter.cpu(), c["x_scale"], c["w_scale"])
     assert close(out[of >= 0], y[of >= 0], mass[of >= 0], k, 16, odt)
+
+
+@pytest.mark.parametrize("B,n_pages,listed,ended", [
+    (2, 6, 0, [0, 1]),                # the second's pages begin on the list and end past it
+    (3, 6, 2, [0, 1, 2]),
+    (9, 5, 0, [1, 4, 8]),             # the sum is past all pages before the last
+    (70, 20, 7, list(range(0, 70, 2))),
+    (1100, 3000, 0, list(range(1100))),   # in the third batch of streams
+    (4096, 700, 100, list(range(5, 4096)))])
+def test_pages_held_twice_go_to_the_list_in_order_until_it_is_full(tts, B, n_pages, listed, ended):  # noqa: F811
+    pool = Pool(tts, B, 64, 16, n_pages, 64, seed=B)
+    pool.n_free.fill_(listed)
+    pool.table.copy_(torch.randint(-1, n_pages, (B, 4), generator=gen(B), device="cuda", dtype=I32))
+    pool.table[:2] = ints([[0, 1, 2, 3], [4, 3, 2, 1]])
+    new = [-1 if b in set(ended) else 0 for b in range(B)]
+    want = pool.step([0] * B, new)    # (compares table, list, maps and flags with the restatement)
+    assert want["n_free"] == n_pages and want["flags"] == {"page"}
+    pool.step([0] * B, [1 if n else 0 for n in new])
