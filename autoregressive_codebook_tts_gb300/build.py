@@ -16,7 +16,8 @@ LIB = os.path.join(BUILD, "libttsdecode.so")
 SOURCES = ["attn.cu", "small_kernels.cu", "api.cu", "noalloc.cu", "sample.cu", "layer.cu", "gemv_mma.cu", "prefill_attn.cu", "prefill_attn_tc.cu",
            "draft_api.cu", "kv_rows.cu", "rope.cu", "tree_attn.cu", "tree_attn_tc.cu",
            "serve_api.cu", "add_norm.cu", "page_plan.cu", "project.cu", "project_many.cu", "adapter_shrink.cu"]
-HEADERS = ["common.cuh", "kernels.h", "table_rows.cuh", "checks.h", "draft_kernels.h", "cache_view.cuh", "tree_plan.cuh", "serve_kernels.h", "project_parts.cuh"]
+HEADERS = ["common.cuh", "kernels.h", "table_rows.cuh", "checks.h", "draft_kernels.h", "cache_view.cuh", "tree_plan.cuh", "serve_kernels.h", "project_parts.cuh",
+           "project_plan.h", "project_tile.h"]
 ROOT = os.path.dirname(HERE)
 PUBLIC_HEADER = os.path.join(ROOT, "include", "tts_decode.h")
 

@@ -8,13 +8,11 @@
 
 #include "cache_view.cuh"
 #include "checks.h"
+#include "project_tile.h"
 #include "serve_kernels.h"
 
 namespace tts {
 namespace {
-
-constexpr int kM = 128;               // rows of a product's first operand a tile
-constexpr int kRowBytes = 128;        // bytes of K a swizzled row holds
 
 // ---------------------------------------------------------------------------
 // The adapter of row r: -1 none, -2 the row is of no request.
