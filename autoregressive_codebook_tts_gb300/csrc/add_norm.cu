@@ -125,9 +125,11 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) add_norm_kernel(const Add
     if (lane == 0) s_top[warp] = top;
     __syncthreads();
     top = __reduce_max_sync(kFull, lane < nt / 32 ? s_top[lane] : 0u);
-    const bool bad = top >= 0x7f800000u, plain = bad || top == 0;   // plain: codes 0
     const float largest = __uint_as_float(top), inv = E4m3Code::kTop / largest;
-    if (t == 0) p.out_scale[row] = bad ? __uint_as_float(0x7fc00000u) : top == 0 ? 0.f : largest * (r / u) * (1.0f / E4m3Code::kTop);
+    // (u may be half the root: y can be past f32's range where the products are not)
+    const float most_y = largest * (r / u);
+    const bool bad = top >= 0x7f800000u || (top != 0 && !(most_y < __uint_as_float(0x7f800000u))), plain = bad || top == 0;   // plain: codes 0
+    if (t == 0) p.out_scale[row] = bad ? __uint_as_float(0x7fc00000u) : top == 0 ? 0.f : most_y * (1.0f / E4m3Code::kTop);
     uint32_t w[V][2], d[V][2];
     bool near = false;
 #pragma unroll

@@ -167,3 +167,23 @@ def test_pages_held_twice_go_to_the_list_in_order_until_it_is_full(tts, B, n_pag
     want = pool.step([0] * B, new)    # (compares table, list, maps and flags with the restatement)
     assert want["n_free"] == n_pages and want["flags"] == {"page"}
     pool.step([0] * B, [1 if n else 0 for n in new])
+
+
+@pytest.mark.parametrize("xdt", ["f32", "bf16"])
+def test_norm_codes_of_rows_past_the_largest_f32(tts, xdt):  # noqa: F811
+    """max |y| past f32's range is an infinity in y: scale NaN, codes 0; below it the scale is finite."""
+    n, rows = 512, 6
+    x = randn(gen(1), rows, n).sign().to(R.TORCH[xdt]) * 1.5      # the mean square is 2.25: y = +-gamma
+    gamma = torch.full((n,), 1e-3, device="cuda")
+    x[1, 7] = 1.9375                   # r is just below 1 / 1.5: y = 1.29 gamma there
+    x[3, 7], x[4, 7] = 1.9375, -1.9375
+    gamma[7] = 3e38
+    x[0, 7], x[2, 7], x[5, 7] = 1.5, 0.5, 0.0
+    out, scale = torch.ones(rows, n, device="cuda").to(R.TORCH["e4m3"]), torch.empty(rows, device="cuda")
+    tts.tts_add_rms_norm(x, None, None, gamma, 0.0, out, out_scale=scale)
+    past = torch.tensor([False, True, False, True, True, False], device="cuda")
+    y = R.norm(x, None, gamma, 0.0, None)[1].abs().amax(-1)
+    assert torch.equal(y > 3.41e38, past) and (y[~past] < 3.1e38).all()
+    assert torch.equal(scale.isnan(), past) and scale[~past].isfinite().all()
+    assert (out[past].view(torch.uint8) == 0).all()
+    assert ((scale[~past].double() - y[~past] / 448).abs() <= 41 * 2.0 ** -24 * y[~past] / 448).all()
