@@ -187,3 +187,118 @@ def test_norm_codes_of_rows_past_the_largest_f32(tts, xdt):  # noqa: F811
     assert torch.equal(scale.isnan(), past) and scale[~past].isfinite().all()
     assert (out[past].view(torch.uint8) == 0).all()
     assert ((scale[~past].double() - y[~past] / 448).abs() <= 41 * 2.0 ** -24 * y[~past] / 448).all()
+
+
+# ---------------------------------------------------------------------------
+# Requests of many rows each: what reaches the adapters' products on the tensor cores
+# ---------------------------------------------------------------------------
+def batch(path, xdt, seed):
+    """A case with its row map and the requests' adapters, four of them and none."""
+    rows, n, k, streams = PATHS[path]
+    c = project_case(seed + rows, rows, n, k, xdt, 4, 32)
+    c["rank"][:] = ints([32, 29, 8, 17])
+    live = torch.arange(32, device="cuda") < c["rank"][:, None]
+    g = gen(seed)
+    c["a"] = torch.where(live[..., None], randn(g, 4, 32, k, std=k ** -0.5), float("nan")).bfloat16()
+    c["b"] = torch.where(live[:, None], randn(g, 4, n, 32, std=0.2), float("nan")).bfloat16()
+    of = segments(path)
+    sa = ints([(3 * i) % 5 - 1 for i in range(streams)])
+    return c, of, sa, torch.where(of >= 0, sa[of.clamp(min=0).long()], -1)
+
+
+@pytest.mark.parametrize("path", list(PATHS))
+@pytest.mark.parametrize("xdt,odt", [("bf16", "f32"), ("e4m3", "bf16")])
+def test_a_bad_adapter_or_row_changes_no_other_row(tts, path, xdt, odt):  # noqa: F811
+    c, of, sa, adapter = batch(path, xdt, 40)
+    n = c["w"].shape[0]
+    clean = run_project(tts, c, row_stream=of, stream_adapter=sa, odt=odt)
+    check_project(c, clean, adapter, dead=of < 0, odt=odt)
+    d = dict(c, a=c["a"].clone(), b=c["b"].clone())
+    d["b"][1, 5, 3], d["b"][1, 7], d["b"][1, n - 1, 28] = float("inf"), float("nan"), float("-inf")
+    d["a"][3, 4, 100] = float("nan")
+    out = run_project(tts, d, row_stream=of, stream_adapter=sa, odt=odt)
+    good = (adapter != 1) & (adapter != 3)
+    assert torch.equal(out[good], clean[good]) and out[adapter == 3].isnan().all()
+    one, ref = out[adapter == 1], clean[adapter == 1]
+    odd = torch.zeros(n, dtype=torch.bool, device="cuda")
+    odd[[5, 7, n - 1]] = True
+    assert one[:, odd].isfinite().sum() == 0 and one[:, 7].isnan().all() and torch.equal(one[:, ~odd], ref[:, ~odd])
+    for r in (0, 17, int((of >= 0).sum()) - 1):
+        d = dict(c, x=c["x"].clone())
+        if xdt == "bf16":
+            d["x"][r, 17] = float("nan")
+        else:
+            d["x_scale"] = c["x_scale"].clone()
+            d["x_scale"][r] = float("nan")
+        out = run_project(tts, d, row_stream=of, stream_adapter=sa, odt=odt)
+        rest = torch.arange(of.numel(), device="cuda") != r
+        assert out[r].isnan().all() and torch.equal(out[rest], clean[rest])
+
+
+@pytest.mark.parametrize("path", list(PATHS))
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+def test_adapters_beside_no_shared_weights(tts, path, odt):  # noqa: F811
+    """W = 0: the output is the adapter's part alone, so its 2-norm shows how x A^T was held."""
+    c, of, sa, adapter = batch(path, "bf16", 50)
+    c["w"].zero_()
+    out = run_project(tts, c, row_stream=of, stream_adapter=sa, odt=odt)
+    y, _ = R.project(c["x"], c["w"], c["a"], c["b"], c["rank"], c["scale"], adapter.cpu())
+    live = of >= 0
+    assert (out[live].double() - y[live]).norm() <= (1e-6 if odt == "f32" else 2.0 ** -8) * y[live].norm()
+
+
+@pytest.mark.parametrize("path", list(PATHS))
+@pytest.mark.parametrize("xdt", ["bf16", "e4m3"])
+def test_a_poisoned_workspace_of_more_rows(tts, path, xdt):  # noqa: F811
+    c, of, sa, adapter = batch(path, xdt, 60)
+    rows, k = c["x"].shape
+    pool = tts.adapters(c["a"], c["b"], rank=c["rank"], scale=c["scale"])
+    ws = tts.project_workspace(rows + 100, c["w"].shape[0], k, xdt, pool)
+    first = run_project(tts, c, row_stream=of, stream_adapter=sa)
+    for fill in (255, 0, 127):    # NaN, 0, and values past any result
+        ws.fill_(fill)
+        assert torch.equal(run_project(tts, c, row_stream=of, stream_adapter=sa, ws=ws), first)
+    few = rows - rows // 8
+    d = dict(c, x=c["x"][:few], x_scale=None if c["x_scale"] is None else c["x_scale"][:few])
+    ws.fill_(255)
+    check_project(d, run_project(tts, d, row_stream=of[:few].contiguous(), stream_adapter=sa, ws=ws), adapter[:few], dead=of[:few] < 0)
+
+
+@pytest.mark.parametrize("path", list(PATHS))
+@pytest.mark.parametrize("xdt,odt", [("bf16", "bf16"), ("e4m3", "f32")])
+def test_requests_replayed_and_on_two_streams(tts, path, xdt, odt):  # noqa: F811
+    c, of, sa, adapter = batch(path, xdt, 70)
+    rows, k = c["x"].shape
+    n = c["w"].shape[0]
+    eager = run_project(tts, c, row_stream=of, stream_adapter=sa, odt=odt)
+    pool = tts.adapters(c["a"], c["b"], rank=c["rank"], scale=c["scale"])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [tts.project_workspace(rows, n, k, xdt, pool) for _ in streams]
+    outs = [torch.zeros_like(eager) for _ in streams]
+    maps = [(of.clone(), sa.clone()) for _ in streams]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        run_project(tts, c, row_stream=maps[0][0], stream_adapter=maps[0][1], ws=spaces[0], out=outs[0], stream=streams[0])
+    for _ in range(4):
+        for o in outs:
+            o.fill_(-77.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(streams[0]):
+            for _ in range(3):
+                graph.replay()
+        with torch.cuda.stream(streams[1]):
+            for _ in range(5):
+                run_project(tts, c, row_stream=maps[1][0], stream_adapter=maps[1][1], ws=spaces[1], out=outs[1])
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], eager) and torch.equal(outs[1], eager)
+    # another batch in the same graph: other requests, other adapters, more rows of none
+    maps[0][0].copy_((of + 1).clamp(max=sa.numel() - 1) * (of >= 0) - (torch.arange(rows, device="cuda") % 9 == 4).to(I32) * 1000)
+    maps[0][1].copy_(sa.flip(0))
+    outs[0].fill_(-77.0)
+    dead = maps[0][0] < 0
+    now = torch.where(dead, -1, maps[0][1][maps[0][0].clamp(min=0).long()])
+    with torch.cuda.stream(streams[0]):
+        graph.replay()
+    torch.cuda.synchronize()
+    check_project(c, outs[0], now, dead=dead, odt=odt)
