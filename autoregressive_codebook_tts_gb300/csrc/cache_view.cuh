@@ -65,8 +65,9 @@ __device__ __forceinline__ void each_marked(uint32_t (&d)[N / 4], const float (&
 // most that, so steps is one more than the roundings.)  The other entries are decided by the exact
 // remainder x - q s, which one fused multiply-add gives with its right sign; one at a time, for half a
 // percent of the entries of a bf16 row are on a border or beside it (none of an f32 row's), which leaves
-// most warps with a few.  (No entry is that far below s that the remainder could underflow: tiny rows
-// are scaled up first.)
+// most warps with a few; but all of a lane's at once where each of its words has one, as in rows whose
+// quotients are ties (16 x 1024 rows of 8 heads of them, bf16 to int8: 39 us, one at a time 59).  (No
+// entry is that far below s that the remainder could underflow: tiny rows are scaled up first.)
 template <typename Code, int N>
 __device__ __forceinline__ bool fast_codes(const float (&x)[N], float inv, int steps, uint32_t (&w)[N / 4], uint32_t (&d)[N / 4]) {
   const float below = __uint_as_float(__float_as_uint(inv) - steps), above = __uint_as_float(__float_as_uint(inv) + steps);
@@ -87,11 +88,20 @@ __device__ __forceinline__ void codes(const float (&x)[N], float s, uint32_t (&w
   if (fast_codes<Code>(x, inv, 3, w, d) || tiny) {
     const float up = tiny ? 1.152921504606846976e18f : 1.0f;   // 2^60
     const float su = s * up, iu = 1.0f / su;
-    if (tiny) {
+    bool all = true;
 #pragma unroll
-      for (int e = 0; e < N / 4; ++e) d[e] = ~0u;
+    for (int e = 0; e < N / 4; ++e) all = all && d[e] != 0;
+    all = all || tiny;
+    if (all) {
+#pragma unroll
+      for (int e = 0; e < N / 4; ++e) {
+        w[e] = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[e] |= Code::nearest(x[4 * e + k] * up, su, iu) << (8 * k);
+      }
+    } else {
+      each_marked(d, x, w, [&](float y, int) { return Code::nearest(y * up, su, iu); });
     }
-    each_marked(d, x, w, [&](float y, int) { return Code::nearest(y * up, su, iu); });
   }
 }
 

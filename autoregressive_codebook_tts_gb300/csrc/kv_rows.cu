@@ -7,7 +7,8 @@
 // K and V of a row go through the same lane (two loads in flight at least); many rows to read
 // are read two a lane.
 //
-// 16001 rows of 8 heads by slot, bf16 into e4m3 and int8: 24.5 us (4.0 TB/s, the quantiser's issue slots),
+// 16001 rows of 8 heads by slot, bf16 into e4m3 24.7 us, into int8 25.8 (4.0 and 3.8 TB/s, 0.61 issue a cycle:
+// a warp's loads, reduction and codes follow one another, one row of K and of V a lane in flight),
 // into bf16 22 (6.0 TB/s); f32 into either 8-bit type 27 (6.1 TB/s, 0.90 of the measured copy rate).
 // (35 us with the borders' test on each mantissa and a whole lane's entries decided again where one
 // was near; 8 entries a lane for bf16: 30 for 28 in e4m3, 32 for 36 in int8 before that went.)  36.8 k rows back to
