@@ -302,3 +302,40 @@ def test_requests_replayed_and_on_two_streams(tts, path, xdt, odt):  # noqa: F81
         graph.replay()
     torch.cuda.synchronize()
     check_project(c, outs[0], now, dead=dead, odt=odt)
+
+
+@pytest.mark.parametrize("rows,n,k,streams", [(1, 1, 8, 1), (200, 1, 8, 200), (200, 1, 8, 5), (400, 5, 24, 7), (1100, 3400, 8, 9),
+                                              (1100, 3400, 40, 9), (257, 9700, 16, 2)])
+@pytest.mark.parametrize("xdt,rank_max", [("bf16", 8), ("e4m3", 24), ("bf16", None)])
+def test_the_smallest_k_and_n(tts, rows, n, k, streams, xdt, rank_max):  # noqa: F811
+    if xdt == "e4m3":
+        k = -(-k // 16) * 16
+    c = project_case(rows + k, rows, n, k, xdt, None if rank_max is None else 3, rank_max)
+    of = (torch.arange(rows, device="cuda") * streams // rows).to(I32)
+    sa = ints([i % 4 - 1 for i in range(streams)])
+    out = run_project(tts, c, row_stream=of, stream_adapter=None if rank_max is None else sa, pad=1)
+    check_project(c, out, None if rank_max is None else sa[of.long()])
+
+
+@pytest.mark.parametrize("streams", [70000, 60, None])   # on the CUDA cores, on pairs, no adapters
+def test_outputs_past_32_bit_offsets(tts, streams):  # noqa: F811
+    rows, n, k = 70000, 32768, 64
+    g = gen(80)
+    x, w = randn(g, rows, k, dt="bf16"), randn(g, n, k, dt="bf16", std=0.05)
+    a, b = randn(g, 5, 8, k, dt="bf16", std=0.1), randn(g, 5, n, 8, dt="bf16", std=0.2)
+    out = torch.full((rows, n), -77.0, dtype=torch.bfloat16, device="cuda")
+    of = sa = pool = ws = None
+    if streams is not None:
+        of = (torch.arange(rows, device="cuda") * streams // rows).to(I32)
+        of[5::997] = -1
+        sa = (torch.arange(streams, device="cuda") % 6 - 1).to(I32)
+        pool = tts.adapters(a, b)
+        ws = tts.project_workspace(rows, n, k, "bf16", pool)
+    tts.tts_project_rows(x, w, out, ws, adapters=pool, stream_adapter=sa, row_stream=of)
+    at = torch.cat([torch.arange(0, rows, 1777, device="cuda"), torch.arange(rows - 40, rows, device="cuda"),
+                    torch.arange(5, rows, 9970, device="cuda")])
+    adapter = torch.full((at.numel(),), -1) if of is None else torch.where(of[at] >= 0, sa[of[at].clamp(min=0).long()], -1).cpu()
+    y, mass = R.project(x[at], w, a, b, [8] * 5, [1.0] * 5, adapter)
+    dead = torch.zeros(at.numel(), dtype=torch.bool, device="cuda") if of is None else of[at] < 0
+    assert close(out[at][~dead], y[~dead], mass[~dead], k, 8, "bf16") and (out[at][dead] == -77.0).all()
+    assert streams is None or dead.any()
