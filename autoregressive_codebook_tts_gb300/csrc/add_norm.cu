@@ -4,7 +4,7 @@
 // is reduced by shuffles and through shared memory, and y leaves in the output's type.  Sums and
 // statistics are in f32.  Nothing is read twice, so the kernel is bound by HBM on many rows and by the
 // launch and one round trip to memory on few.  n 2048: 32 rows 2.7 us; 6001 rows, bf16 throughout 18.2
-// (5.4 TB/s), f32 in and bf16 out 27.6 (6.2 TB/s, 0.92 of the measured copy rate), e4m3 out 22.5 (3.8 TB/s; two
+// (5.4 TB/s), f32 in and bf16 out 27.6 (6.2 TB/s, 0.92 of the measured copy rate), e4m3 out 22.9 (3.8 TB/s; two
 // more reductions a row and the codes).
 //
 // e4m3: the root is common to a row's entries and their largest, so the code of entry i is that

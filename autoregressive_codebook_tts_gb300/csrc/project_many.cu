@@ -9,9 +9,9 @@
 // the same rows of x, whose notes it takes once.
 //
 // K 2048, us: without adapters 4096 rows x 4096 columns in bf16 40.2 (1.71 PFLOP/s; the library's
-// product 36.5), 6000 x 12288 in e4m3 92.7; 4093 rows of 7 requests x 4096, rank 32, bf16 77; 6000 rows x
-// 12288 in e4m3, rank 16, of 40 requests 277.  (With two parts of v for bf16 outputs 76 and 256, and 171
-// with 5 requests; of that form 224 rows and one accumulator took 79, 247 and 202, 4093 rows of 40 requests
+// product 36.5), 6000 x 12288 in e4m3 92.7; 4093 rows of 7 requests x 4096, rank 32, bf16 78; 6000 rows x
+// 12288 in e4m3, rank 16, of 5 requests 180, of 40 278.  (With two parts of v for bf16 outputs 76, 171 and
+// 256; of that form 224 rows and one accumulator took 79, 202 and 247, 4093 rows of 40 requests
 // with rank 64 124 against 105, 1000 rows of ten 90 against 72: runs then have more room, but each epilogue
 // stands between two tiles' products.)
 //

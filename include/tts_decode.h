@@ -604,8 +604,11 @@ tts_status tts_tree_commit(const tts_kv_cache* cache, const tts_kv_desc* desc, c
  * own, over a paged cache whose pages come and go.  The paper has no counterpart.  A step is:
  * tts_page_plan (from the requests' lengths: pages, and every row's request, position and cache
  * slot), then per layer tts_add_rms_norm, tts_project_rows, tts_rope_rows at row_pos,
- * tts_kv_write_slots and an attention over the same block table.  Row counts are fixed on the
- * host and rows without a request are marked on the device, so that a step can be captured.
+ * tts_kv_write_slots and an attention over the same block table: tts_tree_attn takes the rows of a
+ * plan with T > 0 (n_nodes = n_rows, T <= TTS_MAX_TREE_NODES; long prompts go in over several steps).
+ * No attention here takes packed rows (T = 0): they are for one of the caller's own, which row_start
+ * and n_rows describe.  Row counts are fixed on the host and rows without a request are marked on
+ * the device, so that a step can be captured; such rows cost what others do.
  * The conventions above hold (device pointers, stream order, status, err_flag, alignment); the
  * int32 and int64 arrays of tts_page_plan, row_stream, stream_adapter and row_slot need only the
  * alignment of their entries.
@@ -651,8 +654,9 @@ typedef struct {
  * Rows of many requests through one shared projection, with every request's own adapter:
  *   out[r] = x[r] W^T + scale_a (x[r] A_a^T) B_a^T,   a = stream_adapter[s], s = row_stream[r]
  * x and W are bf16, or both E4M3 codes with a scale a row (x[r] stands for x_scale[r] * codes,
- * W's row n for w_scale[n] * codes).  Products accumulate in f32 and x A^T is held in f32; the
- * sum is rounded to out_dtype once.
+ * W's row n for w_scale[n] * codes).  Products accumulate in f32 and x A^T is held in f32 (on the
+ * tensor cores as three bf16 values whose sum it is, exact for entries of 2^-100 and more in
+ * magnitude); the sum is rounded to out_dtype once.
  *   x: device rows of x_dtype, row r at x + r*x_stride elements; w: dense [n][k].
  *   x_scale [rows], w_scale [n]: device f32 for E4M3, else NULL.
  *   k: a multiple of 8 (bf16) or 16 (E4M3), at most 65536; n: at most 2^20; rows at most 2^20.
@@ -660,7 +664,11 @@ typedef struct {
  *   row_stream: device int32 [rows], or NULL: row r is request r's.  A negative entry marks a
  *        row without a request: its out row is left as it was.  Any order is allowed; rows of a
  *        request that lie together are the fastest.
- *   stream_adapter: device int32 [n_streams]; negative: the shared projection alone.
+ *   stream_adapter: device int32 [n_streams]; negative: the shared projection alone.  n_streams
+ *        also stands for the requests of this step where the kernels are chosen: the adapters'
+ *        products go to the tensor cores from 128 rows on where row_stream is given and n_streams is at
+ *        most rows / 8 (for more than 256 rows that fill the device: rows / 32).  With more entries than
+ *        that for few requests of many rows, the result is right but slower.
  *   A request outside [0, n_streams), or an adapter at or above n_adapters, sets
  *        TTS_EFLAG_ID_RANGE and counts as one without an adapter; a rank outside
  *        [0, rank_max] is clamped and sets TTS_EFLAG_NVALID.
