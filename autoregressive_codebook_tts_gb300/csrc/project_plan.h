@@ -18,12 +18,13 @@ constexpr int max_groups(bool wide) { return wide ? 3 : 4; }
 constexpr int max_threads(bool wide) { return max_groups(wide) * 128 + 64; }
 constexpr int kRedLd = kM + 16;       // floats between the rows of a partial
 constexpr int kMaxV = 64 * 1024;      // bytes of v a CTA holds at most
-// Shared memory that a CTA of a cluster asks for at least.  A CTA waits for tensor memory until whoever
-// has it on its SM leaves, and then for its cluster at a barrier: two CTAs that so wait for one another, of one
-// cluster or of clusters that cross, must not meet on an SM.  This is more than half of an SM's, and
-// more than a clustered CTA of gemv_mma.cu leaves (it takes 73 KB at least; the other clustered kernels
-// with tensor memory take 180 KB and more).
-constexpr int kClusterSmem = 160 * 1024;
+// Shared memory that a CTA asks for at least.  A CTA waits for tensor memory until whoever has it on its
+// SM leaves, and then for its cluster at a barrier: two CTAs that so wait for one another, of one cluster
+// or of clusters that cross, must not meet on an SM, nor one of no cluster wait there between two that
+// are of one.  This is more than half of an SM's, and more than a clustered CTA of gemv_mma.cu leaves (it
+// takes 73 KB at least; the other clustered kernels with tensor memory take 180 KB and more).  All
+// columns are asked for, so no SM could work on two CTAs anyway.
+constexpr int kLeastSmem = 160 * 1024;
 
 struct Plan {
   int nb, nbr;          // x rows a tile (a multiple of 16), and that rounded up to 32
@@ -67,7 +68,7 @@ void lay_out(Plan& q, int rank_max, size_t budget) {
   q.b_off = ring + v;
   q.bar_off = q.b_off + b;
   q.smem = 1024 + q.bar_off + kBarBytes;
-  if (q.split > 1 && q.smem < kClusterSmem) q.smem = kClusterSmem;
+  if (q.smem < kLeastSmem) q.smem = kLeastSmem;
 }
 
 // The plan of rows x (n columns of W, k entries of es bytes) with adapters of up to rm ranks (0: none; tc:
